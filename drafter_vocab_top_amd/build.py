@@ -15,7 +15,9 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(HERE, "libtopk_cols.so")
 SOURCES = [os.path.join(CSRC, n) for n in ("topk_col.hip", "topk_row.hip", "topk_onewave.hip",
-                                            "topk_sample.hip", "topk_noalloc.hip", "topk_cols_api.cpp")]
+                                            "topk_sample.hip", "topk_noalloc.hip", "topk_cols_api.cpp",
+                                            "topk_adjust.hip", "topk_count.hip", "topk_verify.hip", "topk_plan.hip",
+                                            "topk_round_api.cpp")]
 OBJDIR = os.path.join(ROOT, "_build")
 # Per-source flags.  The column kernel takes its ticket before ranking and
 # publishing its list and reads the reply afterwards; the compiler's atomic
@@ -31,7 +33,8 @@ EXTRA_FLAGS = {"topk_col.hip": ["-mllvm", "-amdgpu-atomic-optimizer-strategy=Non
 # part of the top-k library).
 STREAM_SOURCE = os.path.join(CSRC, "stream_read.hip")
 STREAM_LIBRARY = os.path.join(HERE, "libstream_read.so")
-HEADERS = [os.path.join(CSRC, n) for n in ("topk_device.hpp", "topk_col_common.hpp", "topk_internal.hpp")] + \
+HEADERS = [os.path.join(CSRC, n) for n in ("topk_device.hpp", "topk_col_common.hpp", "topk_internal.hpp", "topk_draw.hpp",
+                                            "topk_round.hpp")] + \
           [os.path.join(INCLUDE, "topk_cols.h")]
 ARCH = "gfx950"
 

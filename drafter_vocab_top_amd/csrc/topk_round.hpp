@@ -1,0 +1,78 @@
+// The steps around the top-k in a round: launch arguments and entry points
+// of their kernels, and what the kernels share.
+#pragma once
+
+#include "topk_cols.h"
+
+#include "topk_device.hpp"
+
+namespace topk {
+
+// Parts of [0, total): the one of lane l is [start[l], start[l+1]) cut to
+// [0, total), or total / lanes entries each without a start array.
+struct Parts {
+    const int32_t* start;
+    uint32_t total;
+    uint32_t each;  // total / lanes (start == NULL)
+    __device__ __forceinline__ void range(uint32_t l, uint32_t& begin, uint32_t& end) const {
+        if (start) {
+            const int32_t b = start[l], e = start[l + 1];
+            begin = b < 0 ? 0u : min_u32((uint32_t)b, total);
+            end = e < 0 ? 0u : min_u32((uint32_t)e, total);
+            if (end < begin) end = begin;
+        } else {
+            begin = l * each;
+            end = begin + each;
+        }
+    }
+};
+
+// topk_cols_adjust (see the header): sizes narrowed to 32 bits where the
+// entry point has checked them.
+struct AdjustArgs {
+    const void* x;
+    void* out;
+    int64_t ld, out_ld;
+    uint32_t V, C, lanes;
+    Parts cols;               // the lanes' columns
+    const int32_t* counts;    // NULL: no history
+    int64_t counts_ld;
+    const uint32_t* seen;
+    int64_t seen_ld;
+    const float *repetition, *presence, *frequency;
+    const int32_t* drafts;    // NULL: none
+    Parts draft_parts;
+    const int32_t* bias_ids;  // NULL: none
+    const float* bias_values;
+    Parts bias_parts;
+    const uint32_t* mask;     // NULL: none
+    int64_t mask_ld;
+    int32_t mask_count;
+    const int32_t* mask_index;
+};
+hipError_t launch_adjust(int dtype, int layout, const AdjustArgs& a, hipStream_t stream);
+
+struct CountArgs {
+    uint32_t V, lanes;
+    const int32_t* ids;
+    Parts parts;
+    const int32_t *prompt_len, *fresh;
+    uint32_t* counts;
+    int64_t counts_ld;
+    uint32_t* seen;
+    int64_t seen_ld;
+};
+hipError_t launch_count(const CountArgs& a, hipStream_t stream);
+
+struct VerifyArgs {
+    topk_verify_args v;
+    Parts cols, draft_parts;
+};
+hipError_t launch_verify(const VerifyArgs& a, hipStream_t stream);
+
+hipError_t launch_plan_round(const topk_plan_args& a, hipStream_t stream);
+
+// The grid's y size is at most 65,535.
+constexpr int64_t kGridY = 65535;
+
+}  // namespace topk

@@ -34,12 +34,35 @@ LAYOUTS = {"col": 0, "row": 1}
 EXPORTED = ("topk_cols_create", "topk_cols_create_with_segments", "topk_cols_create_tuned",
             "topk_cols_run", "topk_cols_run_n", "topk_cols_run_mapped", "topk_cols_sample",
             "topk_cols_destroy", "topk_cols_status_string", "topk_cols_query", "topk_cols_check",
-            "topk_cols_debug_fail_waits", "topk_cols_run_noalloc")
+            "topk_cols_debug_fail_waits", "topk_cols_run_noalloc", "topk_cols_adjust", "topk_cols_count",
+            "topk_cols_verify", "topk_cols_plan")
 # kernel families of the column-contiguous layout ("one_wave": the baseline
 # design with one wave per column and no vocabulary split)
 ALGOS = {"auto": 0, "workgroup": 1, "one_wave": 3}
 
 _lib = None
+
+
+def _struct(name: str, fields: str):
+    """A ctypes structure from "type name" pairs, in the header's order."""
+    types = {"p": ctypes.c_void_p, "i64": ctypes.c_int64, "i32": ctypes.c_int32, "u64": ctypes.c_uint64,
+             "f64": ctypes.c_double}
+    pairs = [f.split() for f in fields.split(",")]
+    return type(name, (ctypes.Structure,), {"_fields_": [(n, types[t]) for t, n in pairs]})
+
+
+AdjustRulesArgs = _struct("topk_adjust_rules", (
+    "i64 V, i64 C, i64 lanes, i32 dtype, i32 layout, i64 ld, i64 out_ld, p col_start, p counts, i64 counts_ld, "
+    "p seen, i64 seen_ld, p repetition, p presence, p frequency, p drafts, p draft_start, i64 n_drafts, "
+    "p bias_start, p bias_ids, p bias_values, i64 n_bias, p mask, i64 mask_ld, i64 mask_count, p mask_index"))
+VerifyArgs = _struct("topk_verify_args", (
+    "i64 lanes, i32 dtype, i32 k, i32 kq, i64 C, p col_start, p target_values, p target_ids, i64 n_drafts, "
+    "p draft_start, p drafts, p draft_values, p draft_ids, f64 temperature, f64 top_p, u64 seed, u64 offset, "
+    "i64 max_tokens, p out_tokens, p out_count"))
+PlanArgs = _struct("topk_plan_args", (
+    "i64 lanes, i64 capacity, i32 block_size, p lens, p add, p held, p table, i64 table_ld, p free_ids, "
+    "i64 n_free_ids, p free_count, p out_held, p out_free_count, p out_refused, p out_col_start, p out_col_lane, "
+    "p out_col_pos, p out_slots"))
 
 
 class TopkError(RuntimeError):
@@ -85,6 +108,14 @@ def load(path: str = LIBRARY):
     lib.topk_cols_debug_fail_waits.restype = ctypes.c_int
     lib.topk_cols_run_noalloc.argtypes = [i64, i64, i32, i32, i32, i64, p, p, p, p]
     lib.topk_cols_run_noalloc.restype = ctypes.c_int
+    lib.topk_cols_adjust.argtypes = [ctypes.POINTER(AdjustRulesArgs), p, p, p]
+    lib.topk_cols_adjust.restype = ctypes.c_int
+    lib.topk_cols_count.argtypes = [i64, i64, p, i64, p, p, p, p, i64, p, i64, p]
+    lib.topk_cols_count.restype = ctypes.c_int
+    lib.topk_cols_verify.argtypes = [ctypes.POINTER(VerifyArgs), p]
+    lib.topk_cols_verify.restype = ctypes.c_int
+    lib.topk_cols_plan.argtypes = [ctypes.POINTER(PlanArgs), p]
+    lib.topk_cols_plan.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -271,6 +302,236 @@ def run_noalloc(x, V: int, C: int, k: int, dtype: str = "bf16", layout: str = "c
     if rc != TOPK_OK:
         raise TopkError(rc, "topk_cols_run_noalloc")
     return values, ids
+
+
+def _need(name: str, t, numel: int, device, dtype: str = "int32") -> int:
+    """Address of a contiguous GPU tensor of at least numel elements (0 for None)."""
+    if t is None:
+        return 0
+    if not t.is_cuda or t.device != device or str(t.dtype) != "torch." + dtype or t.numel() < numel \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {numel} elements on {device}")
+    return t.data_ptr()
+
+
+def _launch(what: str, device, stream, call) -> None:
+    """call(raw stream) with the tensors' device current (the current stream
+    by default)."""
+    import torch
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    if device.index == torch.cuda.current_device():
+        rc = call(s.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = call(s.cuda_stream)
+    if rc != TOPK_OK:
+        raise TopkError(rc, what)
+
+
+def history(V: int, lanes: int, device="cuda"):
+    """Empty token histories of `lanes` lanes: (counts, seen) as AdjustRules
+    reads and count_tokens updates them, zeroed int32 tensors (lanes, V) and
+    (lanes, ceil(V / 32))."""
+    import torch
+    return (torch.zeros((lanes, V), dtype=torch.int32, device=device),
+            torch.zeros((lanes, (V + 31) // 32), dtype=torch.int32, device=device))
+
+
+class AdjustRules:
+    """Penalties, biases and masks for logits (topk_cols_adjust).
+
+    Describes buffers that the caller keeps (and may update between calls):
+    the object holds references to the tensors and no state of its own.  All
+    are contiguous GPU tensors on one device, int32 unless said otherwise.
+
+    V, C, dtype, layout, ld: the matrix, as for TopkCols; out_ld: the
+        result's leading dimension (default: ld).
+    lanes, col_start: lane l owns columns col_start[l]..col_start[l+1]-1
+        (lanes + 1 entries), or C / lanes each without col_start.
+    counts (lanes, >= V), seen (lanes, >= ceil(V/32)): histories.
+    repetition, presence, frequency: (lanes,) float32.
+    drafts, draft_start: token ids of the lanes' drafts, packed; column j of
+        a lane takes its first j drafts as further output.
+    bias_start, bias_ids, bias_values (float32): packed lists per lane.
+    mask (masks, >= ceil(V/32)): bit r % 32 of word r / 32 allows row r;
+        mask_index (C,): the mask of each column, none where it is outside
+        the range (without it: mask c for column c).
+    """
+
+    def __init__(self, V: int, C: int, dtype: str = "bf16", layout: str = "col", ld: int | None = None,
+                 out_ld: int | None = None, lanes: int = 1, col_start=None, counts=None, seen=None, repetition=None,
+                 presence=None, frequency=None, drafts=None, draft_start=None, bias_start=None, bias_ids=None,
+                 bias_values=None, mask=None, mask_index=None):
+        if dtype not in DTYPES or layout not in LAYOUTS:
+            raise ValueError(f"dtype must be one of {list(DTYPES)}, layout one of {list(LAYOUTS)}")
+        self.V, self.C, self.dtype, self.layout = V, C, dtype, layout
+        self.ld = ld if ld is not None else (V if layout == "col" else C)
+        self.out_ld = out_ld if out_ld is not None else self.ld
+        self._tensors = tensors = dict(
+            col_start=col_start, counts=counts, seen=seen, repetition=repetition, presence=presence,
+            frequency=frequency, drafts=drafts, draft_start=draft_start, bias_start=bias_start, bias_ids=bias_ids,
+            bias_values=bias_values, mask=mask, mask_index=mask_index)
+        devices = {t.device for t in tensors.values() if t is not None}
+        if len(devices) > 1:
+            raise ValueError("the rules' tensors must be on one device")
+        self.device = devices.pop() if devices else None
+        words = (V + 31) // 32
+        for name, t, least in (("counts", counts, V), ("seen", seen, words), ("mask", mask, words)):
+            if t is not None and (t.dim() != 2 or t.shape[1] < least or (name != "mask" and t.shape[0] < lanes)):
+                raise ValueError(f"{name} must be a matrix with rows of at least {least} entries"
+                                 + ("" if name == "mask" else " for every lane"))
+        if (bias_ids is None) != (bias_values is None) or \
+                (bias_ids is not None and bias_ids.numel() != bias_values.numel()):
+            raise ValueError("bias_ids and bias_values must have the same length")
+        sizes = dict(col_start=lanes + 1, repetition=lanes, presence=lanes, frequency=lanes, draft_start=lanes + 1,
+                     bias_start=lanes + 1, mask_index=C)
+        floats = ("repetition", "presence", "frequency", "bias_values")
+        at = {n: _need(n, t, sizes.get(n, 0), self.device, "float32" if n in floats else "int32")
+              for n, t in tensors.items()}
+        # an empty tensor has no address; an empty list is the same as none
+        if bias_ids is not None and bias_ids.numel() == 0:
+            at.update(bias_start=0, bias_ids=0, bias_values=0)
+        if drafts is not None and drafts.numel() == 0:
+            at.update(drafts=0, draft_start=0)
+        self._args = AdjustRulesArgs(
+            V=V, C=C, lanes=lanes, dtype=DTYPES[dtype], layout=LAYOUTS[layout], ld=self.ld, out_ld=self.out_ld,
+            counts_ld=counts.shape[1] if counts is not None else 0, seen_ld=seen.shape[1] if seen is not None else 0,
+            n_drafts=drafts.numel() if drafts is not None else 0,
+            n_bias=bias_ids.numel() if bias_ids is not None else 0,
+            mask_ld=mask.shape[1] if mask is not None else 0, mask_count=mask.shape[0] if mask is not None else 0, **at)
+        self._ref = ctypes.byref(self._args)
+        rows, width = (C, V) if layout == "col" else (V, C)
+        self._numel = (rows - 1) * self.ld + width
+        self._out_numel = (rows - 1) * self.out_ld + width
+
+    def apply(self, x, out=None, stream=None):
+        """Enqueue the rules on logits x; returns out (allocated like x when
+        not given: its padding, and columns of no lane, are then
+        uninitialised).  out=x works in place.  x and out are contiguous GPU
+        tensors of the matrix (bf16 or fp32, or patterns of the same width)."""
+        import torch
+        if out is None:
+            if self.out_ld != self.ld:
+                raise ValueError("out is needed when out_ld differs from ld")
+            out = torch.empty_like(x)
+        size = 2 if self.dtype == "bf16" else 4
+        if not (x.is_cuda and out.is_cuda) or x.device != out.device or self.device not in (None, x.device):
+            raise ValueError("x, out and the rules' tensors must be on one GPU")
+        if x.element_size() != size or out.element_size() != size or x.numel() < self._numel \
+                or out.numel() < self._out_numel or not (x.is_contiguous() and out.is_contiguous()):
+            raise ValueError("x and out must be contiguous and hold the matrix described by the rules")
+        _launch("topk_cols_adjust", x.device, stream,
+                lambda s: load().topk_cols_adjust(self._ref, x.data_ptr(), out.data_ptr(), s))
+        return out
+
+
+def count_tokens(counts, seen, V: int, ids, start=None, prompt_len=None, fresh=None, stream=None):
+    """Add packed token ids to the lanes' histories (topk_cols_count).
+
+    counts (lanes, >= V), seen (lanes, >= ceil(V/32)): int32, updated in place.
+    ids: int32; lane l's are ids[start[l]:start[l+1]] (evenly many without
+        start).  Ids outside [0, V) are skipped.
+    prompt_len (lanes,): how many of a lane's tokens, from the first, are
+        prompt (none without it).  fresh (lanes,): lanes to clear first.
+    Returns (counts, seen).
+    """
+    lanes, dev = counts.shape[0], counts.device
+    if counts.dim() != 2 or seen.dim() != 2 or seen.shape[0] != lanes:
+        raise ValueError("counts and seen must be matrices with a row per lane")
+    args = (V, lanes, _need("ids", ids, 0, dev) if ids.numel() else 0, ids.numel(), _need("start", start, lanes + 1, dev),
+            _need("prompt_len", prompt_len, lanes, dev), _need("fresh", fresh, lanes, dev),
+            _need("counts", counts, 1, dev), counts.shape[1], _need("seen", seen, 1, dev), seen.shape[1])
+    _launch("topk_cols_count", dev, stream, lambda s: load().topk_cols_count(*args, s))
+    return counts, seen
+
+
+def verify(target_values, target_ids, col_start, drafts, draft_start, draft_values=None, draft_ids=None,
+           temperature: float = 1.0, top_p: float = 0.95, seed: int = 0, offset: int = 0, lanes: int | None = None,
+           max_tokens: int | None = None, out_tokens=None, out_count=None, stream=None):
+    """Verify drafts against the target's top-k lists (topk_cols_verify).
+
+    target_values, target_ids: (C, k), as a run on the target's logits wrote
+        them; lane l's columns are col_start[l]..col_start[l+1]-1 (one more
+        than its drafts).
+    drafts: packed token ids, lane l's at draft_start[l]..draft_start[l+1]-1.
+    draft_values, draft_ids: (n, kq), the lists the drafts were sampled from;
+        without them drafts count as certain (greedy drafts).
+    temperature 0 verifies greedily.  col_start and draft_start None: the same
+        number for each of `lanes` lanes.
+    Returns (tokens, count): lane l commits tokens[l, :count[l]], the accepted
+    drafts and one token more; -1 follows.  max_tokens: the row length when
+    out_tokens is not given (default: one more than all drafts, which is
+    enough for any lane; pass the round's draft limit + 1).
+    """
+    import torch
+    dev = target_values.device
+    if lanes is None:
+        if col_start is None:
+            raise ValueError("lanes is needed without col_start")
+        lanes = col_start.numel() - 1
+    if out_tokens is None:
+        out_tokens = torch.empty((lanes, max_tokens or drafts.numel() + 1), dtype=torch.int32, device=dev)
+    if out_count is None:
+        out_count = torch.empty(lanes, dtype=torch.int32, device=dev)
+    if target_values.dim() != 2 or target_ids.shape != target_values.shape or out_tokens.dim() != 2 \
+            or out_tokens.shape[0] < lanes:
+        raise ValueError("target_values and target_ids must be (C, k), out_tokens a matrix with a row per lane")
+    C, k = target_values.shape
+    n = drafts.numel()
+    kq = 0
+    if draft_values is not None:
+        if draft_values.dim() != 2 or draft_ids is None or draft_ids.shape != draft_values.shape \
+                or draft_values.element_size() != target_values.element_size():
+            raise ValueError("draft_values and draft_ids must be (n, kq), of the target lists' types")
+        kq = draft_values.shape[1]
+        # drafts past the lists have no distribution to be judged by
+        n = min(n, draft_values.shape[0])
+    for name, t in (("target_values", target_values), ("draft_values", draft_values)):
+        if t is not None and not (t.is_cuda and t.device == dev and t.is_contiguous() and t.element_size() in (2, 4)):
+            raise ValueError(f"{name} must be a contiguous GPU tensor of bf16 or fp32 (or patterns)")
+    lists = draft_values is not None and n > 0
+    args = VerifyArgs(
+        lanes=lanes, dtype=0 if target_values.element_size() == 2 else 1, k=k, kq=kq if lists else 0, C=C,
+        col_start=_need("col_start", col_start, lanes + 1, dev), target_values=target_values.data_ptr(),
+        target_ids=_need("target_ids", target_ids, 1, dev), n_drafts=n,
+        draft_start=_need("draft_start", draft_start, lanes + 1, dev), drafts=_need("drafts", drafts, 0, dev) if n else 0,
+        draft_values=draft_values.data_ptr() if lists else 0,
+        draft_ids=_need("draft_ids", draft_ids, 0, dev) if lists else 0, temperature=float(temperature),
+        top_p=float(top_p), seed=int(seed), offset=int(offset), max_tokens=out_tokens.shape[1],
+        out_tokens=_need("out_tokens", out_tokens, 1, dev), out_count=_need("out_count", out_count, lanes, dev))
+    _launch("topk_cols_verify", dev, stream, lambda s: load().topk_cols_verify(ctypes.byref(args), s))
+    return out_tokens, out_count
+
+
+def plan(lens, add, held, table, free_ids, free_count, block_size: int, capacity: int, out=None, stream=None) -> dict:
+    """Plan a round: columns, cache blocks and slots (topk_cols_plan).
+
+    lens, add, held: (lanes,) int32, the lanes' tokens in the cache, the
+        columns they want and the blocks they hold.
+    table: (lanes, width) int32 block ids, extended in place.
+    free_ids: int32 stack of free blocks, its first free_count[0] are free.
+    capacity: columns of the round, at most.
+    Returns a dict (or fills `out`, one an earlier call returned) of int32
+    tensors held (lanes,), free_count (1,), refused (1,), col_start
+    (lanes + 1,), col_lane, col_pos (capacity,) and int64 slots (capacity,).
+    """
+    import torch
+    lanes, dev = lens.numel(), lens.device
+    if table.dim() != 2 or table.shape[0] < lanes:
+        raise ValueError("table must be a matrix with a row per lane")
+    sizes = dict(held=lanes, free_count=1, refused=1, col_start=lanes + 1, col_lane=capacity, col_pos=capacity,
+                 slots=capacity)
+    kinds = {n: "int64" if n == "slots" else "int32" for n in sizes}
+    if out is None:
+        out = {n: torch.empty(max(size, 1), dtype=getattr(torch, kinds[n]), device=dev) for n, size in sizes.items()}
+    outs = {"out_" + n: _need(n, out[n], size, dev, kinds[n]) for n, size in sizes.items()}
+    args = PlanArgs(
+        lanes=lanes, capacity=capacity, block_size=block_size, lens=_need("lens", lens, lanes, dev),
+        add=_need("add", add, lanes, dev), held=_need("held", held, lanes, dev), table=_need("table", table, 1, dev),
+        table_ld=table.shape[1], free_ids=_need("free_ids", free_ids, 0, dev) if free_ids.numel() else 0,
+        n_free_ids=free_ids.numel(), free_count=_need("free_count", free_count, 1, dev), **outs)
+    _launch("topk_cols_plan", dev, stream, lambda s: load().topk_cols_plan(ctypes.byref(args), s))
+    return out
 
 
 def topk_cols(x, V: int, C: int, k: int, dtype: str = "bf16", layout: str = "col", ld=None):

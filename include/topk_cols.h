@@ -206,6 +206,249 @@ int topk_cols_sample(const void *values, const int32_t *ids, int64_t C, int32_t 
                      double temperature, double top_p, uint64_t seed, uint64_t offset, int32_t *out_ids,
                      int32_t *out_pos, hipStream_t stream);
 
+/*
+ * The steps around the top-k in a round of speculative decoding.
+ *
+ * A round's matrix has one column per position.  Lane l owns the contiguous
+ * columns col_start[l] .. col_start[l+1]-1 ("pack each lane's active columns
+ * one after another", topk_cols_run_n); a lane with d drafts has d columns
+ * of the drafter's logits, or d + 1 of the target's (column j of the lane
+ * follows its first j drafts).  Where an entry point takes col_start NULL,
+ * every lane has the same number of columns: C / lanes, and C must be a
+ * multiple of lanes.  draft_start packs the drafts of the lanes in the same
+ * way; NULL means n_drafts / lanes each.
+ *
+ *   topk_cols_plan     lays the round out: col_start, each column's lane,
+ *                      position and cache slot, and the blocks it needs;
+ *   topk_cols_adjust   applies penalties, biases and grammar masks to logits;
+ *   topk_cols_verify   accepts or refuses drafts against the target's lists;
+ *   topk_cols_count    adds the tokens a lane gained to its history, which
+ *                      topk_cols_adjust reads.
+ *
+ * All of them are asynchronous on the stream, take no handle, allocate
+ * nothing, keep nothing between calls and may be captured and replayed.
+ * Buffers belong to the caller.  Index arrays are read on the device and
+ * cannot be checked by the call: offsets outside their array are cut to it,
+ * ids outside [0, V) are ignored, and lanes must not overlap.  The argument
+ * structures are read before the call returns.
+ */
+
+/* The rules of topk_cols_adjust.  Zero (NULL) leaves a rule out. */
+typedef struct {
+    int64_t V;                /* rows, 1 <= V <= TOPK_MAX_V */
+    int64_t C;                /* columns of the matrix, >= 1 */
+    int64_t lanes;            /* >= 1 */
+    int32_t dtype;            /* topk_dtype */
+    int32_t layout;           /* topk_layout */
+    int64_t ld;               /* leading dimension of the logits, as for topk_cols_create */
+    int64_t out_ld;           /* leading dimension of the result */
+    const int32_t *col_start; /* device, lanes + 1, or NULL */
+    /* The lanes' histories (written by topk_cols_count), both or neither:
+     * counts[l*counts_ld + r]: bit 31 set if token r occurs in lane l's
+     * prompt, the lower bits how often it occurs in its output;
+     * seen[l*seen_ld + r/32]: bit r % 32 set where that word is not zero. */
+    const int32_t *counts;
+    int64_t counts_ld;        /* >= V */
+    const uint32_t *seen;
+    int64_t seen_ld;          /* >= ceil(V / 32) */
+    const float *repetition;  /* device, lanes values > 0, or NULL: 1 */
+    const float *presence;    /* device, lanes values, or NULL: 0 */
+    const float *frequency;   /* device, lanes values, or NULL: 0 */
+    /* Drafts that precede the columns, both or neither: column j of lane l
+     * takes the lane's first j drafts as further output tokens. */
+    const int32_t *drafts;    /* device, n_drafts token ids */
+    const int32_t *draft_start; /* device, lanes + 1, or NULL: n_drafts / lanes each */
+    int64_t n_drafts;
+    /* Biases, all or none: entries bias_start[l] .. bias_start[l+1]-1 add
+     * bias_values[e] to row bias_ids[e].  Of several entries for one row the
+     * last counts.  Meant for lists of up to a few thousand entries: each
+     * workgroup reads its lane's whole list. */
+    const int32_t *bias_start; /* device, lanes + 1 */
+    const int32_t *bias_ids;   /* device, n_bias */
+    const float *bias_values;  /* device, n_bias */
+    int64_t n_bias;
+    /* Masks: row r of column c is allowed if bit r % 32 of
+     * mask[m*mask_ld + r/32] is set, m = mask_index[c]; a column whose m is
+     * outside [0, mask_count) has no mask.  mask_index NULL: m = c. */
+    const uint32_t *mask;      /* device, mask_count rows of words, or NULL */
+    int64_t mask_ld;           /* >= ceil(V / 32) */
+    int64_t mask_count;        /* >= 1; >= C when mask_index is NULL */
+    const int32_t *mask_index; /* device, C, or NULL */
+} topk_adjust_rules;
+
+/*
+ * Apply penalties, biases and masks to logits.  With x the stored value of
+ * row r in column c (column j of lane l), n the token's count in the lane's
+ * output and the first j drafts, in that order:
+ *   1. r occurs in the prompt or n > 0: x = x > 0 ? x / repetition : x * repetition
+ *   2. n > 0:  x = x - (frequency * n + presence)
+ *   3. r has a bias:  x = x + bias
+ *   4. the mask forbids r:  x = -Inf
+ * Steps 1 to 3 are carried out in binary64 and rounded once to binary32 and,
+ * for TOPK_BF16, from there to bfloat16 (to nearest, ties to even).  An
+ * element that no step applies to keeps its stored bits.  A mask may leave a
+ * column empty: every row is then -Inf, and a top-k of it gives rows 0 to
+ * k-1.
+ *
+ * logits, out: device, aligned to the element size.  out may be logits
+ *   itself (then out_ld must be ld) and must not overlap it otherwise.
+ *   Columns that belong to no lane, and the padding, are neither read nor
+ *   written.
+ *
+ * Returns TOPK_ERR_INVALID_ARG for a NULL or misaligned pointer, a size or
+ * leading dimension out of range, an incomplete group, lanes that do not
+ * divide C (col_start NULL) or n_drafts (draft_start NULL);
+ * TOPK_ERR_UNSUPPORTED for V > TOPK_MAX_V, or C, lanes, n_drafts, n_bias or
+ * mask_count beyond 2^31 - 1; TOPK_ERR_HIP when a launch fails.
+ */
+int topk_cols_adjust(const topk_adjust_rules *rules, const void *logits, void *out, hipStream_t stream);
+
+/*
+ * Add tokens to the lanes' histories (see topk_adjust_rules).
+ *
+ * ids: device, n_ids token ids; lane l's are ids[start[l]] ..
+ *   ids[start[l+1]-1].  Ids outside [0, V) (the -1 behind a lane's tokens in
+ *   topk_cols_verify's output) are skipped.  May be NULL when n_ids is 0.
+ * start: device, lanes + 1, or NULL: n_ids / lanes tokens each.
+ * prompt_len: device, lanes, or NULL.  The first prompt_len[l] of a lane's
+ *   tokens are prompt, the others output.  NULL: all are output.
+ * fresh: device, lanes, or NULL.  A lane with fresh[l] != 0 starts anew: its
+ *   history is cleared first.
+ * counts, seen: device, updated; counts_ld >= V, seen_ld >= ceil(V / 32).
+ *   A count must stay below 2^31.  Words beyond V are left as they are.
+ * The result does not depend on the order of a lane's tokens.  Calls on the
+ * same history must be ordered on a stream.
+ *
+ * Returns TOPK_ERR_INVALID_ARG for a NULL or misaligned pointer, V < 1,
+ * lanes < 1, n_ids < 0, a leading dimension that is too small, or lanes that
+ * do not divide n_ids (start NULL); TOPK_ERR_UNSUPPORTED for V > TOPK_MAX_V,
+ * or lanes or n_ids beyond 2^31 - 1; TOPK_ERR_HIP when a launch fails.
+ */
+int topk_cols_count(int64_t V, int64_t lanes, const int32_t *ids, int64_t n_ids, const int32_t *start,
+                    const int32_t *prompt_len, const int32_t *fresh, int32_t *counts, int64_t counts_ld,
+                    uint32_t *seen, int64_t seen_ld, hipStream_t stream);
+
+typedef struct {
+    int64_t lanes;               /* >= 1 */
+    int32_t dtype;               /* topk_dtype of both lists' values */
+    int32_t k;                   /* entries of a target list, 1 .. TOPK_MAX_K */
+    int32_t kq;                  /* entries of a draft list, 1 .. TOPK_MAX_K (unused without draft lists) */
+    int64_t C;                   /* target columns, >= 1 */
+    const int32_t *col_start;    /* device, lanes + 1, or NULL */
+    const void *target_values;   /* device, C*k, as a topk_cols run on the target's logits wrote them */
+    const int32_t *target_ids;   /* device, C*k */
+    int64_t n_drafts;            /* drafts in the buffers, >= 0 */
+    const int32_t *draft_start;  /* device, lanes + 1, or NULL: n_drafts / lanes each */
+    const int32_t *drafts;       /* device, n_drafts token ids (may be NULL when n_drafts is 0) */
+    const void *draft_values;    /* device, n_drafts*kq, the lists the drafts were sampled from, or NULL */
+    const int32_t *draft_ids;    /* device, n_drafts*kq, or NULL together with draft_values */
+    double temperature;          /* >= 0, finite */
+    double top_p;                /* in (0, 1] */
+    uint64_t seed, offset;       /* as for topk_cols_sample */
+    int64_t max_tokens;          /* >= 1: entries of a lane in out_tokens */
+    int32_t *out_tokens;         /* device, lanes*max_tokens */
+    int32_t *out_count;          /* device, lanes */
+} topk_verify_args;
+
+/*
+ * Verify a round's drafts against the target's top-k lists and draw the
+ * token that follows the last accepted one, so that the tokens are
+ * distributed as samples of the target ("one target verify pass, commit the
+ * longest agreeing run plus one token", the "DFlash2" page, "How it works";
+ * the rule is the published acceptance test of speculative sampling:
+ * Leviathan, Kalman and Matias, 2023).
+ *
+ * A list of values v_0 >= v_1 >= ... stands for the distribution
+ * topk_cols_sample draws from: w_j = exp((v_j - v_0) / temperature), S_m =
+ * w_0 + ... + w_{m-1}, n the smallest m with S_m >= top_p * S_k, and
+ * probability w_j / S_n for j < n, 0 beyond.  With temperature 0, or where
+ * v_0 is not finite, entry 0 has probability 1.  A token's probability is
+ * that of the first entry with its id, 0 if there is none.  Without draft
+ * lists a draft has probability 1 (it was not sampled).
+ *
+ * For lane l let m be the smallest of its draft count, its columns - 1 and
+ * max_tokens - 1.  With p_j the distribution of its column j, d_j its j-th
+ * draft, q_j that draft's list and u, u' two uniforms in [0, 1) of the
+ * column:
+ *   draft j < m is accepted if u * q_j(d_j) < p_j(d_j);
+ *   t is the number of drafts accepted before the first refused one;
+ *   the next token is entry i of column t, the smallest i with
+ *   R_{i+1} > u' * R_k, where R_i sums the first i of the weights
+ *   max(p_t(i) - q_t(id_i), 0) if t < m, or p_t(i) if t = m or those are
+ *   all 0.
+ * out_tokens[l*max_tokens ..] = the t drafts, the token, then -1;
+ * out_count[l] = t + 1.  A lane without columns gets only -1, and count 0.
+ *
+ * u and u' come from Philox4x32-10 as in topk_cols_sample, with counter
+ * (offset & 0xFFFFFFFF, offset >> 32, column, 1) for u and (.., 2) for u',
+ * the column being the target column's index.  (topk_cols_sample uses 0, so
+ * one offset can serve a round.)  Arithmetic is IEEE double in the order
+ * written, exp as in topk_cols_sample: the result is reproducible bit for
+ * bit.
+ *
+ * Returns TOPK_ERR_INVALID_ARG for a NULL or misaligned pointer, a value out
+ * of the ranges above, or lanes that do not divide C (col_start NULL) or
+ * n_drafts (draft_start NULL); TOPK_ERR_UNSUPPORTED for more than
+ * 4,194,304 lanes, or C, n_drafts or max_tokens beyond 2^31 - 1;
+ * TOPK_ERR_HIP when the launch fails.
+ */
+int topk_cols_verify(const topk_verify_args *args, hipStream_t stream);
+
+typedef struct {
+    int64_t lanes;              /* >= 1 */
+    int64_t capacity;           /* columns the outputs hold, >= 1 */
+    int32_t block_size;         /* tokens of a cache block, >= 1 */
+    const int32_t *lens;        /* device, lanes: tokens of each lane in the cache */
+    const int32_t *add;         /* device, lanes: columns wanted this round; <= 0 for none */
+    const int32_t *held;        /* device, lanes: blocks in the lane's table row */
+    int32_t *table;             /* device, lanes rows of table_ld block ids; new ids are written */
+    int64_t table_ld;           /* >= 1: the most blocks a lane can have */
+    const int32_t *free_ids;    /* device, n_free_ids: a stack of free blocks, its top at the end */
+    int64_t n_free_ids;         /* >= 0 */
+    const int32_t *free_count;  /* device, 1: entries of free_ids that are free */
+    int32_t *out_held;          /* device, lanes; not held itself */
+    int32_t *out_free_count;    /* device, 1; not free_count itself */
+    int32_t *out_refused;       /* device, 1: lanes that wanted columns and got none */
+    int32_t *out_col_start;     /* device, lanes + 1 */
+    int32_t *out_col_lane;      /* device, capacity: the column's lane, or -1 */
+    int32_t *out_col_pos;       /* device, capacity: its token's position in the lane, or -1 */
+    int64_t *out_slots;         /* device, capacity: where its keys go, or -1 */
+} topk_plan_args;
+
+/*
+ * Plan a round: give every lane its columns, and the cache blocks its new
+ * tokens need.
+ *
+ * Lane l's new tokens have positions lens[l] .. lens[l] + add[l] - 1; a
+ * position p lies in entry p / block_size of the lane's table row and in
+ * slot table[..] * block_size + p % block_size.  The lane needs
+ *   need = max(0, ceil((lens + add) / block_size) - held)
+ * further blocks (blocks left over from refused drafts count as held).
+ * Lanes are served in order.  A lane with add > 0 is refused when its blocks
+ * do not fit its table row or its tokens exceed 2^31 - 1, when the needs of the lanes up to and including
+ * it (those refused for the former apart) exceed the free blocks and its own
+ * need is not 0, or when the columns of the lanes up to and including it
+ * (those refused for blocks apart) exceed the capacity.  A refused lane gets
+ * no columns and no blocks.
+ *
+ * Served lane l takes free_ids[free_count - 1 - i], free_ids[free_count - 2
+ * - i], ..., i being the blocks taken by the lanes before it, and they are
+ * written to its table row from entry held[l] on.  out_held and
+ * out_free_count state what holds afterwards: pass them as the next round's
+ * held and free_count.  Blocks are given back by writing them to free_ids
+ * behind the free ones and raising the count.  Columns from
+ * out_col_start[lanes] on get lane, position and slot -1, so a round padded
+ * to its capacity can be replayed from a captured graph.
+ * lens < 0 counts as 0, held as cut to [0, table_ld], free_count to [0,
+ * n_free_ids].  Outputs must not overlap the inputs or each other.
+ *
+ * Returns TOPK_ERR_INVALID_ARG for a NULL or misaligned pointer, a size out
+ * of range, out_held == held or out_free_count == free_count;
+ * TOPK_ERR_UNSUPPORTED for lanes, capacity, table_ld or n_free_ids beyond
+ * 2^31 - 1; TOPK_ERR_HIP when the launch fails.
+ */
+int topk_cols_plan(const topk_plan_args *args, hipStream_t stream);
+
 /* A static, human-readable name for a status code.  Never NULL. */
 const char *topk_cols_status_string(int status);
 
