@@ -14,16 +14,19 @@ struct Parts {
     const int32_t* start;
     uint32_t total;
     uint32_t each;  // total / lanes (start == NULL)
+    // from start[l] and start[l + 1] (any values without a start array)
+    __device__ __forceinline__ void cut(uint32_t l, int32_t b, int32_t e, uint32_t& begin, uint32_t& end) const {
+        begin = start ? (b < 0 ? 0u : min_u32((uint32_t)b, total)) : l * each;
+        end = start ? (e < 0 ? 0u : min_u32((uint32_t)e, total)) : begin + each;
+        if (end < begin) end = begin;
+    }
     __device__ __forceinline__ void range(uint32_t l, uint32_t& begin, uint32_t& end) const {
+        int32_t b = 0, e = 0;
         if (start) {
-            const int32_t b = start[l], e = start[l + 1];
-            begin = b < 0 ? 0u : min_u32((uint32_t)b, total);
-            end = e < 0 ? 0u : min_u32((uint32_t)e, total);
-            if (end < begin) end = begin;
-        } else {
-            begin = l * each;
-            end = begin + each;
+            b = start[l];
+            e = start[l + 1];
         }
+        cut(l, b, e, begin, end);
     }
 };
 
