@@ -31,7 +31,6 @@ namespace topk {
 
 namespace {
 
-constexpr uint32_t kTile = 8192;  // rows per workgroup (row-interleaved, sparse)
 
 template <class DT>
 __device__ __forceinline__ float to_float(uint32_t raw) {
@@ -56,11 +55,7 @@ constexpr uint32_t kMinusInf = DT::kPerVec == 8 ? 0xFF80u : 0xFF800000u;
 
 struct LaneRules {
     double rep, inv, pres, freq;
-    __device__ LaneRules(float r, float p, float f, bool has_r = true)
-        : rep(has_r ? (double)r : 1.0), inv(1.0 / rep), pres((double)p), freq((double)f) {}
-    __device__ explicit LaneRules(const AdjustArgs& a, uint32_t l)
-        : LaneRules(a.repetition ? a.repetition[l] : 1.0f, a.presence ? a.presence[l] : 0.0f,
-                    a.frequency ? a.frequency[l] : 0.0f) {}
+    __device__ LaneRules(float r, float p, float f) : rep((double)r), inv(1.0 / rep), pres((double)p), freq((double)f) {}
     __device__ __forceinline__ double apply(double x, bool prompt, uint32_t n, double bias) const {
         if (prompt || n) x = x > 0.0 ? x * inv : x * rep;
         if (n) x -= freq * (double)n + pres;
@@ -108,16 +103,16 @@ __device__ __forceinline__ u32x4 masked(const u32x4& v, uint32_t allowed) {
     return r;
 }
 
-// ------------------------------------------------------ column-contiguous ---
+// ------------------------------------------------------------ touched rows ---
 
-// Rows of a workgroup: one 16-byte vector per thread, in runs of 256 rows that
-// lie `tiles` runs apart.  The ids of a vocabulary sorted by use put most of a
-// history into the first rows; in one contiguous tile they would hold up the
-// whole launch.  256 rows are the most that a workgroup rewrites in one go,
-// and whole cache lines.
-template <class DT>
-struct ColRows {
-    static constexpr uint32_t EPV = DT::kPerVec, RUN = 256, ROWS = kBlock * EPV, WORDS = ROWS / 32;
+// The ROWS rows of a workgroup: runs of 256 that lie `tiles` runs apart.  The
+// ids of a vocabulary sorted by use put most of a history into the first
+// rows; in one contiguous tile they would hold up the whole launch.  256 rows
+// are the most that a workgroup rewrites in one go, and whole cache lines.
+template <uint32_t kRows>
+struct Rows {
+    static constexpr uint32_t RUN = 256, ROWS = kRows, WORDS = ROWS / 32;
+    static_assert(WORDS <= (uint32_t)kBlock, "one word of the rows' bits per thread");
     uint32_t tiles, tile;
     __device__ __forceinline__ uint32_t row(uint32_t at) const { return (at / RUN * tiles + tile) * RUN + at % RUN; }
     // the place of row r, or ROWS if it is another workgroup's
@@ -127,17 +122,14 @@ struct ColRows {
     }
 };
 
-template <class DT, bool kBias>
-struct ColShared {
-    using Rows = ColRows<DT>;
-    alignas(16) uint32_t bias_at[kBias ? Rows::ROWS : 4];  // 1 + the last list entry of a place, or 0
-    uint32_t touched[Rows::WORDS];  // places with a history, a draft or a bias
-    uint32_t drafted[Rows::WORDS];  // places that are drafts
-    uint16_t list[Rows::ROWS];      // the touched places, in any order
+template <uint32_t kRows, bool kBias>
+struct TouchedRows {
+    alignas(16) uint32_t bias_at[kBias ? kRows : 4];  // 1 + the last list entry of a place, or 0
+    uint32_t touched[kRows / 32];  // places with a history, a draft or a bias
+    uint32_t drafted[kRows / 32];  // places that are drafts
+    uint16_t list[kRows];          // the touched places, in any order
     uint32_t n;
 };
-
-constexpr uint32_t kColsAtOnce = 4;  // columns whose vectors a thread has in flight
 
 // An address that can be read in place of an absent array's, so that a read
 // needs no branch (a branch around it would make the next ones wait).
@@ -145,6 +137,117 @@ template <class T>
 __device__ __forceinline__ const T* or_safe(const T* p) {
     return p ? p : (const T*)(uintptr_t)__builtin_amdgcn_kernarg_segment_ptr();
 }
+
+// What hangs on the lane alone, read at once.
+template <uint32_t kRows, bool kBias>
+struct Lane {
+    uint32_t cb, ce, db, de, bb, be;  // its columns, the drafts before its last column, its biases
+    float rep, pres, freq;
+    uint32_t word;                    // the history's bits of this thread's 32 places
+    __device__ __forceinline__ Lane(const AdjustArgs& a, const Rows<kRows>& rows, uint32_t l) {
+        const uint32_t tid = threadIdx.x;
+        const int32_t* cs = a.cols.start ? a.cols.start + l : or_safe<int32_t>(nullptr);
+        const int32_t* ds = a.draft_parts.start ? a.draft_parts.start + l : or_safe<int32_t>(nullptr);
+        const int32_t* bs = kBias ? a.bias_parts.start + l : or_safe<int32_t>(nullptr);
+        const uint32_t r = rows.row(min_u32(tid, Rows<kRows>::WORDS - 1u) * 32u);
+        const uint32_t* sp = a.seen ? a.seen + (int64_t)l * a.seen_ld + (min_u32(r, a.V - 1u) >> 5) : or_safe<uint32_t>(nullptr);
+        const int32_t c0 = cs[0], c1 = cs[1], d0 = ds[0], d1 = ds[1], b0 = bs[0], b1 = bs[1];
+        rep = *(a.repetition ? a.repetition + l : or_safe<float>(nullptr));
+        pres = *(a.presence ? a.presence + l : or_safe<float>(nullptr));
+        freq = *(a.frequency ? a.frequency + l : or_safe<float>(nullptr));
+        word = *sp;
+        a.cols.cut(l, c0, c1, cb, ce);
+        a.draft_parts.cut(l, d0, d1, db, de);
+        a.bias_parts.cut(l, b0, b1, bb, be);
+        if (!a.drafts) de = db;
+        if (ce > cb) de = min_u32(de, db + (ce - cb - 1u));
+        if (!a.repetition) rep = 1.0f;
+        if (!a.presence) pres = 0.0f;
+        if (!a.frequency) freq = 0.0f;
+        if (tid >= Rows<kRows>::WORDS || r >= a.V || !a.seen) word = 0;
+        else if (a.V - r < 32u) word &= (1u << (a.V - r)) - 1u;  // bits past the last row mean nothing
+    }
+};
+
+// Fills sh (list and n are valid after the next barrier).  bias0, draft0: the
+// lane's entries bb + thread and db + thread.
+template <uint32_t kRows, bool kBias>
+__device__ __forceinline__ void make_list(const AdjustArgs& a, const Rows<kRows>& rows, const Lane<kRows, kBias>& lane,
+                                          uint32_t draft0, uint32_t bias0, TouchedRows<kRows, kBias>& sh) {
+    const uint32_t tid = threadIdx.x, ln = tid & 63u;
+    if (tid == 0) sh.n = 0;
+    if (tid < kRows / 32) {
+        sh.touched[tid] = lane.word;
+        sh.drafted[tid] = 0;
+    }
+    if constexpr (kBias)
+        for (uint32_t i = tid; i < kRows / 4; i += kBlock) reinterpret_cast<u32x4*>(sh.bias_at)[i] = u32x4{0u, 0u, 0u, 0u};
+    __syncthreads();
+    if (a.drafts || kBias) {
+        for (uint32_t i = lane.db + tid; i < lane.de; i += kBlock) {
+            const uint32_t at = rows.place(i == lane.db + tid ? draft0 : (uint32_t)a.drafts[i], a.V);
+            if (at == kRows) continue;
+            atomicOr(&sh.touched[at >> 5], 1u << (at & 31u));
+            atomicOr(&sh.drafted[at >> 5], 1u << (at & 31u));
+        }
+        if constexpr (kBias) {
+            for (uint32_t i = lane.bb + tid; i < lane.be; i += kBlock) {
+                const uint32_t at = rows.place(i == lane.bb + tid ? bias0 : (uint32_t)a.bias_ids[i], a.V);
+                if (at == kRows) continue;
+                atomicOr(&sh.touched[at >> 5], 1u << (at & 31u));
+                atomicMax(&sh.bias_at[at], i - lane.bb + 1u);
+            }
+        }
+        __syncthreads();
+    }
+    // a ballot per 64 places, one LDS atomic per wave
+    constexpr uint32_t Q = kRows / kBlock;
+    unsigned long long some[Q];
+    uint32_t total = 0;
+#pragma unroll
+    for (uint32_t q = 0; q < Q; ++q) {
+        some[q] = __ballot(sh.touched[q * (kBlock / 32u) + (tid >> 5)] >> (tid & 31u) & 1u);
+        total += (uint32_t)__popcll(some[q]);
+    }
+    if (total == 0) return;
+    uint32_t pos = 0;
+    if (ln == 0) pos = atomicAdd(&sh.n, total);
+    pos = (uint32_t)__builtin_amdgcn_readfirstlane((int)pos);
+#pragma unroll
+    for (uint32_t q = 0; q < Q; ++q) {
+        if (some[q] >> ln & 1ull) sh.list[pos + lanes_below(some[q])] = (uint16_t)(q * kBlock + tid);
+        pos += (uint32_t)__popcll(some[q]);
+    }
+}
+
+template <uint32_t kRows, bool kBias>
+__device__ __forceinline__ void first_entries(const AdjustArgs& a, const Lane<kRows, kBias>& lane, uint32_t& draft0, uint32_t& bias0) {
+    const uint32_t tid = threadIdx.x;
+    bias0 = kBias ? (uint32_t)a.bias_ids[min_u32(lane.bb + tid, a.bias_parts.total - 1u)] : 0u;
+    draft0 = a.drafts ? (uint32_t)a.drafts[min_u32(lane.db + tid, a.draft_parts.total - 1u)] : 0u;
+}
+
+// Which of a lane's drafts are one row (of a row known to be a draft).
+struct DraftsOfRow {
+    uint64_t first = 0;  // bit i: draft i of the first 64
+    template <class L>
+    __device__ __forceinline__ void find(const AdjustArgs& a, const L& lane, uint32_t row) {
+#pragma unroll 8
+        for (uint32_t i = 0; i < min_u32(lane.de - lane.db, 64u); ++i)
+            first |= (uint32_t)a.drafts[lane.db + i] == row ? 1ull << i : 0ull;
+    }
+    // among the first j
+    template <class L>
+    __device__ __forceinline__ uint32_t before(const AdjustArgs& a, const L& lane, uint32_t row, uint32_t j) const {
+        uint32_t n = (uint32_t)__popcll(j < 64u ? first & ((1ull << j) - 1u) : first);
+        for (uint32_t i = lane.db + 64u; i < min_u32(lane.de, lane.db + j); ++i) n += (uint32_t)a.drafts[i] == row ? 1u : 0u;
+        return n;
+    }
+};
+
+// ------------------------------------------------------ column-contiguous ---
+
+constexpr uint32_t kColsAtOnce = 4;  // columns whose vectors a thread has in flight
 
 // Lane l0 + blockIdx.y, its columns blockIdx.z * U, .. + U - 1, then
 // gridDim.z * U further on.  The columns share the search for the rows that a
@@ -156,33 +259,17 @@ __device__ __forceinline__ const T* or_safe(const T* p) {
 template <class DT, bool kInPlace, bool kBias, bool kMask>
 __global__ __launch_bounds__(kBlock) void adjust_col(AdjustArgs a, uint32_t l0) {
     using storage = typename DT::storage;
-    using Rows = ColRows<DT>;
-    constexpr uint32_t EPV = DT::kPerVec, ALL = (1u << EPV) - 1u, U = kColsAtOnce;
-    __shared__ ColShared<DT, kBias> sh;
+    constexpr uint32_t EPV = DT::kPerVec, ALL = (1u << EPV) - 1u, U = kColsAtOnce, ROWS = kBlock * EPV;
+    __shared__ TouchedRows<ROWS, kBias> sh;
     const uint32_t l = l0 + blockIdx.y, tid = threadIdx.x, V = a.V;
-    const Rows rows{gridDim.x, blockIdx.x};
+    const Rows<ROWS> rows{gridDim.x, blockIdx.x};
     const bool sparse = a.counts || a.drafts || kBias;
-
-    // all that hangs on the lane alone
-    const int32_t* cs = a.cols.start ? a.cols.start + l : or_safe<int32_t>(nullptr);
-    const int32_t* ds = a.draft_parts.start ? a.draft_parts.start + l : or_safe<int32_t>(nullptr);
-    const int32_t* bs = kBias ? a.bias_parts.start + l : or_safe<int32_t>(nullptr);
-    const float* rp = a.repetition ? a.repetition + l : or_safe<float>(nullptr);
-    const float* pp = a.presence ? a.presence + l : or_safe<float>(nullptr);
-    const float* fp = a.frequency ? a.frequency + l : or_safe<float>(nullptr);
-    const uint32_t wr = rows.row(min_u32(tid, Rows::WORDS - 1u) * 32u);  // this thread's 32 rows
-    const uint32_t* sp = a.seen ? a.seen + (int64_t)l * a.seen_ld + (min_u32(wr, V - 1u) >> 5) : or_safe<uint32_t>(nullptr);
-    const int32_t c0s = cs[0], c1s = cs[1], d0s = ds[0], d1s = ds[1], b0s = bs[0], b1s = bs[1];
-    const float rep = *rp, pres = *pp, freq = *fp;
-    uint32_t word = *sp;
-    uint32_t cb, ce, db, de, bb, be;
-    a.cols.cut(l, c0s, c1s, cb, ce);
-    a.draft_parts.cut(l, d0s, d1s, db, de);
-    a.bias_parts.cut(l, b0s, b1s, bb, be);
+    const Lane<ROWS, kBias> lane(a, rows, l);
+    const uint32_t cb = lane.cb, ce = lane.ce;
     const uint32_t c_first = cb + blockIdx.z * U, c_step = gridDim.z * U;
     if (c_first >= ce) return;
-    if (!a.drafts) de = db;
-    de = min_u32(de, db + (ce - cb - 1u));  // the last draft precedes the last column
+    uint32_t draft0, bias0;
+    first_entries(a, lane, draft0, bias0);
 
     // The streamed part copies (out of place) and masks.
     const uint32_t r = rows.row(tid * EPV);          // this thread's rows
@@ -239,43 +326,7 @@ __global__ __launch_bounds__(kBlock) void adjust_col(AdjustArgs a, uint32_t l0) 
     constexpr bool stream = !kInPlace || kMask;
     if constexpr (stream) load_columns(c_first);
 
-    // the touched places as a list
-    if (sparse) {
-        if (tid >= Rows::WORDS || wr >= V || !a.seen) word = 0;
-        else if (V - wr < 32u) word &= (1u << (V - wr)) - 1u;  // bits past the last row mean nothing
-        if (tid == 0) sh.n = 0;
-        if (a.drafts || kBias) {
-            if (tid < Rows::WORDS) {
-                sh.touched[tid] = word;
-                sh.drafted[tid] = 0;
-            }
-            if constexpr (kBias)
-                for (uint32_t i = tid; i < Rows::ROWS / 4; i += kBlock) reinterpret_cast<u32x4*>(sh.bias_at)[i] = u32x4{0u, 0u, 0u, 0u};
-            __syncthreads();
-            for (uint32_t i = db + tid; i < de; i += kBlock) {
-                const uint32_t at = rows.place((uint32_t)a.drafts[i], V);
-                if (at == Rows::ROWS) continue;
-                atomicOr(&sh.touched[at >> 5], 1u << (at & 31u));
-                atomicOr(&sh.drafted[at >> 5], 1u << (at & 31u));
-            }
-            if constexpr (kBias) {
-                for (uint32_t i = bb + tid; i < be; i += kBlock) {
-                    const uint32_t at = rows.place((uint32_t)a.bias_ids[i], V);
-                    if (at == Rows::ROWS) continue;
-                    atomicOr(&sh.touched[at >> 5], 1u << (at & 31u));
-                    atomicMax(&sh.bias_at[at], i - bb + 1u);
-                }
-            }
-            __syncthreads();
-            word = tid < Rows::WORDS ? sh.touched[tid] : 0u;
-        } else {
-            __syncthreads();
-        }
-        if (word) {
-            uint32_t pos = atomicAdd(&sh.n, (uint32_t)__popc(word));
-            for (; word; word &= word - 1u) sh.list[pos++] = (uint16_t)(tid * 32u + (uint32_t)__builtin_ctz(word));
-        }
-    }
+    if (sparse) make_list(a, rows, lane, draft0, bias0, sh);
     if constexpr (stream) {
         store_columns(c_first);
         for (uint32_t c0 = c_first + c_step; c0 < ce; c0 += c_step) {
@@ -286,15 +337,15 @@ __global__ __launch_bounds__(kBlock) void adjust_col(AdjustArgs a, uint32_t l0) 
     if (!sparse) return;
     __syncthreads();  // for the list, and for the streamed stores, which those below replace
 
-    const LaneRules rules(rep, a.presence ? pres : 0.0f, a.frequency ? freq : 0.0f, a.repetition != nullptr);
+    const LaneRules rules(lane.rep, lane.pres, lane.freq);
     const uint32_t n_rows = sh.n;
     const int32_t* counts = a.counts ? a.counts + (int64_t)l * a.counts_ld : nullptr;
     for (uint32_t k = tid; k < n_rows; k += kBlock) {
         const uint32_t at = sh.list[k], row = rows.row(at);
         uint32_t counted = (uint32_t)*(counts ? counts + row : or_safe<int32_t>(nullptr));
         const uint32_t b = kBias ? sh.bias_at[kBias ? at : 0] : 0u;
-        const float bias_value = kBias ? a.bias_values[b ? bb + b - 1u : 0u] : 0.0f;
-        uint64_t drafts = 0;  // bit i: draft i of the first 64 is this row
+        const float bias_value = kBias ? a.bias_values[b ? lane.bb + b - 1u : 0u] : 0.0f;
+        DraftsOfRow drafts;
         bool drafted = false;
         for (uint32_t c0 = c_first; c0 < ce; c0 += c_step) {
             uint32_t raw[U], ok[U];
@@ -312,22 +363,14 @@ __global__ __launch_bounds__(kBlock) void adjust_col(AdjustArgs a, uint32_t l0) 
             }
             if (c0 == c_first) {
                 if (!counts) counted = 0;
-                if (a.drafts) {
-                    drafted = sh.drafted[at >> 5] >> (at & 31u) & 1u;
-                    if (drafted)
-#pragma unroll 8
-                        for (uint32_t i = 0; i < min_u32(de - db, 64u); ++i) drafts |= (uint32_t)a.drafts[db + i] == row ? 1ull << i : 0ull;
-                }
+                drafted = a.drafts && (sh.drafted[at >> 5] >> (at & 31u) & 1u);
+                if (drafted) drafts.find(a, lane, row);
             }
 #pragma unroll
             for (uint32_t u = 0; u < U; ++u) {
                 if (c0 + u >= ce || (kMask && !(ok[u] & 1u))) continue;  // a forbidden element stays -Inf
                 uint32_t times = counted & 0x7FFFFFFFu;
-                if (drafted) {
-                    const uint32_t j = c0 + u - cb;  // drafts before the column
-                    times += (uint32_t)__popcll(j < 64u ? drafts & ((1ull << j) - 1u) : drafts);
-                    for (uint32_t i = db + 64u; i < min_u32(de, db + j); ++i) times += (uint32_t)a.drafts[i] == row ? 1u : 0u;
-                }
+                if (drafted) times += drafts.before(a, lane, row, c0 + u - cb);
                 // (a later column's draft changes nothing here)
                 if (counted >> 31 || times || b)
                     (static_cast<storage*>(a.out) + (int64_t)(c0 + u) * a.out_ld)[row] = (storage)from_double<DT>(
@@ -341,16 +384,36 @@ __global__ __launch_bounds__(kBlock) void adjust_col(AdjustArgs a, uint32_t l0) 
 
 constexpr uint32_t kRowTileVecs = 64;  // at most 64 vectors of a row per workgroup
 
-// Row-interleaved: a workgroup takes 1 << tx_log vectors of a row; each
-// thread one of them over 32 rows, which one word of each column's mask
-// covers.
-template <class DT, bool kInPlace>
+// A workgroup takes 1 << tx_log vectors of a row; each thread one of them over
+// 32 rows, which one word of each column's mask covers.
+template <class DT, bool kInPlace, bool kMask>
 __global__ __launch_bounds__(kBlock) void adjust_row_dense(AdjustArgs a, uint32_t tx_log, uint32_t tile0) {
     using storage = typename DT::storage;
     constexpr uint32_t EPV = DT::kPerVec, ALL = (1u << EPV) - 1u;
     __shared__ uint8_t active[kRowTileVecs * EPV];
-    const uint32_t tid = threadIdx.x;
+    const uint32_t tid = threadIdx.x, V = a.V;
     const uint32_t tile_c = ((tile0 + blockIdx.y) << tx_log) * EPV, tile_n = EPV << tx_log;
+    const uint32_t vc = tid & ((1u << tx_log) - 1u);
+    const uint32_t c = tile_c + vc * EPV;
+    const uint32_t r0 = blockIdx.x * (kBlock >> tx_log) * 32u + (tid >> tx_log) * 32u;
+    uint32_t words[EPV];
+    if constexpr (kMask) {
+        int64_t mi[EPV];
+#pragma unroll
+        for (uint32_t e = 0; e < EPV; ++e) {
+            const uint32_t ce = min_u32(c + e, a.C - 1u);
+            mi[e] = a.mask_index ? (int64_t)a.mask_index[ce] : (int64_t)ce;
+        }
+#pragma unroll
+        for (uint32_t e = 0; e < EPV; ++e) {
+            const bool has = mi[e] >= 0 && mi[e] < a.mask_count;
+            words[e] = a.mask[(has ? mi[e] * a.mask_ld : 0) + (min_u32(r0, V - 1u) >> 5)];
+            mi[e] = has ? 0 : -1;
+        }
+#pragma unroll
+        for (uint32_t e = 0; e < EPV; ++e) words[e] |= (uint32_t)mi[e];
+    }
+    uint32_t mine = c + EPV <= a.C ? ALL : c < a.C ? (1u << (a.C - c)) - 1u : 0u;  // bit e: column c + e is a lane's
     if (a.cols.start) {
         for (uint32_t i = tid; i < tile_n; i += kBlock) active[i] = 0;
         __syncthreads();
@@ -358,138 +421,102 @@ __global__ __launch_bounds__(kBlock) void adjust_row_dense(AdjustArgs a, uint32_
             uint32_t b, e;
             a.cols.range(l, b, e);
             e = min_u32(e, tile_c + tile_n);
-            for (uint32_t c = b < tile_c ? tile_c : b; c < e; ++c) active[c - tile_c] = 1;
+            for (uint32_t k = b < tile_c ? tile_c : b; k < e; ++k) active[k - tile_c] = 1;
         }
         __syncthreads();
-    }
-    const uint32_t vc = tid & ((1u << tx_log) - 1u);
-    const uint32_t c = tile_c + vc * EPV;
-    const uint32_t rows = (kBlock >> tx_log) * 32u;
-    const uint32_t r0 = blockIdx.x * rows + (tid >> tx_log) * 32u;
-    if (c >= a.C || r0 >= a.V) return;
-    uint32_t mine = 0;  // bit e: column c + e is a lane's
-    uint32_t words[EPV];
 #pragma unroll
-    for (uint32_t e = 0; e < EPV; ++e) {
-        words[e] = 0xFFFFFFFFu;
-        if (c + e < a.C && (!a.cols.start || active[vc * EPV + e])) {
-            mine |= 1u << e;
-            if (const uint32_t* m = mask_row(a, c + e)) words[e] = m[r0 >> 5];
-        }
+        for (uint32_t e = 0; e < EPV; ++e) mine &= active[vc * EPV + e] ? ~0u : ~(1u << e);
     }
-    const uint32_t n = min_u32(32u, a.V - r0);
+    if (mine == 0 || r0 >= V) return;
+    const uint32_t n = min_u32(32u, V - r0);
     const storage* x = static_cast<const storage*>(a.x) + (int64_t)r0 * a.ld + c;
     storage* out = static_cast<storage*>(a.out) + (int64_t)r0 * a.out_ld + c;
-#pragma unroll 4
-    for (uint32_t r = 0; r < n; ++r, x += a.ld, out += a.out_ld) {
-        uint32_t allowed = 0;
+    auto allowed = [&](uint32_t r) {
+        if (!kMask) return ALL;
+        uint32_t m = 0;
 #pragma unroll
-        for (uint32_t e = 0; e < EPV; ++e) allowed |= (words[e] >> r & 1u) << e;
-        if (kInPlace && allowed == ALL) continue;
-        if (mine == ALL) {
-            store16(out, masked<DT>(load16(x), allowed));
-        } else {
-            for (uint32_t e = 0; e < EPV; ++e)
-                if ((mine >> e & 1u) && (!kInPlace || !(allowed >> e & 1u)))
-                    out[e] = allowed >> e & 1u ? x[e] : (storage)kMinusInf<DT>;
+        for (uint32_t e = 0; e < EPV; ++e) m |= (words[e] >> r & 1u) << e;
+        return m;
+    };
+    if (mine == ALL) {
+        constexpr uint32_t U = 8;  // rows whose vectors are in flight together
+        for (uint32_t r = 0; r < n; r += U) {
+            u32x4 d[U];
+            uint32_t m[U];
+#pragma unroll
+            for (uint32_t u = 0; u < U; ++u) {
+                m[u] = allowed(r + u);
+                if (!kInPlace) d[u] = load16(x + (int64_t)min_u32(r + u, n - 1u) * a.ld);
+                else if (r + u < n && m[u] != ALL && m[u]) d[u] = load16(x + (int64_t)(r + u) * a.ld);
+            }
+#pragma unroll
+            for (uint32_t u = 0; u < U; ++u)
+                if (r + u < n && (!kInPlace || m[u] != ALL))
+                    store16(out + (int64_t)(r + u) * a.out_ld, kMask ? masked<DT>(d[u], m[u]) : d[u]);
         }
+        return;
+    }
+    for (uint32_t r = 0; r < n; ++r, x += a.ld, out += a.out_ld) {
+        const uint32_t m = allowed(r);
+        for (uint32_t e = 0; e < EPV; ++e)
+            if ((mine >> e & 1u) && (!kInPlace || !(m >> e & 1u))) out[e] = m >> e & 1u ? x[e] : (storage)kMinusInf<DT>;
     }
 }
 
-template <bool kBias>
-struct SparseShared {
-    uint32_t touched[kTile / 32];           // rows of the tile with a history, a draft or a bias
-    uint32_t drafted[kTile / 32];           // rows that are drafts
-    uint32_t bias_at[kBias ? kTile : 1];    // 1 + the last list entry of a row, or 0
-    uint16_t rows[kTile];                   // the touched rows
-    uint32_t wave_sum[kWaves];
-};
+constexpr uint32_t kSparseRows = 4096;
 
-// Lane l0 + blockIdx.y, rows [blockIdx.x * kTile, ...), all the lane's columns.
-template <class DT, bool kBias>
-__global__ __launch_bounds__(kBlock) void adjust_row_sparse(AdjustArgs a, uint32_t l0) {
+// Lane l0 + blockIdx.y, its touched rows; 1 << w_log threads share a row.
+template <class DT, bool kBias, bool kMask>
+__global__ __launch_bounds__(kBlock) void adjust_row_sparse(AdjustArgs a, uint32_t l0, uint32_t w_log) {
     using storage = typename DT::storage;
-    __shared__ SparseShared<kBias> sh;
-    static_assert(kTile / 32 == kBlock, "one word of the tile's rows per thread");
-    const uint32_t tid = threadIdx.x, l = l0 + blockIdx.y, t0 = blockIdx.x * kTile;
-    uint32_t cb, ce;
-    a.cols.range(l, cb, ce);
-    if (ce == cb) return;
-    const uint32_t ncols = ce - cb;
-
-    uint32_t word = 0;
-    if (a.seen && t0 + tid * 32u < a.V) {
-        word = a.seen[(int64_t)l * a.seen_ld + (t0 >> 5) + tid];
-        const uint32_t left = a.V - (t0 + tid * 32u);
-        if (left < 32u) word &= (1u << left) - 1u;  // bits past the last row mean nothing
-    }
-    sh.touched[tid] = word;
-    sh.drafted[tid] = 0;
-    if constexpr (kBias)
-        for (uint32_t i = tid; i < kTile; i += kBlock) sh.bias_at[i] = 0;
+    __shared__ TouchedRows<kSparseRows, kBias> sh;
+    const uint32_t l = l0 + blockIdx.y, tid = threadIdx.x;
+    const Rows<kSparseRows> rows{gridDim.x, blockIdx.x};
+    const Lane<kSparseRows, kBias> lane(a, rows, l);
+    if (lane.ce == lane.cb) return;
+    uint32_t draft0, bias0;
+    first_entries(a, lane, draft0, bias0);
+    make_list(a, rows, lane, draft0, bias0, sh);
     __syncthreads();
-    uint32_t db = 0, de = 0;
-    if (a.drafts) {
-        a.draft_parts.range(l, db, de);
-        de = min_u32(de, db + ncols - 1u);  // the last draft precedes the last column
-        for (uint32_t i = db + tid; i < de; i += kBlock) {
-            const uint32_t r = (uint32_t)a.drafts[i] - t0;
-            if (r < kTile && r < a.V - t0) {
-                atomicOr(&sh.touched[r >> 5], 1u << (r & 31u));
-                atomicOr(&sh.drafted[r >> 5], 1u << (r & 31u));
+
+    const LaneRules rules(lane.rep, lane.pres, lane.freq);
+    const uint32_t n_rows = sh.n, step = kBlock >> w_log;
+    const int32_t* counts = a.counts ? a.counts + (int64_t)l * a.counts_ld : nullptr;
+    for (uint32_t j = tid & ((1u << w_log) - 1u); j < lane.ce - lane.cb; j += 1u << w_log) {
+        const uint32_t c = lane.cb + j;
+        const uint32_t* mask = kMask ? mask_row(a, c) : nullptr;
+        constexpr uint32_t U = 4;  // rows whose reads are in flight together
+        for (uint32_t k0 = tid >> w_log; k0 < n_rows; k0 += step * U) {
+            uint32_t at[U], row[U], counted[U], raw[U], ok[U];
+#pragma unroll
+            for (uint32_t u = 0; u < U; ++u) {
+                at[u] = sh.list[min_u32(k0 + u * step, n_rows - 1u)];
+                row[u] = rows.row(at[u]);
+            }
+#pragma unroll
+            for (uint32_t u = 0; u < U; ++u) {
+                counted[u] = (uint32_t)*(counts ? counts + row[u] : or_safe<int32_t>(nullptr));
+                raw[u] = (uint32_t)static_cast<const storage*>(a.x)[(int64_t)row[u] * a.ld + c];
+                ok[u] = kMask ? *(mask ? mask + (row[u] >> 5) : or_safe<uint32_t>(nullptr)) : 0u;
+            }
+#pragma unroll
+            for (uint32_t u = 0; u < U; ++u) {
+                if (k0 + u * step >= n_rows || (mask && !(ok[u] >> (row[u] & 31u) & 1u))) continue;  // stays -Inf
+                const uint32_t word = counts ? counted[u] : 0u;
+                uint32_t times = word & 0x7FFFFFFFu;
+                if (a.drafts && (sh.drafted[at[u] >> 5] >> (at[u] & 31u) & 1u)) {
+                    DraftsOfRow drafts;
+                    drafts.find(a, lane, row[u]);
+                    times += drafts.before(a, lane, row[u], j);
+                }
+                const uint32_t b = kBias ? sh.bias_at[kBias ? at[u] : 0] : 0u;
+                const double bias = b ? (double)a.bias_values[lane.bb + b - 1u] : 0.0;
+                // (a later column's draft changes nothing here)
+                if (word >> 31 || times || b)
+                    static_cast<storage*>(a.out)[(int64_t)row[u] * a.out_ld + c] =
+                        (storage)from_double<DT>(rules.apply((double)to_float<DT>(raw[u]), word >> 31, times, bias));
             }
         }
-    }
-    uint32_t bb = 0, be = 0;
-    if constexpr (kBias) {
-        a.bias_parts.range(l, bb, be);
-        for (uint32_t i = bb + tid; i < be; i += kBlock) {
-            const uint32_t r = (uint32_t)a.bias_ids[i] - t0;
-            if (r < kTile && r < a.V - t0) {
-                atomicOr(&sh.touched[r >> 5], 1u << (r & 31u));
-                atomicMax(&sh.bias_at[r], i - bb + 1u);
-            }
-        }
-    }
-    __syncthreads();
-
-    // the touched rows as a list
-    word = sh.touched[tid];
-    const uint32_t lane = tid & 63u, mine = (uint32_t)__popc(word);
-    uint32_t upto = mine;
-#pragma unroll
-    for (uint32_t d = 1; d < 64; d <<= 1) {
-        const uint32_t o = __shfl_up(upto, d);
-        if (lane >= d) upto += o;
-    }
-    if (lane == 63u) sh.wave_sum[tid >> 6] = upto;
-    __syncthreads();
-    uint32_t base = upto - mine, nrows = 0;
-#pragma unroll
-    for (uint32_t w = 0; w < (uint32_t)kWaves; ++w) {
-        if (w < tid >> 6) base += sh.wave_sum[w];
-        nrows += sh.wave_sum[w];
-    }
-    for (; word; word &= word - 1u) sh.rows[base++] = (uint16_t)(tid * 32u + (uint32_t)__builtin_ctz(word));
-    __syncthreads();
-
-    const LaneRules rules(a, l);
-    const uint64_t items = (uint64_t)nrows * ncols;
-    for (uint64_t it = tid; it < items; it += kBlock) {
-        // neighbouring threads: neighbouring columns of a row
-        const uint32_t i = (uint32_t)(it / ncols), j = (uint32_t)(it % ncols);
-        const uint32_t r = sh.rows[i], row = t0 + r, c = cb + j;
-        const uint32_t w = a.counts ? (uint32_t)a.counts[(int64_t)l * a.counts_ld + row] : 0u;
-        uint32_t n = w & 0x7FFFFFFFu;
-        if (sh.drafted[r >> 5] >> (r & 31u) & 1u)
-            for (uint32_t d = db; d < min_u32(de, db + j); ++d) n += (uint32_t)a.drafts[d] == row ? 1u : 0u;
-        const uint32_t at = kBias ? sh.bias_at[kBias ? r : 0] : 0u;
-        if (!(w >> 31) && n == 0 && at == 0) continue;  // a later column's draft
-        const uint32_t* mask = mask_row(a, c);
-        if (mask && !(mask[row >> 5] >> (row & 31u) & 1u)) continue;
-        const double v = (double)to_float<DT>((uint32_t)static_cast<const storage*>(a.x)[(int64_t)row * a.ld + c]);
-        const double bias = at ? (double)a.bias_values[bb + at - 1u] : 0.0;
-        static_cast<storage*>(a.out)[(int64_t)row * a.out_ld + c] = (storage)from_double<DT>(rules.apply(v, w >> 31, n, bias));
     }
 }
 
@@ -497,7 +524,7 @@ __global__ __launch_bounds__(kBlock) void adjust_row_sparse(AdjustArgs a, uint32
 
 template <class DT, bool kInPlace, bool kBias, bool kMask>
 hipError_t launch_col(const AdjustArgs& a, hipStream_t stream) {
-    const uint32_t rows = ColRows<DT>::ROWS, tiles = (a.V + rows - 1) / rows;
+    const uint32_t rows = kBlock * DT::kPerVec, tiles = (a.V + rows - 1) / rows;
     // a workgroup per kColsAtOnce columns of a lane of average size
     const uint32_t z = min(((a.C + a.lanes - 1) / a.lanes + kColsAtOnce - 1) / kColsAtOnce, (uint32_t)kGridY);
     for (int64_t l0 = 0; l0 < a.lanes; l0 += kGridY) {
@@ -515,7 +542,7 @@ hipError_t launch_col(const AdjustArgs& a, hipStream_t stream) {
     return a.mask ? launch_col<DT, kInPlace, false, true>(a, stream) : launch_col<DT, kInPlace, false, false>(a, stream);
 }
 
-template <class DT, bool kInPlace>
+template <class DT, bool kInPlace, bool kMask>
 hipError_t launch_row_dense(const AdjustArgs& a, hipStream_t stream) {
     const uint32_t vecs = (a.C + DT::kPerVec - 1) / DT::kPerVec;
     uint32_t tx_log = 0;
@@ -524,21 +551,29 @@ hipError_t launch_row_dense(const AdjustArgs& a, hipStream_t stream) {
     const uint32_t col_tiles = (vecs + (1u << tx_log) - 1) >> tx_log;
     for (uint32_t t = 0; t < col_tiles; t += (uint32_t)kGridY) {
         const dim3 grid((a.V + rows - 1) / rows, min(col_tiles - t, (uint32_t)kGridY));
-        hipLaunchKernelGGL((adjust_row_dense<DT, kInPlace>), grid, dim3(kBlock), 0, stream, a, tx_log, t);
+        hipLaunchKernelGGL((adjust_row_dense<DT, kInPlace, kMask>), grid, dim3(kBlock), 0, stream, a, tx_log, t);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
     return hipSuccess;
 }
 
-template <class DT, bool kBias>
+template <class DT, bool kBias, bool kMask>
 hipError_t launch_row_sparse(const AdjustArgs& a, hipStream_t stream) {
-    const uint32_t tiles = (a.V + kTile - 1) / kTile;
+    const uint32_t tiles = (a.V + kSparseRows - 1) / kSparseRows, cols = (a.C + a.lanes - 1) / a.lanes;
+    uint32_t w_log = 0;
+    while (w_log < 6 && (1u << w_log) < cols) ++w_log;
     for (int64_t l0 = 0; l0 < a.lanes; l0 += kGridY) {
         const dim3 grid(tiles, (uint32_t)(a.lanes - l0 < kGridY ? a.lanes - l0 : kGridY));
-        hipLaunchKernelGGL((adjust_row_sparse<DT, kBias>), grid, dim3(kBlock), 0, stream, a, (uint32_t)l0);
+        hipLaunchKernelGGL((adjust_row_sparse<DT, kBias, kMask>), grid, dim3(kBlock), 0, stream, a, (uint32_t)l0, w_log);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
     return hipSuccess;
+}
+
+template <class DT>
+hipError_t launch_row_sparse(const AdjustArgs& a, hipStream_t stream) {
+    if (a.bias_ids) return a.mask ? launch_row_sparse<DT, true, true>(a, stream) : launch_row_sparse<DT, true, false>(a, stream);
+    return a.mask ? launch_row_sparse<DT, false, true>(a, stream) : launch_row_sparse<DT, false, false>(a, stream);
 }
 
 template <class DT>
@@ -548,13 +583,13 @@ hipError_t launch_dt(int layout, const AdjustArgs& a, hipStream_t stream) {
     if (in_place && !sparse && !a.mask) return hipSuccess;
     if (layout == TOPK_COL_CONTIG)
         return in_place ? launch_col<DT, true>(a, stream) : launch_col<DT, false>(a, stream);
-    if (!in_place)
-        if (const hipError_t e = launch_row_dense<DT, false>(a, stream); e != hipSuccess) return e;
-    if (sparse) {
-        const hipError_t e = a.bias_ids ? launch_row_sparse<DT, true>(a, stream) : launch_row_sparse<DT, false>(a, stream);
+    if (!in_place) {
+        const hipError_t e = a.mask ? launch_row_dense<DT, false, true>(a, stream) : launch_row_dense<DT, false, false>(a, stream);
         if (e != hipSuccess) return e;
     }
-    return in_place && a.mask ? launch_row_dense<DT, true>(a, stream) : hipSuccess;
+    if (sparse)
+        if (const hipError_t e = launch_row_sparse<DT>(a, stream); e != hipSuccess) return e;
+    return in_place && a.mask ? launch_row_dense<DT, true, true>(a, stream) : hipSuccess;
 }
 
 }  // namespace
