@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 LIBRARY = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtopk_cols.so")
 
@@ -44,22 +45,25 @@ _lib = None
 
 
 def _struct(name: str, fields: str):
-    """A ctypes structure from "type name" pairs, in the header's order."""
-    types = {"p": ctypes.c_void_p, "i64": ctypes.c_int64, "i32": ctypes.c_int32, "u64": ctypes.c_uint64,
-             "f64": ctypes.c_double}
+    """A structure of the header from "type name" pairs in its order: a ctypes
+    class, and the packer of its fields (a call packs one in a fraction of the
+    time that filling the class takes)."""
+    types = {"p": (ctypes.c_void_p, "P"), "i64": (ctypes.c_int64, "q"), "i32": (ctypes.c_int32, "i"),
+             "u64": (ctypes.c_uint64, "Q"), "f64": (ctypes.c_double, "d")}
     pairs = [f.split() for f in fields.split(",")]
-    return type(name, (ctypes.Structure,), {"_fields_": [(n, types[t]) for t, n in pairs]})
+    cls = type(name, (ctypes.Structure,), {"_fields_": [(n, types[t][0]) for t, n in pairs]})
+    return cls, struct.Struct("@" + "".join(types[t][1] for t, n in pairs)).pack
 
 
-AdjustRulesArgs = _struct("topk_adjust_rules", (
+AdjustRulesArgs, _ = _struct("topk_adjust_rules", (
     "i64 V, i64 C, i64 lanes, i32 dtype, i32 layout, i64 ld, i64 out_ld, p col_start, p counts, i64 counts_ld, "
     "p seen, i64 seen_ld, p repetition, p presence, p frequency, p drafts, p draft_start, i64 n_drafts, "
     "p bias_start, p bias_ids, p bias_values, i64 n_bias, p mask, i64 mask_ld, i64 mask_count, p mask_index"))
-VerifyArgs = _struct("topk_verify_args", (
+VerifyArgs, _pack_verify = _struct("topk_verify_args", (
     "i64 lanes, i32 dtype, i32 k, i32 kq, i64 C, p col_start, p target_values, p target_ids, i64 n_drafts, "
     "p draft_start, p drafts, p draft_values, p draft_ids, f64 temperature, f64 top_p, u64 seed, u64 offset, "
     "i64 max_tokens, p out_tokens, p out_count"))
-PlanArgs = _struct("topk_plan_args", (
+PlanArgs, _pack_plan = _struct("topk_plan_args", (
     "i64 lanes, i64 capacity, i32 block_size, p lens, p add, p held, p table, i64 table_ld, p free_ids, "
     "i64 n_free_ids, p free_count, p out_held, p out_free_count, p out_refused, p out_col_start, p out_col_lane, "
     "p out_col_pos, p out_slots"))
@@ -108,13 +112,13 @@ def load(path: str = LIBRARY):
     lib.topk_cols_debug_fail_waits.restype = ctypes.c_int
     lib.topk_cols_run_noalloc.argtypes = [i64, i64, i32, i32, i32, i64, p, p, p, p]
     lib.topk_cols_run_noalloc.restype = ctypes.c_int
-    lib.topk_cols_adjust.argtypes = [ctypes.POINTER(AdjustRulesArgs), p, p, p]
+    lib.topk_cols_adjust.argtypes = [p, p, p, p]
     lib.topk_cols_adjust.restype = ctypes.c_int
     lib.topk_cols_count.argtypes = [i64, i64, p, i64, p, p, p, p, i64, p, i64, p]
     lib.topk_cols_count.restype = ctypes.c_int
-    lib.topk_cols_verify.argtypes = [ctypes.POINTER(VerifyArgs), p]
+    lib.topk_cols_verify.argtypes = [p, p]
     lib.topk_cols_verify.restype = ctypes.c_int
-    lib.topk_cols_plan.argtypes = [ctypes.POINTER(PlanArgs), p]
+    lib.topk_cols_plan.argtypes = [p, p]
     lib.topk_cols_plan.restype = ctypes.c_int
     _lib = lib
     return lib
@@ -304,26 +308,25 @@ def run_noalloc(x, V: int, C: int, k: int, dtype: str = "bf16", layout: str = "c
     return values, ids
 
 
-def _need(name: str, t, numel: int, device, dtype: str = "int32") -> int:
-    """Address of a contiguous GPU tensor of at least numel elements (0 for None)."""
+def _need(name: str, t, numel: int, index: int, dtype) -> int:
+    """Address of a contiguous tensor of at least numel elements on GPU
+    `index` (0 for None)."""
     if t is None:
         return 0
-    if not t.is_cuda or t.device != device or str(t.dtype) != "torch." + dtype or t.numel() < numel \
-            or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {numel} elements on {device}")
+    if t.dtype is not dtype or t.get_device() != index or index < 0 or t.numel() < numel or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {numel} elements on GPU {index}")
     return t.data_ptr()
 
 
-def _launch(what: str, device, stream, call) -> None:
-    """call(raw stream) with the tensors' device current (the current stream
-    by default)."""
+def _launch(what: str, function, index: int, stream, *args) -> None:
+    """function(*args, raw stream) with GPU `index` current, on its current
+    stream by default."""
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    if device.index == torch.cuda.current_device():
-        rc = call(s.cuda_stream)
+    if index == torch._C._cuda_getDevice():
+        rc = function(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
     else:
-        with torch.cuda.device(device):
-            rc = call(s.cuda_stream)
+        with torch.cuda.device(index):
+            rc = function(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
     if rc != TOPK_OK:
         raise TopkError(rc, what)
 
@@ -371,10 +374,11 @@ class AdjustRules:
             col_start=col_start, counts=counts, seen=seen, repetition=repetition, presence=presence,
             frequency=frequency, drafts=drafts, draft_start=draft_start, bias_start=bias_start, bias_ids=bias_ids,
             bias_values=bias_values, mask=mask, mask_index=mask_index)
-        devices = {t.device for t in tensors.values() if t is not None}
+        import torch
+        devices = {t.get_device() for t in tensors.values() if t is not None}
         if len(devices) > 1:
-            raise ValueError("the rules' tensors must be on one device")
-        self.device = devices.pop() if devices else None
+            raise ValueError("the rules' tensors must be on one GPU")
+        self._index = devices.pop() if devices else None
         words = (V + 31) // 32
         for name, t, least in (("counts", counts, V), ("seen", seen, words), ("mask", mask, words)):
             if t is not None and (t.dim() != 2 or t.shape[1] < least or (name != "mask" and t.shape[0] < lanes)):
@@ -386,7 +390,7 @@ class AdjustRules:
         sizes = dict(col_start=lanes + 1, repetition=lanes, presence=lanes, frequency=lanes, draft_start=lanes + 1,
                      bias_start=lanes + 1, mask_index=C)
         floats = ("repetition", "presence", "frequency", "bias_values")
-        at = {n: _need(n, t, sizes.get(n, 0), self.device, "float32" if n in floats else "int32")
+        at = {n: _need(n, t, sizes.get(n, 0), self._index, torch.float32 if n in floats else torch.int32)
               for n, t in tensors.items()}
         # an empty tensor has no address; an empty list is the same as none
         if bias_ids is not None and bias_ids.numel() == 0:
@@ -400,6 +404,8 @@ class AdjustRules:
             n_bias=bias_ids.numel() if bias_ids is not None else 0,
             mask_ld=mask.shape[1] if mask is not None else 0, mask_count=mask.shape[0] if mask is not None else 0, **at)
         self._ref = ctypes.byref(self._args)
+        self._function = load().topk_cols_adjust
+        self._size = 2 if dtype == "bf16" else 4
         rows, width = (C, V) if layout == "col" else (V, C)
         self._numel = (rows - 1) * self.ld + width
         self._out_numel = (rows - 1) * self.out_ld + width
@@ -409,19 +415,18 @@ class AdjustRules:
         not given: its padding, and columns of no lane, are then
         uninitialised).  out=x works in place.  x and out are contiguous GPU
         tensors of the matrix (bf16 or fp32, or patterns of the same width)."""
-        import torch
         if out is None:
+            import torch
             if self.out_ld != self.ld:
                 raise ValueError("out is needed when out_ld differs from ld")
             out = torch.empty_like(x)
-        size = 2 if self.dtype == "bf16" else 4
-        if not (x.is_cuda and out.is_cuda) or x.device != out.device or self.device not in (None, x.device):
+        index = x.get_device()
+        if index < 0 or out.get_device() != index or self._index not in (None, index):
             raise ValueError("x, out and the rules' tensors must be on one GPU")
-        if x.element_size() != size or out.element_size() != size or x.numel() < self._numel \
+        if x.element_size() != self._size or out.element_size() != self._size or x.numel() < self._numel \
                 or out.numel() < self._out_numel or not (x.is_contiguous() and out.is_contiguous()):
             raise ValueError("x and out must be contiguous and hold the matrix described by the rules")
-        _launch("topk_cols_adjust", x.device, stream,
-                lambda s: load().topk_cols_adjust(self._ref, x.data_ptr(), out.data_ptr(), s))
+        _launch("topk_cols_adjust", self._function, index, stream, self._ref, x.data_ptr(), out.data_ptr())
         return out
 
 
@@ -435,13 +440,15 @@ def count_tokens(counts, seen, V: int, ids, start=None, prompt_len=None, fresh=N
         prompt (none without it).  fresh (lanes,): lanes to clear first.
     Returns (counts, seen).
     """
-    lanes, dev = counts.shape[0], counts.device
+    import torch
+    i32, index, lanes = torch.int32, counts.get_device(), counts.shape[0]
     if counts.dim() != 2 or seen.dim() != 2 or seen.shape[0] != lanes:
         raise ValueError("counts and seen must be matrices with a row per lane")
-    args = (V, lanes, _need("ids", ids, 0, dev) if ids.numel() else 0, ids.numel(), _need("start", start, lanes + 1, dev),
-            _need("prompt_len", prompt_len, lanes, dev), _need("fresh", fresh, lanes, dev),
-            _need("counts", counts, 1, dev), counts.shape[1], _need("seen", seen, 1, dev), seen.shape[1])
-    _launch("topk_cols_count", dev, stream, lambda s: load().topk_cols_count(*args, s))
+    n = ids.numel()
+    _launch("topk_cols_count", load().topk_cols_count, index, stream, V, lanes,
+            _need("ids", ids, 0, index, i32) if n else 0, n, _need("start", start, lanes + 1, index, i32),
+            _need("prompt_len", prompt_len, lanes, index, i32), _need("fresh", fresh, lanes, index, i32),
+            _need("counts", counts, 1, index, i32), counts.shape[1], _need("seen", seen, 1, index, i32), seen.shape[1])
     return counts, seen
 
 
@@ -464,42 +471,40 @@ def verify(target_values, target_ids, col_start, drafts, draft_start, draft_valu
     enough for any lane; pass the round's draft limit + 1).
     """
     import torch
-    dev = target_values.device
+    i32, index = torch.int32, target_values.get_device()
     if lanes is None:
         if col_start is None:
             raise ValueError("lanes is needed without col_start")
         lanes = col_start.numel() - 1
+    n = drafts.numel()
     if out_tokens is None:
-        out_tokens = torch.empty((lanes, max_tokens or drafts.numel() + 1), dtype=torch.int32, device=dev)
+        out_tokens = torch.empty((lanes, max_tokens or n + 1), dtype=i32, device=target_values.device)
     if out_count is None:
-        out_count = torch.empty(lanes, dtype=torch.int32, device=dev)
+        out_count = torch.empty(lanes, dtype=i32, device=target_values.device)
     if target_values.dim() != 2 or target_ids.shape != target_values.shape or out_tokens.dim() != 2 \
             or out_tokens.shape[0] < lanes:
         raise ValueError("target_values and target_ids must be (C, k), out_tokens a matrix with a row per lane")
     C, k = target_values.shape
-    n = drafts.numel()
-    kq = 0
+    size = target_values.element_size()
+    if index < 0 or size not in (2, 4) or not target_values.is_contiguous():
+        raise ValueError("target_values must be a contiguous GPU tensor of bf16 or fp32 (or patterns)")
+    kq = qv = qi = 0
     if draft_values is not None:
         if draft_values.dim() != 2 or draft_ids is None or draft_ids.shape != draft_values.shape \
-                or draft_values.element_size() != target_values.element_size():
-            raise ValueError("draft_values and draft_ids must be (n, kq), of the target lists' types")
-        kq = draft_values.shape[1]
+                or draft_values.element_size() != size or draft_values.get_device() != index \
+                or not draft_values.is_contiguous():
+            raise ValueError("draft_values and draft_ids must be contiguous (n, kq) tensors of the target lists' types")
         # drafts past the lists have no distribution to be judged by
         n = min(n, draft_values.shape[0])
-    for name, t in (("target_values", target_values), ("draft_values", draft_values)):
-        if t is not None and not (t.is_cuda and t.device == dev and t.is_contiguous() and t.element_size() in (2, 4)):
-            raise ValueError(f"{name} must be a contiguous GPU tensor of bf16 or fp32 (or patterns)")
-    lists = draft_values is not None and n > 0
-    args = VerifyArgs(
-        lanes=lanes, dtype=0 if target_values.element_size() == 2 else 1, k=k, kq=kq if lists else 0, C=C,
-        col_start=_need("col_start", col_start, lanes + 1, dev), target_values=target_values.data_ptr(),
-        target_ids=_need("target_ids", target_ids, 1, dev), n_drafts=n,
-        draft_start=_need("draft_start", draft_start, lanes + 1, dev), drafts=_need("drafts", drafts, 0, dev) if n else 0,
-        draft_values=draft_values.data_ptr() if lists else 0,
-        draft_ids=_need("draft_ids", draft_ids, 0, dev) if lists else 0, temperature=float(temperature),
-        top_p=float(top_p), seed=int(seed), offset=int(offset), max_tokens=out_tokens.shape[1],
-        out_tokens=_need("out_tokens", out_tokens, 1, dev), out_count=_need("out_count", out_count, lanes, dev))
-    _launch("topk_cols_verify", dev, stream, lambda s: load().topk_cols_verify(ctypes.byref(args), s))
+        if n:
+            kq, qv, qi = draft_values.shape[1], draft_values.data_ptr(), _need("draft_ids", draft_ids, 0, index, i32)
+    args = _pack_verify(
+        lanes, 0 if size == 2 else 1, k, kq, C, _need("col_start", col_start, lanes + 1, index, i32),
+        target_values.data_ptr(), _need("target_ids", target_ids, 1, index, i32), n,
+        _need("draft_start", draft_start, lanes + 1, index, i32), _need("drafts", drafts, 0, index, i32) if n else 0, qv,
+        qi, temperature, top_p, seed, offset, out_tokens.shape[1], _need("out_tokens", out_tokens, 1, index, i32),
+        _need("out_count", out_count, lanes, index, i32))
+    _launch("topk_cols_verify", load().topk_cols_verify, index, stream, args)
     return out_tokens, out_count
 
 
@@ -516,21 +521,26 @@ def plan(lens, add, held, table, free_ids, free_count, block_size: int, capacity
     (lanes + 1,), col_lane, col_pos (capacity,) and int64 slots (capacity,).
     """
     import torch
-    lanes, dev = lens.numel(), lens.device
+    i32, index, lanes = torch.int32, lens.get_device(), lens.numel()
     if table.dim() != 2 or table.shape[0] < lanes:
         raise ValueError("table must be a matrix with a row per lane")
-    sizes = dict(held=lanes, free_count=1, refused=1, col_start=lanes + 1, col_lane=capacity, col_pos=capacity,
-                 slots=capacity)
-    kinds = {n: "int64" if n == "slots" else "int32" for n in sizes}
     if out is None:
-        out = {n: torch.empty(max(size, 1), dtype=getattr(torch, kinds[n]), device=dev) for n, size in sizes.items()}
-    outs = {"out_" + n: _need(n, out[n], size, dev, kinds[n]) for n, size in sizes.items()}
-    args = PlanArgs(
-        lanes=lanes, capacity=capacity, block_size=block_size, lens=_need("lens", lens, lanes, dev),
-        add=_need("add", add, lanes, dev), held=_need("held", held, lanes, dev), table=_need("table", table, 1, dev),
-        table_ld=table.shape[1], free_ids=_need("free_ids", free_ids, 0, dev) if free_ids.numel() else 0,
-        n_free_ids=free_ids.numel(), free_count=_need("free_count", free_count, 1, dev), **outs)
-    _launch("topk_cols_plan", dev, stream, lambda s: load().topk_cols_plan(ctypes.byref(args), s))
+        sizes = dict(held=lanes, free_count=1, refused=1, col_start=lanes + 1, col_lane=capacity, col_pos=capacity,
+                     slots=capacity)
+        out = {n: torch.empty(size, dtype=torch.int64 if n == "slots" else i32, device=lens.device)
+               for n, size in sizes.items()}
+    n_free = free_ids.numel()
+    args = _pack_plan(
+        lanes, capacity, block_size, _need("lens", lens, lanes, index, i32), _need("add", add, lanes, index, i32),
+        _need("held", held, lanes, index, i32), _need("table", table, 1, index, i32), table.shape[1],
+        _need("free_ids", free_ids, 0, index, i32) if n_free else 0, n_free,
+        _need("free_count", free_count, 1, index, i32), _need("out held", out["held"], lanes, index, i32),
+        _need("out free_count", out["free_count"], 1, index, i32), _need("out refused", out["refused"], 1, index, i32),
+        _need("out col_start", out["col_start"], lanes + 1, index, i32),
+        _need("out col_lane", out["col_lane"], capacity, index, i32),
+        _need("out col_pos", out["col_pos"], capacity, index, i32),
+        _need("out slots", out["slots"], capacity, index, torch.int64))
+    _launch("topk_cols_plan", load().topk_cols_plan, index, stream, args)
     return out
 
 
