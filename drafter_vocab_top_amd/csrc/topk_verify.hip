@@ -10,12 +10,12 @@
 // of p - q otherwise leaves each token distributed as p.
 //
 // One workgroup per lane, one wave per column: a column's test and the token
-// it would give do not depend on the other columns, so the waves compute
-// both at once and only then agree on the first refusal.  List entry i lies
-// in lane i (k <= 64).
+// it would give do not depend on the other columns, so the waves compute them
+// at once and only then agree on the first refusal.  List entry i lies in lane
+// i (k <= 64), and a running sum is a scan over the wave.
 //
 // The decisions are integers made by floating point, so every step is IEEE
-// double in a fixed order with no contraction; sums run in list order.
+// double in a fixed order with no contraction.
 #include "topk_draw.hpp"
 #include "topk_round.hpp"
 
@@ -23,36 +23,50 @@ namespace topk {
 
 namespace {
 
-constexpr uint32_t kVerifyWaves = 8;  // columns judged at once
-constexpr uint32_t kVerifyThreads = kVerifyWaves * 64;
-
-// Lane m gets x_0 + ... + x_m (x_0 .. x_{n-1}, added in this order; lanes
-// past the end hold the total).
-__device__ __forceinline__ double ordered_sums(double x, int32_t n) {
-#pragma clang fp contract(off)
-    const int32_t lane = (int32_t)(threadIdx.x & 63u);
-    double acc = 0.0;
-    for (int32_t j = 0; j < n; ++j) {
-        const double xj = lane_value(x, j);
-        if (j <= lane) acc = acc + xj;
-    }
-    return acc;
+// x of lane - N of the same 16 lanes (0.0 where there is none).
+template <int kCtrl, int kRowMask>
+__device__ __forceinline__ double dpp_or_zero(double x) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, kCtrl, kRowMask, 0xF, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), kCtrl, kRowMask, 0xF, true);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
-// The probability of this lane's entry of a list (0 past the nucleus).
+// Lane m gets x_0 + ... + x_m: within each 16 lanes in steps of 1, 2, 4 and
+// 8, then the sum of the first 16 onto the second and of the third onto the
+// fourth, then the sum of the first 32 onto the others.  (A sum in list order
+// would be 64 dependent additions instead of 6.)
+__device__ __forceinline__ double running_sum(double x) {
+#pragma clang fp contract(off)
+    x = x + dpp_or_zero<0x111, 0xF>(x);  // row_shr:1
+    x = x + dpp_or_zero<0x112, 0xF>(x);
+    x = x + dpp_or_zero<0x114, 0xF>(x);
+    x = x + dpp_or_zero<0x118, 0xF>(x);
+    x = x + dpp_or_zero<0x142, 0xA>(x);  // row_bcast:15
+    x = x + dpp_or_zero<0x143, 0xC>(x);  // row_bcast:31
+    return x;
+}
+
+// This lane's entry of a list: its value, and the list's first.
 template <class DT>
-__device__ __forceinline__ double probability(const typename DT::storage* v, int32_t k, double temperature,
-                                              double top_p) {
+__device__ __forceinline__ void load_entry(const void* values, int64_t row, int32_t k, double& v, double& v0) {
+    const typename DT::storage* p = static_cast<const typename DT::storage*>(values) + row * k;
+    const int32_t lane = (int32_t)(threadIdx.x & 63u);
+    v = stored_value<DT>(p, lane < k ? lane : 0);
+    v0 = lane_value(v, 0);
+}
+
+// The probability of this lane's entry (0 past the nucleus of n entries).
+__device__ __forceinline__ double probability(double v, double v0, int32_t k, double temperature, double top_p, int32_t& n) {
 #pragma clang fp contract(off)
     const int32_t lane = (int32_t)(threadIdx.x & 63u);
-    const double v0 = stored_value<DT>(v, 0);
+    n = 1;
     if (temperature == 0.0 || !__builtin_isfinite(v0)) return lane == 0 ? 1.0 : 0.0;
     const bool in = lane < k;
-    const double w = in ? fixed_exp((stored_value<DT>(v, lane) - v0) / temperature) : 0.0;
-    const double sums = ordered_sums(w, k);
-    const double need = top_p * lane_value(sums, k - 1);
-    const unsigned long long reach = __ballot(in && sums >= need);
-    const int32_t n = reach ? (int32_t)first_lane(reach) + 1 : k;
+    const double w = in ? fixed_exp((v - v0) / temperature) : 0.0;
+    const double sums = running_sum(w);
+    const unsigned long long reach = __ballot(in && sums >= top_p * lane_value(sums, k - 1));
+    n = reach ? (int32_t)first_lane(reach) + 1 : k;
     return lane < n ? w / lane_value(sums, n - 1) : 0.0;
 }
 
@@ -62,14 +76,14 @@ __device__ __forceinline__ double probability_of(int32_t d, int32_t id, double p
     return m ? lane_value(p, (int)first_lane(m)) : 0.0;
 }
 
-template <class DT>
-__global__ __launch_bounds__(kVerifyThreads) void verify_kernel(VerifyArgs args) {
+template <class DT, uint32_t kWavesPerLane>
+__global__ __launch_bounds__(kWavesPerLane * 64) void verify_kernel(VerifyArgs args) {
 #pragma clang fp contract(off)
-    using storage = typename DT::storage;
-    __shared__ int32_t token[kVerifyWaves];
-    __shared__ uint32_t refused[kVerifyWaves];
+    __shared__ int32_t token[kWavesPerLane];
+    __shared__ uint32_t refused[kWavesPerLane];
     const topk_verify_args& a = args.v;
-    const uint32_t l = blockIdx.x, tid = threadIdx.x, wave = tid >> 6;
+    const uint32_t l = blockIdx.x, tid = threadIdx.x;
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(tid >> 6));
     const int32_t lane = (int32_t)(tid & 63u);
     int32_t* out = a.out_tokens + (int64_t)l * a.max_tokens;
     uint32_t cb, ce, db, de;
@@ -78,54 +92,64 @@ __global__ __launch_bounds__(kVerifyThreads) void verify_kernel(VerifyArgs args)
     uint32_t count = 0;  // tokens of the lane
     if (ce > cb) {
         const uint32_t m = min_u32(min_u32(de - db, ce - cb - 1u), (uint32_t)a.max_tokens - 1u);
-        for (uint32_t j0 = 0;; j0 += kVerifyWaves) {
+        for (uint32_t j0 = 0;; j0 += kWavesPerLane) {
             const uint32_t j = j0 + wave;
             if (j <= m) {  // wave-uniform
-                const int64_t c = (int64_t)cb + j;
-                const int32_t id = lane < a.k ? a.target_ids[c * a.k + lane] : 0;
-                const double p = probability<DT>(static_cast<const storage*>(a.target_values) + c * a.k, a.k,
-                                                 a.temperature, a.top_p);
+                const int64_t c = (int64_t)cb + j, row = (int64_t)db + j;
+                const bool judged = j < m, listed = judged && a.draft_values;
+                // everything the column reads
+                const int32_t id = a.target_ids[c * a.k + (lane < a.k ? lane : 0)];
+                double v, v0, qv = 0.0, qv0 = 0.0;
+                load_entry<DT>(a.target_values, c, a.k, v, v0);
+                int32_t d = 0, qid = 0;
+                if (judged) d = a.drafts[row];
+                if (listed) {
+                    qid = a.draft_ids[row * a.kq + (lane < a.kq ? lane : 0)];
+                    load_entry<DT>(a.draft_values, row, a.kq, qv, qv0);
+                }
+                int32_t n, nq = 1;
+                const double p = probability(v, v0, a.k, a.temperature, a.top_p, n);
+                double q = 0.0, q_d = 1.0;
                 bool accept = false;
-                double rest = p;
-                if (j < m) {
-                    const int64_t row = (int64_t)db + j;
-                    const int32_t d = a.drafts[row];
-                    double q_d = 1.0, q_at = lane < a.k && id == d ? 1.0 : 0.0;
-                    if (a.draft_values) {
-                        const int32_t qid = lane < a.kq ? a.draft_ids[row * a.kq + lane] : 0;
-                        const double q = probability<DT>(static_cast<const storage*>(a.draft_values) + row * a.kq, a.kq,
-                                                         a.temperature, a.top_p);
+                if (judged) {
+                    if (listed) {
+                        q = probability(qv, qv0, a.kq, a.temperature, a.top_p, nq);
                         q_d = probability_of(d, qid, q, a.kq);
-                        bool found = false;
-                        q_at = 0.0;
-                        for (int32_t t = 0; t < a.kq; ++t) {
-                            const double qt = lane_value(q, t);
-                            if (!found && __builtin_amdgcn_readlane(qid, t) == id) {
-                                found = true;
-                                q_at = qt;
+                    }
+                    accept = philox_uniform(a.seed, a.offset, (uint32_t)c, 1u) * q_d < probability_of(d, id, p, a.k);
+                }
+                int32_t next = 0;
+                if (!accept) {  // (the token after an accepted draft is the next column's)
+                    double rest = p;
+                    if (judged) {
+                        double q_at = lane < a.k && id == d ? 1.0 : 0.0;
+                        if (listed) {
+                            q_at = 0.0;
+                            // from the last, so that the first entry of an id stays
+                            for (int32_t t = nq - 1; t >= 0; --t) {
+                                const double qt = lane_value(q, t);
+                                if (__builtin_amdgcn_readlane(qid, t) == id) q_at = qt;
                             }
                         }
+                        const double diff = p - q_at;
+                        rest = diff > 0.0 ? diff : 0.0;
+                        if (__ballot(rest > 0.0) == 0ull) rest = p;
                     }
-                    const double u = philox_uniform(a.seed, a.offset, (uint32_t)c, 1u);
-                    accept = u * q_d < probability_of(d, id, p, a.k);
-                    const double diff = p - q_at;
-                    rest = diff > 0.0 ? diff : 0.0;
-                    if (__ballot(rest > 0.0) == 0ull) rest = p;
+                    const double sums = running_sum(rest);
+                    const double target = philox_uniform(a.seed, a.offset, (uint32_t)c, 2u) * lane_value(sums, a.k - 1);
+                    const unsigned long long some = __ballot(rest > 0.0);
+                    const unsigned long long above = __ballot(rest > 0.0 && sums > target);
+                    // (a product rounded up to the total leaves none above it: the last entry that can be drawn)
+                    const uint32_t pick = above ? first_lane(above) : some ? 63u - (uint32_t)__builtin_clzll(some) : 0u;
+                    next = __builtin_amdgcn_readlane(id, (int)pick);
                 }
-                const double sums = ordered_sums(rest, a.k);
-                const double target = philox_uniform(a.seed, a.offset, (uint32_t)c, 2u) * lane_value(sums, a.k - 1);
-                const unsigned long long above = __ballot(lane < a.k && sums > target);
-                const unsigned long long some = __ballot(lane < a.k && rest > 0.0);
-                // (a product rounded up to the total leaves none above it: the last entry that can be drawn)
-                const uint32_t pick = above ? first_lane(above) : some ? 63u - (uint32_t)__builtin_clzll(some) : 0u;
-                const int32_t next = __builtin_amdgcn_readlane(id, (int)pick);
                 if (lane == 0) {
                     token[wave] = next;
                     refused[wave] = accept ? 0u : 1u;
                 }
             }
             __syncthreads();
-            const uint32_t n = min_u32(kVerifyWaves, m + 1u - j0);  // columns of this step
+            const uint32_t n = min_u32(kWavesPerLane, m + 1u - j0);  // columns of this step
             uint32_t t = 0;
             while (t < n && !refused[t]) ++t;  // column m is never accepted
             if (tid < t) out[j0 + tid] = a.drafts[(int64_t)db + j0 + tid];
@@ -137,17 +161,25 @@ __global__ __launch_bounds__(kVerifyThreads) void verify_kernel(VerifyArgs args)
             __syncthreads();  // the next step writes token and refused again
         }
     }
-    for (uint32_t i = count + tid; i < (uint32_t)a.max_tokens; i += kVerifyThreads) out[i] = -1;
+    for (uint32_t i = count + tid; i < (uint32_t)a.max_tokens; i += kWavesPerLane * 64u) out[i] = -1;
     if (tid == 0) a.out_count[l] = (int32_t)count;
+}
+
+template <class DT>
+hipError_t launch_dt(const VerifyArgs& a, hipStream_t stream) {
+    const dim3 grid((uint32_t)a.v.lanes);
+    // a wave for every column of a lane of average size, up to 16
+    const int64_t columns = (a.v.C + a.v.lanes - 1) / a.v.lanes;
+    if (columns <= 4) hipLaunchKernelGGL((verify_kernel<DT, 4>), grid, dim3(256), 0, stream, a);
+    else if (columns <= 8) hipLaunchKernelGGL((verify_kernel<DT, 8>), grid, dim3(512), 0, stream, a);
+    else hipLaunchKernelGGL((verify_kernel<DT, 16>), grid, dim3(1024), 0, stream, a);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t stream) {
-    const dim3 grid((uint32_t)a.v.lanes), block(kVerifyThreads);
-    if (a.v.dtype == TOPK_BF16) hipLaunchKernelGGL(verify_kernel<Bf16>, grid, block, 0, stream, a);
-    else hipLaunchKernelGGL(verify_kernel<F32>, grid, block, 0, stream, a);
-    return hipGetLastError();
+    return a.v.dtype == TOPK_BF16 ? launch_dt<Bf16>(a, stream) : launch_dt<F32>(a, stream);
 }
 
 }  // namespace topk

@@ -372,10 +372,10 @@ typedef struct {
  * column:
  *   draft j < m is accepted if u * q_j(d_j) < p_j(d_j);
  *   t is the number of drafts accepted before the first refused one;
- *   the next token is entry i of column t, the smallest i with
- *   R_{i+1} > u' * R_k, where R_i sums the first i of the weights
+ *   the next token is entry i of column t, the smallest i of positive weight
+ *   with R_{i+1} > u' * R_k, where R_i sums the first i of the weights
  *   max(p_t(i) - q_t(id_i), 0) if t < m, or p_t(i) if t = m or those are
- *   all 0.
+ *   all 0 (the last entry of positive weight where rounding leaves none).
  * out_tokens[l*max_tokens ..] = the t drafts, the token, then -1;
  * out_count[l] = t + 1.  A lane without columns gets only -1, and count 0.
  *
@@ -383,8 +383,10 @@ typedef struct {
  * (offset & 0xFFFFFFFF, offset >> 32, column, 1) for u and (.., 2) for u',
  * the column being the target column's index.  (topk_cols_sample uses 0, so
  * one offset can serve a round.)  Arithmetic is IEEE double in the order
- * written, exp as in topk_cols_sample: the result is reproducible bit for
- * bit.
+ * written, exp as in topk_cols_sample, and a running sum is a scan: within
+ * each 16 entries in steps of 1, 2, 4 and 8, then the sums of entries 0-15
+ * and 32-47 onto the 16 that follow, then that of the first 32 onto the rest.
+ * The result is reproducible bit for bit.
  *
  * Returns TOPK_ERR_INVALID_ARG for a NULL or misaligned pointer, a value out
  * of the ranges above, or lanes that do not divide C (col_start NULL) or
