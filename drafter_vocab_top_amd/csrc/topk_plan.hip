@@ -4,8 +4,8 @@
 // Everything is whole numbers: over the lanes, in order, the running sum of
 // the blocks needed decides who is served, and the running sum of the served
 // lanes' columns where theirs begin.  One launch: every workgroup runs both
-// sums over all lanes (they are few, and stay in the caches), 1,024 lanes at
-// a time, and then writes its own range of columns, finding each column's
+// sums over all lanes (they are few, and stay in the caches), 256 or 1,024
+// lanes at a time, and then writes its own range of columns, finding each column's
 // lane by bisection in LDS.  Workgroup 0 writes what there is per lane; new
 // table entries are spread over all workgroups.
 //
@@ -18,39 +18,51 @@ namespace topk {
 
 namespace {
 
-constexpr uint32_t kPlanLanes = 1024;             // lanes per step
-constexpr uint32_t kPer = kPlanLanes / kBlock;    // consecutive lanes of a thread
-constexpr uint32_t kPlanColumns = 2048;           // columns per workgroup
+constexpr uint32_t kPlanColumns = 1024;           // columns per workgroup
 
+struct alignas(16) PlanLane {
+    uint32_t base;       // position - column, of the lane's columns
+    uint32_t held;
+    uint32_t free_base;  // its table entry e >= held is free_ids[free_base - e]
+    uint32_t unused;
+};
+
+template <uint32_t kLanes>
 struct PlanShared {
-    uint32_t end[kPlanLanes];    // columns of the lanes up to and including this one
-    uint32_t taken[kPlanLanes];  // blocks of the served lanes up to and including this one
-    uint32_t need[kPlanLanes];
-    uint32_t len[kPlanLanes];
-    uint32_t held[kPlanLanes];
-    int64_t wave_sum[kWaves];
+    PlanLane lane[kLanes];
+    uint32_t end[kLanes];    // columns of the lanes up to and including this one
+    uint32_t taken[kLanes];  // blocks of the served lanes up to and including this one
+    int64_t wave_sum[2][kWaves];
     uint32_t served, taken_to, refused;
 };
 
+template <int kCtrl, int kRowMask>
+__device__ __forceinline__ int64_t dpp_or_zero(int64_t x) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)x, kCtrl, kRowMask, 0xF, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)((uint64_t)x >> 32), kCtrl, kRowMask, 0xF, true);
+    return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
 // Sum of the values of the threads before this one; total: of all threads.
-__device__ __forceinline__ int64_t block_sum_before(PlanShared& sh, int64_t v, int64_t& total) {
+// sums: kWaves values of LDS that no other call before the next barrier uses.
+__device__ __forceinline__ int64_t block_sum_before(int64_t* sums, int64_t v, int64_t& total) {
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
     int64_t upto = v;
-#pragma unroll
-    for (uint32_t d = 1; d < 64; d <<= 1) {
-        const int64_t o = __shfl_up(upto, d);
-        if (lane >= d) upto += o;
-    }
-    if (lane == 63u) sh.wave_sum[wave] = upto;
+    upto += dpp_or_zero<0x111, 0xF>(upto);  // row_shr:1, 2, 4, 8
+    upto += dpp_or_zero<0x112, 0xF>(upto);
+    upto += dpp_or_zero<0x114, 0xF>(upto);
+    upto += dpp_or_zero<0x118, 0xF>(upto);
+    upto += dpp_or_zero<0x142, 0xA>(upto);  // row_bcast:15, 31
+    upto += dpp_or_zero<0x143, 0xC>(upto);
+    if (lane == 63u) sums[wave] = upto;
     __syncthreads();
     int64_t before = upto - v;
     total = 0;
 #pragma unroll
     for (uint32_t w = 0; w < (uint32_t)kWaves; ++w) {
-        if (w < wave) before += sh.wave_sum[w];
-        total += sh.wave_sum[w];
+        if (w < wave) before += sums[w];
+        total += sums[w];
     }
-    __syncthreads();
     return before;
 }
 
@@ -65,8 +77,11 @@ __device__ __forceinline__ uint32_t first_above(const uint32_t* v, uint32_t n, u
     return lo;
 }
 
+// kPer: consecutive lanes of a thread.
+template <uint32_t kPer>
 __global__ __launch_bounds__(kBlock) void plan_kernel(topk_plan_args a) {
-    __shared__ PlanShared sh;
+    constexpr uint32_t kPlanLanes = kBlock * kPer;  // lanes per step
+    __shared__ PlanShared<kPlanLanes> sh;
     const uint32_t tid = threadIdx.x;
     const bool first_wg = blockIdx.x == 0;
     const uint32_t bs = (uint32_t)a.block_size, capacity = (uint32_t)a.capacity;
@@ -82,26 +97,26 @@ __global__ __launch_bounds__(kBlock) void plan_kernel(topk_plan_args a) {
         uint32_t add[kPer], need[kPer], len[kPer], held[kPer], total[kPer];
         bool want[kPer];
         int64_t blocks = 0;
+        int32_t ln[kPer], ad[kPer], hl[kPer];
+#pragma unroll
+        for (uint32_t q = 0; q < kPer; ++q) {  // (at the last lane past the end: no branch between the reads)
+            const uint32_t l = l0 + min_u32(tid * kPer + q, n - 1u);
+            ln[q] = a.lens[l];
+            ad[q] = a.add[l];
+            hl[q] = a.held[l];
+        }
 #pragma unroll
         for (uint32_t q = 0; q < kPer; ++q) {
-            const uint32_t i = tid * kPer + q, l = l0 + i;
-            add[q] = need[q] = len[q] = held[q] = total[q] = 0;
-            want[q] = false;
-            if (i < n) {
-                const int32_t ln = a.lens[l], ad = a.add[l], h = a.held[l];
-                len[q] = ln < 0 ? 0u : (uint32_t)ln;
-                add[q] = ad < 0 ? 0u : (uint32_t)ad;
-                held[q] = h < 0 ? 0u : min_u32((uint32_t)h, (uint32_t)a.table_ld);
-                if (add[q] != 0) {
-                    total[q] = (len[q] + add[q] - 1u) / bs + 1u;
-                    want[q] = total[q] <= (uint32_t)a.table_ld && len[q] + add[q] <= 0x7FFFFFFFu;
-                    if (want[q] && total[q] > held[q]) need[q] = total[q] - held[q];
-                }
-            }
+            len[q] = ln[q] < 0 ? 0u : (uint32_t)ln[q];
+            add[q] = ad[q] < 0 || tid * kPer + q >= n ? 0u : (uint32_t)ad[q];
+            held[q] = hl[q] < 0 ? 0u : min_u32((uint32_t)hl[q], (uint32_t)a.table_ld);
+            total[q] = add[q] ? (len[q] + add[q] - 1u) / bs + 1u : 0u;
+            want[q] = add[q] != 0 && total[q] <= (uint32_t)a.table_ld && len[q] + add[q] <= 0x7FFFFFFFu;
+            need[q] = want[q] && total[q] > held[q] ? total[q] - held[q] : 0u;
             blocks += need[q];
         }
         int64_t step_total;
-        int64_t upto = blocks_before + block_sum_before(sh, blocks, step_total);
+        int64_t upto = blocks_before + block_sum_before(sh.wave_sum[0], blocks, step_total);
         blocks_before += step_total;
         int64_t taken[kPer], columns = 0;
         bool ok[kPer];
@@ -112,7 +127,7 @@ __global__ __launch_bounds__(kBlock) void plan_kernel(topk_plan_args a) {
             ok[q] = want[q] && (need[q] == 0 || upto <= (int64_t)free_n);
             columns += ok[q] ? add[q] : 0u;
         }
-        upto = columns_before + block_sum_before(sh, columns, step_total);
+        upto = columns_before + block_sum_before(sh.wave_sum[1], columns, step_total);
         columns_before += step_total;
         uint32_t top = 0, top_taken = 0, refused = 0;
         int64_t end[kPer];
@@ -125,44 +140,62 @@ __global__ __launch_bounds__(kBlock) void plan_kernel(topk_plan_args a) {
             if (ok[q] && need[q]) top_taken = max_u32(top_taken, (uint32_t)taken[q]);
             refused += add[q] != 0 && !ok[q] ? 1u : 0u;
         }
-        if (top) atomicMax(&sh.served, top);
-        if (top_taken) atomicMax(&sh.taken_to, top_taken);
         if (refused) atomicAdd(&sh.refused, refused);
-        __syncthreads();
         const uint32_t served_from = served, taken_from = taken_to;
-        served = sh.served;
-        taken_to = sh.taken_to;
+        if (columns_before <= (int64_t)capacity && blocks_before <= (int64_t)free_n) {
+            // everyone who wants columns is served (all threads agree)
+            served = (uint32_t)columns_before;
+            taken_to = (uint32_t)blocks_before;
+        } else {
+            if (top) atomicMax(&sh.served, top);
+            if (top_taken) atomicMax(&sh.taken_to, top_taken);
+            __syncthreads();
+            served = max_u32(served, sh.served);
+            taken_to = max_u32(taken_to, sh.taken_to);
+        }
 #pragma unroll
         for (uint32_t q = 0; q < kPer; ++q) {
             const uint32_t i = tid * kPer + q;
             const uint32_t e = end[q] <= (int64_t)capacity ? (uint32_t)end[q] : served;
             sh.end[i] = e;
             sh.taken[i] = taken[q] < (int64_t)taken_to ? (uint32_t)taken[q] : taken_to;
-            sh.need[i] = need[q];
-            sh.len[i] = len[q];
-            sh.held[i] = held[q];
+            // (of a lane that is not served, no column or block looks at these)
+            sh.lane[i] = PlanLane{len[q] - (e - add[q]), held[q], free_n - 1u - ((uint32_t)taken[q] - need[q]) + held[q], 0u};
             if (first_wg && i < n) {
                 a.out_col_start[l0 + i + 1] = (int32_t)e;
                 a.out_held[l0 + i] = (int32_t)(ok[q] ? max_u32(total[q], held[q]) : held[q]);
             }
         }
         __syncthreads();
-        // this workgroup's columns of these lanes
+        // this workgroup's columns of these lanes, all of a thread's at once
         const uint32_t ka = k0 > served_from ? k0 : served_from, kb = min_u32(k1, served);
-        for (uint32_t t = ka + tid; t < kb; t += kBlock) {
-            const uint32_t i = first_above(sh.end, n, t), l = l0 + i;
-            const uint32_t pos = sh.len[i] + (t - (i ? sh.end[i - 1] : served_from));
-            const uint32_t bi = pos / bs, h = sh.held[i];
-            const int32_t id = bi < h ? a.table[(int64_t)l * a.table_ld + bi]
-                                      : a.free_ids[free_n - 1u - (sh.taken[i] - sh.need[i] + (bi - h))];
-            a.out_col_lane[t] = (int32_t)l;
-            a.out_col_pos[t] = (int32_t)pos;
-            a.out_slots[t] = (int64_t)id * bs + (pos - bi * bs);
+        if (ka < kb) {
+            constexpr uint32_t U = kPlanColumns / kBlock;
+            uint32_t l[U], pos[U], bi[U];
+            int32_t id[U];
+#pragma unroll
+            for (uint32_t u = 0; u < U; ++u) {
+                const uint32_t t = min_u32(ka + u * kBlock + tid, kb - 1u);
+                const uint32_t i = first_above(sh.end, n, t);
+                const PlanLane p = sh.lane[i];
+                l[u] = l0 + i;
+                pos[u] = p.base + t;
+                bi[u] = pos[u] / bs;
+                id[u] = *(bi[u] < p.held ? a.table + (int64_t)l[u] * a.table_ld + bi[u] : a.free_ids + (p.free_base - bi[u]));
+            }
+#pragma unroll
+            for (uint32_t u = 0; u < U; ++u) {
+                const uint32_t t = ka + u * kBlock + tid;
+                if (t >= kb) break;
+                a.out_col_lane[t] = (int32_t)l[u];
+                a.out_col_pos[t] = (int32_t)pos[u];
+                a.out_slots[t] = (int64_t)id[u] * bs + (pos[u] - bi[u] * bs);
+            }
         }
         // and its share of the new table entries
         for (uint32_t b = taken_from + blockIdx.x * kBlock + tid; b < taken_to; b += gridDim.x * kBlock) {
             const uint32_t i = first_above(sh.taken, n, b);
-            const uint32_t at = sh.held[i] + (b - (sh.taken[i] - sh.need[i]));
+            const uint32_t at = b + sh.lane[i].free_base - (free_n - 1u);
             a.table[(int64_t)(l0 + i) * a.table_ld + at] = a.free_ids[free_n - 1u - b];
         }
         __syncthreads();
@@ -183,7 +216,8 @@ __global__ __launch_bounds__(kBlock) void plan_kernel(topk_plan_args a) {
 
 hipError_t launch_plan_round(const topk_plan_args& a, hipStream_t stream) {
     const uint32_t blocks = (uint32_t)((a.capacity + kPlanColumns - 1) / kPlanColumns);
-    hipLaunchKernelGGL(plan_kernel, dim3(blocks), dim3(kBlock), 0, stream, a);
+    if (a.lanes <= kBlock) hipLaunchKernelGGL(plan_kernel<1>, dim3(blocks), dim3(kBlock), 0, stream, a);
+    else hipLaunchKernelGGL(plan_kernel<4>, dim3(blocks), dim3(kBlock), 0, stream, a);
     return hipGetLastError();
 }
 
