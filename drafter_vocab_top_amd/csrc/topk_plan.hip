@@ -4,8 +4,8 @@
 // Everything is whole numbers: over the lanes, in order, the running sum of
 // the blocks needed decides who is served, and the running sum of the served
 // lanes' columns where theirs begin.  One launch: every workgroup runs both
-// sums over all lanes (they are few, and stay in the caches), 256 or 1,024
-// lanes at a time, and then writes its own range of columns, finding each column's
+// sums over all lanes (they are few, and stay in the caches), 256 to
+// 1,024 lanes at a time, and then writes its own range of columns, finding each column's
 // lane by bisection in LDS.  Workgroup 0 writes what there is per lane; new
 // table entries are spread over all workgroups.
 //
@@ -18,7 +18,8 @@ namespace topk {
 
 namespace {
 
-constexpr uint32_t kPlanColumns = 1024;           // columns per workgroup
+
+constexpr int64_t kFewColumns = 262144;
 
 struct alignas(16) PlanLane {
     uint32_t base;       // position - column, of the lane's columns
@@ -34,6 +35,19 @@ struct PlanShared {
     uint32_t taken[kLanes];  // blocks of the served lanes up to and including this one
     int64_t wave_sum[2][kWaves];
     uint32_t served, taken_to, refused;
+};
+
+// x / block size, for x < 2^31: with s the least exponent for which 2^s is no
+// less than the size, m = ceil(2^(31+s) / size) exceeds the quotient by less
+// than 1, so x * m / 2^(31+s) exceeds x / size by less than
+// x / (2^(31+s)) <= 1 / size.
+struct BlockOf {
+    uint32_t mul, shift;
+    explicit BlockOf(uint32_t size) : shift(31) {
+        while ((1ull << (shift - 31)) < size) ++shift;
+        mul = (uint32_t)(((1ull << shift) + size - 1u) / size);
+    }
+    __device__ __forceinline__ uint32_t operator()(uint32_t x) const { return (uint32_t)((uint64_t)x * mul >> shift); }
 };
 
 template <int kCtrl, int kRowMask>
@@ -66,9 +80,8 @@ __device__ __forceinline__ int64_t block_sum_before(int64_t* sums, int64_t v, in
     return before;
 }
 
-// The first of n ascending values that is above x (one is).
-__device__ __forceinline__ uint32_t first_above(const uint32_t* v, uint32_t n, uint32_t x) {
-    uint32_t lo = 0, hi = n - 1u;
+// The first of the ascending values v[lo .. hi] that is above x (v[hi] is).
+__device__ __forceinline__ uint32_t first_above(const uint32_t* v, uint32_t lo, uint32_t hi, uint32_t x) {
     while (lo < hi) {
         const uint32_t mid = (lo + hi) / 2u;
         if (v[mid] > x) hi = mid;
@@ -77,10 +90,11 @@ __device__ __forceinline__ uint32_t first_above(const uint32_t* v, uint32_t n, u
     return lo;
 }
 
-// kPer: consecutive lanes of a thread.
-template <uint32_t kPer>
-__global__ __launch_bounds__(kBlock) void plan_kernel(topk_plan_args a) {
+// kPer: consecutive lanes of a thread; U: columns of a thread.
+template <uint32_t kPer, uint32_t U>
+__global__ __launch_bounds__(kBlock) void plan_kernel(topk_plan_args a, BlockOf block_of) {
     constexpr uint32_t kPlanLanes = kBlock * kPer;  // lanes per step
+    constexpr uint32_t kPlanColumns = kBlock * U;   // columns of a workgroup
     __shared__ PlanShared<kPlanLanes> sh;
     const uint32_t tid = threadIdx.x;
     const bool first_wg = blockIdx.x == 0;
@@ -110,8 +124,9 @@ __global__ __launch_bounds__(kBlock) void plan_kernel(topk_plan_args a) {
             len[q] = ln[q] < 0 ? 0u : (uint32_t)ln[q];
             add[q] = ad[q] < 0 || tid * kPer + q >= n ? 0u : (uint32_t)ad[q];
             held[q] = hl[q] < 0 ? 0u : min_u32((uint32_t)hl[q], (uint32_t)a.table_ld);
-            total[q] = add[q] ? (len[q] + add[q] - 1u) / bs + 1u : 0u;
-            want[q] = add[q] != 0 && total[q] <= (uint32_t)a.table_ld && len[q] + add[q] <= 0x7FFFFFFFu;
+            const bool some = add[q] != 0 && len[q] + add[q] <= 0x7FFFFFFFu;
+            total[q] = some ? block_of(len[q] + add[q] - 1u) + 1u : 0u;
+            want[q] = some && total[q] <= (uint32_t)a.table_ld;
             need[q] = want[q] && total[q] > held[q] ? total[q] - held[q] : 0u;
             blocks += need[q];
         }
@@ -138,17 +153,21 @@ __global__ __launch_bounds__(kBlock) void plan_kernel(topk_plan_args a) {
             ok[q] = ok[q] && upto <= (int64_t)capacity;
             if (upto <= (int64_t)capacity) top = max_u32(top, (uint32_t)upto);
             if (ok[q] && need[q]) top_taken = max_u32(top_taken, (uint32_t)taken[q]);
-            refused += add[q] != 0 && !ok[q] ? 1u : 0u;
+            refused += (uint32_t)__popcll(__ballot(add[q] != 0 && !ok[q]));
         }
-        if (refused) atomicAdd(&sh.refused, refused);
+        if (refused && (tid & 63u) == 0) atomicAdd(&sh.refused, refused);
         const uint32_t served_from = served, taken_from = taken_to;
         if (columns_before <= (int64_t)capacity && blocks_before <= (int64_t)free_n) {
             // everyone who wants columns is served (all threads agree)
             served = (uint32_t)columns_before;
             taken_to = (uint32_t)blocks_before;
         } else {
-            if (top) atomicMax(&sh.served, top);
-            if (top_taken) atomicMax(&sh.taken_to, top_taken);
+            top = wave_max_u32(top);
+            top_taken = wave_max_u32(top_taken);
+            if ((tid & 63u) == 0) {
+                atomicMax(&sh.served, top);
+                atomicMax(&sh.taken_to, top_taken);
+            }
             __syncthreads();
             served = max_u32(served, sh.served);
             taken_to = max_u32(taken_to, sh.taken_to);
@@ -170,17 +189,19 @@ __global__ __launch_bounds__(kBlock) void plan_kernel(topk_plan_args a) {
         // this workgroup's columns of these lanes, all of a thread's at once
         const uint32_t ka = k0 > served_from ? k0 : served_from, kb = min_u32(k1, served);
         if (ka < kb) {
-            constexpr uint32_t U = kPlanColumns / kBlock;
+            // the lanes of the first and last column (known where they are the step's)
+            const uint32_t lo = ka == served_from ? 0u : first_above(sh.end, 0, n - 1u, ka);
+            const uint32_t hi = kb == served ? n - 1u : first_above(sh.end, lo, n - 1u, kb - 1u);
             uint32_t l[U], pos[U], bi[U];
             int32_t id[U];
 #pragma unroll
             for (uint32_t u = 0; u < U; ++u) {
                 const uint32_t t = min_u32(ka + u * kBlock + tid, kb - 1u);
-                const uint32_t i = first_above(sh.end, n, t);
+                const uint32_t i = first_above(sh.end, lo, hi, t);
                 const PlanLane p = sh.lane[i];
                 l[u] = l0 + i;
                 pos[u] = p.base + t;
-                bi[u] = pos[u] / bs;
+                bi[u] = block_of(pos[u]);
                 id[u] = *(bi[u] < p.held ? a.table + (int64_t)l[u] * a.table_ld + bi[u] : a.free_ids + (p.free_base - bi[u]));
             }
 #pragma unroll
@@ -194,7 +215,7 @@ __global__ __launch_bounds__(kBlock) void plan_kernel(topk_plan_args a) {
         }
         // and its share of the new table entries
         for (uint32_t b = taken_from + blockIdx.x * kBlock + tid; b < taken_to; b += gridDim.x * kBlock) {
-            const uint32_t i = first_above(sh.taken, n, b);
+            const uint32_t i = first_above(sh.taken, 0, n - 1u, b);
             const uint32_t at = b + sh.lane[i].free_base - (free_n - 1u);
             a.table[(int64_t)(l0 + i) * a.table_ld + at] = a.free_ids[free_n - 1u - b];
         }
@@ -214,11 +235,28 @@ __global__ __launch_bounds__(kBlock) void plan_kernel(topk_plan_args a) {
 
 }  // namespace
 
-hipError_t launch_plan_round(const topk_plan_args& a, hipStream_t stream) {
-    const uint32_t blocks = (uint32_t)((a.capacity + kPlanColumns - 1) / kPlanColumns);
-    if (a.lanes <= kBlock) hipLaunchKernelGGL(plan_kernel<1>, dim3(blocks), dim3(kBlock), 0, stream, a);
-    else hipLaunchKernelGGL(plan_kernel<4>, dim3(blocks), dim3(kBlock), 0, stream, a);
+namespace {
+
+template <uint32_t U>
+hipError_t launch_columns(const topk_plan_args& a, hipStream_t stream) {
+    const dim3 grid((uint32_t)((a.capacity + kBlock * U - 1) / (kBlock * U))), block(kBlock);
+    const BlockOf block_of((uint32_t)a.block_size);
+    // one step for up to 1,024 lanes, with no more lanes to a thread than it takes
+    if (a.lanes <= kBlock) hipLaunchKernelGGL((plan_kernel<1, U>), grid, block, 0, stream, a, block_of);
+    else if (a.lanes <= 2 * kBlock) hipLaunchKernelGGL((plan_kernel<2, U>), grid, block, 0, stream, a, block_of);
+    else hipLaunchKernelGGL((plan_kernel<4, U>), grid, block, 0, stream, a, block_of);
     return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_plan_round(const topk_plan_args& a, hipStream_t stream) {
+    // One column per thread is the shortest chain (512 columns: 3.5 us, in
+    // fours 5.0; 262,144: 5.6 and 6.6), until the workgroups that repeat the
+    // sums over the lanes outnumber those that run at once (524,288 columns:
+    // 12.2 us, in fours 8.2).
+    if (a.capacity <= kFewColumns) return launch_columns<1>(a, stream);
+    return launch_columns<4>(a, stream);
 }
 
 }  // namespace topk
