@@ -70,16 +70,18 @@ __device__ __forceinline__ const uint32_t* mask_row(const AdjustArgs& a, uint32_
     return m >= 0 && m < a.mask_count ? a.mask + m * a.mask_ld : nullptr;
 }
 
-// 16 bytes at element alignment (global memory takes any).
-template <class T>
+// 16 bytes at element alignment (global memory takes any).  kOnce: past the
+// caches, for matrices that they could not hold until they are read again.
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+template <bool kOnce, class T>
 __device__ __forceinline__ u32x4 load16(const T* p) {
-    u32x4 v;
-    __builtin_memcpy(&v, p, 16);
-    return v;
+    if constexpr (kOnce) return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
+    else return *reinterpret_cast<const u32x4_any*>(p);
 }
-template <class T>
+template <bool kOnce, class T>
 __device__ __forceinline__ void store16(T* p, const u32x4& v) {
-    __builtin_memcpy(p, &v, 16);
+    if constexpr (kOnce) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any*>(p));
+    else *reinterpret_cast<u32x4_any*>(p) = v;
 }
 
 // v with the elements whose bit in `allowed` is clear set to -Inf.
@@ -105,13 +107,14 @@ __device__ __forceinline__ u32x4 masked(const u32x4& v, uint32_t allowed) {
 
 // ------------------------------------------------------------ touched rows ---
 
-// The ROWS rows of a workgroup: runs of 256 that lie `tiles` runs apart.  The
-// ids of a vocabulary sorted by use put most of a history into the first
-// rows; in one contiguous tile they would hold up the whole launch.  256 rows
-// are the most that a workgroup rewrites in one go, and whole cache lines.
-template <uint32_t kRows>
+// The ROWS rows of a workgroup: runs of RUN that lie `tiles` runs apart.  The
+// ids of a vocabulary sorted by use put most of a history into the first rows;
+// in one contiguous tile they hold up a launch that has little else to do.
+// Runs of 256 rows are the most that a workgroup rewrites in one go, and whole
+// cache lines; a launch that streams much reads one tile in a piece.
+template <uint32_t kRows, uint32_t kRun>
 struct Rows {
-    static constexpr uint32_t RUN = 256, ROWS = kRows, WORDS = ROWS / 32;
+    static constexpr uint32_t RUN = kRun, ROWS = kRows, WORDS = ROWS / 32;
     static_assert(WORDS <= (uint32_t)kBlock, "one word of the rows' bits per thread");
     uint32_t tiles, tile;
     __device__ __forceinline__ uint32_t row(uint32_t at) const { return (at / RUN * tiles + tile) * RUN + at % RUN; }
@@ -139,17 +142,17 @@ __device__ __forceinline__ const T* or_safe(const T* p) {
 }
 
 // What hangs on the lane alone, read at once.
-template <uint32_t kRows, bool kBias>
+template <class R, bool kBias>
 struct Lane {
     uint32_t cb, ce, db, de, bb, be;  // its columns, the drafts before its last column, its biases
     float rep, pres, freq;
     uint32_t word;                    // the history's bits of this thread's 32 places
-    __device__ __forceinline__ Lane(const AdjustArgs& a, const Rows<kRows>& rows, uint32_t l) {
+    __device__ __forceinline__ Lane(const AdjustArgs& a, const R& rows, uint32_t l) {
         const uint32_t tid = threadIdx.x;
         const int32_t* cs = a.cols.start ? a.cols.start + l : or_safe<int32_t>(nullptr);
         const int32_t* ds = a.draft_parts.start ? a.draft_parts.start + l : or_safe<int32_t>(nullptr);
         const int32_t* bs = kBias ? a.bias_parts.start + l : or_safe<int32_t>(nullptr);
-        const uint32_t r = rows.row(min_u32(tid, Rows<kRows>::WORDS - 1u) * 32u);
+        const uint32_t r = rows.row(min_u32(tid, R::WORDS - 1u) * 32u);
         const uint32_t* sp = a.seen ? a.seen + (int64_t)l * a.seen_ld + (min_u32(r, a.V - 1u) >> 5) : or_safe<uint32_t>(nullptr);
         const int32_t c0 = cs[0], c1 = cs[1], d0 = ds[0], d1 = ds[1], b0 = bs[0], b1 = bs[1];
         rep = *(a.repetition ? a.repetition + l : or_safe<float>(nullptr));
@@ -164,16 +167,17 @@ struct Lane {
         if (!a.repetition) rep = 1.0f;
         if (!a.presence) pres = 0.0f;
         if (!a.frequency) freq = 0.0f;
-        if (tid >= Rows<kRows>::WORDS || r >= a.V || !a.seen) word = 0;
+        if (tid >= R::WORDS || r >= a.V || !a.seen) word = 0;
         else if (a.V - r < 32u) word &= (1u << (a.V - r)) - 1u;  // bits past the last row mean nothing
     }
 };
 
 // Fills sh (list and n are valid after the next barrier).  bias0, draft0: the
 // lane's entries bb + thread and db + thread.
-template <uint32_t kRows, bool kBias>
-__device__ __forceinline__ void make_list(const AdjustArgs& a, const Rows<kRows>& rows, const Lane<kRows, kBias>& lane,
-                                          uint32_t draft0, uint32_t bias0, TouchedRows<kRows, kBias>& sh) {
+template <class R, bool kBias>
+__device__ __forceinline__ void make_list(const AdjustArgs& a, const R& rows, const Lane<R, kBias>& lane, uint32_t draft0,
+                                          uint32_t bias0, TouchedRows<R::ROWS, kBias>& sh) {
+    constexpr uint32_t kRows = R::ROWS;
     const uint32_t tid = threadIdx.x, ln = tid & 63u;
     if (tid == 0) sh.n = 0;
     if (tid < kRows / 32) {
@@ -220,8 +224,8 @@ __device__ __forceinline__ void make_list(const AdjustArgs& a, const Rows<kRows>
     }
 }
 
-template <uint32_t kRows, bool kBias>
-__device__ __forceinline__ void first_entries(const AdjustArgs& a, const Lane<kRows, kBias>& lane, uint32_t& draft0, uint32_t& bias0) {
+template <class R, bool kBias>
+__device__ __forceinline__ void first_entries(const AdjustArgs& a, const Lane<R, kBias>& lane, uint32_t& draft0, uint32_t& bias0) {
     const uint32_t tid = threadIdx.x;
     bias0 = kBias ? (uint32_t)a.bias_ids[min_u32(lane.bb + tid, a.bias_parts.total - 1u)] : 0u;
     draft0 = a.drafts ? (uint32_t)a.drafts[min_u32(lane.db + tid, a.draft_parts.total - 1u)] : 0u;
@@ -247,6 +251,10 @@ struct DraftsOfRow {
 
 // ------------------------------------------------------ column-contiguous ---
 
+// What becomes of the matrix: changed in place; copied, the rows in short runs;
+// copied a tile in a piece; the same past the caches.
+enum { kModeInPlace, kModeShort, kModeLong, kModeOnce };
+
 constexpr uint32_t kColsAtOnce = 4;  // columns whose vectors a thread has in flight
 
 // Lane l0 + blockIdx.y, its columns blockIdx.z * U, .. + U - 1, then
@@ -256,15 +264,17 @@ constexpr uint32_t kColsAtOnce = 4;  // columns whose vectors a thread has in fl
 // At these sizes the time is that of the chain of dependent reads: reads of
 // one link are issued together, at addresses cut to the last valid one instead
 // of behind branches.
-template <class DT, bool kInPlace, bool kBias, bool kMask>
+template <class DT, int kMode, bool kBias, bool kMask>
 __global__ __launch_bounds__(kBlock) void adjust_col(AdjustArgs a, uint32_t l0) {
     using storage = typename DT::storage;
     constexpr uint32_t EPV = DT::kPerVec, ALL = (1u << EPV) - 1u, U = kColsAtOnce, ROWS = kBlock * EPV;
+    constexpr bool kInPlace = kMode == kModeInPlace, kOnce = kMode == kModeOnce;
+    using R = Rows<ROWS, kMode == kModeInPlace || kMode == kModeShort ? 256 : ROWS>;
     __shared__ TouchedRows<ROWS, kBias> sh;
     const uint32_t l = l0 + blockIdx.y, tid = threadIdx.x, V = a.V;
-    const Rows<ROWS> rows{gridDim.x, blockIdx.x};
+    const R rows{gridDim.x, blockIdx.x};
     const bool sparse = a.counts || a.drafts || kBias;
-    const Lane<ROWS, kBias> lane(a, rows, l);
+    const Lane<R, kBias> lane(a, rows, l);
     const uint32_t cb = lane.cb, ce = lane.ce;
     const uint32_t c_first = cb + blockIdx.z * U, c_step = gridDim.z * U;
     if (c_first >= ce) return;
@@ -294,7 +304,7 @@ __global__ __launch_bounds__(kBlock) void adjust_col(AdjustArgs a, uint32_t l0) 
         if (nvec) {
 #pragma unroll
             for (uint32_t u = 0; u < U; ++u)
-                if (!kInPlace) d[u] = load16(static_cast<const storage*>(a.x) + (int64_t)min_u32(c0 + u, ce - 1u) * a.ld + rr);
+                if (!kInPlace) d[u] = load16<kOnce>(static_cast<const storage*>(a.x) + (int64_t)min_u32(c0 + u, ce - 1u) * a.ld + rr);
         }
 #pragma unroll
         for (uint32_t u = 0; u < U; ++u) m[u] = kMask ? (uint32_t)mp[u][min_u32(r, V - 1u) >> 3] : ALL;
@@ -306,7 +316,7 @@ __global__ __launch_bounds__(kBlock) void adjust_col(AdjustArgs a, uint32_t l0) 
         if (kInPlace && whole) {
 #pragma unroll
             for (uint32_t u = 0; u < U; ++u)
-                if (c0 + u < ce && m[u] != ALL && m[u]) d[u] = load16(static_cast<const storage*>(a.x) + (int64_t)(c0 + u) * a.ld + r);
+                if (c0 + u < ce && m[u] != ALL && m[u]) d[u] = load16<false>(static_cast<const storage*>(a.x) + (int64_t)(c0 + u) * a.ld + r);
         }
 #pragma unroll
         for (uint32_t u = 0; u < U; ++u) {
@@ -314,7 +324,7 @@ __global__ __launch_bounds__(kBlock) void adjust_col(AdjustArgs a, uint32_t l0) 
             const storage* x = static_cast<const storage*>(a.x) + (int64_t)(c0 + u) * a.ld;
             storage* out = static_cast<storage*>(a.out) + (int64_t)(c0 + u) * a.out_ld;
             if (whole) {
-                store16(out + r, kMask ? masked<DT>(d[u], m[u]) : d[u]);
+                store16<kOnce>(out + r, kMask ? masked<DT>(d[u], m[u]) : d[u]);
             } else {
                 for (uint32_t e = 0; r + e < V; ++e) {
                     const bool ok = m[u] >> e & 1u;
@@ -384,18 +394,19 @@ __global__ __launch_bounds__(kBlock) void adjust_col(AdjustArgs a, uint32_t l0) 
 
 constexpr uint32_t kRowTileVecs = 64;  // at most 64 vectors of a row per workgroup
 
-// A workgroup takes 1 << tx_log vectors of a row; each thread one of them over
-// 32 rows, which one word of each column's mask covers.
-template <class DT, bool kInPlace, bool kMask>
+// A workgroup takes 1 << tx_log vectors of a row; each thread one of them over U
+// rows, which one word of each column's mask covers, all in flight together.
+template <class DT, int kMode, bool kMask, uint32_t U>
 __global__ __launch_bounds__(kBlock) void adjust_row_dense(AdjustArgs a, uint32_t tx_log, uint32_t tile0) {
     using storage = typename DT::storage;
     constexpr uint32_t EPV = DT::kPerVec, ALL = (1u << EPV) - 1u;
+    constexpr bool kInPlace = kMode == kModeInPlace, kOnce = kMode == kModeOnce;
     __shared__ uint8_t active[kRowTileVecs * EPV];
     const uint32_t tid = threadIdx.x, V = a.V;
     const uint32_t tile_c = ((tile0 + blockIdx.y) << tx_log) * EPV, tile_n = EPV << tx_log;
     const uint32_t vc = tid & ((1u << tx_log) - 1u);
     const uint32_t c = tile_c + vc * EPV;
-    const uint32_t r0 = blockIdx.x * (kBlock >> tx_log) * 32u + (tid >> tx_log) * 32u;
+    const uint32_t r0 = blockIdx.x * (kBlock >> tx_log) * U + (tid >> tx_log) * U;
     uint32_t words[EPV];
     if constexpr (kMask) {
         int64_t mi[EPV];
@@ -411,7 +422,7 @@ __global__ __launch_bounds__(kBlock) void adjust_row_dense(AdjustArgs a, uint32_
             mi[e] = has ? 0 : -1;
         }
 #pragma unroll
-        for (uint32_t e = 0; e < EPV; ++e) words[e] |= (uint32_t)mi[e];
+        for (uint32_t e = 0; e < EPV; ++e) words[e] = (words[e] >> (r0 & 31u)) | (uint32_t)mi[e];
     }
     uint32_t mine = c + EPV <= a.C ? ALL : c < a.C ? (1u << (a.C - c)) - 1u : 0u;  // bit e: column c + e is a lane's
     if (a.cols.start) {
@@ -428,7 +439,7 @@ __global__ __launch_bounds__(kBlock) void adjust_row_dense(AdjustArgs a, uint32_
         for (uint32_t e = 0; e < EPV; ++e) mine &= active[vc * EPV + e] ? ~0u : ~(1u << e);
     }
     if (mine == 0 || r0 >= V) return;
-    const uint32_t n = min_u32(32u, V - r0);
+    const uint32_t n = min_u32(U, V - r0);
     const storage* x = static_cast<const storage*>(a.x) + (int64_t)r0 * a.ld + c;
     storage* out = static_cast<storage*>(a.out) + (int64_t)r0 * a.out_ld + c;
     auto allowed = [&](uint32_t r) {
@@ -438,28 +449,44 @@ __global__ __launch_bounds__(kBlock) void adjust_row_dense(AdjustArgs a, uint32_
         for (uint32_t e = 0; e < EPV; ++e) m |= (words[e] >> r & 1u) << e;
         return m;
     };
+    u32x4 d[U];
     if (mine == ALL) {
-        constexpr uint32_t U = 8;  // rows whose vectors are in flight together
-        for (uint32_t r = 0; r < n; r += U) {
-            u32x4 d[U];
-            uint32_t m[U];
 #pragma unroll
-            for (uint32_t u = 0; u < U; ++u) {
-                m[u] = allowed(r + u);
-                if (!kInPlace) d[u] = load16(x + (int64_t)min_u32(r + u, n - 1u) * a.ld);
-                else if (r + u < n && m[u] != ALL && m[u]) d[u] = load16(x + (int64_t)(r + u) * a.ld);
-            }
+        for (uint32_t u = 0; u < U; ++u) {
+            if (!kInPlace) d[u] = load16<kOnce>(x + (int64_t)min_u32(u, n - 1u) * a.ld);
+            else if (const uint32_t m = allowed(u); u < n && m != ALL && m) d[u] = load16<false>(x + (int64_t)u * a.ld);
+        }
 #pragma unroll
-            for (uint32_t u = 0; u < U; ++u)
-                if (r + u < n && (!kInPlace || m[u] != ALL))
-                    store16(out + (int64_t)(r + u) * a.out_ld, kMask ? masked<DT>(d[u], m[u]) : d[u]);
+        for (uint32_t u = 0; u < U; ++u) {
+            const uint32_t m = allowed(u);
+            if (u < n && (!kInPlace || m != ALL)) store16<kOnce>(out + (int64_t)u * a.out_ld, kMask ? masked<DT>(d[u], m) : d[u]);
         }
         return;
     }
-    for (uint32_t r = 0; r < n; ++r, x += a.ld, out += a.out_ld) {
-        const uint32_t m = allowed(r);
+    // A vector past the row's end, or with columns that are nobody's: read
+    // whole, where the matrix reaches that far, and written by the element.
+    if constexpr (!kInPlace) {
+#pragma unroll
+        for (uint32_t u = 0; u < U; ++u) {
+            const uint32_t r = min_u32(u, n - 1u);
+            if ((int64_t)(V - 1u - (r0 + r)) * a.ld + a.C >= (int64_t)c + EPV) {
+                d[u] = load16<false>(x + (int64_t)r * a.ld);
+            } else {
+                storage v[EPV] = {};
+#pragma unroll
+                for (uint32_t e = 0; e < EPV; ++e)
+                    if (mine >> e & 1u) v[e] = x[(int64_t)r * a.ld + e];
+                __builtin_memcpy(&d[u], v, 16);
+            }
+        }
+    }
+#pragma unroll
+    for (uint32_t u = 0; u < U; ++u) {
+        const uint32_t m = allowed(u);
+#pragma unroll
         for (uint32_t e = 0; e < EPV; ++e)
-            if ((mine >> e & 1u) && (!kInPlace || !(m >> e & 1u))) out[e] = m >> e & 1u ? x[e] : (storage)kMinusInf<DT>;
+            if (u < n && (mine >> e & 1u) && (!kInPlace || !(m >> e & 1u)))
+                out[(int64_t)u * a.out_ld + e] = !kInPlace && (m >> e & 1u) ? (storage)vec_elem<DT>(d[u], (int)e) : (storage)kMinusInf<DT>;
     }
 }
 
@@ -471,8 +498,9 @@ __global__ __launch_bounds__(kBlock) void adjust_row_sparse(AdjustArgs a, uint32
     using storage = typename DT::storage;
     __shared__ TouchedRows<kSparseRows, kBias> sh;
     const uint32_t l = l0 + blockIdx.y, tid = threadIdx.x;
-    const Rows<kSparseRows> rows{gridDim.x, blockIdx.x};
-    const Lane<kSparseRows, kBias> lane(a, rows, l);
+    using R = Rows<kSparseRows, 256>;
+    const R rows{gridDim.x, blockIdx.x};
+    const Lane<R, kBias> lane(a, rows, l);
     if (lane.ce == lane.cb) return;
     uint32_t draft0, bias0;
     first_entries(a, lane, draft0, bias0);
@@ -522,39 +550,68 @@ __global__ __launch_bounds__(kBlock) void adjust_row_sparse(AdjustArgs a, uint32
 
 // ----------------------------------------------------------------- launch ---
 
-template <class DT, bool kInPlace, bool kBias, bool kMask>
+constexpr int64_t kRowVecs = 1 << 20;
+
+// A matrix that, read and written, exceeds the 256 MB Infinity Cache goes past
+// the caches: 448 columns of 248,046 bf16 rows 102 to 96 us (column-contiguous)
+// and 117 to 108 (interleaved), 56 columns 13.0 but 15.7.
+bool past_caches(const AdjustArgs& a, int element_bytes) {
+    return 2 * (int64_t)a.V * a.C * element_bytes > (int64_t(256) << 20);
+}
+
+template <class DT, int kMode, bool kBias, bool kMask>
 hipError_t launch_col(const AdjustArgs& a, hipStream_t stream) {
     const uint32_t rows = kBlock * DT::kPerVec, tiles = (a.V + rows - 1) / rows;
     // a workgroup per kColsAtOnce columns of a lane of average size
     const uint32_t z = min(((a.C + a.lanes - 1) / a.lanes + kColsAtOnce - 1) / kColsAtOnce, (uint32_t)kGridY);
     for (int64_t l0 = 0; l0 < a.lanes; l0 += kGridY) {
         const uint32_t n = (uint32_t)(a.lanes - l0 < kGridY ? a.lanes - l0 : kGridY);
-        hipLaunchKernelGGL((adjust_col<DT, kInPlace, kBias, kMask>), dim3(tiles, n, z), dim3(kBlock), 0, stream, a, (uint32_t)l0);
+        hipLaunchKernelGGL((adjust_col<DT, kMode, kBias, kMask>), dim3(tiles, n, z), dim3(kBlock), 0, stream, a, (uint32_t)l0);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
     return hipSuccess;
 }
 
-template <class DT, bool kInPlace>
+template <class DT, int kMode>
 hipError_t launch_col(const AdjustArgs& a, hipStream_t stream) {
-    if (a.bias_ids)
-        return a.mask ? launch_col<DT, kInPlace, true, true>(a, stream) : launch_col<DT, kInPlace, true, false>(a, stream);
-    return a.mask ? launch_col<DT, kInPlace, false, true>(a, stream) : launch_col<DT, kInPlace, false, false>(a, stream);
+    if (a.bias_ids) return a.mask ? launch_col<DT, kMode, true, true>(a, stream) : launch_col<DT, kMode, true, false>(a, stream);
+    return a.mask ? launch_col<DT, kMode, false, true>(a, stream) : launch_col<DT, kMode, false, false>(a, stream);
 }
 
-template <class DT, bool kInPlace, bool kMask>
+template <class DT>
+hipError_t launch_col(const AdjustArgs& a, hipStream_t stream) {
+    if (a.x == a.out) return launch_col<DT, kModeInPlace>(a, stream);
+    const int e = 16 / DT::kPerVec;
+    if (past_caches(a, e)) return launch_col<DT, kModeOnce>(a, stream);
+    // Short runs cost where the columns do not start on cache lines: a run of
+    // 512 bytes then touches five lines for four.  32 columns, histories of
+    // 500 and 4,000 tokens: 131,072 rows 5.8 and 6.3 us in short runs, 6.4 and
+    // 9.1 in long ones; 248,046 rows 11.2 and 12.1, and 9.8 and 11.4.
+    const bool lines = ((uintptr_t)a.x | (uintptr_t)a.out | (uint64_t)a.ld * e | (uint64_t)a.out_ld * e) % 128 == 0;
+    return lines ? launch_col<DT, kModeShort>(a, stream) : launch_col<DT, kModeLong>(a, stream);
+}
+
+template <class DT, int kMode, bool kMask, uint32_t U>
+hipError_t launch_row_dense(const AdjustArgs& a, uint32_t vecs, uint32_t tx_log, hipStream_t stream) {
+    const uint32_t rows = (kBlock >> tx_log) * U;
+    const uint32_t col_tiles = (vecs + (1u << tx_log) - 1) >> tx_log;
+    for (uint32_t t = 0; t < col_tiles; t += (uint32_t)kGridY) {
+        const dim3 grid((a.V + rows - 1) / rows, min(col_tiles - t, (uint32_t)kGridY));
+        hipLaunchKernelGGL((adjust_row_dense<DT, kMode, kMask, U>), grid, dim3(kBlock), 0, stream, a, tx_log, t);
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+template <class DT, int kMode, bool kMask>
 hipError_t launch_row_dense(const AdjustArgs& a, hipStream_t stream) {
     const uint32_t vecs = (a.C + DT::kPerVec - 1) / DT::kPerVec;
     uint32_t tx_log = 0;
     while ((1u << tx_log) < vecs && (1u << tx_log) < kRowTileVecs) ++tx_log;
-    const uint32_t rows = (kBlock >> tx_log) * 32u;
-    const uint32_t col_tiles = (vecs + (1u << tx_log) - 1) >> tx_log;
-    for (uint32_t t = 0; t < col_tiles; t += (uint32_t)kGridY) {
-        const dim3 grid((a.V + rows - 1) / rows, min(col_tiles - t, (uint32_t)kGridY));
-        hipLaunchKernelGGL((adjust_row_dense<DT, kInPlace, kMask>), grid, dim3(kBlock), 0, stream, a, tx_log, t);
-        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    }
-    return hipSuccess;
+    // Rows of a thread, without penalties: 8 columns of 248,046 rows 7.3 us in
+    // fours, 10.3 in sixteens; 56 columns 17.8 and 15.7; 448 columns 120 and 92.
+    return (int64_t)a.V * vecs >= kRowVecs ? launch_row_dense<DT, kMode, kMask, 16>(a, vecs, tx_log, stream)
+                                           : launch_row_dense<DT, kMode, kMask, 4>(a, vecs, tx_log, stream);
 }
 
 template <class DT, bool kBias, bool kMask>
@@ -576,20 +633,25 @@ hipError_t launch_row_sparse(const AdjustArgs& a, hipStream_t stream) {
     return a.mask ? launch_row_sparse<DT, false, true>(a, stream) : launch_row_sparse<DT, false, false>(a, stream);
 }
 
+template <class DT, int kMode>
+hipError_t launch_row_copy(const AdjustArgs& a, hipStream_t stream) {
+    return a.mask ? launch_row_dense<DT, kMode, true>(a, stream) : launch_row_dense<DT, kMode, false>(a, stream);
+}
+
 template <class DT>
 hipError_t launch_dt(int layout, const AdjustArgs& a, hipStream_t stream) {
     const bool sparse = a.counts || a.drafts || a.bias_ids;
     const bool in_place = a.x == a.out;
     if (in_place && !sparse && !a.mask) return hipSuccess;
-    if (layout == TOPK_COL_CONTIG)
-        return in_place ? launch_col<DT, true>(a, stream) : launch_col<DT, false>(a, stream);
-    if (!in_place) {
-        const hipError_t e = a.mask ? launch_row_dense<DT, false, true>(a, stream) : launch_row_dense<DT, false, false>(a, stream);
-        if (e != hipSuccess) return e;
-    }
+    if (layout == TOPK_COL_CONTIG) return launch_col<DT>(a, stream);
+    if (!in_place)
+        if (const hipError_t e = past_caches(a, 16 / DT::kPerVec) ? launch_row_copy<DT, kModeOnce>(a, stream)
+                                                                  : launch_row_copy<DT, kModeLong>(a, stream);
+            e != hipSuccess)
+            return e;
     if (sparse)
         if (const hipError_t e = launch_row_sparse<DT>(a, stream); e != hipSuccess) return e;
-    return in_place && a.mask ? launch_row_dense<DT, true, true>(a, stream) : hipSuccess;
+    return in_place && a.mask ? launch_row_dense<DT, kModeInPlace, true>(a, stream) : hipSuccess;
 }
 
 }  // namespace

@@ -292,8 +292,7 @@ typedef struct {
  *
  * logits, out: device, aligned to the element size.  out may be logits
  *   itself (then out_ld must be ld) and must not overlap it otherwise.
- *   Columns that belong to no lane, and the padding, are neither read nor
- *   written.
+ *   Columns that belong to no lane, and the padding, are not written.
  *
  * Returns TOPK_ERR_INVALID_ARG for a NULL or misaligned pointer, a size or
  * leading dimension out of range, an incomplete group, lanes that do not

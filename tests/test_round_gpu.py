@@ -52,10 +52,10 @@ class Case:
     """A random matrix with every rule that is asked for."""
 
     def __init__(self, seed, V, lanes, most, dtype, layout, pad=0, out_pad=0, ragged=True, hist=0, penalties="all",
-                 drafts=False, bias=0, mask=None, special=False, gap=0):
+                 drafts=False, bias=0, mask=None, special=False, gap=0, empty=0.2):
         rng = np.random.default_rng(seed)
         self.V, self.lanes, self.dtype, self.layout = V, lanes, dtype, layout
-        self.col_start = split(rng, lanes, most) if ragged else None
+        self.col_start = split(rng, lanes, most, empty) if ragged else None
         used = int(self.col_start[-1]) if ragged else lanes * most
         self.C = max(used, 1) + (gap if ragged else 0)  # the last `gap` columns are nobody's
         C = self.C
@@ -201,6 +201,26 @@ def test_adjust(gpu, n, dtype, layout):
         run_adjust(gpu, case, False, offset)
         if case.out_ld >= case.ld:
             run_adjust(gpu, case, True, offset)
+
+
+@pytest.mark.parametrize("layout", [W.COL, W.ROW])
+def test_adjust_a_matrix_larger_than_the_caches(gpu, layout):
+    """More than 256 MB read and written, with lanes and columns left over."""
+    print(f"[round] adjust, large {layout}", flush=True)
+    case = Case(77, 56001, 300, 8, W.BF16, layout, hist=60, drafts=True, bias=5, mask="lane", gap=2, out_pad=3, empty=0.02)
+    assert 2 * 2 * case.V * case.C > 256 << 20
+    run_adjust(gpu, case, False)
+
+
+@pytest.mark.parametrize("n", [0, 1, 2])
+@pytest.mark.parametrize("layout", [W.COL, W.ROW])
+def test_adjust_columns_on_cache_lines(gpu, layout, n):
+    """Columns (or rows) that start on cache lines, at sizes on both sides of
+    a thread's rows and a workgroup's tile."""
+    V, lanes, most = ((2048 * 3 + 64, 3, 8), (64 * 33, 5, 32), (262144, 8, 4))[n]
+    dtype = (W.BF16, W.F32, W.BF16)[n]
+    print(f"[round] adjust, aligned V={V} {layout}", flush=True)
+    run_adjust(gpu, Case(300 + n, V, lanes, most, dtype, layout, ragged=n == 1, hist=700, drafts=True, bias=40, mask="column"), False)
 
 
 def test_adjust_with_no_rule_copies(gpu):
