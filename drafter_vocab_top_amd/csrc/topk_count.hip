@@ -48,7 +48,6 @@ __global__ __launch_bounds__(kBlock) void count_add(CountArgs a) {
     atomicOr(a.seen + (int64_t)l * a.seen_ld + (r >> 5), 1u << (r & 31u));
 }
 
-constexpr uint32_t kOwnTokens = 512;  // tokens per lane from which workgroups own rows
 constexpr uint32_t kOwnThreads = 1024;
 constexpr uint32_t kOwnRows = 8192;  // rows of a workgroup, at most (32 KB of LDS)
 
@@ -121,9 +120,11 @@ __global__ __launch_bounds__(kOwnThreads) void count_own(CountArgs a, uint32_t l
 }  // namespace
 
 hipError_t launch_count(const CountArgs& a, hipStream_t stream) {
-    // Atomics cost by the token, owned rows by the lane: 8 tokens a lane 3.2
-    // against 9 us (64 lanes), 26,000 tokens a lane 158 against 12 us (8 lanes).
-    if (!a.fresh && a.parts.total / a.lanes < kOwnTokens) {
+    // Atomics cost by the tokens of a lane that meet in one word, owned rows by
+    // the lane.  Equal (248,046 rows) near 1,024 tokens a lane for 1 lane (4.6
+    // and 5.1 us) and 8 (5.4 and 5.5), near 4,096 for 64 (28.9 and 27.1); 8
+    // tokens of 64 lanes 3.0 and 17.0, 26,000 of 8 lanes 158 and 10.
+    if (!a.fresh && a.parts.total / a.lanes < 1024u + 48u * (uint64_t)a.lanes) {
         if (a.parts.total == 0) return hipSuccess;
         hipLaunchKernelGGL(count_add, dim3((a.parts.total + kBlock - 1) / kBlock), dim3(kBlock), 0, stream, a);
         return hipGetLastError();

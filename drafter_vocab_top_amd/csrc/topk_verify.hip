@@ -9,10 +9,10 @@
 // Accepting with probability min(1, p/q) and drawing from the positive part
 // of p - q otherwise leaves each token distributed as p.
 //
-// One workgroup per lane, one wave per column: a column's test and the token
-// it would give do not depend on the other columns, so the waves compute them
-// at once and only then agree on the first refusal.  List entry i lies in lane
-// i (k <= 64), and a running sum is a scan over the wave.
+// One workgroup per lane, one wave per column: a column's test does not depend
+// on the other columns, so the waves make them at once, agree on the first
+// refusal, and that column's wave draws the token.  List entry i lies in lane i
+// (k <= 64), and a running sum is a scan over the wave.
 //
 // The decisions are integers made by floating point, so every step is IEEE
 // double in a fixed order with no contraction.
@@ -79,7 +79,6 @@ __device__ __forceinline__ double probability_of(int32_t d, int32_t id, double p
 template <class DT, uint32_t kWavesPerLane>
 __global__ __launch_bounds__(kWavesPerLane * 64) void verify_kernel(VerifyArgs args) {
 #pragma clang fp contract(off)
-    __shared__ int32_t token[kWavesPerLane];
     __shared__ uint32_t refused[kWavesPerLane];
     const topk_verify_args& a = args.v;
     const uint32_t l = blockIdx.x, tid = threadIdx.x;
@@ -94,41 +93,48 @@ __global__ __launch_bounds__(kWavesPerLane * 64) void verify_kernel(VerifyArgs a
         const uint32_t m = min_u32(min_u32(de - db, ce - cb - 1u), (uint32_t)a.max_tokens - 1u);
         for (uint32_t j0 = 0;; j0 += kWavesPerLane) {
             const uint32_t j = j0 + wave;
+            const int64_t c = (int64_t)cb + min_u32(j, m), row = (int64_t)db + j;
+            const bool judged = j < m, listed = judged && a.draft_values;
+            int32_t id = 0, d = 0, qid = 0, n, nq = 1;
+            double p = 0.0, q = 0.0;
+            bool accept = false;
             if (j <= m) {  // wave-uniform
-                const int64_t c = (int64_t)cb + j, row = (int64_t)db + j;
-                const bool judged = j < m, listed = judged && a.draft_values;
                 // everything the column reads
-                const int32_t id = a.target_ids[c * a.k + (lane < a.k ? lane : 0)];
+                id = a.target_ids[c * a.k + (lane < a.k ? lane : 0)];
                 double v, v0, qv = 0.0, qv0 = 0.0;
                 load_entry<DT>(a.target_values, c, a.k, v, v0);
-                int32_t d = 0, qid = 0;
                 if (judged) d = a.drafts[row];
                 if (listed) {
                     qid = a.draft_ids[row * a.kq + (lane < a.kq ? lane : 0)];
                     load_entry<DT>(a.draft_values, row, a.kq, qv, qv0);
                 }
-                int32_t n, nq = 1;
-                const double p = probability(v, v0, a.k, a.temperature, a.top_p, n);
-                double q = 0.0, q_d = 1.0;
-                bool accept = false;
+                p = probability(v, v0, a.k, a.temperature, a.top_p, n);
                 if (judged) {
+                    double q_d = 1.0;
                     if (listed) {
                         q = probability(qv, qv0, a.kq, a.temperature, a.top_p, nq);
                         q_d = probability_of(d, qid, q, a.kq);
                     }
                     accept = philox_uniform(a.seed, a.offset, (uint32_t)c, 1u) * q_d < probability_of(d, id, p, a.k);
                 }
-                int32_t next = 0;
-                if (!accept) {  // (the token after an accepted draft is the next column's)
+                if (lane == 0) refused[wave] = accept ? 0u : 1u;
+            }
+            __syncthreads();
+            const uint32_t columns = min_u32(kWavesPerLane, m + 1u - j0);  // of this step
+            uint32_t t = 0;
+            while (t < columns && !refused[t]) ++t;  // column m is never accepted
+            if (tid < t) out[j0 + tid] = a.drafts[(int64_t)db + j0 + tid];
+            if (t < columns) {
+                if (wave == t) {
                     double rest = p;
                     if (judged) {
                         double q_at = lane < a.k && id == d ? 1.0 : 0.0;
                         if (listed) {
                             q_at = 0.0;
                             // from the last, so that the first entry of an id stays
-                            for (int32_t t = nq - 1; t >= 0; --t) {
-                                const double qt = lane_value(q, t);
-                                if (__builtin_amdgcn_readlane(qid, t) == id) q_at = qt;
+                            for (int32_t i = nq - 1; i >= 0; --i) {
+                                const double qi = lane_value(q, i);
+                                if (__builtin_amdgcn_readlane(qid, i) == id) q_at = qi;
                             }
                         }
                         const double diff = p - q_at;
@@ -141,24 +147,13 @@ __global__ __launch_bounds__(kWavesPerLane * 64) void verify_kernel(VerifyArgs a
                     const unsigned long long above = __ballot(rest > 0.0 && sums > target);
                     // (a product rounded up to the total leaves none above it: the last entry that can be drawn)
                     const uint32_t pick = above ? first_lane(above) : some ? 63u - (uint32_t)__builtin_clzll(some) : 0u;
-                    next = __builtin_amdgcn_readlane(id, (int)pick);
+                    const int32_t next = __builtin_amdgcn_readlane(id, (int)pick);
+                    if (lane == 0) out[j0 + t] = next;
                 }
-                if (lane == 0) {
-                    token[wave] = next;
-                    refused[wave] = accept ? 0u : 1u;
-                }
-            }
-            __syncthreads();
-            const uint32_t n = min_u32(kWavesPerLane, m + 1u - j0);  // columns of this step
-            uint32_t t = 0;
-            while (t < n && !refused[t]) ++t;  // column m is never accepted
-            if (tid < t) out[j0 + tid] = a.drafts[(int64_t)db + j0 + tid];
-            if (t < n) {
-                if (tid == 0) out[j0 + t] = token[t];
                 count = j0 + t + 1u;
                 break;
             }
-            __syncthreads();  // the next step writes token and refused again
+            __syncthreads();  // the next step writes refused again
         }
     }
     for (uint32_t i = count + tid; i < (uint32_t)a.max_tokens; i += kWavesPerLane * 64u) out[i] = -1;

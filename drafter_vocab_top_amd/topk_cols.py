@@ -313,7 +313,7 @@ def _need(name: str, t, numel: int, index: int, dtype) -> int:
     `index` (0 for None)."""
     if t is None:
         return 0
-    if t.dtype is not dtype or t.get_device() != index or index < 0 or t.numel() < numel or not t.is_contiguous():
+    if t.dtype is not dtype or t.get_device() != index or t.numel() < numel or not t.is_contiguous() or index < 0:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {numel} elements on GPU {index}")
     return t.data_ptr()
 
@@ -441,14 +441,14 @@ def count_tokens(counts, seen, V: int, ids, start=None, prompt_len=None, fresh=N
     Returns (counts, seen).
     """
     import torch
-    i32, index, lanes = torch.int32, counts.get_device(), counts.shape[0]
-    if counts.dim() != 2 or seen.dim() != 2 or seen.shape[0] != lanes:
+    i32, index, shape, seen_shape = torch.int32, counts.get_device(), counts.shape, seen.shape
+    if len(shape) != 2 or len(seen_shape) != 2 or seen_shape[0] != shape[0]:
         raise ValueError("counts and seen must be matrices with a row per lane")
-    n = ids.numel()
+    lanes, n = shape[0], ids.numel()
     _launch("topk_cols_count", load().topk_cols_count, index, stream, V, lanes,
             _need("ids", ids, 0, index, i32) if n else 0, n, _need("start", start, lanes + 1, index, i32),
             _need("prompt_len", prompt_len, lanes, index, i32), _need("fresh", fresh, lanes, index, i32),
-            _need("counts", counts, 1, index, i32), counts.shape[1], _need("seen", seen, 1, index, i32), seen.shape[1])
+            _need("counts", counts, 1, index, i32), shape[1], _need("seen", seen, 1, index, i32), seen_shape[1])
     return counts, seen
 
 
@@ -481,28 +481,27 @@ def verify(target_values, target_ids, col_start, drafts, draft_start, draft_valu
         out_tokens = torch.empty((lanes, max_tokens or n + 1), dtype=i32, device=target_values.device)
     if out_count is None:
         out_count = torch.empty(lanes, dtype=i32, device=target_values.device)
-    if target_values.dim() != 2 or target_ids.shape != target_values.shape or out_tokens.dim() != 2 \
-            or out_tokens.shape[0] < lanes:
+    shape, out_shape, size = target_values.shape, out_tokens.shape, target_values.element_size()
+    if len(shape) != 2 or target_ids.shape != shape or len(out_shape) != 2 or out_shape[0] < lanes:
         raise ValueError("target_values and target_ids must be (C, k), out_tokens a matrix with a row per lane")
-    C, k = target_values.shape
-    size = target_values.element_size()
     if index < 0 or size not in (2, 4) or not target_values.is_contiguous():
         raise ValueError("target_values must be a contiguous GPU tensor of bf16 or fp32 (or patterns)")
+    C, k = shape
     kq = qv = qi = 0
     if draft_values is not None:
-        if draft_values.dim() != 2 or draft_ids is None or draft_ids.shape != draft_values.shape \
-                or draft_values.element_size() != size or draft_values.get_device() != index \
-                or not draft_values.is_contiguous():
+        shape = draft_values.shape
+        if len(shape) != 2 or draft_ids is None or draft_ids.shape != shape or draft_values.element_size() != size \
+                or draft_values.get_device() != index or not draft_values.is_contiguous():
             raise ValueError("draft_values and draft_ids must be contiguous (n, kq) tensors of the target lists' types")
         # drafts past the lists have no distribution to be judged by
-        n = min(n, draft_values.shape[0])
+        n = min(n, shape[0])
         if n:
-            kq, qv, qi = draft_values.shape[1], draft_values.data_ptr(), _need("draft_ids", draft_ids, 0, index, i32)
+            kq, qv, qi = shape[1], draft_values.data_ptr(), _need("draft_ids", draft_ids, 0, index, i32)
     args = _pack_verify(
         lanes, 0 if size == 2 else 1, k, kq, C, _need("col_start", col_start, lanes + 1, index, i32),
         target_values.data_ptr(), _need("target_ids", target_ids, 1, index, i32), n,
         _need("draft_start", draft_start, lanes + 1, index, i32), _need("drafts", drafts, 0, index, i32) if n else 0, qv,
-        qi, temperature, top_p, seed, offset, out_tokens.shape[1], _need("out_tokens", out_tokens, 1, index, i32),
+        qi, temperature, top_p, seed, offset, out_shape[1], _need("out_tokens", out_tokens, 1, index, i32),
         _need("out_count", out_count, lanes, index, i32))
     _launch("topk_cols_verify", load().topk_cols_verify, index, stream, args)
     return out_tokens, out_count
