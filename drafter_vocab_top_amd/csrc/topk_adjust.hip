@@ -56,10 +56,11 @@ constexpr uint32_t kMinusInf = DT::kPerVec == 8 ? 0xFF80u : 0xFF800000u;
 struct LaneRules {
     double rep, inv, pres, freq;
     __device__ LaneRules(float r, float p, float f) : rep((double)r), inv(1.0 / rep), pres((double)p), freq((double)f) {}
-    __device__ __forceinline__ double apply(double x, bool prompt, uint32_t n, double bias) const {
-        if (prompt || n) x = x > 0.0 ? x * inv : x * rep;
-        if (n) x -= freq * (double)n + pres;
-        return x + bias;
+    // what n occurrences take off
+    __device__ __forceinline__ double penalty(uint32_t n) const { return n ? freq * (double)n + pres : 0.0; }
+    __device__ __forceinline__ double apply(double x, bool seen, double penalty, bool biased, double bias) const {
+        const double y = (seen ? x > 0.0 ? x * inv : x * rep : x) - penalty;
+        return biased ? y + bias : y;
     }
 };
 
@@ -255,8 +256,6 @@ struct DraftsOfRow {
 // copied a tile in a piece; the same past the caches.
 enum { kModeInPlace, kModeShort, kModeLong, kModeOnce };
 
-constexpr uint32_t kColsAtOnce = 4;  // columns whose vectors a thread has in flight
-
 // Lane l0 + blockIdx.y, its columns blockIdx.z * U, .. + U - 1, then
 // gridDim.z * U further on.  The columns share the search for the rows that a
 // penalty or bias touches and the reading of their counts.
@@ -264,10 +263,10 @@ constexpr uint32_t kColsAtOnce = 4;  // columns whose vectors a thread has in fl
 // At these sizes the time is that of the chain of dependent reads: reads of
 // one link are issued together, at addresses cut to the last valid one instead
 // of behind branches.
-template <class DT, int kMode, bool kBias, bool kMask>
+template <class DT, int kMode, uint32_t U, bool kBias, bool kMask>
 __global__ __launch_bounds__(kBlock) void adjust_col(AdjustArgs a, uint32_t l0) {
     using storage = typename DT::storage;
-    constexpr uint32_t EPV = DT::kPerVec, ALL = (1u << EPV) - 1u, U = kColsAtOnce, ROWS = kBlock * EPV;
+    constexpr uint32_t EPV = DT::kPerVec, ALL = (1u << EPV) - 1u, ROWS = kBlock * EPV;
     constexpr bool kInPlace = kMode == kModeInPlace, kOnce = kMode == kModeOnce;
     using R = Rows<ROWS, kMode == kModeInPlace || kMode == kModeShort ? 256 : ROWS>;
     __shared__ TouchedRows<ROWS, kBias> sh;
@@ -285,7 +284,8 @@ __global__ __launch_bounds__(kBlock) void adjust_col(AdjustArgs a, uint32_t l0) 
     const uint32_t r = rows.row(tid * EPV);          // this thread's rows
     const uint32_t nvec = V / EPV;                   // whole vectors of a column
     const bool whole = r / EPV < nvec;
-    const uint32_t rr = whole ? r : 0u;              // a vector that can be read, if there is one
+    // the vector read: the column's last whole one for the rows behind it
+    const uint32_t rr = whole ? r : nvec ? V - EPV : 0u;
     u32x4 d[U];
     uint32_t m[U];
     auto load_columns = [&](uint32_t c0) {
@@ -325,6 +325,13 @@ __global__ __launch_bounds__(kBlock) void adjust_col(AdjustArgs a, uint32_t l0) 
             storage* out = static_cast<storage*>(a.out) + (int64_t)(c0 + u) * a.out_ld;
             if (whole) {
                 store16<kOnce>(out + r, kMask ? masked<DT>(d[u], m[u]) : d[u]);
+            } else if (nvec) {
+                const uint32_t skip = EPV - (V - r);  // elements of the vector read that other threads write
+#pragma unroll
+                for (uint32_t e = 0; e < EPV; ++e) {
+                    const bool ok = m[u] << skip >> e & 1u;
+                    if (e >= skip && (!kInPlace || !ok)) out[rr + e] = !kInPlace && ok ? (storage)vec_elem<DT>(d[u], (int)e) : (storage)kMinusInf<DT>;
+                }
             } else {
                 for (uint32_t e = 0; r + e < V; ++e) {
                     const bool ok = m[u] >> e & 1u;
@@ -356,7 +363,9 @@ __global__ __launch_bounds__(kBlock) void adjust_col(AdjustArgs a, uint32_t l0) 
         const uint32_t b = kBias ? sh.bias_at[kBias ? at : 0] : 0u;
         const float bias_value = kBias ? a.bias_values[b ? lane.bb + b - 1u : 0u] : 0.0f;
         DraftsOfRow drafts;
-        bool drafted = false;
+        bool drafted = false, seen = false;
+        uint32_t times = 0;
+        double penalty = 0.0;
         for (uint32_t c0 = c_first; c0 < ce; c0 += c_step) {
             uint32_t raw[U], ok[U];
 #pragma unroll
@@ -373,19 +382,30 @@ __global__ __launch_bounds__(kBlock) void adjust_col(AdjustArgs a, uint32_t l0) 
             }
             if (c0 == c_first) {
                 if (!counts) counted = 0;
+                times = counted & 0x7FFFFFFFu;
+                penalty = rules.penalty(times);
+                seen = counted != 0;
                 drafted = a.drafts && (sh.drafted[at >> 5] >> (at & 31u) & 1u);
                 if (drafted) drafts.find(a, lane, row);
             }
+            uint32_t y[U];
+            bool write[U];
 #pragma unroll
             for (uint32_t u = 0; u < U; ++u) {
-                if (c0 + u >= ce || (kMask && !(ok[u] & 1u))) continue;  // a forbidden element stays -Inf
-                uint32_t times = counted & 0x7FFFFFFFu;
-                if (drafted) times += drafts.before(a, lane, row, c0 + u - cb);
-                // (a later column's draft changes nothing here)
-                if (counted >> 31 || times || b)
-                    (static_cast<storage*>(a.out) + (int64_t)(c0 + u) * a.out_ld)[row] = (storage)from_double<DT>(
-                        rules.apply((double)to_float<DT>(raw[u]), counted >> 31, times, b ? (double)bias_value : 0.0));
+                bool seen_u = seen;
+                double penalty_u = penalty;
+                if (drafted) {
+                    const uint32_t n = times + drafts.before(a, lane, row, c0 + u - cb);
+                    seen_u = seen || n;
+                    penalty_u = rules.penalty(n);
+                }
+                // (a forbidden element stays -Inf, a later column's draft changes nothing here)
+                write[u] = c0 + u < ce && (!kMask || (ok[u] & 1u)) && (seen_u || b);
+                y[u] = from_double<DT>(rules.apply((double)to_float<DT>(raw[u]), seen_u, penalty_u, b != 0, (double)bias_value));
             }
+#pragma unroll
+            for (uint32_t u = 0; u < U; ++u)
+                if (write[u]) (static_cast<storage*>(a.out) + (int64_t)(c0 + u) * a.out_ld)[row] = (storage)y[u];
         }
     }
 }
@@ -539,10 +559,11 @@ __global__ __launch_bounds__(kBlock) void adjust_row_sparse(AdjustArgs a, uint32
                 }
                 const uint32_t b = kBias ? sh.bias_at[kBias ? at[u] : 0] : 0u;
                 const double bias = b ? (double)a.bias_values[lane.bb + b - 1u] : 0.0;
+                const bool seen = word != 0 || times;
                 // (a later column's draft changes nothing here)
-                if (word >> 31 || times || b)
-                    static_cast<storage*>(a.out)[(int64_t)row[u] * a.out_ld + c] =
-                        (storage)from_double<DT>(rules.apply((double)to_float<DT>(raw[u]), word >> 31, times, bias));
+                if (seen || b)
+                    static_cast<storage*>(a.out)[(int64_t)row[u] * a.out_ld + c] = (storage)from_double<DT>(
+                        rules.apply((double)to_float<DT>(raw[u]), seen, rules.penalty(times), b != 0, bias));
             }
         }
     }
@@ -559,30 +580,41 @@ bool past_caches(const AdjustArgs& a, int element_bytes) {
     return 2 * (int64_t)a.V * a.C * element_bytes > (int64_t(256) << 20);
 }
 
-template <class DT, int kMode, bool kBias, bool kMask>
+template <class DT, int kMode, uint32_t U, bool kBias, bool kMask>
 hipError_t launch_col(const AdjustArgs& a, hipStream_t stream) {
     const uint32_t rows = kBlock * DT::kPerVec, tiles = (a.V + rows - 1) / rows;
-    // a workgroup per kColsAtOnce columns of a lane of average size
-    const uint32_t z = min(((a.C + a.lanes - 1) / a.lanes + kColsAtOnce - 1) / kColsAtOnce, (uint32_t)kGridY);
+    // a workgroup per U columns of a lane of average size
+    const uint32_t z = min(((a.C + a.lanes - 1) / a.lanes + U - 1) / U, (uint32_t)kGridY);
     for (int64_t l0 = 0; l0 < a.lanes; l0 += kGridY) {
         const uint32_t n = (uint32_t)(a.lanes - l0 < kGridY ? a.lanes - l0 : kGridY);
-        hipLaunchKernelGGL((adjust_col<DT, kMode, kBias, kMask>), dim3(tiles, n, z), dim3(kBlock), 0, stream, a, (uint32_t)l0);
+        hipLaunchKernelGGL((adjust_col<DT, kMode, U, kBias, kMask>), dim3(tiles, n, z), dim3(kBlock), 0, stream, a, (uint32_t)l0);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
     return hipSuccess;
 }
 
+template <class DT, int kMode, uint32_t U>
+hipError_t launch_col(const AdjustArgs& a, hipStream_t stream) {
+    if (a.bias_ids) return a.mask ? launch_col<DT, kMode, U, true, true>(a, stream) : launch_col<DT, kMode, U, true, false>(a, stream);
+    return a.mask ? launch_col<DT, kMode, U, false, true>(a, stream) : launch_col<DT, kMode, U, false, false>(a, stream);
+}
+
+// Columns of a workgroup: one, as long as all workgroups run at once (the
+// scattered reads of the touched rows then spread over the CUs), else four
+// that share a list.  7 columns of 16,384 rows 4.4 us by ones, 7.0 by fours;
+// of 248,046 rows 5.7 and 8.9; 56 columns 17.4 and 16.6, in place 12.1 and 7.3.
 template <class DT, int kMode>
 hipError_t launch_col(const AdjustArgs& a, hipStream_t stream) {
-    if (a.bias_ids) return a.mask ? launch_col<DT, kMode, true, true>(a, stream) : launch_col<DT, kMode, true, false>(a, stream);
-    return a.mask ? launch_col<DT, kMode, false, true>(a, stream) : launch_col<DT, kMode, false, false>(a, stream);
+    const uint32_t rows = kBlock * DT::kPerVec;
+    const uint64_t wgs = (uint64_t)((a.V + rows - 1) / rows) * (a.C > a.lanes ? a.C : a.lanes);
+    return wgs <= 2048 ? launch_col<DT, kMode, 1>(a, stream) : launch_col<DT, kMode, 4>(a, stream);
 }
 
 template <class DT>
 hipError_t launch_col(const AdjustArgs& a, hipStream_t stream) {
     if (a.x == a.out) return launch_col<DT, kModeInPlace>(a, stream);
     const int e = 16 / DT::kPerVec;
-    if (past_caches(a, e)) return launch_col<DT, kModeOnce>(a, stream);
+    if (past_caches(a, e)) return launch_col<DT, kModeOnce, 4>(a, stream);
     // Short runs cost where the columns do not start on cache lines: a run of
     // 512 bytes then touches five lines for four.  32 columns, histories of
     // 500 and 4,000 tokens: 131,072 rows 5.8 and 6.3 us in short runs, 6.4 and
