@@ -52,7 +52,7 @@ int topk_cols_adjust(const topk_adjust_rules* r, const void* logits, void* out, 
     } else if (r->mask_index) {
         return TOPK_ERR_INVALID_ARG;
     }
-    if (r->V > TOPK_MAX_V || r->C > kMax32 || r->lanes > kMax32 || r->n_drafts > kMax32 || r->n_bias > kMax32 ||
+    if (r->V > TOPK_MAX_V || r->C > kMax32 || r->lanes > TOPK_MAX_LANES || r->n_drafts > kMax32 || r->n_bias > kMax32 ||
         (r->mask && r->mask_count > kMax32))
         return TOPK_ERR_UNSUPPORTED;
     topk::AdjustArgs a = {};
@@ -94,7 +94,7 @@ int topk_cols_count(int64_t V, int64_t lanes, const int32_t* ids, int64_t n_ids,
     if (misaligned(ids, 4) || misaligned(prompt_len, 4) || misaligned(fresh, 4) || misaligned(counts, 4) ||
         misaligned(seen, 4))
         return TOPK_ERR_INVALID_ARG;
-    if (V > TOPK_MAX_V || lanes > kMax32 || n_ids > kMax32) return TOPK_ERR_UNSUPPORTED;
+    if (V > TOPK_MAX_V || lanes > TOPK_MAX_LANES || n_ids > kMax32) return TOPK_ERR_UNSUPPORTED;
     topk::CountArgs a = {};
     if (make_parts(&a.parts, start, n_ids, lanes) != TOPK_OK) return TOPK_ERR_INVALID_ARG;
     a.V = (uint32_t)V;
@@ -124,8 +124,7 @@ int topk_cols_verify(const topk_verify_args* v, hipStream_t stream) {
         misaligned(v->draft_ids, 4) || misaligned(v->drafts, 4) || misaligned(v->out_tokens, 4) ||
         misaligned(v->out_count, 4))
         return TOPK_ERR_INVALID_ARG;
-    // one workgroup of 512 threads per lane: a grid holds less than 2^32 threads
-    if (v->lanes > (1 << 22) || v->C > kMax32 || v->n_drafts > kMax32 || v->max_tokens > kMax32) return TOPK_ERR_UNSUPPORTED;
+    if (v->lanes > TOPK_MAX_LANES || v->C > kMax32 || v->n_drafts > kMax32 || v->max_tokens > kMax32) return TOPK_ERR_UNSUPPORTED;
     topk::VerifyArgs a = {};
     a.v = *v;
     if (make_parts(&a.cols, v->col_start, v->C, v->lanes) != TOPK_OK ||
@@ -148,7 +147,7 @@ int topk_cols_plan(const topk_plan_args* p, hipStream_t stream) {
         misaligned(p->out_free_count, 4) || misaligned(p->out_refused, 4) || misaligned(p->out_col_start, 4) ||
         misaligned(p->out_col_lane, 4) || misaligned(p->out_col_pos, 4) || misaligned(p->out_slots, 8))
         return TOPK_ERR_INVALID_ARG;
-    if (p->lanes > kMax32 || p->capacity > kMax32 || p->table_ld > kMax32 || p->n_free_ids > kMax32)
+    if (p->lanes > TOPK_MAX_LANES || p->capacity > kMax32 || p->table_ld > kMax32 || p->n_free_ids > kMax32)
         return TOPK_ERR_UNSUPPORTED;
     return topk::launch_plan_round(*p, stream) == hipSuccess ? TOPK_OK : TOPK_ERR_HIP;
 }

@@ -29,6 +29,9 @@ TOPK_ERR_TIMEOUT = -5
 TOPK_MAX_K = 64
 TOPK_MAX_V = (1 << 24) - 1
 
+TOPK_MAX_LANES = 1 << 20
+_U64 = (1 << 64) - 1  # seeds and offsets wrap, as ctypes passes them
+
 DTYPES = {"bf16": 0, "f32": 1}
 LAYOUTS = {"col": 0, "row": 1}
 
@@ -501,7 +504,7 @@ def verify(target_values, target_ids, col_start, drafts, draft_start, draft_valu
         lanes, 0 if size == 2 else 1, k, kq, C, _need("col_start", col_start, lanes + 1, index, i32),
         target_values.data_ptr(), _need("target_ids", target_ids, 1, index, i32), n,
         _need("draft_start", draft_start, lanes + 1, index, i32), _need("drafts", drafts, 0, index, i32) if n else 0, qv,
-        qi, temperature, top_p, seed, offset, out_shape[1], _need("out_tokens", out_tokens, 1, index, i32),
+        qi, temperature, top_p, seed & _U64, offset & _U64, out_shape[1], _need("out_tokens", out_tokens, 1, index, i32),
         _need("out_count", out_count, lanes, index, i32))
     _launch("topk_cols_verify", load().topk_cols_verify, index, stream, args)
     return out_tokens, out_count
@@ -521,8 +524,8 @@ def plan(lens, add, held, table, free_ids, free_count, block_size: int, capacity
     """
     import torch
     i32, index, lanes = torch.int32, lens.get_device(), lens.numel()
-    if table.dim() != 2 or table.shape[0] < lanes:
-        raise ValueError("table must be a matrix with a row per lane")
+    if table.dim() != 2 or table.shape[0] < lanes or not 0 < block_size < 1 << 31 or not 0 < capacity < 1 << 31:
+        raise ValueError("table must be a matrix with a row per lane, block_size and capacity positive 32-bit numbers")
     if out is None:
         sizes = dict(held=lanes, free_count=1, refused=1, col_start=lanes + 1, col_lane=capacity, col_pos=capacity,
                      slots=capacity)

@@ -233,6 +233,10 @@ int topk_cols_sample(const void *values, const int32_t *ids, int64_t C, int32_t 
  * structures are read before the call returns.
  */
 
+/* Most lanes of a call of these entry points (each of them looks at every
+ * lane, whether it has columns or not). */
+#define TOPK_MAX_LANES ((int64_t)1 << 20)
+
 /* The rules of topk_cols_adjust.  Zero (NULL) leaves a rule out. */
 typedef struct {
     int64_t V;                /* rows, 1 <= V <= TOPK_MAX_V */
@@ -297,8 +301,9 @@ typedef struct {
  * Returns TOPK_ERR_INVALID_ARG for a NULL or misaligned pointer, a size or
  * leading dimension out of range, an incomplete group, lanes that do not
  * divide C (col_start NULL) or n_drafts (draft_start NULL);
- * TOPK_ERR_UNSUPPORTED for V > TOPK_MAX_V, or C, lanes, n_drafts, n_bias or
- * mask_count beyond 2^31 - 1; TOPK_ERR_HIP when a launch fails.
+ * TOPK_ERR_UNSUPPORTED for V > TOPK_MAX_V, lanes > TOPK_MAX_LANES, or C,
+ * n_drafts, n_bias or mask_count beyond 2^31 - 1; TOPK_ERR_HIP when a launch
+ * fails.
  */
 int topk_cols_adjust(const topk_adjust_rules *rules, const void *logits, void *out, hipStream_t stream);
 
@@ -321,7 +326,8 @@ int topk_cols_adjust(const topk_adjust_rules *rules, const void *logits, void *o
  * Returns TOPK_ERR_INVALID_ARG for a NULL or misaligned pointer, V < 1,
  * lanes < 1, n_ids < 0, a leading dimension that is too small, or lanes that
  * do not divide n_ids (start NULL); TOPK_ERR_UNSUPPORTED for V > TOPK_MAX_V,
- * or lanes or n_ids beyond 2^31 - 1; TOPK_ERR_HIP when a launch fails.
+ * lanes > TOPK_MAX_LANES or n_ids beyond 2^31 - 1; TOPK_ERR_HIP when a launch
+ * fails.
  */
 int topk_cols_count(int64_t V, int64_t lanes, const int32_t *ids, int64_t n_ids, const int32_t *start,
                     const int32_t *prompt_len, const int32_t *fresh, int32_t *counts, int64_t counts_ld,
@@ -389,8 +395,8 @@ typedef struct {
  *
  * Returns TOPK_ERR_INVALID_ARG for a NULL or misaligned pointer, a value out
  * of the ranges above, or lanes that do not divide C (col_start NULL) or
- * n_drafts (draft_start NULL); TOPK_ERR_UNSUPPORTED for more than
- * 4,194,304 lanes, or C, n_drafts or max_tokens beyond 2^31 - 1;
+ * n_drafts (draft_start NULL); TOPK_ERR_UNSUPPORTED for lanes >
+ * TOPK_MAX_LANES, or C, n_drafts or max_tokens beyond 2^31 - 1;
  * TOPK_ERR_HIP when the launch fails.
  */
 int topk_cols_verify(const topk_verify_args *args, hipStream_t stream);
@@ -445,8 +451,8 @@ typedef struct {
  *
  * Returns TOPK_ERR_INVALID_ARG for a NULL or misaligned pointer, a size out
  * of range, out_held == held or out_free_count == free_count;
- * TOPK_ERR_UNSUPPORTED for lanes, capacity, table_ld or n_free_ids beyond
- * 2^31 - 1; TOPK_ERR_HIP when the launch fails.
+ * TOPK_ERR_UNSUPPORTED for lanes > TOPK_MAX_LANES, or capacity, table_ld or
+ * n_free_ids beyond 2^31 - 1; TOPK_ERR_HIP when the launch fails.
  */
 int topk_cols_plan(const topk_plan_args *args, hipStream_t stream);
 

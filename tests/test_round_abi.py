@@ -55,7 +55,7 @@ def test_adjust_refuses_pointers_and_limits(lib):
     assert lib.topk_cols_adjust(ctypes.byref(rules(out_ld=101)), P, P, None) == T.TOPK_ERR_INVALID_ARG  # in place
     assert lib.topk_cols_adjust(ctypes.byref(rules(dtype=1)), P + 2, P, None) == T.TOPK_ERR_INVALID_ARG
     big = 1 << 24
-    for kw in (dict(V=big, ld=big, out_ld=big), dict(C=1 << 31), dict(lanes=1 << 31, col_start=P),
+    for kw in (dict(V=big, ld=big, out_ld=big), dict(C=1 << 31), dict(lanes=(1 << 20) + 1, col_start=P),
                dict(BIAS, n_bias=1 << 31), dict(drafts=P, n_drafts=1 << 31),
                dict(mask=P, mask_ld=4, mask_count=1 << 31)):
         assert lib.topk_cols_adjust(ctypes.byref(rules(**kw)), P, 2 * P, None) == T.TOPK_ERR_UNSUPPORTED, kw
@@ -71,7 +71,7 @@ def test_count_refuses(lib):
                dict(prompt_len=P + 2), dict(fresh=P + 2), dict(counts=None), dict(counts=P + 2), dict(counts_ld=99),
                dict(seen=None), dict(seen=P + 1), dict(seen_ld=3), dict(ids=P + 1)):
         assert call(**kw) == T.TOPK_ERR_INVALID_ARG, kw
-    for kw in (dict(V=1 << 24, counts_ld=1 << 24, seen_ld=1 << 20), dict(lanes=1 << 31), dict(n_ids=1 << 31)):
+    for kw in (dict(V=1 << 24, counts_ld=1 << 24, seen_ld=1 << 20), dict(lanes=(1 << 20) + 1), dict(n_ids=1 << 31)):
         assert call(**kw) == T.TOPK_ERR_UNSUPPORTED, kw
 
 
@@ -92,7 +92,7 @@ def test_verify_refuses(lib):
                dict(top_p=float("nan")), dict(max_tokens=0), dict(out_tokens=None), dict(out_tokens=P + 2),
                dict(out_count=None), dict(out_count=P + 1)):
         assert call(**kw) == T.TOPK_ERR_INVALID_ARG, kw
-    for kw in (dict(lanes=(1 << 22) + 1), dict(C=1 << 31), dict(n_drafts=1 << 31), dict(max_tokens=1 << 31)):
+    for kw in (dict(lanes=(1 << 20) + 1), dict(C=1 << 31), dict(n_drafts=1 << 31), dict(max_tokens=1 << 31)):
         assert call(**kw) == T.TOPK_ERR_UNSUPPORTED, kw
     assert lib.topk_cols_verify(None, None) == T.TOPK_ERR_INVALID_ARG
 
@@ -111,8 +111,8 @@ def test_plan_refuses(lib):
     bad += [{n: None} for n in pointers] + [{n: P + 2} for n in pointers]
     for kw in bad:
         assert call(**kw) == T.TOPK_ERR_INVALID_ARG, kw
-    for n in ("lanes", "capacity", "table_ld", "n_free_ids"):
-        assert call(**{n: 1 << 31}) == T.TOPK_ERR_UNSUPPORTED, n
+    for n, most in (("lanes", 1 << 20), ("capacity", 2**31 - 1), ("table_ld", 2**31 - 1), ("n_free_ids", 2**31 - 1)):
+        assert call(**{n: most + 1}) == T.TOPK_ERR_UNSUPPORTED, n
     assert lib.topk_cols_plan(None, None) == T.TOPK_ERR_INVALID_ARG
 
 

@@ -223,6 +223,43 @@ def test_adjust_columns_on_cache_lines(gpu, layout, n):
     run_adjust(gpu, Case(300 + n, V, lanes, most, dtype, layout, ragged=n == 1, hist=700, drafts=True, bias=40, mask="column"), False)
 
 
+@pytest.mark.parametrize("layout", [W.COL, W.ROW])
+def test_adjust_offsets_past_32_bits(gpu, layout):
+    """Elements, history words and mask words more than 2^32 bytes into their
+    arrays."""
+    torch, T = gpu
+    V, lanes, ld = 70, 3, 2**31 // 2 + 8
+    rng = np.random.default_rng(4)
+    rows, width = (lanes, V) if layout == W.COL else (V, lanes)
+    if layout == W.ROW:
+        ld = 2**32 // 2 // (V - 1) + 1   # the last row begins past 2^32 bytes
+    x = W.bf16_bits_from_f32((rng.standard_normal((lanes, V)) * 4).astype(np.float32))
+    m = x if layout == W.COL else np.ascontiguousarray(x.T)
+    word = rng.integers(0, 3, (lanes, V)).astype(np.int32)
+    mask = packed(rng.random((lanes, V)) < 0.7)
+    wide = 2**30 + 4  # words: 4 GiB and more to a row
+    print(f"[round] adjust, offsets past 32 bits {layout}", flush=True)
+
+    def spread(a, columns, dtype):
+        t = torch.zeros((a.shape[0], columns), dtype=dtype, device="cuda")
+        t[:, :a.shape[1]] = torch.from_numpy(a.view(np.int16 if a.itemsize == 2 else np.int32)).cuda()
+        return t
+    dx = spread(m, ld, torch.int16)
+    rules = dict(repetition=np.float32([1.5, 0.5, 2.0]), presence=np.float32([0.1, 0.2, 0.3]))
+    seen = packed(word != 0)
+    r = T.AdjustRules(V, lanes, W.BF16, layout, ld, lanes=lanes, counts=spread(word, wide, torch.int32),
+                      seen=dev(torch, seen), mask=spread(mask, wide, torch.int32),
+                      **{k: dev(torch, v) for k, v in rules.items()})
+    r.apply(dx, dx)
+    torch.cuda.synchronize()
+    got = host(dx[:, :width].contiguous(), W.BF16)
+    assert int((dx[:, width:] != 0).sum()) == 0
+    got = got if layout == W.COL else np.ascontiguousarray(got.T)
+    expect = R.adjust(x, V, lanes, lanes, W.BF16, counts=word, mask=mask, **rules)
+    for c in range(lanes):
+        R.check_adjusted(got[c].copy(), x[c], W.BF16, c, expect[c])
+
+
 def test_adjust_with_no_rule_copies(gpu):
     torch, T = gpu
     case = Case(7, 5003, 2, 3, W.BF16, W.COL, penalties=None, special=True)
