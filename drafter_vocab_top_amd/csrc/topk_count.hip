@@ -9,6 +9,11 @@
 // a lane's rows in LDS, reads all of the lane's tokens, counts its own and
 // writes its rows, so that nothing is cleared first and the many occurrences
 // of frequent tokens meet in LDS instead of in one cache line.
+//
+// One MI355X, replayed from a graph: 64 lanes of up to 8 tokens 2.9 us, a
+// launch and one chain of reads and atomics; 8 fresh lanes of 25,000 tokens
+// each 10.3 us, about 5 of them the reading of each lane's tokens by all 32
+// workgroups of the lane (L2), 2 their LDS atomics and 2 the 8 MB of rows.
 #include "topk_round.hpp"
 
 #include "topk_col_common.hpp"
