@@ -547,9 +547,10 @@ __global__ __launch_bounds__(kBlock) void adjust_row_sparse(AdjustArgs a, uint32
     for (uint32_t j = tid & ((1u << w_log) - 1u); j < lane.ce - lane.cb; j += 1u << w_log) {
         const uint32_t c = lane.cb + j;
         const uint32_t* mask = kMask ? mask_row(a, c) : nullptr;
-        constexpr uint32_t U = 4;  // rows whose reads are in flight together
+        constexpr uint32_t U = 2;  // rows whose reads are in flight together
         for (uint32_t k0 = tid >> w_log; k0 < n_rows; k0 += step * U) {
-            uint32_t at[U], row[U], counted[U], raw[U], ok[U];
+            uint32_t at[U], row[U], counted[U], raw[U], ok[U], b[U];
+            float bias[U];
 #pragma unroll
             for (uint32_t u = 0; u < U; ++u) {
                 at[u] = sh.list[min_u32(k0 + u * step, n_rows - 1u)];
@@ -560,6 +561,8 @@ __global__ __launch_bounds__(kBlock) void adjust_row_sparse(AdjustArgs a, uint32
                 counted[u] = (uint32_t)*(counts ? counts + row[u] : or_safe<int32_t>(nullptr));
                 raw[u] = (uint32_t)static_cast<const storage*>(a.x)[(int64_t)row[u] * a.ld + c];
                 ok[u] = kMask ? *(mask ? mask + (row[u] >> 5) : or_safe<uint32_t>(nullptr)) : 0u;
+                b[u] = kBias ? sh.bias_at[kBias ? at[u] : 0] : 0u;
+                bias[u] = kBias ? a.bias_values[b[u] ? lane.bb + b[u] - 1u : 0u] : 0.0f;
             }
 #pragma unroll
             for (uint32_t u = 0; u < U; ++u) {
@@ -571,13 +574,11 @@ __global__ __launch_bounds__(kBlock) void adjust_row_sparse(AdjustArgs a, uint32
                     drafts.find(a, lane, row[u]);
                     times += drafts.before(a, lane, row[u], j);
                 }
-                const uint32_t b = kBias ? sh.bias_at[kBias ? at[u] : 0] : 0u;
-                const double bias = b ? (double)a.bias_values[lane.bb + b - 1u] : 0.0;
                 const bool seen = word != 0 || times;
                 // (a later column's draft changes nothing here)
-                if (seen || b)
+                if (seen || b[u])
                     static_cast<storage*>(a.out)[(int64_t)row[u] * a.out_ld + c] = (storage)from_double<DT>(
-                        rules.apply((double)to_float<DT>(raw[u]), seen, rules.penalty(times), b != 0, bias));
+                        rules.apply((double)to_float<DT>(raw[u]), seen, rules.penalty(times), b[u] != 0, (double)bias[u]));
             }
         }
     }
