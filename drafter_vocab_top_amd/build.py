@@ -1,13 +1,15 @@
-"""Builds libtopk_cols.so (HIP kernels + C ABI) for gfx950 with hipcc, in-tree.
+"""Builds libtopk_cols.so (HIP kernels + C ABI) for gfx950 with hipcc, in-tree,
+and the compiled part of its Python binding with g++.
 
     python -m drafter_vocab_top_amd.build
 
-The library is placed next to this file; the Python binding loads it from
+The libraries are placed next to this file; the Python binding loads them from
 there.  hipcc cross-compiles for gfx950 without a GPU.
 """
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -36,6 +38,9 @@ STREAM_LIBRARY = os.path.join(HERE, "libstream_read.so")
 HEADERS = [os.path.join(CSRC, n) for n in ("topk_device.hpp", "topk_col_common.hpp", "topk_internal.hpp", "topk_draw.hpp",
                                             "topk_round.hpp")] + \
           [os.path.join(INCLUDE, "topk_cols.h")]
+# The compiled part of the Python binding (host code against torch's headers).
+BINDING_SOURCE = os.path.join(CSRC, "round_binding.cpp")
+BINDING_LIBRARY = os.path.join(HERE, "_round_binding.so")
 ARCH = "gfx950"
 
 
@@ -50,6 +55,18 @@ def flags():
             # keep the compiler from emitting packed fp32 instructions
             "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
             "-Wall", "-Wno-unused-result", "-I", INCLUDE, "-I", CSRC]
+
+
+def binding_command(output):
+    """The g++ line of the binding's compiled part."""
+    import torch
+    base = os.path.dirname(torch.__file__)
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-D__HIP_PLATFORM_AMD__", "-I", INCLUDE,
+            "-isystem", os.path.join(rocm, "include"), "-isystem", sysconfig.get_paths()["include"],
+            "-isystem", os.path.join(base, "include"), "-o", output, BINDING_SOURCE, "-L", os.path.join(base, "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
 def command(output=LIBRARY):
@@ -79,6 +96,11 @@ def build(verbose=False):
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
         objs.append(obj)
+    binding_tmp = BINDING_LIBRARY + ".tmp"
+    cmd = binding_command(binding_tmp)
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    procs.append((BINDING_SOURCE, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
     for src, pr in procs:
         out, err = pr.communicate()
         _check(subprocess.CompletedProcess(pr.args, pr.returncode, out, err), os.path.basename(src), verbose)
@@ -89,14 +111,15 @@ def build(verbose=False):
             print(" ".join(cmd), flush=True)
         _check(subprocess.run(cmd, capture_output=True, text=True), "link", verbose)
         os.replace(tmp, lib)
+    os.replace(binding_tmp, BINDING_LIBRARY)
     return LIBRARY
 
 
 def stale():
-    if not os.path.exists(LIBRARY):
+    if not os.path.exists(LIBRARY) or not os.path.exists(BINDING_LIBRARY):
         return True
-    t = os.path.getmtime(LIBRARY)
-    return any(os.path.getmtime(p) > t for p in SOURCES + HEADERS)
+    t = min(os.path.getmtime(LIBRARY), os.path.getmtime(BINDING_LIBRARY))
+    return any(os.path.getmtime(p) > t for p in SOURCES + HEADERS + [BINDING_SOURCE])
 
 
 if __name__ == "__main__":

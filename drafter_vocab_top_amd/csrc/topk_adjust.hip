@@ -27,7 +27,7 @@
 //
 // What bounds it (one MI355X, replayed from a graph).  Large matrices: memory.
 // 448 interleaved columns of 248,046 rows, bf16: 83 us for the dense part (449
-// MB, 5.4 TB/s, the rate of a plain copy) and 20 for the touched rows; 448
+// MB, 5.4 TB/s, the rate of a plain copy) and 18 for the touched rows; 448
 // column-contiguous ones 95.  64 columns of 131,072 rows, fp32, half of them in
 // use: 10.8 us (34 MB).  Small ones: the chain launch, col_start and history
 // bits, list, counts and elements, store: 6.4 us for one lane's 8 columns (8

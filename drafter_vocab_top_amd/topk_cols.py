@@ -10,13 +10,13 @@ and the stream.
     h.close()
 
 Loading fails loudly when the library is missing or cannot be loaded.  There
-is no fallback path.
+is no fallback path.  (The calls around the top-k go through a compiled
+module, _round_binding, that reads their many tensors faster than Python does.)
 """
 from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 LIBRARY = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtopk_cols.so")
 
@@ -30,7 +30,6 @@ TOPK_MAX_K = 64
 TOPK_MAX_V = (1 << 24) - 1
 
 TOPK_MAX_LANES = 1 << 20
-_U64 = (1 << 64) - 1  # seeds and offsets wrap, as ctypes passes them
 
 DTYPES = {"bf16": 0, "f32": 1}
 LAYOUTS = {"col": 0, "row": 1}
@@ -48,25 +47,22 @@ _lib = None
 
 
 def _struct(name: str, fields: str):
-    """A structure of the header from "type name" pairs in its order: a ctypes
-    class, and the packer of its fields (a call packs one in a fraction of the
-    time that filling the class takes)."""
-    types = {"p": (ctypes.c_void_p, "P"), "i64": (ctypes.c_int64, "q"), "i32": (ctypes.c_int32, "i"),
-             "u64": (ctypes.c_uint64, "Q"), "f64": (ctypes.c_double, "d")}
+    """A structure of the header, from "type name" pairs in its order."""
+    types = {"p": ctypes.c_void_p, "i64": ctypes.c_int64, "i32": ctypes.c_int32, "u64": ctypes.c_uint64,
+             "f64": ctypes.c_double}
     pairs = [f.split() for f in fields.split(",")]
-    cls = type(name, (ctypes.Structure,), {"_fields_": [(n, types[t][0]) for t, n in pairs]})
-    return cls, struct.Struct("@" + "".join(types[t][1] for t, n in pairs)).pack
+    return type(name, (ctypes.Structure,), {"_fields_": [(n, types[t]) for t, n in pairs]})
 
 
-AdjustRulesArgs, _ = _struct("topk_adjust_rules", (
+AdjustRulesArgs = _struct("topk_adjust_rules", (
     "i64 V, i64 C, i64 lanes, i32 dtype, i32 layout, i64 ld, i64 out_ld, p col_start, p counts, i64 counts_ld, "
     "p seen, i64 seen_ld, p repetition, p presence, p frequency, p drafts, p draft_start, i64 n_drafts, "
     "p bias_start, p bias_ids, p bias_values, i64 n_bias, p mask, i64 mask_ld, i64 mask_count, p mask_index"))
-VerifyArgs, _pack_verify = _struct("topk_verify_args", (
+VerifyArgs = _struct("topk_verify_args", (
     "i64 lanes, i32 dtype, i32 k, i32 kq, i64 C, p col_start, p target_values, p target_ids, i64 n_drafts, "
     "p draft_start, p drafts, p draft_values, p draft_ids, f64 temperature, f64 top_p, u64 seed, u64 offset, "
     "i64 max_tokens, p out_tokens, p out_count"))
-PlanArgs, _pack_plan = _struct("topk_plan_args", (
+PlanArgs = _struct("topk_plan_args", (
     "i64 lanes, i64 capacity, i32 block_size, p lens, p add, p held, p table, i64 table_ld, p free_ids, "
     "i64 n_free_ids, p free_count, p out_held, p out_free_count, p out_refused, p out_col_start, p out_col_lane, "
     "p out_col_pos, p out_slots"))
@@ -321,15 +317,48 @@ def _need(name: str, t, numel: int, index: int, dtype) -> int:
     return t.data_ptr()
 
 
-def _launch(what: str, function, index: int, stream, *args) -> None:
-    """function(*args, raw stream) with GPU `index` current, on its current
-    stream by default."""
+_round = None
+
+
+def _round_binding():
+    """The compiled part of the binding: it takes tensors apart for
+    AdjustRules.apply, count_tokens, verify and plan, and calls the loaded
+    library."""
+    global _round
+    if _round is None:
+        import torch  # noqa: F401  (the module needs its libraries in the process)
+        lib = load()
+        try:
+            from . import _round_binding as module
+        except ImportError as e:
+            raise OSError(f"_round_binding is missing or does not load ({e}): build it with "
+                          "`python -m drafter_vocab_top_amd.build`") from e
+        module.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                      for f in (lib.topk_cols_adjust, lib.topk_cols_count, lib.topk_cols_verify, lib.topk_cols_plan)))
+        _round = module
+    return _round
+
+
+def _raw_stream(index: int, stream) -> int:
+    """The raw handle of a stream, by default the current one of GPU `index`."""
+    if stream is not None:
+        return stream.cuda_stream
     import torch
+    if index < 0:
+        raise ValueError("the tensors must be on a GPU")
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _launch(what: str, function, index: int, *args) -> None:
+    """function(*args) with GPU `index` current."""
+    import torch
+    if index < 0:
+        raise ValueError("the tensors must be on a GPU")
     if index == torch._C._cuda_getDevice():
-        rc = function(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+        rc = function(*args)
     else:
         with torch.cuda.device(index):
-            rc = function(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+            rc = function(*args)
     if rc != TOPK_OK:
         raise TopkError(rc, what)
 
@@ -406,8 +435,7 @@ class AdjustRules:
             n_drafts=drafts.numel() if drafts is not None else 0,
             n_bias=bias_ids.numel() if bias_ids is not None else 0,
             mask_ld=mask.shape[1] if mask is not None else 0, mask_count=mask.shape[0] if mask is not None else 0, **at)
-        self._ref = ctypes.byref(self._args)
-        self._function = load().topk_cols_adjust
+        self._address = ctypes.addressof(self._args)
         self._size = 2 if dtype == "bf16" else 4
         rows, width = (C, V) if layout == "col" else (V, C)
         self._numel = (rows - 1) * self.ld + width
@@ -424,12 +452,10 @@ class AdjustRules:
                 raise ValueError("out is needed when out_ld differs from ld")
             out = torch.empty_like(x)
         index = x.get_device()
-        if index < 0 or out.get_device() != index or self._index not in (None, index):
+        if self._index not in (None, index):
             raise ValueError("x, out and the rules' tensors must be on one GPU")
-        if x.element_size() != self._size or out.element_size() != self._size or x.numel() < self._numel \
-                or out.numel() < self._out_numel or not (x.is_contiguous() and out.is_contiguous()):
-            raise ValueError("x and out must be contiguous and hold the matrix described by the rules")
-        _launch("topk_cols_adjust", self._function, index, stream, self._ref, x.data_ptr(), out.data_ptr())
+        _launch("topk_cols_adjust", _round_binding().adjust, index, _raw_stream(index, stream), self._address, x, out,
+                self._size, self._numel, self._out_numel, index)
         return out
 
 
@@ -443,15 +469,9 @@ def count_tokens(counts, seen, V: int, ids, start=None, prompt_len=None, fresh=N
         prompt (none without it).  fresh (lanes,): lanes to clear first.
     Returns (counts, seen).
     """
-    import torch
-    i32, index, shape, seen_shape = torch.int32, counts.get_device(), counts.shape, seen.shape
-    if len(shape) != 2 or len(seen_shape) != 2 or seen_shape[0] != shape[0]:
-        raise ValueError("counts and seen must be matrices with a row per lane")
-    lanes, n = shape[0], ids.numel()
-    _launch("topk_cols_count", load().topk_cols_count, index, stream, V, lanes,
-            _need("ids", ids, 0, index, i32) if n else 0, n, _need("start", start, lanes + 1, index, i32),
-            _need("prompt_len", prompt_len, lanes, index, i32), _need("fresh", fresh, lanes, index, i32),
-            _need("counts", counts, 1, index, i32), shape[1], _need("seen", seen, 1, index, i32), seen_shape[1])
+    index = counts.get_device()
+    _launch("topk_cols_count", _round_binding().count, index, _raw_stream(index, stream), V, counts, seen, ids, start,
+            prompt_len, fresh)
     return counts, seen
 
 
@@ -473,40 +493,19 @@ def verify(target_values, target_ids, col_start, drafts, draft_start, draft_valu
     out_tokens is not given (default: one more than all drafts, which is
     enough for any lane; pass the round's draft limit + 1).
     """
-    import torch
-    i32, index = torch.int32, target_values.get_device()
+    index = target_values.get_device()
     if lanes is None:
         if col_start is None:
             raise ValueError("lanes is needed without col_start")
         lanes = col_start.numel() - 1
-    n = drafts.numel()
-    if out_tokens is None:
-        out_tokens = torch.empty((lanes, max_tokens or n + 1), dtype=i32, device=target_values.device)
-    if out_count is None:
-        out_count = torch.empty(lanes, dtype=i32, device=target_values.device)
-    shape, out_shape, size = target_values.shape, out_tokens.shape, target_values.element_size()
-    if len(shape) != 2 or target_ids.shape != shape or len(out_shape) != 2 or out_shape[0] < lanes:
-        raise ValueError("target_values and target_ids must be (C, k), out_tokens a matrix with a row per lane")
-    if index < 0 or size not in (2, 4) or not target_values.is_contiguous():
-        raise ValueError("target_values must be a contiguous GPU tensor of bf16 or fp32 (or patterns)")
-    C, k = shape
-    kq = qv = qi = 0
-    if draft_values is not None:
-        shape = draft_values.shape
-        if len(shape) != 2 or draft_ids is None or draft_ids.shape != shape or draft_values.element_size() != size \
-                or draft_values.get_device() != index or not draft_values.is_contiguous():
-            raise ValueError("draft_values and draft_ids must be contiguous (n, kq) tensors of the target lists' types")
-        # drafts past the lists have no distribution to be judged by
-        n = min(n, shape[0])
-        if n:
-            kq, qv, qi = shape[1], draft_values.data_ptr(), _need("draft_ids", draft_ids, 0, index, i32)
-    args = _pack_verify(
-        lanes, 0 if size == 2 else 1, k, kq, C, _need("col_start", col_start, lanes + 1, index, i32),
-        target_values.data_ptr(), _need("target_ids", target_ids, 1, index, i32), n,
-        _need("draft_start", draft_start, lanes + 1, index, i32), _need("drafts", drafts, 0, index, i32) if n else 0, qv,
-        qi, temperature, top_p, seed & _U64, offset & _U64, out_shape[1], _need("out_tokens", out_tokens, 1, index, i32),
-        _need("out_count", out_count, lanes, index, i32))
-    _launch("topk_cols_verify", load().topk_cols_verify, index, stream, args)
+    if out_tokens is None or out_count is None:
+        import torch
+        if out_tokens is None:
+            out_tokens = torch.empty((lanes, max_tokens or drafts.numel() + 1), dtype=torch.int32, device=target_values.device)
+        if out_count is None:
+            out_count = torch.empty(lanes, dtype=torch.int32, device=target_values.device)
+    _launch("topk_cols_verify", _round_binding().verify, index, _raw_stream(index, stream), lanes, target_values, target_ids,
+            col_start, drafts, draft_start, draft_values, draft_ids, temperature, top_p, seed, offset, out_tokens, out_count)
     return out_tokens, out_count
 
 
@@ -522,27 +521,17 @@ def plan(lens, add, held, table, free_ids, free_count, block_size: int, capacity
     tensors held (lanes,), free_count (1,), refused (1,), col_start
     (lanes + 1,), col_lane, col_pos (capacity,) and int64 slots (capacity,).
     """
-    import torch
-    i32, index, lanes = torch.int32, lens.get_device(), lens.numel()
-    if table.dim() != 2 or table.shape[0] < lanes or not 0 < block_size < 1 << 31 or not 0 < capacity < 1 << 31:
-        raise ValueError("table must be a matrix with a row per lane, block_size and capacity positive 32-bit numbers")
+    index = lens.get_device()
     if out is None:
+        import torch
+        lanes = lens.numel()
         sizes = dict(held=lanes, free_count=1, refused=1, col_start=lanes + 1, col_lane=capacity, col_pos=capacity,
                      slots=capacity)
-        out = {n: torch.empty(size, dtype=torch.int64 if n == "slots" else i32, device=lens.device)
+        out = {n: torch.empty(size, dtype=torch.int64 if n == "slots" else torch.int32, device=lens.device)
                for n, size in sizes.items()}
-    n_free = free_ids.numel()
-    args = _pack_plan(
-        lanes, capacity, block_size, _need("lens", lens, lanes, index, i32), _need("add", add, lanes, index, i32),
-        _need("held", held, lanes, index, i32), _need("table", table, 1, index, i32), table.shape[1],
-        _need("free_ids", free_ids, 0, index, i32) if n_free else 0, n_free,
-        _need("free_count", free_count, 1, index, i32), _need("out held", out["held"], lanes, index, i32),
-        _need("out free_count", out["free_count"], 1, index, i32), _need("out refused", out["refused"], 1, index, i32),
-        _need("out col_start", out["col_start"], lanes + 1, index, i32),
-        _need("out col_lane", out["col_lane"], capacity, index, i32),
-        _need("out col_pos", out["col_pos"], capacity, index, i32),
-        _need("out slots", out["slots"], capacity, index, torch.int64))
-    _launch("topk_cols_plan", load().topk_cols_plan, index, stream, args)
+    _launch("topk_cols_plan", _round_binding().plan, index, _raw_stream(index, stream), lens, add, held, table, free_ids,
+            free_count, block_size, capacity, out["held"], out["free_count"], out["refused"], out["col_start"],
+            out["col_lane"], out["col_pos"], out["slots"])
     return out
 
 

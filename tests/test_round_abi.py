@@ -160,6 +160,37 @@ def test_binding_refuses_tensors_that_do_not_fit():
         T.plan(i32(2), i32(2), i32(2), i32(1, 4), i32(4), i32(1), 16, 8)
 
 
+def test_compiled_binding_refuses_before_it_calls():
+    """Host tensors, wrong types and missing tensors: Python errors, no call."""
+    import torch
+    b = T._round_binding()
+    i32 = lambda *n: torch.zeros(n, dtype=torch.int32)  # noqa: E731
+    v = torch.zeros(8, 4)
+    outs = [i32(2), i32(1), i32(1), i32(3), i32(8), i32(8), torch.zeros(8, dtype=torch.int64)]
+    x = torch.zeros(14, 100, dtype=torch.bfloat16)
+    calls = [
+        (b.adjust, (0, 0, x, x, 2, 1400, 1400, 0)),
+        (b.adjust, (0, 0, x, x, 4, 1400, 1400, 0)),
+        (b.count, (0, 100, i32(2, 100), i32(2, 4), i32(6), None, None, None)),
+        (b.count, (0, 100, i32(2, 100), i32(1, 4), i32(6), None, None, None)),
+        (b.count, (0, 100)),
+        (b.verify, (0, 1, v, i32(8, 4), None, i32(7), None, None, None, 1.0, 0.9, 0, 0, i32(1, 8), i32(1))),
+        (b.verify, (0, 1, v, i32(8, 3), None, i32(7), None, None, None, 1.0, 0.9, 0, 0, i32(1, 8), i32(1))),
+        (b.plan, (0, i32(2), i32(2), i32(2), i32(2, 4), i32(4), i32(1), 16, 8, *outs)),
+        (b.plan, (0, i32(2), i32(2), i32(2), i32(2, 4), i32(4), i32(1), 0, 8, *outs)),
+        (b.plan, (0, i32(2), i32(2), i32(2), i32(2, 4), i32(4), i32(1), 16, 1 << 40, *outs)),
+    ]
+    for f, args in calls:
+        with pytest.raises(ValueError):
+            f(*args)
+    with pytest.raises(TypeError):
+        b.count(0, 100, None, i32(2, 4), i32(6), None, None, None)
+    with pytest.raises(TypeError):
+        b.plan(0, [1, 2], i32(2), i32(2), i32(2, 4), i32(4), i32(1), 16, 8, *outs)
+    with pytest.raises(TypeError):
+        b.plan(0, i32(2), i32(2), i32(2), i32(2, 4), i32(4), i32(1), "16", 8, *outs)
+
+
 def test_entry_points_without_a_device_fail_cleanly():
     import torch
     if torch.cuda.is_available():
