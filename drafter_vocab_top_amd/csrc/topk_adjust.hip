@@ -620,18 +620,20 @@ hipError_t launch_col(const AdjustArgs& a, hipStream_t stream) {
 // scattered reads of the touched rows then spread over the CUs), else four
 // that share a list.  7 columns of 16,384 rows 4.4 us by ones, 7.0 by fours;
 // of 248,046 rows 5.7 and 8.9; 56 columns 17.4 and 16.6, in place 12.1 and 7.3.
+// Lanes of one column have nothing to share: 256 of them 73 and 119 us (of two,
+// 64 lanes 37 and 39, in place 21 and 14).
 template <class DT, int kMode>
 hipError_t launch_col(const AdjustArgs& a, hipStream_t stream) {
     const uint32_t rows = kBlock * DT::kPerVec;
     const uint64_t wgs = (uint64_t)((a.V + rows - 1) / rows) * (a.C > a.lanes ? a.C : a.lanes);
-    return wgs <= 2048 ? launch_col<DT, kMode, 1>(a, stream) : launch_col<DT, kMode, 4>(a, stream);
+    return wgs <= 2048 || a.C < 2 * (uint64_t)a.lanes ? launch_col<DT, kMode, 1>(a, stream) : launch_col<DT, kMode, 4>(a, stream);
 }
 
 template <class DT>
 hipError_t launch_col(const AdjustArgs& a, hipStream_t stream) {
     if (a.x == a.out) return launch_col<DT, kModeInPlace>(a, stream);
     const int e = 16 / DT::kPerVec;
-    if (past_caches(a, e)) return launch_col<DT, kModeOnce, 4>(a, stream);
+    if (past_caches(a, e)) return launch_col<DT, kModeOnce>(a, stream);
     // Short runs cost where the columns do not start on cache lines: a run of
     // 512 bytes then touches five lines for four.  32 columns, histories of
     // 500 and 4,000 tokens: 131,072 rows 5.8 and 6.3 us in short runs, 6.4 and
