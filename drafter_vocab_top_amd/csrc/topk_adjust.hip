@@ -148,13 +148,6 @@ struct TouchedRows {
     uint32_t n;
 };
 
-// An address that can be read in place of an absent array's, so that a read
-// needs no branch (a branch around it would make the next ones wait).
-template <class T>
-__device__ __forceinline__ const T* safe() {
-    return (const T*)(uintptr_t)__builtin_amdgcn_kernarg_segment_ptr();
-}
-
 // What hangs on the lane alone, read at once.
 template <class R, bool kBias>
 struct Lane {
@@ -163,9 +156,9 @@ struct Lane {
     uint32_t word;                    // the history's bits of this thread's 32 places
     __device__ __forceinline__ Lane(const AdjustArgs& a, const R& rows, uint32_t l) {
         const uint32_t tid = threadIdx.x;
-        const int32_t* cs = a.cols.start ? a.cols.start + l : safe<int32_t>();
-        const int32_t* ds = a.draft_parts.start ? a.draft_parts.start + l : safe<int32_t>();
-        const int32_t* bs = kBias ? a.bias_parts.start + l : safe<int32_t>();
+        const int32_t* cs = a.cols.at(l);
+        const int32_t* ds = a.draft_parts.at(l);
+        const int32_t* bs = a.bias_parts.at(l);
         const uint32_t r = rows.row(min_u32(tid, R::WORDS - 1u) * 32u);
         const uint32_t* sp = a.seen ? a.seen + (int64_t)l * a.seen_ld + (min_u32(r, a.V - 1u) >> 5) : safe<uint32_t>();
         const int32_t c0 = cs[0], c1 = cs[1], d0 = ds[0], d1 = ds[1], b0 = bs[0], b1 = bs[1];

@@ -22,11 +22,6 @@ namespace topk {
 
 namespace {
 
-// The prompt's tokens set the flag, the others add one.
-__device__ __forceinline__ int64_t prompt_tokens(const CountArgs& a, uint32_t l) {
-    return a.prompt_len ? (int64_t)a.prompt_len[l] : 0;
-}
-
 __global__ __launch_bounds__(kBlock) void count_add(CountArgs a) {
     const uint32_t i = blockIdx.x * kBlock + threadIdx.x;
     if (i >= a.parts.total) return;
@@ -48,7 +43,8 @@ __global__ __launch_bounds__(kBlock) void count_add(CountArgs a) {
     const uint32_t r = (uint32_t)a.ids[i];
     if (i < b || i >= e || r >= a.V) return;
     uint32_t* word = a.counts + (int64_t)l * a.counts_ld + r;
-    if ((int64_t)(i - b) < prompt_tokens(a, l)) atomicOr(word, 0x80000000u);
+    // the prompt's tokens set the flag, the others add one
+    if (a.prompt_len && (int64_t)(i - b) < (int64_t)a.prompt_len[l]) atomicOr(word, 0x80000000u);
     else atomicAdd(word, 1u);
     atomicOr(a.seen + (int64_t)l * a.seen_ld + (r >> 5), 1u << (r & 31u));
 }
@@ -63,11 +59,14 @@ constexpr uint32_t kOwnRows = 8192;  // rows of a workgroup, at most (32 KB of L
 __global__ __launch_bounds__(kOwnThreads) void count_own(CountArgs a, uint32_t l0, uint32_t tiles_log) {
     __shared__ alignas(16) uint32_t own[kOwnRows];
     const uint32_t l = l0 + blockIdx.y, tid = threadIdx.x, tile = blockIdx.x, tiles_mask = (1u << tiles_log) - 1u;
+    const int32_t* start = a.parts.at(l);
+    const int32_t b0 = start[0], e0 = start[1], fresh0 = *(a.fresh ? a.fresh + l : safe<int32_t>()),
+                  prompt0 = *(a.prompt_len ? a.prompt_len + l : safe<int32_t>());
     uint32_t b, e;
-    a.parts.range(l, b, e);
-    const bool fresh = a.fresh && a.fresh[l] != 0;
+    a.parts.cut(l, b0, e0, b, e);
+    const bool fresh = a.fresh && fresh0 != 0;
     if (!fresh && b == e) return;
-    const int64_t prompt = prompt_tokens(a, l);
+    const int64_t prompt = a.prompt_len ? (int64_t)prompt0 : 0;
     const uint32_t groups = (a.V + 31u) / 32u;
     const uint32_t mine = tile < groups ? ((groups - 1u - tile) >> tiles_log) + 1u : 0u;  // groups of this workgroup
     for (uint32_t i = tid; i < mine * 8u; i += kOwnThreads) reinterpret_cast<u32x4*>(own)[i] = u32x4{0u, 0u, 0u, 0u};

@@ -8,6 +8,13 @@
 
 namespace topk {
 
+// An address that can be read in place of an absent array's, so that a read
+// needs no branch (a branch around it would make the next ones wait).
+template <class T>
+__device__ __forceinline__ const T* safe() {
+    return (const T*)(uintptr_t)__builtin_amdgcn_kernarg_segment_ptr();
+}
+
 // Parts of [0, total): the one of lane l is [start[l], start[l+1]) cut to
 // [0, total), or total / lanes entries each without a start array.
 struct Parts {
@@ -20,9 +27,11 @@ struct Parts {
         end = start ? (e < 0 ? 0u : min_u32((uint32_t)e, total)) : begin + each;
         if (end < begin) end = begin;
     }
+    // where start[l] and start[l + 1] can be read
+    __device__ __forceinline__ const int32_t* at(uint32_t l) const { return start ? start + l : safe<int32_t>(); }
     __device__ __forceinline__ void range(uint32_t l, uint32_t& begin, uint32_t& end) const {
         int32_t b = 0, e = 0;
-        if (start) {
+        if (start) {  // (a uniform branch: the reads stay scalar)
             b = start[l];
             e = start[l + 1];
         }
