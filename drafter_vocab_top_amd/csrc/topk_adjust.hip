@@ -148,6 +148,8 @@ struct TouchedRows {
     uint32_t n;
 };
 
+__device__ __forceinline__ uint32_t scalar(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
+
 // What hangs on the lane alone, read at once.
 template <class R, bool kBias>
 struct Lane {
@@ -171,6 +173,8 @@ struct Lane {
         a.bias_parts.cut(l, b0, b1, bb, be);
         if (!a.drafts) de = db;
         if (ce > cb) de = min_u32(de, db + (ce - cb - 1u));
+        // (equal in all threads, which the compiler cannot know of such reads)
+        cb = scalar(cb), ce = scalar(ce), db = scalar(db), de = scalar(de), bb = scalar(bb), be = scalar(be);
         if (!a.repetition) rep = 1.0f;
         if (!a.presence) pres = 0.0f;
         if (!a.frequency) freq = 0.0f;
