@@ -40,6 +40,14 @@ bool fits(const at::Tensor& t, int64_t numel, int index) {
            t.is_contiguous();
 }
 
+// Values of `size` bytes as the library stores them: bfloat16, float32 or
+// integer patterns (not float16, which has the size of bfloat16).
+bool holds_values(const at::Tensor& t, int64_t size) {
+    const at::ScalarType type = t.scalar_type();
+    const bool known = type == at::kBFloat16 || type == at::kFloat || at::isIntegralType(type, /*includeBool=*/false);
+    return known && t.element_size() == size;
+}
+
 // Address of a contiguous tensor of at least numel elements on GPU index (None: NULL).
 template <class T>
 T* need(PyObject* o, const char* name, int64_t numel, int index, at::ScalarType type = at::kInt) {
@@ -111,7 +119,7 @@ PyObject* adjust(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor &x = tensor(a[2], "x"), &out = tensor(a[3], "out");
         const int64_t size = whole(a[4]);
         const int index = (int)whole(a[7]);
-        if (x.element_size() != size || out.element_size() != size || !fits(x, whole(a[5]), index) ||
+        if (!holds_values(x, size) || !holds_values(out, size) || !fits(x, whole(a[5]), index) ||
             !fits(out, whole(a[6]), index))
             fail("x and out must be contiguous, on the rules' GPU, and hold the matrix described by the rules");
         return g_adjust(reinterpret_cast<const topk_adjust_rules*>((uintptr_t)wrapped(a[1])), x.data_ptr(), out.data_ptr(),
@@ -148,7 +156,7 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (values.dim() != 2 || ids.sizes() != values.sizes() || tokens.dim() != 2 || tokens.size(0) < v.lanes)
             fail("target_values and target_ids must be (C, k), out_tokens a matrix with a row per lane");
         const int64_t size = values.element_size();
-        if ((size != 2 && size != 4) || !fits(values, 0, index))
+        if ((size != 2 && size != 4) || !holds_values(values, size) || !fits(values, 0, index))
             fail("target_values must be a contiguous GPU tensor of bf16 or fp32 (or patterns)");
         v.dtype = size == 2 ? TOPK_BF16 : TOPK_F32;
         v.C = values.size(0);
@@ -158,7 +166,7 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (a[7] != Py_None) {
             const at::Tensor& qv = tensor(a[7], "draft_values");
             if (qv.dim() != 2 || a[8] == Py_None || tensor(a[8], "draft_ids").sizes() != qv.sizes() ||
-                qv.element_size() != size || !fits(qv, 0, index) || qv.size(1) > TOPK_MAX_K)
+                !holds_values(qv, size) || !fits(qv, 0, index) || qv.size(1) > TOPK_MAX_K)
                 fail("draft_values and draft_ids must be contiguous (n, kq) tensors of the target lists' types");
             // drafts past the lists have no distribution to be judged by
             if (qv.size(0) < v.n_drafts) v.n_drafts = qv.size(0);

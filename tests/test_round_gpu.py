@@ -447,6 +447,75 @@ def test_verify(gpu, n, dtype):
         assert np.array_equal(host(cnt), count) and np.array_equal(host(got), want)
 
 
+@pytest.mark.parametrize("dtype", [W.BF16, W.F32])
+def test_verify_with_repeated_ids(gpu, dtype):
+    """Lists in which ids occur several times (rows mapped to the same token):
+    the first entry of an id counts."""
+    torch, T = gpu
+    rng = np.random.default_rng(21)
+    lanes, most, k = 50, 6, 12
+    have = rng.integers(0, most + 1, lanes)
+    cs = np.concatenate([[0], np.cumsum(have + 1)]).astype(np.int32)
+    ds = np.concatenate([[0], np.cumsum(have)]).astype(np.int32)
+    C, D = int(cs[-1]), max(int(ds[-1]), 1)
+    tb, tv, _ = lists(rng, C, k, dtype, 70)
+    qb, qv, _ = lists(rng, D, k, dtype, 70)
+    ti, qi = rng.integers(0, 5, (C, k)).astype(np.int32), rng.integers(0, 6, (D, k)).astype(np.int32)
+    drafts = rng.integers(0, 6, D).astype(np.int32)
+    for sampled in (True, False):
+        args = dict(draft_values=dev(torch, qb), draft_ids=dev(torch, qi)) if sampled else {}
+        got, cnt = T.verify(dev(torch, tb), dev(torch, ti), dev(torch, cs), dev(torch, drafts), dev(torch, ds), top_p=0.9,
+                            seed=-3, offset=1, max_tokens=most + 1, **args)
+        want, count, margin = R.verify(tv, ti, R.parts(cs, C, lanes), drafts, R.parts(ds, D, lanes), qv if sampled else None,
+                                       qi if sampled else None, 1.0, 0.9, 2**64 - 3, 1, most + 1)
+        assert margin > 2.0**-40
+        assert np.array_equal(host(cnt), count) and np.array_equal(host(got), want)
+
+
+def test_binding_refuses_on_the_gpu(gpu):
+    """What the binding and the library refuse when the tensors are on the GPU."""
+    torch, T = gpu
+    i32 = lambda *n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    x = torch.zeros((14, 100), dtype=torch.bfloat16, device="cuda")
+    rules = T.AdjustRules(100, 14, lanes=2)
+    for args in ((x[:13],), (x.float(),), (x, x[:13]), (x, torch.zeros(28, 50, dtype=torch.bfloat16, device="cuda").t()),
+                 (x.cpu(),), (x, x.cpu()), (x.half(),), (x, x.half())):
+        with pytest.raises((ValueError, TypeError)):
+            rules.apply(*args)
+    with pytest.raises(ValueError):
+        T.AdjustRules(100, 14, lanes=2, out_ld=101).apply(x)      # out is needed
+    with pytest.raises(T.TopkError):
+        T.AdjustRules(100, 14, lanes=3).apply(x)                  # lanes do not divide the columns
+    with pytest.raises(T.TopkError):
+        T.AdjustRules(100, 14, lanes=2, counts=i32(2, 100)).apply(x)   # counts without seen
+    with pytest.raises(T.TopkError):
+        T.count_tokens(i32(2, 100), i32(2, 4), 101, i32(6))       # more rows than counts has
+    with pytest.raises(T.TopkError):
+        T.count_tokens(i32(2, 100), i32(2, 4), 100, i32(7))       # lanes do not divide the tokens
+    with pytest.raises(ValueError):
+        T.count_tokens(i32(2, 100), i32(2, 4), 100, i32(6).long())
+    values, ids = torch.zeros((16, 8), device="cuda"), i32(16, 8)
+    with pytest.raises(T.TopkError):
+        T.verify(values, ids, None, i32(14), None, lanes=2, temperature=-1.0)
+    with pytest.raises(ValueError):
+        T.verify(torch.zeros((16, 65), device="cuda"), i32(16, 65), None, i32(14), None, lanes=2)
+    with pytest.raises(ValueError):
+        T.verify(values, ids, None, i32(14), None, draft_values=torch.zeros((14, 8), device="cuda"), lanes=2)
+    with pytest.raises(ValueError):
+        T.verify(values.half(), ids, None, i32(14), None, draft_values=torch.zeros((14, 8), device="cuda"),
+                 draft_ids=i32(14, 8), lanes=2)
+    with pytest.raises(ValueError):
+        T.verify(values.half(), ids, None, i32(14), None, lanes=2)      # float16 is not bfloat16
+    with pytest.raises(ValueError):
+        T.plan(i32(2), i32(2), i32(2), i32(2, 4), i32(4), i32(1), 0, 8)
+    out = T.plan(i32(2), i32(2), i32(2), i32(2, 4), i32(4), i32(1), 16, 8)
+    with pytest.raises(T.TopkError):
+        T.plan(i32(2), i32(2), out["held"], i32(2, 4), i32(4), i32(1), 16, 8, out=out)   # written over its input
+    with pytest.raises(ValueError):
+        T.plan(i32(2), i32(2), i32(2), i32(2, 4), i32(4), i32(1), 16, 9, out=out)        # outputs too short
+    torch.cuda.synchronize()
+
+
 def test_verify_keeps_the_targets_distribution(gpu):
     """The committed first token of many lanes is distributed as the target's
     nucleus, whatever the drafter's list: chi-square over 4 tokens."""
