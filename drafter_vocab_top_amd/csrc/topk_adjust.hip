@@ -438,7 +438,10 @@ __global__ __launch_bounds__(kBlock) void adjust_row_dense(AdjustArgs a, uint32_
     const uint32_t tid = threadIdx.x, V = a.V;
     const uint32_t tile_c = ((tile0 + blockIdx.y) << tx_log) * EPV, tile_n = EPV << tx_log;
     const uint32_t vc = tid & ((1u << tx_log) - 1u);
-    const uint32_t c = tile_c + vc * EPV;
+    // The row's last vector, if it is not whole, moves up: what it shares with
+    // the one before it both write alike.
+    uint32_t c = tile_c + vc * EPV;
+    if (c < a.C && c + EPV > a.C && a.C >= tile_c + EPV) c = a.C - EPV;
     const uint32_t r0 = blockIdx.x * (kBlock >> tx_log) * U + (tid >> tx_log) * U;
     uint32_t words[EPV];
     if constexpr (kMask) {
@@ -469,7 +472,7 @@ __global__ __launch_bounds__(kBlock) void adjust_row_dense(AdjustArgs a, uint32_
         }
         __syncthreads();
 #pragma unroll
-        for (uint32_t e = 0; e < EPV; ++e) mine &= active[vc * EPV + e] ? ~0u : ~(1u << e);
+        for (uint32_t e = 0; e < EPV; ++e) mine &= c < a.C && active[c - tile_c + e] ? ~0u : ~(1u << e);
     }
     if (mine == 0 || r0 >= V) return;
     const uint32_t n = min_u32(U, V - r0);
@@ -496,7 +499,7 @@ __global__ __launch_bounds__(kBlock) void adjust_row_dense(AdjustArgs a, uint32_
         }
         return;
     }
-    // A vector past the row's end, or with columns that are nobody's: read
+    // A vector with columns that are nobody's, or a row of less than one: read
     // whole, where the matrix reaches that far, and written by the element.
     if constexpr (!kInPlace) {
 #pragma unroll
