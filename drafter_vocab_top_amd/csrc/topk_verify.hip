@@ -19,9 +19,9 @@
 //
 // One MI355X, replayed from a graph: one lane of 7 drafts, k = 20, 4.2 us (a
 // launch and the chain starts, lists, exp, sums, test, token); 512 lanes of up
-// to 15 drafts, k = 64, fp32, 10.1 us for 6.2 MB of lists: some 700
-// instructions per column, six columns to a SIMD.  With sums in list order (64
-// dependent additions, three times) and a token for every column it was 27.7.
+// to 15 drafts, k = 64, fp32, 6.7 us for at most 6.2 MB of lists: some 700
+// instructions per column.  With sums in list order (64 dependent additions,
+// three times) and a token for every column it was 27.7.
 #include "topk_draw.hpp"
 #include "topk_round.hpp"
 
@@ -169,11 +169,13 @@ __global__ __launch_bounds__(kWavesPerLane * 64) void verify_kernel(VerifyArgs a
 template <class DT>
 hipError_t launch_dt(const VerifyArgs& a, hipStream_t stream) {
     const dim3 grid((uint32_t)a.v.lanes);
-    // a wave for every column of a lane of average size, up to 16
-    const int64_t columns = (a.v.C + a.v.lanes - 1) / a.v.lanes;
-    if (columns <= 4) hipLaunchKernelGGL((verify_kernel<DT, 4>), grid, dim3(256), 0, stream, a);
-    else if (columns <= 8) hipLaunchKernelGGL((verify_kernel<DT, 8>), grid, dim3(512), 0, stream, a);
-    else hipLaunchKernelGGL((verify_kernel<DT, 16>), grid, dim3(1024), 0, stream, a);
+    // Four waves for up to four columns a lane (2,048 lanes of 4: 9.5 us, with
+    // eight waves 12.4), eight for more (512 lanes of 8: 7.2, with four 7.6).
+    // Sixteen would judge columns that an earlier refusal makes useless (512
+    // lanes of 16: 11.1 against 7.4; both steps are needed only where the first
+    // eight are accepted).
+    if ((a.v.C + a.v.lanes - 1) / a.v.lanes <= 4) hipLaunchKernelGGL((verify_kernel<DT, 4>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((verify_kernel<DT, 8>), grid, dim3(512), 0, stream, a);
     return hipGetLastError();
 }
 
