@@ -212,6 +212,12 @@ def test_adjust_a_matrix_larger_than_the_caches(gpu, layout):
     run_adjust(gpu, case, False)
 
 
+@pytest.mark.parametrize("layout", [W.COL, W.ROW])
+def test_adjust_more_lanes_than_a_grid_is_high(gpu, layout):
+    print(f"[round] adjust, 66,000 lanes {layout}", flush=True)
+    run_adjust(gpu, Case(78, 40, 66000, 1, W.F32, layout, hist=3, bias=1, mask="shared", gap=1), False)
+
+
 @pytest.mark.parametrize("n", [0, 1, 2])
 @pytest.mark.parametrize("layout", [W.COL, W.ROW])
 def test_adjust_columns_on_cache_lines(gpu, layout, n):
@@ -315,6 +321,8 @@ COUNT = [
     (40001, 2, 20000, True, True),
     (131072, 3, 9000, False, True),
     (257, 300, 5, True, True),
+    (35, 66000, 2, True, True),
+    (35, 66000, 2, True, False),
 ]
 
 
@@ -329,8 +337,7 @@ def test_count(gpu, n):
     ids[bad] = rng.choice([-1, V, 2**31 - 1, -2**31], bad.sum())
     counts = np.zeros((lanes, V + 2), np.int32)
     counts[:, V:] = 9
-    for l in range(lanes):
-        counts[l, zipf(rng, 50, V)] = rng.integers(1, 5)
+    counts[np.arange(lanes).repeat(50), zipf(rng, 50 * lanes, V)] = rng.integers(1, 5, 50 * lanes)
     seen = np.zeros((lanes, (V + 31) // 32 + 1), np.uint32)
     seen[:, :-1] = packed(counts[:, :V] != 0)
     if V % 32:
@@ -573,6 +580,7 @@ PLAN = [
     (1025, 9, 90, 8, 9000, 3, 0.9),
     (3000, 4, 40, 1, 9000, 0, 0.97),
     (3, 5000, 9000, 256, 15001, 0, 1.0),
+    (66000, 2, 20, 4, 60000, 0, 0.99),
 ]
 
 
