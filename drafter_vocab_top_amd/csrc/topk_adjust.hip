@@ -183,16 +183,17 @@ struct Lane {
     }
 };
 
-// Fills sh (list and n are valid after the next barrier).  bias0, draft0: the
-// lane's entries bb + thread and db + thread.
+// Fills sh (list and n are valid after the next barrier) with the touched places
+// of the words that are `part` modulo parts (a power of two).  bias0, draft0:
+// the lane's entries bb + thread and db + thread.
 template <class R, bool kBias>
 __device__ __forceinline__ void make_list(const AdjustArgs& a, const R& rows, const Lane<R, kBias>& lane, uint32_t draft0,
-                                          uint32_t bias0, TouchedRows<R::ROWS, kBias>& sh) {
+                                          uint32_t bias0, TouchedRows<R::ROWS, kBias>& sh, uint32_t part = 0, uint32_t parts = 1) {
     constexpr uint32_t kRows = R::ROWS;
     const uint32_t tid = threadIdx.x, ln = tid & 63u;
     if (tid == 0) sh.n = 0;
     if (tid < kRows / 32) {
-        sh.touched[tid] = lane.word;
+        sh.touched[tid] = (tid & (parts - 1u)) == part ? lane.word : 0u;
         sh.drafted[tid] = 0;
     }
     if constexpr (kBias)
@@ -201,14 +202,14 @@ __device__ __forceinline__ void make_list(const AdjustArgs& a, const R& rows, co
     if (a.drafts || kBias) {
         for (uint32_t i = lane.db + tid; i < lane.de; i += kBlock) {
             const uint32_t at = rows.place(i == lane.db + tid ? draft0 : (uint32_t)a.drafts[i], a.V);
-            if (at == kRows) continue;
+            if (at == kRows || (at >> 5 & (parts - 1u)) != part) continue;
             atomicOr(&sh.touched[at >> 5], 1u << (at & 31u));
             atomicOr(&sh.drafted[at >> 5], 1u << (at & 31u));
         }
         if constexpr (kBias) {
             for (uint32_t i = lane.bb + tid; i < lane.be; i += kBlock) {
                 const uint32_t at = rows.place(i == lane.bb + tid ? bias0 : (uint32_t)a.bias_ids[i], a.V);
-                if (at == kRows) continue;
+                if (at == kRows || (at >> 5 & (parts - 1u)) != part) continue;
                 atomicOr(&sh.touched[at >> 5], 1u << (at & 31u));
                 atomicMax(&sh.bias_at[at], i - lane.bb + 1u);
             }
@@ -528,7 +529,9 @@ __global__ __launch_bounds__(kBlock) void adjust_row_dense(AdjustArgs a, uint32_
 
 constexpr uint32_t kSparseRows = 4096;
 
-// Lane l0 + blockIdx.y, its touched rows; 1 << w_log threads share a row.
+// Lane l0 + blockIdx.y, its touched rows, 1 << w_log threads to a row; of the
+// gridDim.z (a power of two) workgroups with the same rows, each takes every
+// gridDim.z-th group of 32.
 template <class DT, bool kBias, bool kMask>
 __global__ __launch_bounds__(kBlock) void adjust_row_sparse(AdjustArgs a, uint32_t l0, uint32_t w_log) {
     using storage = typename DT::storage;
@@ -540,7 +543,7 @@ __global__ __launch_bounds__(kBlock) void adjust_row_sparse(AdjustArgs a, uint32
     if (lane.ce == lane.cb) return;
     uint32_t draft0, bias0;
     first_entries(a, lane, draft0, bias0);
-    make_list(a, rows, lane, draft0, bias0, sh);
+    make_list(a, rows, lane, draft0, bias0, sh, blockIdx.z, gridDim.z);
     __syncthreads();
 
     const LaneRules rules(lane.rep, lane.pres, lane.freq);
@@ -670,8 +673,13 @@ hipError_t launch_row_sparse(const AdjustArgs& a, hipStream_t stream) {
     const uint32_t tiles = (a.V + kSparseRows - 1) / kSparseRows, cols = (a.C + a.lanes - 1) / a.lanes;
     uint32_t w_log = 0;
     while (w_log < 6 && (1u << w_log) < cols) ++w_log;
+    // In few tiles a history may touch nearly all rows; as long as the CUs have
+    // room, several workgroups share them: 41 lanes of 9 columns, 1,532 rows,
+    // in place 37 us by ones, 8.8 by sixteens.
+    uint32_t z = 1;
+    while (z < 16 && tiles * z < 32 && (uint64_t)tiles * a.lanes * z < 1024) z *= 2;
     for (int64_t l0 = 0; l0 < a.lanes; l0 += kGridY) {
-        const dim3 grid(tiles, (uint32_t)(a.lanes - l0 < kGridY ? a.lanes - l0 : kGridY));
+        const dim3 grid(tiles, (uint32_t)(a.lanes - l0 < kGridY ? a.lanes - l0 : kGridY), z);
         hipLaunchKernelGGL((adjust_row_sparse<DT, kBias, kMask>), grid, dim3(kBlock), 0, stream, a, (uint32_t)l0, w_log);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }

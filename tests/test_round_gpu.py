@@ -187,6 +187,8 @@ ADJUST = [
     (30001, 2, 2, dict(penalties=None, mask="column", out_pad=6)),
     (9001, 300, 1, dict(hist=5, mask="shared")),
     (1021, 6, 100, dict(hist=50, drafts=True, bias=9, mask="lane", gap=11)),
+    (1532, 41, 9, dict(hist=6000, bias=20, drafts=True)),      # nearly every row touched
+    (4097, 3, 5, dict(hist=9000, bias=60, mask="column", gap=3)),
 ]
 
 
