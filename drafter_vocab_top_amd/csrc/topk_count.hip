@@ -12,8 +12,8 @@
 //
 // One MI355X, replayed from a graph: 64 lanes of up to 8 tokens 2.9 us, a
 // launch and one chain of reads and atomics; 8 fresh lanes of 25,000 tokens
-// each 10.3 us, about 5 of them the reading of each lane's tokens by all 32
-// workgroups of the lane (L2), 2 their LDS atomics and 2 the 8 MB of rows.
+// each 8.4 us; one of 120,000 tokens 16.4.  Every workgroup of a lane looks
+// at all of its tokens, some 16 instructions each: that bounds it.
 #include "topk_round.hpp"
 
 #include "topk_col_common.hpp"
@@ -66,17 +66,19 @@ __global__ __launch_bounds__(kOwnThreads) void count_own(CountArgs a, uint32_t l
     a.parts.cut(l, b0, e0, b, e);
     const bool fresh = a.fresh && fresh0 != 0;
     if (!fresh && b == e) return;
-    const int64_t prompt = a.prompt_len ? (int64_t)prompt0 : 0;
+    const uint32_t prompt = a.prompt_len && prompt0 > 0 ? (uint32_t)prompt0 : 0u;
     const uint32_t groups = (a.V + 31u) / 32u;
     const uint32_t mine = tile < groups ? ((groups - 1u - tile) >> tiles_log) + 1u : 0u;  // groups of this workgroup
     for (uint32_t i = tid; i < mine * 8u; i += kOwnThreads) reinterpret_cast<u32x4*>(own)[i] = u32x4{0u, 0u, 0u, 0u};
     __syncthreads();
-    constexpr uint32_t U = 4;  // reads of four tokens in flight
+    constexpr uint32_t U = 2;  // reads of four tokens in flight (more are no faster: instructions bound it)
+    // Token i of the lane.  (Every instruction outside the branch is taken by
+    // every workgroup for every token.)
     auto add = [&](uint32_t i, uint32_t r) {
-        const uint32_t g = r >> 5;
-        if (r < a.V && (g & tiles_mask) == tile) {
-            uint32_t* word = &own[(g >> tiles_log) * 32u + (r & 31u)];
-            if ((int64_t)(i - b) < prompt) {
+        if (((r >> 5) & tiles_mask) == tile && r < a.V) {
+            uint32_t* word = &own[(r >> 5 >> tiles_log) * 32u + (r & 31u)];
+            if (i < prompt) {
+                // (a frequent token's flag once: 120,000 equal tokens 59 us, not 104)
                 if (!(*word >> 31)) atomicOr(word, 0x80000000u);
             } else {
                 atomicAdd(word, 1u);
@@ -92,15 +94,13 @@ __global__ __launch_bounds__(kOwnThreads) void count_own(CountArgs a, uint32_t l
         for (uint32_t u = 0; u < U; ++u) {
             const uint32_t q = q0 + u * kOwnThreads;
             if (q >= n4) break;
-            const uint32_t i = b + q * 4u;
-            const uint32_t vx = v[u].x, vy = v[u].y, vz = v[u].z, vw = v[u].w;
-            add(i, vx);
-            add(i + 1u, vy);
-            add(i + 2u, vz);
-            add(i + 3u, vw);
+            add(q * 4u, v[u].x);
+            add(q * 4u + 1u, v[u].y);
+            add(q * 4u + 2u, v[u].z);
+            add(q * 4u + 3u, v[u].w);
         }
     }
-    if (tid < ((e - b) & 3u)) add(b + n4 * 4u + tid, (uint32_t)a.ids[b + n4 * 4u + tid]);
+    if (tid < ((e - b) & 3u)) add(n4 * 4u + tid, (uint32_t)a.ids[b + n4 * 4u + tid]);
     __syncthreads();
     // half a wave per group of 32 rows
     for (uint32_t g = tid >> 5; g < mine; g += kOwnThreads / 32u) {
@@ -124,17 +124,27 @@ __global__ __launch_bounds__(kOwnThreads) void count_own(CountArgs a, uint32_t l
 }  // namespace
 
 hipError_t launch_count(const CountArgs& a, hipStream_t stream) {
-    // Atomics cost by the tokens of a lane that meet in one word, owned rows by
-    // the lane.  Equal (248,046 rows) near 1,024 tokens a lane for 1 lane (4.6
-    // and 5.1 us) and 8 (5.4 and 5.5), near 4,096 for 64 (28.9 and 27.1); 8
-    // tokens of 64 lanes 3.0 and 17.0, 26,000 of 8 lanes 158 and 10.
-    if (!a.fresh && a.parts.total / a.lanes < 1024u + 48u * (uint64_t)a.lanes) {
+    // Atomics cost some 4 ns for each token of a lane and 0.06 more for each
+    // lane; owned rows a start, 4 ns a workgroup and 0.6 us per million rows.
+    // Measured, atomics and owned rows, in us:
+    //   one lane, 1,024 rows        128 tokens 2.8 and 3.1, 512 5.0 and 3.0
+    //   8 lanes, 32,768 rows        128 tokens 3.2 and 3.7, 512 4.6 and 3.8
+    //   64 lanes, 248,046 rows      8 tokens 3.1 and 18.1, 2,048 19.0 and 23.2
+    //   512 lanes, 8,192 rows       128 tokens 6.4 and 7.2, 512 16.9 and 8.2
+    //   65,000 lanes, 1,024 rows    8 tokens 32 and 304, 128 466 and 329
+    const uint64_t lanes = a.lanes, tiles = ((uint64_t)a.V + kOwnRows - 1) / kOwnRows;
+    if (!a.fresh && a.parts.total / lanes * (200u + 3u * lanes) < 35000u + lanes * (200u * tiles + (uint64_t)a.V * 7u / 200u)) {
         if (a.parts.total == 0) return hipSuccess;
         hipLaunchKernelGGL(count_add, dim3((a.parts.total + kBlock - 1) / kBlock), dim3(kBlock), 0, stream, a);
         return hipGetLastError();
     }
     uint32_t tiles_log = 0;
     while (((uint64_t)kOwnRows << tiles_log) < (uint64_t)(a.V + 31u) / 32u * 32u) ++tiles_log;
+    // Few lanes: more workgroups, each with fewer rows to rewrite, as long as every
+    // one has a CU of its own (5 lanes of 3,400 tokens, 30,281 rows: 20
+    // workgroups 7.8 us, 160 4.1, 320 5.0; 248,046 rows, 4,000 tokens: 32
+    // workgroups 6.4, 256 3.7).
+    while (((uint64_t)a.lanes << tiles_log) <= 128 && a.V >> tiles_log > 512u) ++tiles_log;
     for (int64_t l0 = 0; l0 < a.lanes; l0 += kGridY) {
         const dim3 grid(1u << tiles_log, (uint32_t)(a.lanes - l0 < kGridY ? a.lanes - l0 : kGridY));
         hipLaunchKernelGGL(count_own, grid, dim3(kOwnThreads), 0, stream, a, (uint32_t)l0, tiles_log);

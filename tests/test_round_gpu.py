@@ -325,6 +325,10 @@ COUNT = [
     (257, 300, 5, True, True),
     (35, 66000, 2, True, True),
     (35, 66000, 2, True, False),
+    (30281, 5, 3400, True, False),
+    (130001, 1, 4000, True, False),
+    (1183, 13, 600, True, False),
+    (50003, 90, 60, True, False),
 ]
 
 
