@@ -12,12 +12,15 @@
 // forbids), finds the rows that a penalty or bias touches from one bit per row
 // of the history, and rewrites those in every column from the original.
 //
-// Row-interleaved: two kernels.  The dense one streams the matrix: it copies
-// the elements (nothing to copy in place) and writes -Inf where the mask
-// forbids them.  The sparse one rewrites the elements that a penalty or a
-// bias touches: a few thousand of a column's 248,046 rows.  It reads the
-// originals, so it follows the dense one out of place and precedes it in
-// place; forbidden elements it leaves alone.
+// Row-interleaved: a part that streams the matrix (out of place it copies the
+// elements; it writes -Inf where the mask forbids them) and one that rewrites
+// the elements that a penalty or a bias touches: a few thousand of a column's
+// 248,046 rows.  It reads the originals and leaves forbidden elements alone.
+// Out of place it is a second launch.  In place the two write different
+// elements and are one launch: one lane's 8 columns 8.2 us, in two 12.7; 448
+// columns, of whose elements 5 % are forbidden, 57 and 76.  (Forbidden elements
+// are then written alone, not with the vector around them: the same time but
+// where half of 448 columns' are forbidden, 134 and 132.)
 //
 // Reading every count would add 4 bytes per row and lane to the 2 to 8 that an
 // element costs; the bits add an eighth of a byte, and a list of the touched
@@ -430,20 +433,22 @@ constexpr uint32_t kRowTileVecs = 64;  // at most 64 vectors of a row per workgr
 
 // A workgroup takes 1 << tx_log vectors of a row; each thread one of them over U
 // rows, which one word of each column's mask covers, all in flight together.
+// In place only forbidden elements are written, so that others may rewrite the
+// allowed ones meanwhile.
 template <class DT, int kMode, bool kMask, uint32_t U>
-__global__ __launch_bounds__(kBlock) void adjust_row_dense(AdjustArgs a, uint32_t tx_log, uint32_t tile0) {
+__device__ __forceinline__ void row_dense(const AdjustArgs& a, uint32_t tx_log, uint32_t row_tile, uint32_t column_tile,
+                                          uint8_t* active) {
     using storage = typename DT::storage;
     constexpr uint32_t EPV = DT::kPerVec, ALL = (1u << EPV) - 1u;
     constexpr bool kInPlace = kMode == kModeInPlace, kOnce = kMode == kModeOnce;
-    __shared__ uint8_t active[kRowTileVecs * EPV];
     const uint32_t tid = threadIdx.x, V = a.V;
-    const uint32_t tile_c = ((tile0 + blockIdx.y) << tx_log) * EPV, tile_n = EPV << tx_log;
+    const uint32_t tile_c = (column_tile << tx_log) * EPV, tile_n = EPV << tx_log;
     const uint32_t vc = tid & ((1u << tx_log) - 1u);
     // The row's last vector, if it is not whole, moves up: what it shares with
     // the one before it both write alike.
     uint32_t c = tile_c + vc * EPV;
     if (c < a.C && c + EPV > a.C && a.C >= tile_c + EPV) c = a.C - EPV;
-    const uint32_t r0 = blockIdx.x * (kBlock >> tx_log) * U + (tid >> tx_log) * U;
+    const uint32_t r0 = row_tile * (kBlock >> tx_log) * U + (tid >> tx_log) * U;
     uint32_t words[EPV];
     if constexpr (kMask) {
         int64_t mi[EPV];
@@ -487,34 +492,42 @@ __global__ __launch_bounds__(kBlock) void adjust_row_dense(AdjustArgs a, uint32_
         return m;
     };
     u32x4 d[U];
+    if constexpr (kInPlace) {
+#pragma unroll
+        for (uint32_t u = 0; u < U; ++u) {
+            const uint32_t no = ~allowed(u) & mine;
+            if (u >= n) break;
+            if (no == ALL) {
+                store16<false>(out + (int64_t)u * a.out_ld, masked<DT>(u32x4{0u, 0u, 0u, 0u}, 0u));
+                continue;
+            }
+#pragma unroll
+            for (uint32_t e = 0; e < EPV; ++e)
+                if (no >> e & 1u) out[(int64_t)u * a.out_ld + e] = (storage)kMinusInf<DT>;
+        }
+        return;
+    }
     if (mine == ALL) {
 #pragma unroll
-        for (uint32_t u = 0; u < U; ++u) {
-            if (!kInPlace) d[u] = load16<kOnce>(x + (int64_t)min_u32(u, n - 1u) * a.ld);
-            else if (const uint32_t m = allowed(u); u < n && m != ALL && m) d[u] = load16<false>(x + (int64_t)u * a.ld);
-        }
+        for (uint32_t u = 0; u < U; ++u) d[u] = load16<kOnce>(x + (int64_t)min_u32(u, n - 1u) * a.ld);
 #pragma unroll
-        for (uint32_t u = 0; u < U; ++u) {
-            const uint32_t m = allowed(u);
-            if (u < n && (!kInPlace || m != ALL)) store16<kOnce>(out + (int64_t)u * a.out_ld, kMask ? masked<DT>(d[u], m) : d[u]);
-        }
+        for (uint32_t u = 0; u < U; ++u)
+            if (u < n) store16<kOnce>(out + (int64_t)u * a.out_ld, kMask ? masked<DT>(d[u], allowed(u)) : d[u]);
         return;
     }
     // A vector with columns that are nobody's, or a row of less than one: read
     // whole, where the matrix reaches that far, and written by the element.
-    if constexpr (!kInPlace) {
 #pragma unroll
-        for (uint32_t u = 0; u < U; ++u) {
-            const uint32_t r = min_u32(u, n - 1u);
-            if ((int64_t)(V - 1u - (r0 + r)) * a.ld + a.C >= (int64_t)c + EPV) {
-                d[u] = load16<false>(x + (int64_t)r * a.ld);
-            } else {
-                storage v[EPV] = {};
+    for (uint32_t u = 0; u < U; ++u) {
+        const uint32_t r = min_u32(u, n - 1u);
+        if ((int64_t)(V - 1u - (r0 + r)) * a.ld + a.C >= (int64_t)c + EPV) {
+            d[u] = load16<false>(x + (int64_t)r * a.ld);
+        } else {
+            storage v[EPV] = {};
 #pragma unroll
-                for (uint32_t e = 0; e < EPV; ++e)
-                    if (mine >> e & 1u) v[e] = x[(int64_t)r * a.ld + e];
-                __builtin_memcpy(&d[u], v, 16);
-            }
+            for (uint32_t e = 0; e < EPV; ++e)
+                if (mine >> e & 1u) v[e] = x[(int64_t)r * a.ld + e];
+            __builtin_memcpy(&d[u], v, 16);
         }
     }
 #pragma unroll
@@ -522,28 +535,34 @@ __global__ __launch_bounds__(kBlock) void adjust_row_dense(AdjustArgs a, uint32_
         const uint32_t m = allowed(u);
 #pragma unroll
         for (uint32_t e = 0; e < EPV; ++e)
-            if (u < n && (mine >> e & 1u) && (!kInPlace || !(m >> e & 1u)))
-                out[(int64_t)u * a.out_ld + e] = !kInPlace && (m >> e & 1u) ? (storage)vec_elem<DT>(d[u], (int)e) : (storage)kMinusInf<DT>;
+            if (u < n && (mine >> e & 1u))
+                out[(int64_t)u * a.out_ld + e] = m >> e & 1u ? (storage)vec_elem<DT>(d[u], (int)e) : (storage)kMinusInf<DT>;
     }
+}
+
+template <class DT, int kMode, bool kMask, uint32_t U>
+__global__ __launch_bounds__(kBlock) void adjust_row_dense(AdjustArgs a, uint32_t tx_log, uint32_t tile0) {
+    __shared__ uint8_t active[kRowTileVecs * DT::kPerVec];
+    row_dense<DT, kMode, kMask, U>(a, tx_log, blockIdx.x, tile0 + blockIdx.y, active);
 }
 
 constexpr uint32_t kSparseRows = 4096;
 
-// Lane l0 + blockIdx.y, its touched rows, 1 << w_log threads to a row; of the
-// gridDim.z (a power of two) workgroups with the same rows, each takes every
-// gridDim.z-th group of 32.
+// Lane l, its touched rows in tile `tile` of `tiles`, 1 << w_log threads to a
+// row; of the parts (a power of two) workgroups with the same rows, each takes
+// every parts-th group of 32.
 template <class DT, bool kBias, bool kMask>
-__global__ __launch_bounds__(kBlock) void adjust_row_sparse(AdjustArgs a, uint32_t l0, uint32_t w_log) {
+__device__ __forceinline__ void row_sparse(const AdjustArgs& a, uint32_t tile, uint32_t tiles, uint32_t l, uint32_t part, uint32_t parts,
+                                           uint32_t w_log, TouchedRows<kSparseRows, kBias>& sh) {
     using storage = typename DT::storage;
-    __shared__ TouchedRows<kSparseRows, kBias> sh;
-    const uint32_t l = l0 + blockIdx.y, tid = threadIdx.x;
+    const uint32_t tid = threadIdx.x;
     using R = Rows<kSparseRows, 256>;
-    const R rows{gridDim.x, blockIdx.x};
+    const R rows{tiles, tile};
     const Lane<R, kBias> lane(a, rows, l);
     if (lane.ce == lane.cb) return;
     uint32_t draft0, bias0;
     first_entries(a, lane, draft0, bias0);
-    make_list(a, rows, lane, draft0, bias0, sh, blockIdx.z, gridDim.z);
+    make_list(a, rows, lane, draft0, bias0, sh, part, parts);
     __syncthreads();
 
     const LaneRules rules(lane.rep, lane.pres, lane.freq);
@@ -589,9 +608,34 @@ __global__ __launch_bounds__(kBlock) void adjust_row_sparse(AdjustArgs a, uint32
     }
 }
 
+template <class DT, bool kBias, bool kMask>
+__global__ __launch_bounds__(kBlock) void adjust_row_sparse(AdjustArgs a, uint32_t l0, uint32_t w_log) {
+    __shared__ TouchedRows<kSparseRows, kBias> sh;
+    row_sparse<DT, kBias, kMask>(a, blockIdx.x, gridDim.x, l0 + blockIdx.y, blockIdx.z, gridDim.z, w_log, sh);
+}
+
+// In place, with masks: the two write different elements, so one launch does
+// both.  The first n_sparse workgroups take the touched rows from lane l0 on,
+// `parts` to each of a lane's `tiles`, the others the masks, a column tile after
+// the other.
+template <class DT, bool kBias, uint32_t U>
+__global__ __launch_bounds__(kBlock) void adjust_row_in_place(AdjustArgs a, uint32_t l0, uint32_t n_sparse, uint32_t tiles, uint32_t parts,
+                                                              uint32_t w_log, uint32_t row_tiles, uint32_t tx_log) {
+    __shared__ TouchedRows<kSparseRows, kBias> sh;
+    __shared__ uint8_t active[kRowTileVecs * DT::kPerVec];
+    if (blockIdx.x < n_sparse) {
+        const uint32_t p = blockIdx.x / tiles, l = p / parts;
+        row_sparse<DT, kBias, true>(a, blockIdx.x - p * tiles, tiles, l0 + l, p - l * parts, parts, w_log, sh);
+    } else {
+        const uint32_t i = blockIdx.x - n_sparse, t = i / row_tiles;
+        row_dense<DT, kModeInPlace, true, U>(a, tx_log, i - t * row_tiles, t, active);
+    }
+}
+
 // ----------------------------------------------------------------- launch ---
 
 constexpr int64_t kRowVecs = 1 << 20;
+constexpr int64_t kInPlaceWgs = 1 << 22;  // a grid has at most 2^32 threads
 
 // A matrix that, read and written, exceeds the 256 MB Infinity Cache goes past
 // the caches: 448 columns of 248,046 bf16 rows 102 to 96 us (column-contiguous)
@@ -645,45 +689,74 @@ hipError_t launch_col(const AdjustArgs& a, hipStream_t stream) {
     return lines ? launch_col<DT, kModeShort>(a, stream) : launch_col<DT, kModeLong>(a, stream);
 }
 
-template <class DT, int kMode, bool kMask, uint32_t U>
-hipError_t launch_row_dense(const AdjustArgs& a, uint32_t vecs, uint32_t tx_log, hipStream_t stream) {
-    const uint32_t rows = (kBlock >> tx_log) * U;
-    const uint32_t col_tiles = (vecs + (1u << tx_log) - 1) >> tx_log;
-    for (uint32_t t = 0; t < col_tiles; t += (uint32_t)kGridY) {
-        const dim3 grid((a.V + rows - 1) / rows, min(col_tiles - t, (uint32_t)kGridY));
-        hipLaunchKernelGGL((adjust_row_dense<DT, kMode, kMask, U>), grid, dim3(kBlock), 0, stream, a, tx_log, t);
-        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+// How the row kernels cut the work.
+template <class DT>
+struct RowCut {
+    uint32_t vecs, tx_log = 0, rows;          // masks and copies: vectors of a row, of a workgroup, rows of a thread
+    uint32_t tiles, parts = 1, w_log = 0;     // touched rows
+    explicit RowCut(const AdjustArgs& a) {
+        vecs = (a.C + DT::kPerVec - 1) / DT::kPerVec;
+        while ((1u << tx_log) < vecs && (1u << tx_log) < kRowTileVecs) ++tx_log;
+        // Without penalties: 8 columns of 248,046 rows 7.3 us in fours, 10.3 in
+        // sixteens; 56 columns 17.8 and 15.7; 448 columns 120 and 92.
+        rows = (int64_t)a.V * vecs >= kRowVecs ? 16 : 4;
+        tiles = (a.V + kSparseRows - 1) / kSparseRows;
+        const uint32_t cols = (a.C + a.lanes - 1) / a.lanes;
+        while (w_log < 6 && (1u << w_log) < cols) ++w_log;
+        // In few tiles a history may touch nearly all rows; as long as the CUs have
+        // room, several workgroups share them: 41 lanes of 9 columns, 1,532 rows,
+        // in place 37 us by ones, 8.8 by sixteens.
+        while (parts < 16 && tiles * parts < 32 && (uint64_t)tiles * a.lanes * parts < 1024) parts *= 2;
     }
-    return hipSuccess;
-}
+    uint32_t row_tiles(const AdjustArgs& a) const {
+        const uint32_t n = (kBlock >> tx_log) * rows;
+        return (a.V + n - 1) / n;
+    }
+    uint32_t col_tiles() const { return (vecs + (1u << tx_log) - 1) >> tx_log; }
+};
 
 template <class DT, int kMode, bool kMask>
 hipError_t launch_row_dense(const AdjustArgs& a, hipStream_t stream) {
-    const uint32_t vecs = (a.C + DT::kPerVec - 1) / DT::kPerVec;
-    uint32_t tx_log = 0;
-    while ((1u << tx_log) < vecs && (1u << tx_log) < kRowTileVecs) ++tx_log;
-    // Rows of a thread, without penalties: 8 columns of 248,046 rows 7.3 us in
-    // fours, 10.3 in sixteens; 56 columns 17.8 and 15.7; 448 columns 120 and 92.
-    return (int64_t)a.V * vecs >= kRowVecs ? launch_row_dense<DT, kMode, kMask, 16>(a, vecs, tx_log, stream)
-                                           : launch_row_dense<DT, kMode, kMask, 4>(a, vecs, tx_log, stream);
+    const RowCut<DT> cut(a);
+    for (uint32_t t = 0; t < cut.col_tiles(); t += (uint32_t)kGridY) {
+        const dim3 grid(cut.row_tiles(a), min(cut.col_tiles() - t, (uint32_t)kGridY));
+        if (cut.rows == 16) hipLaunchKernelGGL((adjust_row_dense<DT, kMode, kMask, 16>), grid, dim3(kBlock), 0, stream, a, cut.tx_log, t);
+        else hipLaunchKernelGGL((adjust_row_dense<DT, kMode, kMask, 4>), grid, dim3(kBlock), 0, stream, a, cut.tx_log, t);
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 template <class DT, bool kBias, bool kMask>
 hipError_t launch_row_sparse(const AdjustArgs& a, hipStream_t stream) {
-    const uint32_t tiles = (a.V + kSparseRows - 1) / kSparseRows, cols = (a.C + a.lanes - 1) / a.lanes;
-    uint32_t w_log = 0;
-    while (w_log < 6 && (1u << w_log) < cols) ++w_log;
-    // In few tiles a history may touch nearly all rows; as long as the CUs have
-    // room, several workgroups share them: 41 lanes of 9 columns, 1,532 rows,
-    // in place 37 us by ones, 8.8 by sixteens.
-    uint32_t z = 1;
-    while (z < 16 && tiles * z < 32 && (uint64_t)tiles * a.lanes * z < 1024) z *= 2;
+    const RowCut<DT> cut(a);
     for (int64_t l0 = 0; l0 < a.lanes; l0 += kGridY) {
-        const dim3 grid(tiles, (uint32_t)(a.lanes - l0 < kGridY ? a.lanes - l0 : kGridY), z);
-        hipLaunchKernelGGL((adjust_row_sparse<DT, kBias, kMask>), grid, dim3(kBlock), 0, stream, a, (uint32_t)l0, w_log);
+        const dim3 grid(cut.tiles, (uint32_t)(a.lanes - l0 < kGridY ? a.lanes - l0 : kGridY), cut.parts);
+        hipLaunchKernelGGL((adjust_row_sparse<DT, kBias, kMask>), grid, dim3(kBlock), 0, stream, a, (uint32_t)l0, cut.w_log);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
     return hipSuccess;
+}
+
+template <class DT, bool kBias, uint32_t U>
+hipError_t launch_row_in_place(const AdjustArgs& a, const RowCut<DT>& cut, bool sparse, hipStream_t stream) {
+    // the masks with the first of the lanes (all of them, unless those are very many)
+    const int64_t each = (int64_t)cut.tiles * cut.parts, most = each < kInPlaceWgs ? kInPlaceWgs / each : 1;
+    for (int64_t l0 = 0; l0 < (sparse ? (int64_t)a.lanes : 1); l0 += most) {
+        const uint32_t n = sparse ? (uint32_t)(each * (a.lanes - l0 < most ? a.lanes - l0 : most)) : 0u;
+        const uint32_t masks = l0 == 0 ? cut.row_tiles(a) * cut.col_tiles() : 0u;
+        hipLaunchKernelGGL((adjust_row_in_place<DT, kBias, U>), dim3(n + masks), dim3(kBlock), 0, stream, a, (uint32_t)l0, n, cut.tiles,
+                           cut.parts, cut.w_log, cut.row_tiles(a), cut.tx_log);
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+template <class DT, bool kBias>
+hipError_t launch_row_in_place(const AdjustArgs& a, bool sparse, hipStream_t stream) {
+    const RowCut<DT> cut(a);
+    return cut.rows == 16 ? launch_row_in_place<DT, kBias, 16>(a, cut, sparse, stream)
+                          : launch_row_in_place<DT, kBias, 4>(a, cut, sparse, stream);
 }
 
 template <class DT>
@@ -703,14 +776,13 @@ hipError_t launch_dt(int layout, const AdjustArgs& a, hipStream_t stream) {
     const bool in_place = a.x == a.out;
     if (in_place && !sparse && !a.mask) return hipSuccess;
     if (layout == TOPK_COL_CONTIG) return launch_col<DT>(a, stream);
+    if (in_place && a.mask) return a.bias_ids ? launch_row_in_place<DT, true>(a, sparse, stream) : launch_row_in_place<DT, false>(a, sparse, stream);
     if (!in_place)
         if (const hipError_t e = past_caches(a, 16 / DT::kPerVec) ? launch_row_copy<DT, kModeOnce>(a, stream)
                                                                   : launch_row_copy<DT, kModeLong>(a, stream);
             e != hipSuccess)
             return e;
-    if (sparse)
-        if (const hipError_t e = launch_row_sparse<DT>(a, stream); e != hipSuccess) return e;
-    return in_place && a.mask ? launch_row_dense<DT, kModeInPlace, true>(a, stream) : hipSuccess;
+    return sparse ? launch_row_sparse<DT>(a, stream) : hipSuccess;
 }
 
 }  // namespace

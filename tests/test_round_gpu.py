@@ -311,6 +311,34 @@ def test_adjust_at_the_largest_values(gpu):
     assert (y[4:] == x[0, 4:]).all()
 
 
+def test_adjust_in_place_more_lanes_than_a_launch_takes(gpu):
+    """2^20 lanes of five tiles of rows each; three of them own a column."""
+    torch, T = gpu
+    V, lanes, C = 16411, 1 << 20, 3
+    owners = [0, 838865, lanes - 1]
+    rng = np.random.default_rng(61)
+    col_start, bias_start = np.zeros(lanes + 1, np.int32), np.zeros(lanes + 1, np.int32)
+    for l in owners:
+        col_start[l + 1:] += 1
+        bias_start[l + 1:] += 4
+    x = rng.integers(-99, 99, (V, C)).astype(np.float32)
+    ids = np.stack([rng.choice(V, 4, False) for _ in owners]).astype(np.int32)
+    values = rng.integers(1, 9, ids.shape).astype(np.float32)
+    allowed = rng.random((C, V)) < 0.7
+    expect = x.copy()
+    for c in range(C):
+        expect[ids[c], c] += values[c]  # small whole numbers: exact
+    expect[~allowed.T] = -np.inf
+    print(f"[round] adjust in place, lanes={lanes}", flush=True)
+    r = T.AdjustRules(V, C, "f32", "row", lanes=lanes, col_start=dev(torch, col_start), bias_start=dev(torch, bias_start),
+                      bias_ids=dev(torch, ids.ravel()), bias_values=dev(torch, values.ravel()),
+                      mask=dev(torch, packed(allowed).view(np.int32)))
+    t = dev(torch, x)
+    r.apply(t, t)
+    torch.cuda.synchronize()
+    assert np.array_equal(host(t), expect)
+
+
 # ------------------------------------------------------------------ count ---
 
 COUNT = [
