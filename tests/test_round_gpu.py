@@ -214,6 +214,13 @@ def test_adjust_a_matrix_larger_than_the_caches(gpu, layout):
     run_adjust(gpu, case, False)
 
 
+@pytest.mark.parametrize("ragged", [True, False])
+def test_adjust_in_place_by_few_workgroups(gpu, ragged):
+    """Columns in place that share one list of touched rows, several after each other."""
+    print(f"[round] adjust, 150 lanes of 13 columns in place, ragged={ragged}", flush=True)
+    run_adjust(gpu, Case(79, 4097, 150, 13, W.F32, W.COL, hist=40, drafts=True, bias=4, ragged=ragged, empty=0.02), True)
+
+
 @pytest.mark.parametrize("layout", [W.COL, W.ROW])
 def test_adjust_more_lanes_than_a_grid_is_high(gpu, layout):
     print(f"[round] adjust, 66,000 lanes {layout}", flush=True)
