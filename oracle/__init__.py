@@ -75,6 +75,10 @@ def topk_cols(x, V, C, k, dtype, layout, ld, nthreads=1, lib=None):
     need = (C - 1) * ld + V if layout == COL_CONTIG else (V - 1) * ld + C
     if x.size < need:
         raise ValueError(f"x holds {x.size} elements, the layout needs {need}")
+    if lib is not None:
+        # a planted mistake may read elsewhere in the matrix (rows and columns
+        # exchanged): the elements it can reach are there, and zero
+        x = np.concatenate([x.reshape(-1), np.zeros(max(max(V, C) * ld - x.size, 0), x.dtype)])
     values = np.empty((C, k), dtype=x.dtype)
     ids = np.empty((C, k), dtype=np.int32)
     rc = (lib or _load()).oracle_topk_cols(V, C, k, dtype, layout, ld, x.ctypes.data,

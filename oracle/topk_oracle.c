@@ -103,7 +103,8 @@ static int64_t element_index(const oracle_job *j, int64_t r, int64_t c) {
 
 static void *run_columns(void *arg) {
     oracle_job *j = (oracle_job *)arg;
-    oracle_pair *pairs = (oracle_pair *)malloc((size_t)j->V * sizeof(oracle_pair));
+    /* zeroed: a build with a planted mistake may leave a pair unset */
+    oracle_pair *pairs = (oracle_pair *)calloc((size_t)j->V, sizeof(oracle_pair));
     if (!pairs) {
         j->failed = 1;
         return NULL;
