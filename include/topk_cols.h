@@ -228,9 +228,10 @@ int topk_cols_sample(const void *values, const int32_t *ids, int64_t C, int32_t 
  * All of them are asynchronous on the stream, take no handle, allocate
  * nothing, keep nothing between calls and may be captured and replayed.
  * Buffers belong to the caller.  Index arrays are read on the device and
- * cannot be checked by the call: offsets outside their array are cut to it,
- * ids outside [0, V) are ignored, and lanes must not overlap.  The argument
- * structures are read before the call returns.
+ * cannot be checked by the call: offsets outside their array are cut to it, a
+ * lane that ends before it starts is empty, ids outside [0, V) are ignored, and
+ * lanes must not overlap.  The argument structures are read before the call
+ * returns.
  */
 
 /* Most lanes of a call of these entry points (each of them looks at every
