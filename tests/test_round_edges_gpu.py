@@ -3,7 +3,8 @@ import numpy as np
 import pytest
 
 import round_reference as R
-from test_round_gpu import dev, host, zipf
+from drafter_vocab_top_amd import workloads as W
+from test_round_gpu import dev, host, packed, zipf
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +61,65 @@ def test_count_starts_of_many_lanes(gpu, lanes, order):
     T.count_tokens(counts, seen, V, dev(torch, ids), dev(torch, start), prompt_len=dev(torch, prompt))
     c, s = R.count(np.zeros((lanes, V), np.int32), np.zeros((lanes, 10), np.uint32), V, ids, start, prompt)
     assert np.array_equal(host(counts).view(np.uint32), c) and np.array_equal(host(seen).view(np.uint32), s)
+
+
+# ----------------------------------------------------------------- adjust ---
+
+def to_storage(y, dtype):
+    """binary64 values rounded to binary32 and, for bf16, from there to bf16."""
+    f = y.astype(np.float32)
+    return W.bf16_bits_from_f32(f) if dtype == W.BF16 else f.view(np.uint32)
+
+
+@pytest.mark.parametrize("layout", [W.COL, W.ROW])
+@pytest.mark.parametrize("dtype", [W.BF16, W.F32])
+def test_adjust_divides(gpu, dtype, layout):
+    """x / repetition is a division: where a penalty cancels the quotient,
+    what is left is zero, not the error of a reciprocal."""
+    torch, T = gpu
+    V, lanes = 70, 128
+    rng = np.random.default_rng(8)
+    rep = (1 + np.arange(lanes) / 128).astype(np.float32) if dtype == W.BF16 else (1 + rng.random(lanes)).astype(np.float32)
+    assert ((1.0 / rep.astype(np.float64)) * rep != 1.0).any()
+    times = np.tile(np.float64([1, 2, 4, 0.5, -1]), V // 5)
+    x = to_storage(rep[:, None] * times, dtype)
+    assert np.array_equal(R.widen(x, dtype), rep[:, None] * times)  # stored exactly
+    ones = np.ones((lanes, V), np.int32)
+    r = T.AdjustRules(V, lanes, dtype, layout, lanes=lanes, counts=dev(torch, ones), seen=dev(torch, packed(ones != 0)),
+                      repetition=dev(torch, rep), presence=dev(torch, np.ones(lanes, np.float32)))
+    y = rep.astype(np.float64)[:, None] * np.where(times > 0, 0, times * rep[:, None]) + np.where(times > 0, times, 0) - 1.0
+    m = x if layout == W.COL else np.ascontiguousarray(x.T)
+    got = host(r.apply(dev(torch, m)), dtype)
+    got = got if layout == W.COL else np.ascontiguousarray(got.T)
+    assert (got[:, 0::5] == 0).all()
+    assert np.array_equal(got, to_storage(y, dtype))
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("layout", [W.COL, W.ROW])
+@pytest.mark.parametrize("dtype", [W.BF16, W.F32])
+def test_adjust_rounds_as_written(gpu, dtype, layout, in_place):
+    """The chain in binary64, operation by operation, and one rounding: the
+    result is that of the formula bit for bit, for counts up to 2^31 - 1."""
+    torch, T = gpu
+    V, lanes = 3001, 5
+    rng = np.random.default_rng(18)
+    x = to_storage(rng.standard_normal((lanes, V)) * 4, dtype)
+    n = np.minimum(2.0 ** rng.uniform(0, 31, (lanes, V)), 2**31 - 1).astype(np.int64) * (rng.random((lanes, V)) < 0.8)
+    prompt = rng.random((lanes, V)) < 0.3
+    words = n.astype(np.uint32) | np.where(prompt, R.FLAG, np.uint32(0))
+    rep, pres, freq = ((0.4 + rng.random(lanes) * 2).astype(np.float32) for _ in range(3))
+    freq[2:] *= np.float32(2.0**-20)
+    bias = (rng.standard_normal((lanes, V)) * 3).astype(np.float32)
+    r = T.AdjustRules(V, lanes, dtype, layout, lanes=lanes, counts=dev(torch, words.view(np.int32)),
+                      seen=dev(torch, packed(words != 0)), repetition=dev(torch, rep), presence=dev(torch, pres),
+                      frequency=dev(torch, freq), bias_start=dev(torch, np.arange(lanes + 1, dtype=np.int32) * V),
+                      bias_ids=dev(torch, np.tile(np.arange(V, dtype=np.int32), lanes)), bias_values=dev(torch, bias.ravel()))
+    rep, pres, freq = (v.astype(np.float64)[:, None] for v in (rep, pres, freq))
+    y = R.widen(x, dtype)
+    y = np.where(words != 0, np.where(y > 0, y / rep, y * rep), y)
+    y = np.where(n > 0, y - (freq * n + pres), y) + bias
+    m = dev(torch, x if layout == W.COL else np.ascontiguousarray(x.T))
+    got = host(r.apply(m, m if in_place else None), dtype)
+    got = got if layout == W.COL else np.ascontiguousarray(got.T)
+    assert np.array_equal(got, to_storage(y, dtype))
