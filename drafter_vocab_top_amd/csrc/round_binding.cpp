@@ -168,8 +168,12 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
             if (qv.dim() != 2 || a[8] == Py_None || tensor(a[8], "draft_ids").sizes() != qv.sizes() ||
                 !holds_values(qv, size) || !fits(qv, 0, index) || qv.size(1) > TOPK_MAX_K)
                 fail("draft_values and draft_ids must be contiguous (n, kq) tensors of the target lists' types");
-            // drafts past the lists have no distribution to be judged by
-            if (qv.size(0) < v.n_drafts) v.n_drafts = qv.size(0);
+            if (qv.size(0) < v.n_drafts) {
+                // drafts past the lists have no distribution to be judged by; split evenly, the drafts that have
+                // one would be other lanes' than the rest
+                if (a[6] == Py_None) fail("without draft_start, every draft needs a list");
+                v.n_drafts = qv.size(0);
+            }
             if (v.n_drafts) {
                 v.kq = (int32_t)qv.size(1);
                 v.draft_values = qv.data_ptr();

@@ -485,7 +485,9 @@ def verify(target_values, target_ids, col_start, drafts, draft_start, draft_valu
         than its drafts).
     drafts: packed token ids, lane l's at draft_start[l]..draft_start[l+1]-1.
     draft_values, draft_ids: (n, kq), the lists the drafts were sampled from;
-        without them drafts count as certain (greedy drafts).
+        without them drafts count as certain (greedy drafts).  Drafts past the
+        n lists are not judged (the padding of a buffer); without draft_start
+        there must be a list for every draft.
     temperature 0 verifies greedily.  col_start and draft_start None: the same
         number for each of `lanes` lanes.
     Returns (tokens, count): lane l commits tokens[l, :count[l]], the accepted

@@ -123,3 +123,25 @@ def test_adjust_rounds_as_written(gpu, dtype, layout, in_place):
     got = host(r.apply(m, m if in_place else None), dtype)
     got = got if layout == W.COL else np.ascontiguousarray(got.T)
     assert np.array_equal(got, to_storage(y, dtype))
+
+
+# ----------------------------------------------------------------- verify ---
+
+def test_verify_refuses_lists_it_would_misplace(gpu):
+    """Without draft_start the drafts are split evenly, and so are their
+    lists: fewer lists than drafts belong to no lane in particular.  With
+    draft_start, drafts past the lists are not judged."""
+    torch, T = gpu
+    i32 = lambda *n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    values, ids = torch.zeros((16, 8), device="cuda"), i32(16, 8)
+    for n in (12, 13, 0):
+        with pytest.raises(ValueError, match="draft_start"):
+            T.verify(values, ids, None, i32(14), None, torch.zeros((n, 8), device="cuda"), i32(n, 8), lanes=2, max_tokens=8)
+    # more lists than drafts: the rest is unused
+    tokens, count = T.verify(values, ids, None, i32(14), None, torch.zeros((20, 8), device="cuda"), i32(20, 8), lanes=2,
+                             max_tokens=8)
+    assert count.tolist() == [8, 8]
+    start = dev(torch, np.int32([0, 7, 14]))
+    tokens, count = T.verify(values, ids, None, i32(14), start, torch.zeros((12, 8), device="cuda"), i32(12, 8), lanes=2,
+                             max_tokens=8)
+    assert count.tolist() == [8, 6]
