@@ -163,6 +163,7 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (values.size(1) > TOPK_MAX_K) fail("lists must have at most 64 entries");
         v.k = (int32_t)values.size(1);
         v.n_drafts = drafts.numel();
+        if (a[7] == Py_None && a[8] != Py_None) fail("draft_ids without draft_values");
         if (a[7] != Py_None) {
             const at::Tensor& qv = tensor(a[7], "draft_values");
             if (qv.dim() != 2 || a[8] == Py_None || tensor(a[8], "draft_ids").sizes() != qv.sizes() ||

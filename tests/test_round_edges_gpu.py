@@ -145,3 +145,11 @@ def test_verify_refuses_lists_it_would_misplace(gpu):
     tokens, count = T.verify(values, ids, None, i32(14), start, torch.zeros((12, 8), device="cuda"), i32(12, 8), lanes=2,
                              max_tokens=8)
     assert count.tolist() == [8, 6]
+
+
+def test_verify_refuses_half_a_list(gpu):
+    torch, T = gpu
+    i32 = lambda *n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    values, ids = torch.zeros((16, 8), device="cuda"), i32(16, 8)
+    with pytest.raises(ValueError, match="draft_ids"):
+        T.verify(values, ids, None, i32(14), None, draft_ids=i32(14, 8), lanes=2, max_tokens=8)
