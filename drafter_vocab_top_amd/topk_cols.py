@@ -416,6 +416,8 @@ class AdjustRules:
             if t is not None and (t.dim() != 2 or t.shape[1] < least or (name != "mask" and t.shape[0] < lanes)):
                 raise ValueError(f"{name} must be a matrix with rows of at least {least} entries"
                                  + ("" if name == "mask" else " for every lane"))
+        if mask is not None and mask.shape[0] == 0:  # (its address is NULL, which means no mask)
+            raise ValueError("mask must have at least one row")
         if (bias_ids is None) != (bias_values is None) or \
                 (bias_ids is not None and bias_ids.numel() != bias_values.numel()):
             raise ValueError("bias_ids and bias_values must have the same length")
