@@ -9,6 +9,11 @@ and the stream.
     values, ids = h.run(x)            # x: torch tensor on the GPU
     h.close()
 
+Calls are enqueued on the current stream unless they are given one (stream=).
+Outputs that a call allocates then belong to that stream, as if it were the
+current one; what is passed in has to be ready there, and kept until the
+call is done.
+
 Loading fails loudly when the library is missing or cannot be loaded.  There
 is no fallback path.  (The calls around the top-k go through a compiled
 module, _round_binding, that reads their many tensors faster than Python does.)
@@ -132,6 +137,16 @@ def _torch_dtype(dtype: str):
     return torch.bfloat16 if dtype == "bf16" else torch.float32
 
 
+def _allocate(stream):
+    """A context in which outputs are allocated for a call on `stream` (None:
+    the current one): from that stream's memory.  Memory of another stream
+    may still be in use there, and goes back to it as soon as the tensor is
+    dropped, with the call still writing."""
+    import contextlib
+    import torch
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+
+
 class TopkCols:
     """One top-k shape on the current GPU (a handle of the C library)."""
 
@@ -215,10 +230,12 @@ class TopkCols:
             raise ValueError("x does not hold the matrix described at creation")
         if not x.is_contiguous():
             raise ValueError("x must be contiguous")
-        if values is None:
-            values = torch.empty((self.C, self.k), dtype=x.dtype, device=x.device)
-        if ids is None:
-            ids = torch.empty((self.C, self.k), dtype=torch.int32, device=x.device)
+        if values is None or ids is None:
+            with _allocate(stream):
+                if values is None:
+                    values = torch.empty((self.C, self.k), dtype=x.dtype, device=x.device)
+                if ids is None:
+                    ids = torch.empty((self.C, self.k), dtype=torch.int32, device=x.device)
         if values.numel() < self.C * self.k or ids.numel() < self.C * self.k:
             raise ValueError("output buffers are too small")
         map_ptr = None
@@ -266,10 +283,12 @@ def sample(values, ids, temperature: float = 1.0, top_p: float = 0.95, seed: int
         raise ValueError("values and ids must be contiguous GPU tensors")
     C, k = values.shape
     dtype = 0 if values.element_size() == 2 else 1
-    if out_ids is None:
-        out_ids = torch.empty(C, dtype=torch.int32, device=values.device)
-    if out_pos is None:
-        out_pos = torch.empty(C, dtype=torch.int32, device=values.device)
+    if out_ids is None or out_pos is None:
+        with _allocate(stream):
+            if out_ids is None:
+                out_ids = torch.empty(C, dtype=torch.int32, device=values.device)
+            if out_pos is None:
+                out_pos = torch.empty(C, dtype=torch.int32, device=values.device)
     s = stream if stream is not None else torch.cuda.current_stream(values.device)
     rc = load().topk_cols_sample(values.data_ptr(), ids.data_ptr(), C, k, dtype, float(temperature),
                                  float(top_p), int(seed), int(offset), out_ids.data_ptr(), out_pos.data_ptr(),
@@ -293,10 +312,12 @@ def run_noalloc(x, V: int, C: int, k: int, dtype: str = "bf16", layout: str = "c
     need = (C - 1) * ld + V if layout == "col" else (V - 1) * ld + C
     if x.numel() < need or x.element_size() != (2 if dtype == "bf16" else 4):
         raise ValueError("x does not hold the matrix described")
-    if values is None:
-        values = torch.empty((C, k), dtype=x.dtype, device=x.device)
-    if ids is None:
-        ids = torch.empty((C, k), dtype=torch.int32, device=x.device)
+    if values is None or ids is None:
+        with _allocate(stream):
+            if values is None:
+                values = torch.empty((C, k), dtype=x.dtype, device=x.device)
+            if ids is None:
+                ids = torch.empty((C, k), dtype=torch.int32, device=x.device)
     if values.numel() < C * k or ids.numel() < C * k:
         raise ValueError("output buffers are too small")
     s = stream if stream is not None else torch.cuda.current_stream(x.device)
@@ -452,7 +473,8 @@ class AdjustRules:
             import torch
             if self.out_ld != self.ld:
                 raise ValueError("out is needed when out_ld differs from ld")
-            out = torch.empty_like(x)
+            with _allocate(stream):
+                out = torch.empty_like(x)
         index = x.get_device()
         if self._index not in (None, index):
             raise ValueError("x, out and the rules' tensors must be on one GPU")
@@ -504,10 +526,12 @@ def verify(target_values, target_ids, col_start, drafts, draft_start, draft_valu
         lanes = col_start.numel() - 1
     if out_tokens is None or out_count is None:
         import torch
-        if out_tokens is None:
-            out_tokens = torch.empty((lanes, max_tokens or drafts.numel() + 1), dtype=torch.int32, device=target_values.device)
-        if out_count is None:
-            out_count = torch.empty(lanes, dtype=torch.int32, device=target_values.device)
+        with _allocate(stream):
+            if out_tokens is None:
+                out_tokens = torch.empty((lanes, max_tokens or drafts.numel() + 1), dtype=torch.int32,
+                                         device=target_values.device)
+            if out_count is None:
+                out_count = torch.empty(lanes, dtype=torch.int32, device=target_values.device)
     _launch("topk_cols_verify", _round_binding().verify, index, _raw_stream(index, stream), lanes, target_values, target_ids,
             col_start, drafts, draft_start, draft_values, draft_ids, temperature, top_p, seed, offset, out_tokens, out_count)
     return out_tokens, out_count
@@ -531,8 +555,9 @@ def plan(lens, add, held, table, free_ids, free_count, block_size: int, capacity
         lanes = lens.numel()
         sizes = dict(held=lanes, free_count=1, refused=1, col_start=lanes + 1, col_lane=capacity, col_pos=capacity,
                      slots=capacity)
-        out = {n: torch.empty(size, dtype=torch.int64 if n == "slots" else torch.int32, device=lens.device)
-               for n, size in sizes.items()}
+        with _allocate(stream):
+            out = {n: torch.empty(size, dtype=torch.int64 if n == "slots" else torch.int32, device=lens.device)
+                   for n, size in sizes.items()}
     _launch("topk_cols_plan", _round_binding().plan, index, _raw_stream(index, stream), lens, add, held, table, free_ids,
             free_count, block_size, capacity, out["held"], out["free_count"], out["refused"], out["col_start"],
             out["col_lane"], out["col_pos"], out["slots"])

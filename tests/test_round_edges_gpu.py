@@ -153,3 +153,49 @@ def test_verify_refuses_half_a_list(gpu):
     values, ids = torch.zeros((16, 8), device="cuda"), i32(16, 8)
     with pytest.raises(ValueError, match="draft_ids"):
         T.verify(values, ids, None, i32(14), None, draft_ids=i32(14, 8), lanes=2, max_tokens=8)
+
+
+# ---------------------------------------------------------------- streams ---
+
+def stream_of(torch, t):
+    """The stream whose memory a tensor lies in."""
+    at = t.data_ptr()
+    return next(s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] <= at < s["address"] + s["total_size"])
+
+
+def test_outputs_made_for_another_stream(gpu):
+    """Calls on a side stream that allocate their outputs: these lie in that
+    stream's memory, and hold what the calls on the current stream give."""
+    torch, T = gpu
+    rng = np.random.default_rng(4)
+    V, lanes, n, k = 5003, 4, 3, 8
+    C = lanes * n
+    x = dev(torch, W.random_matrix(3, V, C, W.BF16, W.COL, kind="normal")).view(torch.bfloat16).reshape(C, V)
+    i32 = lambda a: dev(torch, np.asarray(a, np.int32))  # noqa: E731
+    drafts = i32(rng.integers(0, V, lanes * (n - 1)))
+    rules = T.AdjustRules(V, C, lanes=lanes, presence=dev(torch, np.ones(lanes, np.float32)), drafts=drafts)
+    inputs = [i32(a) for a in (np.full(lanes, 5), np.full(lanes, n), np.full(lanes, 2), rng.integers(0, 9, (lanes, 4)),
+                               np.arange(9), [9])]
+    handle = T.TopkCols(V, C, k)
+
+    def calls(stream):
+        y = rules.apply(x, stream=stream)
+        v, i = handle.run(y, stream=stream)
+        v2, i2 = T.run_noalloc(y, V, C, k, stream=stream)
+        s = T.sample(v, i, seed=1, stream=stream)
+        t = T.verify(v, i, None, drafts, None, lanes=lanes, max_tokens=n, stream=stream)
+        p = T.plan(*inputs, 4, C, stream=stream)
+        return [y, v, i, v2, i2, *s, *t, *p.values()]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    here = calls(None)
+    torch.cuda.synchronize()
+    print("[round] outputs made for another stream", flush=True)
+    there = calls(side)
+    side.synchronize()
+    assert len(here) == 16
+    for a, b in zip(here, there):
+        assert stream_of(torch, a) == 0 and stream_of(torch, b) == side.cuda_stream
+        assert torch.equal(a.view(torch.int16) if a.dtype == torch.bfloat16 else a,
+                           b.view(torch.int16) if b.dtype == torch.bfloat16 else b)
+    handle.close()
