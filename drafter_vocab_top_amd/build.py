@@ -4,7 +4,9 @@ and the compiled part of its Python binding with g++.
     python -m drafter_vocab_top_amd.build
 
 The libraries are placed next to this file; the Python binding loads them from
-there.  hipcc cross-compiles for gfx950 without a GPU.
+there.  hipcc cross-compiles for gfx950 without a GPU.  libtopk_cols.so needs
+nothing but ROCm: it is in place before the binding is compiled, which is left
+out where there is no torch to bind to.
 """
 import os
 import subprocess
@@ -39,6 +41,7 @@ HEADERS = [os.path.join(CSRC, n) for n in ("topk_device.hpp", "topk_col_common.h
                                             "topk_round.hpp")] + \
           [os.path.join(INCLUDE, "topk_cols.h")]
 # The compiled part of the Python binding (host code against torch's headers).
+# It holds what it was built for, since it fits no other torch or Python.
 BINDING_SOURCE = os.path.join(CSRC, "round_binding.cpp")
 BINDING_LIBRARY = os.path.join(HERE, "_round_binding.so")
 ARCH = "gfx950"
@@ -57,12 +60,22 @@ def flags():
             "-Wall", "-Wno-unused-result", "-I", INCLUDE, "-I", CSRC]
 
 
+def built_for():
+    """What the binding's compiled part depends on, torch and Python (None
+    without torch)."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    return f"torch {torch.__version__}, Python {sys.version_info.major}.{sys.version_info.minor}"
+
+
 def binding_command(output):
     """The g++ line of the binding's compiled part."""
     import torch
     base = os.path.dirname(torch.__file__)
     rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
-    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f'-DTOPK_BUILT_FOR="{built_for()}"',
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-D__HIP_PLATFORM_AMD__", "-I", INCLUDE,
             "-isystem", os.path.join(rocm, "include"), "-isystem", sysconfig.get_paths()["include"],
             "-isystem", os.path.join(base, "include"), "-o", output, BINDING_SOURCE, "-L", os.path.join(base, "lib"),
@@ -76,50 +89,77 @@ def command(output=LIBRARY):
     return [hipcc()] + flags() + extra + ["-shared", "-o", output] + SOURCES
 
 
-def _check(res, what, verbose):
+def _run(cmd, verbose):
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
+
+
+def _check(process, what, verbose):
+    _, err = process.communicate()
     noise = "is not a recognized feature for this target"
-    err = "\n".join(l for l in res.stderr.splitlines() if noise not in l)
-    if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed on {what} ({res.returncode}):\n{err}")
+    err = "\n".join(l for l in err.splitlines() if noise not in l)
+    if process.returncode != 0:
+        raise RuntimeError(f"{os.path.basename(process.args[0])} failed on {what} ({process.returncode}):\n{err}")
     if verbose and err.strip():
         print(err, file=sys.stderr)
 
 
 def build(verbose=False):
-    """Compiles every source to an object in parallel, then links the library."""
+    """Compiles every source to an object and the binding in parallel, and
+    links the library.  Where the binding fails it raises, with the library in
+    place."""
     os.makedirs(OBJDIR, exist_ok=True)
     objs, procs = [], []
     for src in SOURCES + [STREAM_SOURCE]:
         obj = os.path.join(OBJDIR, os.path.basename(src) + ".o")
-        cmd = [hipcc()] + flags() + EXTRA_FLAGS.get(os.path.basename(src), []) + ["-c", "-o", obj, src]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
+        extra = EXTRA_FLAGS.get(os.path.basename(src), [])
+        procs.append((src, _run([hipcc()] + flags() + extra + ["-c", "-o", obj, src], verbose)))
         objs.append(obj)
-    binding_tmp = BINDING_LIBRARY + ".tmp"
-    cmd = binding_command(binding_tmp)
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    procs.append((BINDING_SOURCE, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
-    for src, pr in procs:
-        out, err = pr.communicate()
-        _check(subprocess.CompletedProcess(pr.args, pr.returncode, out, err), os.path.basename(src), verbose)
+    binding = _start_binding(verbose)
+    for src, process in procs:
+        _check(process, os.path.basename(src), verbose)
     for lib, lib_objs in ((LIBRARY, objs[:-1]), (STREAM_LIBRARY, objs[-1:])):
         tmp = lib + ".tmp"
-        cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + lib_objs
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        _check(subprocess.run(cmd, capture_output=True, text=True), "link", verbose)
+        _check(_run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + lib_objs, verbose), "link", verbose)
         os.replace(tmp, lib)
-    os.replace(binding_tmp, BINDING_LIBRARY)
+    # one that was built for the library before this one does not stay
+    if os.path.exists(BINDING_LIBRARY):
+        os.remove(BINDING_LIBRARY)
+    if isinstance(binding, OSError):
+        raise RuntimeError(f"the library is built, its Python binding is not: {binding}") from binding
+    if binding is not None:
+        _check(binding, "the Python binding (the library is built)", verbose)
+        os.replace(BINDING_LIBRARY + ".tmp", BINDING_LIBRARY)
     return LIBRARY
 
 
+def _start_binding(verbose):
+    """The compiler of the binding, the error that kept it from starting, or
+    None without a torch to bind to."""
+    if built_for() is None:
+        print("no torch: the Python binding is left out", file=sys.stderr)
+        return None
+    try:
+        return _run(binding_command(BINDING_LIBRARY + ".tmp"), verbose)
+    except OSError as e:
+        return e
+
+
 def stale():
-    if not os.path.exists(LIBRARY) or not os.path.exists(BINDING_LIBRARY):
+    """Whether a library is missing, older than its sources or, the binding,
+    built for another torch or Python."""
+    def older(library, sources):
+        return not os.path.exists(library) or any(os.path.getmtime(p) > os.path.getmtime(library) for p in sources)
+    if older(LIBRARY, SOURCES + HEADERS):
         return True
-    t = min(os.path.getmtime(LIBRARY), os.path.getmtime(BINDING_LIBRARY))
-    return any(os.path.getmtime(p) > t for p in SOURCES + HEADERS + [BINDING_SOURCE])
+    this = built_for()
+    if this is None:
+        return False
+    if older(BINDING_LIBRARY, [BINDING_SOURCE] + HEADERS):
+        return True
+    with open(BINDING_LIBRARY, "rb") as f:
+        return this.encode() + b"\0" not in f.read()
 
 
 if __name__ == "__main__":

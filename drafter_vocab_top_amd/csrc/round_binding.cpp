@@ -243,4 +243,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_round_binding", nullptr, -1, meth
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__round_binding() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__round_binding() {
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", TOPK_BUILT_FOR) != 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

@@ -354,6 +354,10 @@ def _round_binding():
         except ImportError as e:
             raise OSError(f"_round_binding is missing or does not load ({e}): build it with "
                           "`python -m drafter_vocab_top_amd.build`") from e
+        from . import build
+        if module.built_for != build.built_for():
+            raise OSError(f"_round_binding was built for {module.built_for}, this is {build.built_for()}: build it again "
+                          "with `python -m drafter_vocab_top_amd.build`")
         module.bind(*(ctypes.cast(f, ctypes.c_void_p).value
                       for f in (lib.topk_cols_adjust, lib.topk_cols_count, lib.topk_cols_verify, lib.topk_cols_plan)))
         _round = module
