@@ -734,8 +734,12 @@ hipError_t launch_row_dense(const AdjustArgs& a, hipStream_t stream) {
     const RowCut<DT> cut(a);
     for (uint32_t t = 0; t < cut.col_tiles(); t += (uint32_t)kGridY) {
         const dim3 grid(cut.row_tiles(a), min(cut.col_tiles() - t, (uint32_t)kGridY));
-        if (cut.rows == 16) hipLaunchKernelGGL((adjust_row_dense<DT, kMode, kMask, 16>), grid, dim3(kBlock), 0, stream, a, cut.tx_log, t);
-        else hipLaunchKernelGGL((adjust_row_dense<DT, kMode, kMask, 4>), grid, dim3(kBlock), 0, stream, a, cut.tx_log, t);
+        // (a matrix past the caches has more than kRowVecs vectors)
+        if (kMode == kModeOnce || cut.rows == 16)
+            hipLaunchKernelGGL((adjust_row_dense<DT, kMode, kMask, 16>), grid, dim3(kBlock), 0, stream, a, cut.tx_log, t);
+        else
+            hipLaunchKernelGGL((adjust_row_dense<DT, kMode == kModeOnce ? kModeLong : kMode, kMask, 4>), grid, dim3(kBlock), 0, stream, a,
+                               cut.tx_log, t);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
     return hipSuccess;
