@@ -69,13 +69,21 @@ __device__ __forceinline__ uint32_t from_double(double y) {
 template <class DT>
 constexpr uint32_t kMinusInf = DT::kPerVec == 8 ? 0xFF80u : 0xFF800000u;
 
-// The operations as they are written, each rounded (no fused ones).  A division
-// takes some 10 instructions more than a product with a reciprocal, whose error
-// would be what is left of a cancelled logit: 448 interleaved columns 104.4 and
-// 104.2 us, a lane with every row in its history 9.4 and 8.5.
+// The operations as they are written, each rounded (no fused ones).
 struct LaneRules {
-    double rep, pres, freq;
-    __device__ LaneRules(float r, float p, float f) : rep((double)r), pres((double)p), freq((double)f) {}
+    double rep, inv, pres, freq;
+    __device__ LaneRules(float r, float p, float f) : rep((double)r), inv(1.0 / rep), pres((double)p), freq((double)f) {}
+    // x / rep, rounded to nearest, of binary32 values.  q is off by at most two of
+    // its last places, so x - q rep takes some 26 bits and is exact; adding its
+    // quotient, off by less than 2^-51 of a last place, rounds as x / rep does,
+    // which with operands of 24 bits is no nearer than 2^-25 of a last place to
+    // where the rounding changes.  Where an operand is infinite or zero, q is the
+    // quotient.  Eight lanes in place 7.70 us, with a division 7.83, with q alone
+    // 7.60; one lane with every row in its history 8.85, 9.42 and 8.48.
+    __device__ __forceinline__ double quotient(double x) const {
+        const double q = x * inv, rest = __builtin_fma(-q, rep, x);
+        return __builtin_isfinite(rest) ? __builtin_fma(rest, inv, q) : q;
+    }
     // what n occurrences take off
     __device__ __forceinline__ double penalty(uint32_t n) const {
 #pragma clang fp contract(off)
@@ -83,7 +91,7 @@ struct LaneRules {
     }
     __device__ __forceinline__ double apply(double x, bool seen, double penalty, bool biased, double bias) const {
 #pragma clang fp contract(off)
-        const double y = (seen ? x > 0.0 ? x / rep : x * rep : x) - penalty;
+        const double y = (seen ? x > 0.0 ? quotient(x) : x * rep : x) - penalty;
         return biased ? y + bias : y;
     }
 };

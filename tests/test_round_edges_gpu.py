@@ -95,6 +95,26 @@ def test_adjust_divides(gpu, dtype, layout):
     assert np.array_equal(got, to_storage(y, dtype))
 
 
+@pytest.mark.parametrize("layout", [W.COL, W.ROW])
+def test_adjust_divides_the_largest_and_smallest(gpu, layout):
+    """Subnormal, largest and infinite logits and penalties."""
+    torch, T = gpu
+    rep = np.float32([1e-45, 1.5e-42, 1.1754944e-38, 0.7, 1, 1.7, 3.4028235e38, np.inf])
+    row = np.float32([1e-45, 7e-45, 1.1754944e-38, 0.3, 1, 2.9, 3.4028235e38, np.inf, -1e-45, -3.4028235e38, -np.inf, 0.0, -0.0])
+    lanes, V = len(rep), len(row)
+    ones = np.ones((lanes, V), np.int32)
+    r = T.AdjustRules(V, lanes, "f32", layout, lanes=lanes, counts=dev(torch, ones), seen=dev(torch, packed(ones != 0)),
+                      repetition=dev(torch, rep))
+    x = np.tile(row, (lanes, 1))
+    with np.errstate(all="ignore"):
+        a, b = x.astype(np.float64), rep.astype(np.float64)[:, None]
+        y = (np.where(a > 0, a / b, a * b) - 0.0).astype(np.float32)
+    got = host(r.apply(dev(torch, x if layout == W.COL else np.ascontiguousarray(x.T))))
+    got = got if layout == W.COL else np.ascontiguousarray(got.T)
+    assert np.array_equal(np.isnan(got), np.isnan(y))
+    assert np.array_equal(got[~np.isnan(y)].view(np.uint32), y[~np.isnan(y)].view(np.uint32))
+
+
 @pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("layout", [W.COL, W.ROW])
 @pytest.mark.parametrize("dtype", [W.BF16, W.F32])
