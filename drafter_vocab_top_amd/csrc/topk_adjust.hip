@@ -29,12 +29,12 @@
 // where the list takes 7 (56 columns in place).
 //
 // What bounds it (one MI355X, replayed from a graph).  Large matrices: memory.
-// 448 interleaved columns of 248,046 rows, bf16: 83 us for the dense part (449
-// MB, 5.4 TB/s, the rate of a plain copy) and 18 for the touched rows; 448
-// column-contiguous ones 95.  64 columns of 131,072 rows, fp32, half of them in
-// use: 10.8 us (34 MB).  Small ones: the chain launch, col_start and history
-// bits, list, counts and elements, store: 6.4 us for one lane's 8 columns (8
-// MB), 7.3 for 56 in place (scattered elements), 12 with masks (14 MB of -Inf).
+// 448 interleaved columns of 248,046 rows, bf16: 82 us for the dense part (461
+// MB, 5.6 TB/s, the rate of a plain copy) and 19 for the touched rows; 448
+// column-contiguous ones 91.  64 columns of 131,072 rows, fp32, half of them in
+// use: 11.2 us (34 MB).  Small ones: the chain launch, col_start and history
+// bits, list, counts and elements, store: 6.7 us for one lane's 8 columns (8
+// MB), 7.7 for 56 in place (scattered elements), 12 with masks (14 MB of -Inf).
 //
 // The penalised value is a chain of four operations.  Each is carried out in
 // binary64, and the last result is rounded to binary32 and then to the type:

@@ -10,10 +10,10 @@
 // writes its rows, so that nothing is cleared first and the many occurrences
 // of frequent tokens meet in LDS instead of in one cache line.
 //
-// One MI355X, replayed from a graph: 64 lanes of up to 8 tokens 2.9 us, a
+// One MI355X, replayed from a graph: 64 lanes of up to 8 tokens 3.0 us, a
 // launch and one chain of reads and atomics; 8 fresh lanes of 25,000 tokens
-// each 8.4 us; one of 120,000 tokens 16.4.  Every workgroup of a lane looks
-// at all of its tokens, some 16 instructions each: that bounds it.
+// each 9.4 us; one lane's 120,000 prompt tokens 18.9.  Every workgroup of a lane
+// looks at all of its tokens, some 12 instructions each: that bounds it.
 #include "topk_round.hpp"
 
 #include "topk_col_common.hpp"
@@ -123,7 +123,7 @@ __global__ __launch_bounds__(kOwnThreads) void count_own(CountArgs a, uint32_t l
         if (((r >> 5) & tiles_mask) == tile && r < a.V) {
             uint32_t* word = &own[(r >> 5 >> tiles_log) * 32u + (r & 31u)];
             if (i < prompt) {
-                // (a frequent token's flag once: 120,000 equal tokens 59 us, not 104)
+                // (a frequent token's flag once: 120,000 equal tokens 18.6 us, not 104; tokens as they come 19.4, not 15.3)
                 if (!(*word >> 31)) atomicOr(word, 0x80000000u);
             } else {
                 atomicAdd(word, 1u);

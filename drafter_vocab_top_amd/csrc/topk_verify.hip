@@ -17,11 +17,12 @@
 // The decisions are integers made by floating point, so every step is IEEE
 // double in a fixed order with no contraction.
 //
-// One MI355X, replayed from a graph: one lane of 7 drafts, k = 20, 4.2 us (a
+// One MI355X, replayed from a graph: one lane of 7 drafts, k = 20, 4.3 us (a
 // launch and the chain starts, lists, exp, sums, test, token); 512 lanes of up
-// to 15 drafts, k = 64, fp32, 6.7 us for at most 6.2 MB of lists: some 700
-// instructions per column.  With sums in list order (64 dependent additions,
-// three times) and a token for every column it was 27.7.
+// to 15 drafts, k = 64, fp32, 6.8 us for at most 6.2 MB of lists: some 590
+// instructions a wave, half of them vector instructions.  With sums in list
+// order (64 dependent additions, three times) and a token for every column it
+// was 27.7.
 #include "topk_draw.hpp"
 #include "topk_round.hpp"
 
