@@ -123,14 +123,18 @@ def build(verbose=False):
         tmp = lib + ".tmp"
         _check(_run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + lib_objs, verbose), "link", verbose)
         os.replace(tmp, lib)
-    # one that was built for the library before this one does not stay
-    if os.path.exists(BINDING_LIBRARY):
-        os.remove(BINDING_LIBRARY)
-    if isinstance(binding, OSError):
-        raise RuntimeError(f"the library is built, its Python binding is not: {binding}") from binding
-    if binding is not None:
-        _check(binding, "the Python binding (the library is built)", verbose)
-        os.replace(BINDING_LIBRARY + ".tmp", BINDING_LIBRARY)
+    bound = False
+    try:
+        if isinstance(binding, OSError):
+            raise RuntimeError(f"the library is built, its Python binding is not: {binding}") from binding
+        if binding is not None:
+            _check(binding, "the Python binding (the library is built)", verbose)
+            os.replace(BINDING_LIBRARY + ".tmp", BINDING_LIBRARY)
+            bound = True
+    finally:
+        # one that was built for the library before this one does not stay
+        if not bound and os.path.exists(BINDING_LIBRARY):
+            os.remove(BINDING_LIBRARY)
     return LIBRARY
 
 

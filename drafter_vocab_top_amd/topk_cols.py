@@ -20,6 +20,7 @@ module, _round_binding, that reads their many tensors faster than Python does.)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -137,14 +138,18 @@ def _torch_dtype(dtype: str):
     return torch.bfloat16 if dtype == "bf16" else torch.float32
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _allocate(stream):
     """A context in which outputs are allocated for a call on `stream` (None:
     the current one): from that stream's memory.  Memory of another stream
     may still be in use there, and goes back to it as soon as the tensor is
     dropped, with the call still writing."""
-    import contextlib
+    if stream is None:
+        return _HERE
     import torch
-    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+    return torch.cuda.stream(stream)
 
 
 class TopkCols:
