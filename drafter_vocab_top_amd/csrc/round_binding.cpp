@@ -1,15 +1,18 @@
-// CPython module behind AdjustRules.apply, count_tokens, verify and plan of the
-// binding: takes their tensors apart, checks them and calls the C ABI.
+// CPython module behind AdjustRules.apply, count_tokens, verify, plan, tree,
+// verify_tree and KeyCache of the binding: takes their tensors apart, checks
+// them and calls the C ABI.
 //
 // A round's calls run kernels of 3 to 5 us; checking a dozen tensors from
 // Python takes as long.  Reading them here takes a call from 7 - 9 us to 4 - 5,
-// of which the runtime's launch is 2.6.  Nothing else happens here: the
-// checks are the binding's (each tensor's type, device, size and contiguity),
-// every other argument is checked by the library.
+// of which the runtime's launch is 2.6.  Nothing else happens here, but for the
+// workspace of attend: the checks are the binding's (each tensor's type,
+// device, size and contiguity), every other argument is checked by the library.
 //
 // The library's functions are bound at load time (bind), so that the binding
 // keeps choosing which library is in use.
 #include <torch/csrc/autograd/python_variable.h>
+
+#include <ATen/ops/empty.h>
 
 #include "topk_cols.h"
 
@@ -19,6 +22,12 @@ decltype(&topk_cols_adjust) g_adjust = nullptr;
 decltype(&topk_cols_count) g_count = nullptr;
 decltype(&topk_cols_verify) g_verify = nullptr;
 decltype(&topk_cols_plan) g_plan = nullptr;
+decltype(&topk_cols_tree) g_tree = nullptr;
+decltype(&topk_cols_cache_write) g_cache_write = nullptr;
+decltype(&topk_cols_cache_move) g_cache_move = nullptr;
+decltype(&topk_cols_attend) g_attend = nullptr;
+decltype(&topk_cols_attend_workspace) g_attend_workspace = nullptr;
+decltype(&topk_cols_verify_tree) g_verify_tree = nullptr;
 
 struct Failed {};  // a Python error is set
 
@@ -55,7 +64,7 @@ T* need(PyObject* o, const char* name, int64_t numel, int index, at::ScalarType 
     const at::Tensor& t = tensor(o, name);
     if (t.scalar_type() != type || !fits(t, numel, index)) {
         PyErr_Format(PyExc_ValueError, "%s must be a contiguous torch.%s tensor of at least %lld elements on GPU %d", name,
-                     type == at::kInt ? "int32" : "int64", (long long)numel, index);
+                     type == at::kInt ? "int32" : type == at::kLong ? "int64" : "float32", (long long)numel, index);
         throw Failed{};
     }
     return static_cast<T*>(t.data_ptr());
@@ -100,14 +109,21 @@ PyObject* guarded(const F& f) {
     }
 }
 
-// bind(adjust, count, verify, plan): addresses of the library's functions
+// bind(adjust, count, verify, plan, tree, cache_write, cache_move, attend, attend_workspace, verify_tree): addresses of
+// the library's functions
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&] {
-        expect(n, 4);
+        expect(n, 10);
         g_adjust = reinterpret_cast<decltype(g_adjust)>((uintptr_t)wrapped(a[0]));
         g_count = reinterpret_cast<decltype(g_count)>((uintptr_t)wrapped(a[1]));
         g_verify = reinterpret_cast<decltype(g_verify)>((uintptr_t)wrapped(a[2]));
         g_plan = reinterpret_cast<decltype(g_plan)>((uintptr_t)wrapped(a[3]));
+        g_tree = reinterpret_cast<decltype(g_tree)>((uintptr_t)wrapped(a[4]));
+        g_cache_write = reinterpret_cast<decltype(g_cache_write)>((uintptr_t)wrapped(a[5]));
+        g_cache_move = reinterpret_cast<decltype(g_cache_move)>((uintptr_t)wrapped(a[6]));
+        g_attend = reinterpret_cast<decltype(g_attend)>((uintptr_t)wrapped(a[7]));
+        g_attend_workspace = reinterpret_cast<decltype(g_attend_workspace)>((uintptr_t)wrapped(a[8]));
+        g_verify_tree = reinterpret_cast<decltype(g_verify_tree)>((uintptr_t)wrapped(a[9]));
         return 0;
     });
 }
@@ -231,12 +247,181 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// tree(stream, lanes, parents, lens, col_start, mask, positions)
+PyObject* tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        expect(n, 7);
+        const at::Tensor &parents = tensor(a[2], "parents"), &mask = tensor(a[5], "mask");
+        const int index = gpu_of(parents);
+        const int64_t lanes = whole(a[1]), C = parents.numel();
+        if (mask.dim() != 2 || mask.size(0) < C) fail("mask must be a matrix with a row per column");
+        return g_tree(lanes, C, need<int32_t>(a[4], "col_start", lanes + 1, index), need<int32_t>(a[2], "parents", 1, index),
+                      need<int32_t>(a[3], "lens", lanes, index), need<uint32_t>(a[5], "mask", 1, index), mask.size(1),
+                      need<int32_t>(a[6], "positions", C, index), stream_of(a[0]));
+    });
+}
+
+// verify_tree(stream, lanes, target_values, target_ids, col_start, tokens, parents, uniforms, draft_values, draft_ids,
+//             temperature, top_p, out_tokens, out_columns, out_count)
+PyObject* verify_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        expect(n, 15);
+        const at::Tensor &values = tensor(a[2], "target_values"), &ids = tensor(a[3], "target_ids");
+        const at::Tensor &tokens = tensor(a[12], "out_tokens"), &columns = tensor(a[13], "out_columns");
+        const int index = gpu_of(values);
+        topk_verify_tree_args v = {};
+        v.lanes = whole(a[1]);
+        if (values.dim() != 2 || ids.sizes() != values.sizes()) fail("target_values and target_ids must be (C, k)");
+        if (tokens.dim() != 2 || tokens.size(0) < v.lanes || columns.dim() != 2 || columns.size(0) < v.lanes ||
+            columns.size(1) != tokens.size(1))
+            fail("out_tokens and out_columns must be matrices of one width with a row per lane");
+        const int64_t size = values.element_size();
+        if ((size != 2 && size != 4) || !holds_values(values, size) || !fits(values, 0, index))
+            fail("target_values must be a contiguous GPU tensor of bf16 or fp32 (or patterns)");
+        v.dtype = size == 2 ? TOPK_BF16 : TOPK_F32;
+        v.C = values.size(0);
+        if (values.size(1) > TOPK_MAX_K) fail("lists must have at most 64 entries");
+        v.k = (int32_t)values.size(1);
+        if (a[8] == Py_None && a[9] != Py_None) fail("draft_ids without draft_values");
+        if (a[8] != Py_None) {
+            const at::Tensor& qv = tensor(a[8], "draft_values");
+            if (qv.dim() != 2 || a[9] == Py_None || tensor(a[9], "draft_ids").sizes() != qv.sizes() || qv.size(0) < v.C ||
+                !holds_values(qv, size) || !fits(qv, 1, index) || qv.size(1) > TOPK_MAX_K)
+                fail("draft_values and draft_ids must be contiguous (C, kq) tensors of the target lists' types");
+            v.kq = (int32_t)qv.size(1);
+            v.draft_values = qv.data_ptr();
+            v.draft_ids = need<int32_t>(a[9], "draft_ids", 0, index);
+        }
+        v.col_start = need<int32_t>(a[4], "col_start", v.lanes + 1, index);
+        v.target_values = values.data_ptr();
+        v.target_ids = need<int32_t>(a[3], "target_ids", 1, index);
+        v.tokens = need<int32_t>(a[5], "tokens", v.C, index);
+        v.parents = need<int32_t>(a[6], "parents", v.C, index);
+        v.uniforms = need<float>(a[7], "uniforms", 2 * v.C, index, at::kFloat);
+        v.temperature = real(a[10]);
+        v.top_p = real(a[11]);
+        v.max_tokens = tokens.size(1);
+        v.out_tokens = need<int32_t>(a[12], "out_tokens", 1, index);
+        v.out_columns = need<int32_t>(a[13], "out_columns", 1, index);
+        v.out_count = need<int32_t>(a[14], "out_count", v.lanes, index);
+        return g_verify_tree(&v, stream_of(a[0]));
+    });
+}
+
+// A stride as the library takes it: none where there is one entry.
+int64_t stride_of(const at::Tensor& t, int64_t dim) { return t.size(dim) == 1 ? 0 : t.stride(dim); }
+
+// Rows (C, heads, dim) on GPU index, whose strides the library checks but for the last.
+const at::Tensor& rows(PyObject* o, const char* name, int64_t heads, int64_t dim, int index) {
+    const at::Tensor& t = tensor(o, name);
+    if (t.layout() != at::kStrided || t.dim() != 3 || (heads > 0 && t.size(1) != heads) || t.size(2) != dim ||
+        t.stride(2) != 1 || gpu_of(t) != index) {
+        PyErr_Format(PyExc_ValueError, "%s must be a (columns, heads, dim) tensor of the cache's sizes on GPU %d, its last stride 1",
+                     name, index);
+        throw Failed{};
+    }
+    return t;
+}
+
+// cache_write(stream, address of the cache, GPU, k, v, slots, layer)
+PyObject* cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        expect(n, 7);
+        const topk_cache* c = reinterpret_cast<const topk_cache*>((uintptr_t)wrapped(a[1]));
+        const int index = (int)whole(a[2]);
+        const at::Tensor &k = rows(a[3], "k", c->heads, c->dim, index), &v = rows(a[4], "v", c->heads, c->dim, index);
+        if ((k.scalar_type() != at::kBFloat16 && k.scalar_type() != at::kFloat) || v.scalar_type() != k.scalar_type() ||
+            v.size(0) != k.size(0))
+            fail("k and v must both be bfloat16 or float32, with a row per column");
+        topk_cache_write_args w = {};
+        w.C = k.size(0);
+        w.layer = whole(a[6]);
+        w.dtype = k.scalar_type() == at::kBFloat16 ? TOPK_BF16 : TOPK_F32;
+        w.keys = k.data_ptr();
+        w.values = v.data_ptr();
+        w.key_stride = stride_of(k, 0);
+        w.key_head_stride = stride_of(k, 1);
+        w.value_stride = stride_of(v, 0);
+        w.value_head_stride = stride_of(v, 1);
+        w.slots = need<int64_t>(a[5], "slots", w.C, index, at::kLong);
+        return g_cache_write(c, &w, stream_of(a[0]));
+    });
+}
+
+// attend(stream, address of the cache, GPU, q, lens, table, col_start, mask, positions, window, scale, layer, out)
+PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        expect(n, 13);
+        const topk_cache* c = reinterpret_cast<const topk_cache*>((uintptr_t)wrapped(a[1]));
+        const int index = (int)whole(a[2]);
+        const at::Tensor &q = rows(a[3], "q", 0, c->dim, index), &out = rows(a[12], "out", q.size(1), c->dim, index);
+        const at::Tensor &lens = tensor(a[4], "lens"), &table = tensor(a[5], "table");
+        if (q.scalar_type() != at::kBFloat16 || out.scalar_type() != at::kBFloat16 || out.size(0) < q.size(0))
+            fail("q and out must be bfloat16, out with a row per column");
+        topk_attend_args t = {};
+        t.lanes = a[6] == Py_None ? lens.numel() : tensor(a[6], "col_start").numel() - 1;
+        if (table.dim() != 2 || table.size(0) < t.lanes) fail("table must be a matrix with a row per lane");
+        const int64_t window = whole(a[9]);
+        if (window < 0 || window > INT32_MAX) fail("window must be a 32-bit number, 0 for none");
+        t.C = q.size(0);
+        t.layer = whole(a[11]);
+        if (q.size(1) > INT32_MAX) fail("too many heads");
+        t.heads = (int32_t)q.size(1);
+        t.window = (int32_t)window;
+        t.scale = (float)real(a[10]);
+        t.q = q.data_ptr();
+        t.q_stride = stride_of(q, 0);
+        t.q_head_stride = stride_of(q, 1);
+        t.col_start = need<int32_t>(a[6], "col_start", t.lanes + 1, index);
+        t.lens = need<int32_t>(a[4], "lens", t.lanes, index);
+        t.table = need<int32_t>(a[5], "table", 1, index);
+        t.table_ld = table.size(1);
+        if (a[7] != Py_None) {
+            const at::Tensor& mask = tensor(a[7], "mask");
+            if (mask.dim() != 2 || mask.size(0) < t.C || mask.size(1) < 1) fail("mask must be a matrix with a row per column");
+            t.mask = need<uint32_t>(a[7], "mask", 1, index);
+            t.mask_ld = mask.size(1);
+        }
+        t.positions = need<int32_t>(a[8], "positions", t.C, index);
+        t.out = out.data_ptr();
+        t.out_stride = stride_of(out, 0);
+        t.out_head_stride = stride_of(out, 1);
+        if (const int bad = g_attend_workspace(c, &t, &t.workspace_bytes)) return bad;
+        at::Tensor workspace;  // its memory goes back to the stream that the call is ordered on
+        if (t.workspace_bytes > 0) {
+            workspace = at::empty({t.workspace_bytes}, q.options().dtype(at::kByte));
+            t.workspace = workspace.data_ptr();
+        }
+        return g_attend(c, &t, stream_of(a[0]));
+    });
+}
+
+// cache_move(stream, address of the cache, GPU, lens, table, columns)
+PyObject* cache_move(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        expect(n, 6);
+        const int index = (int)whole(a[2]);
+        const at::Tensor &lens = tensor(a[3], "lens"), &table = tensor(a[4], "table"), &columns = tensor(a[5], "columns");
+        const int64_t lanes = lens.numel();
+        if (table.dim() != 2 || table.size(0) < lanes || columns.dim() != 2 || columns.size(0) < lanes)
+            fail("table and columns must be matrices with a row per lane");
+        return g_cache_move(reinterpret_cast<const topk_cache*>((uintptr_t)wrapped(a[1])), lanes,
+                            need<int32_t>(a[3], "lens", lanes, index), need<int32_t>(a[4], "table", 1, index), table.size(1),
+                            need<int32_t>(a[5], "columns", 1, index), columns.size(1), stream_of(a[0]));
+    });
+}
+
 PyMethodDef methods[] = {
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL, nullptr},
     {"adjust", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(adjust)), METH_FASTCALL, nullptr},
     {"count", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(count)), METH_FASTCALL, nullptr},
     {"verify", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(verify)), METH_FASTCALL, nullptr},
     {"plan", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(plan)), METH_FASTCALL, nullptr},
+    {"tree", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(tree)), METH_FASTCALL, nullptr},
+    {"verify_tree", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(verify_tree)), METH_FASTCALL, nullptr},
+    {"cache_write", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_write)), METH_FASTCALL, nullptr},
+    {"attend", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attend)), METH_FASTCALL, nullptr},
+    {"cache_move", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_move)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_round_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,156 @@
+// Verification of a tree of drafts against the target's top-k lists, for
+// gfx950, from given random numbers.
+//
+// At column c, with weights w = p_c and their sum W, each child x in turn is
+// accepted if u_x q(x) < w(x) / W; a refused one leaves w = max(w - W q, 0), the
+// part of the normalised weights above q, scaled by W (a scale changes nothing:
+// only quotients by the new sum are used).  Where no child is accepted the
+// token is drawn from what is left.
+//
+// One workgroup per lane, one wave per column: what a column's children meet does
+// not depend on the other columns, so the waves judge the columns that follow
+// the current one at once, and the path through them is then a walk in LDS.
+// Parents come before their children, so the walk only goes forward.
+//
+// The decisions are integers made by floating point, so every step is IEEE
+// double in a fixed order with no contraction.
+#include "topk_cache.hpp"
+#include "topk_lists.hpp"
+
+namespace topk {
+
+namespace {
+
+// The probabilities in a draft list of this lane's target token (0 where it has
+// none, and past the target list): that of the first entry with its id.
+__device__ __forceinline__ double probability_at(int32_t id, double q, int32_t qid, int32_t nq) {
+    double at = 0.0;
+    for (int32_t i = nq - 1; i >= 0; --i) {  // from the last, so that the first entry of an id stays
+        const double qi = lane_value(q, i);
+        if (__builtin_amdgcn_readlane(qid, i) == id) at = qi;
+    }
+    return at;
+}
+
+template <class DT, uint32_t kWaves>
+__global__ __launch_bounds__(kWaves * 64) void verify_tree_kernel(VerifyTreeArgs args) {
+#pragma clang fp contract(off)
+    __shared__ int32_t chosen[kWaves];  // the accepted child of each column, or -1
+    const topk_verify_tree_args& a = args.v;
+    const uint32_t l = blockIdx.x, tid = threadIdx.x;
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(tid >> 6));
+    const int32_t lane = (int32_t)(tid & 63u);
+    int32_t* tokens = a.out_tokens + (int64_t)l * a.max_tokens;
+    int32_t* columns = a.out_columns + (int64_t)l * a.max_tokens;
+    const uint32_t most = (uint32_t)a.max_tokens;
+    uint32_t cb, ce;
+    args.cols.range(l, cb, ce);
+    const uint32_t n = ce - cb;
+    uint32_t t = 0;  // accepted drafts
+    bool some = n > 0;
+    uint32_t now = 0;  // the column where the path stands
+    while (some) {
+        const uint32_t first = now, j = first + wave;
+        double w = 0.0, p = 0.0;
+        int32_t id = 0;
+        if (j < n) {  // wave-uniform
+            const int64_t c = (int64_t)cb + j;
+            double v, v0, qv = 0.0, qv0 = 0.0;
+            int32_t qid = 0;
+            id = a.target_ids[c * a.k + (lane < a.k ? lane : 0)];
+            load_entry<DT>(a.target_values, c, a.k, v, v0);
+            if (a.draft_values) {
+                qid = a.draft_ids[c * a.kq + (lane < a.kq ? lane : 0)];
+                load_entry<DT>(a.draft_values, c, a.kq, qv, qv0);
+            }
+            int32_t np, nq = 0;
+            p = probability(v, v0, a.k, a.temperature, a.top_p, np);
+            w = p;
+            double W = 1.0, q = 0.0, q_at = 0.0;
+            bool have_q = false, have_at = false;
+            int32_t accepted = -1;
+            for (uint32_t x0 = j + 1u; x0 < n && accepted < 0; x0 += 64u) {
+                const uint32_t x = x0 + (uint32_t)lane;
+                const int64_t cx = (int64_t)cb + min_u32(x, n - 1u);
+                const int32_t parent = a.parents[cx], token = a.tokens[cx];
+                const float u = a.uniforms[2 * cx];
+                unsigned long long kids = __ballot(x < n && parent == (int32_t)j);
+                while (kids) {
+                    const uint32_t i = first_lane(kids);
+                    kids &= kids - 1ull;
+                    const int32_t d = __builtin_amdgcn_readlane(token, (int)i);
+                    const double u_x = (double)__builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, u), (int)i));
+                    double q_x = 1.0;
+                    if (a.draft_values) {
+                        if (!have_q) q = probability(qv, qv0, a.kq, a.temperature, a.top_p, nq);
+                        have_q = true;
+                        q_x = probability_of(d, qid, q, a.kq);
+                    }
+                    const double w_x = probability_of(d, id, w, a.k);
+                    if (u_x * q_x * W < w_x) {
+                        accepted = (int32_t)(x0 + i);
+                        break;
+                    }
+                    if (!a.draft_values) {
+                        q_at = lane < a.k && id == d ? 1.0 : 0.0;
+                    } else if (!have_at) {
+                        q_at = probability_at(id, q, qid, nq);
+                        have_at = true;
+                    }
+                    const double left = w - W * q_at;
+                    const double rest = left > 0.0 ? left : 0.0;
+                    const double total = lane_value(running_sum(rest), a.k - 1);
+                    w = total > 0.0 ? rest : p;
+                    W = total > 0.0 ? total : 1.0;
+                }
+            }
+            if (lane == 0) chosen[wave] = accepted;
+        }
+        __syncthreads();
+        bool last = false;
+        while (!last && now - first < kWaves) {
+            const int32_t down = chosen[now - first];
+            if (tid == 0) columns[t] = (int32_t)now;
+            last = down < 0 || t + 1u == most;
+            if (last) break;
+            if (tid == 0) tokens[t] = a.tokens[(int64_t)cb + (uint32_t)down];
+            ++t;
+            now = (uint32_t)down;
+        }
+        if (last) {
+            if (wave == now - first) {
+                if (t + 1u == most) w = p;  // no child was judged
+                const double sums = running_sum(w);
+                const double target = (double)a.uniforms[2 * ((int64_t)cb + now) + 1] * lane_value(sums, a.k - 1);
+                const unsigned long long positive = __ballot(w > 0.0);
+                const unsigned long long above = __ballot(w > 0.0 && sums > target);
+                // (a product rounded up to the total leaves none above it: the last entry that can be drawn)
+                const uint32_t pick = above ? first_lane(above) : positive ? 63u - (uint32_t)__builtin_clzll(positive) : 0u;
+                const int32_t next = __builtin_amdgcn_readlane(id, (int)pick);
+                if (lane == 0) tokens[t] = next;
+            }
+            break;
+        }
+        __syncthreads();  // the next step writes chosen again
+    }
+    const uint32_t count = some ? t + 1u : 0u;
+    for (uint32_t i = count + tid; i < most; i += kWaves * 64u) {
+        tokens[i] = -1;
+        columns[i] = -1;
+    }
+    if (tid == 0) a.out_count[l] = (int32_t)count;
+}
+
+template <class DT>
+hipError_t launch_dt(const VerifyTreeArgs& a, hipStream_t stream) {
+    hipLaunchKernelGGL((verify_tree_kernel<DT, 8>), dim3((uint32_t)a.v.lanes), dim3(512), 0, stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_verify_tree(const VerifyTreeArgs& a, hipStream_t stream) {
+    return a.v.dtype == TOPK_BF16 ? launch_dt<Bf16>(a, stream) : launch_dt<F32>(a, stream);
+}
+
+}  // namespace topk

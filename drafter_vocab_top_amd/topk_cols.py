@@ -44,7 +44,8 @@ EXPORTED = ("topk_cols_create", "topk_cols_create_with_segments", "topk_cols_cre
             "topk_cols_run", "topk_cols_run_n", "topk_cols_run_mapped", "topk_cols_sample",
             "topk_cols_destroy", "topk_cols_status_string", "topk_cols_query", "topk_cols_check",
             "topk_cols_debug_fail_waits", "topk_cols_run_noalloc", "topk_cols_adjust", "topk_cols_count",
-            "topk_cols_verify", "topk_cols_plan")
+            "topk_cols_verify", "topk_cols_plan", "topk_cols_tree", "topk_cols_cache_write", "topk_cols_cache_move",
+            "topk_cols_attend", "topk_cols_attend_workspace", "topk_cols_verify_tree")
 # kernel families of the column-contiguous layout ("one_wave": the baseline
 # design with one wave per column and no vocabulary split)
 ALGOS = {"auto": 0, "workgroup": 1, "one_wave": 3}
@@ -55,7 +56,7 @@ _lib = None
 def _struct(name: str, fields: str):
     """A structure of the header, from "type name" pairs in its order."""
     types = {"p": ctypes.c_void_p, "i64": ctypes.c_int64, "i32": ctypes.c_int32, "u64": ctypes.c_uint64,
-             "f64": ctypes.c_double}
+             "f64": ctypes.c_double, "f32": ctypes.c_float}
     pairs = [f.split() for f in fields.split(",")]
     return type(name, (ctypes.Structure,), {"_fields_": [(n, types[t]) for t, n in pairs]})
 
@@ -72,6 +73,22 @@ PlanArgs = _struct("topk_plan_args", (
     "i64 lanes, i64 capacity, i32 block_size, p lens, p add, p held, p table, i64 table_ld, p free_ids, "
     "i64 n_free_ids, p free_count, p out_held, p out_free_count, p out_refused, p out_col_start, p out_col_lane, "
     "p out_col_pos, p out_slots"))
+
+CacheArgs = _struct("topk_cache", (
+    "i64 layers, i64 blocks, i32 block_size, i32 heads, i32 dim, i32 format, p keys, p values, i64 layer_stride, "
+    "i64 block_stride, i64 slot_stride, i64 head_stride, p key_scales, p value_scales, i64 scale_layer_stride, "
+    "i64 scale_block_stride, i64 scale_slot_stride, i64 scale_head_stride"))
+CacheWriteArgs = _struct("topk_cache_write_args", (
+    "i64 C, i64 layer, i32 dtype, p keys, p values, i64 key_stride, i64 key_head_stride, i64 value_stride, "
+    "i64 value_head_stride, p slots"))
+AttendArgs = _struct("topk_attend_args", (
+    "i64 lanes, i64 C, i64 layer, i32 heads, i32 window, f32 scale, p q, i64 q_stride, i64 q_head_stride, p col_start, "
+    "p lens, p table, i64 table_ld, p mask, i64 mask_ld, p positions, p out, i64 out_stride, i64 out_head_stride, "
+    "p workspace, i64 workspace_bytes"))
+VerifyTreeArgs = _struct("topk_verify_tree_args", (
+    "i64 lanes, i32 dtype, i32 k, i32 kq, i64 C, p col_start, p target_values, p target_ids, p tokens, p parents, "
+    "p draft_values, p draft_ids, p uniforms, f64 temperature, f64 top_p, i64 max_tokens, p out_tokens, p out_columns, "
+    "p out_count"))
 
 
 class TopkError(RuntimeError):
@@ -125,6 +142,18 @@ def load(path: str = LIBRARY):
     lib.topk_cols_verify.restype = ctypes.c_int
     lib.topk_cols_plan.argtypes = [p, p]
     lib.topk_cols_plan.restype = ctypes.c_int
+    lib.topk_cols_tree.argtypes = [i64, i64, p, p, p, p, i64, p, p]
+    lib.topk_cols_tree.restype = ctypes.c_int
+    lib.topk_cols_cache_write.argtypes = [p, p, p]
+    lib.topk_cols_cache_write.restype = ctypes.c_int
+    lib.topk_cols_cache_move.argtypes = [p, i64, p, p, i64, p, i64, p]
+    lib.topk_cols_cache_move.restype = ctypes.c_int
+    lib.topk_cols_attend.argtypes = [p, p, p]
+    lib.topk_cols_attend.restype = ctypes.c_int
+    lib.topk_cols_attend_workspace.argtypes = [p, p, ctypes.POINTER(i64)]
+    lib.topk_cols_attend_workspace.restype = ctypes.c_int
+    lib.topk_cols_verify_tree.argtypes = [p, p]
+    lib.topk_cols_verify_tree.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -348,8 +377,8 @@ _round = None
 
 def _round_binding():
     """The compiled part of the binding: it takes tensors apart for
-    AdjustRules.apply, count_tokens, verify and plan, and calls the loaded
-    library."""
+    AdjustRules.apply, count_tokens, verify, plan, tree, verify_tree and
+    KeyCache, and calls the loaded library."""
     global _round
     if _round is None:
         import torch  # noqa: F401  (the module needs its libraries in the process)
@@ -364,7 +393,9 @@ def _round_binding():
             raise OSError(f"_round_binding was built for {module.built_for}, this is {build.built_for()}: build it again "
                           "with `python -m drafter_vocab_top_amd.build`")
         module.bind(*(ctypes.cast(f, ctypes.c_void_p).value
-                      for f in (lib.topk_cols_adjust, lib.topk_cols_count, lib.topk_cols_verify, lib.topk_cols_plan)))
+                      for f in (lib.topk_cols_adjust, lib.topk_cols_count, lib.topk_cols_verify, lib.topk_cols_plan,
+                                lib.topk_cols_tree, lib.topk_cols_cache_write, lib.topk_cols_cache_move, lib.topk_cols_attend,
+                                lib.topk_cols_attend_workspace, lib.topk_cols_verify_tree)))
         _round = module
     return _round
 
@@ -571,6 +602,187 @@ def plan(lens, add, held, table, free_ids, free_count, block_size: int, capacity
             free_count, block_size, capacity, out["held"], out["free_count"], out["refused"], out["col_start"],
             out["col_lane"], out["col_pos"], out["slots"])
     return out
+
+
+def tree(parents, lens=None, col_start=None, lanes: int | None = None, words: int | None = None, mask=None,
+         positions=None, stream=None):
+    """Masks and positions of a round's trees (topk_cols_tree).
+
+    parents (C,): int32, for each column the column of its lane that it
+        follows (-1: none, as for a lane's column 0).
+    lens (lanes,): int32, the lanes' tokens before their columns (0 without).
+    col_start (lanes + 1,), or C / lanes columns for each of `lanes` lanes.
+    words: 32-bit words of a mask's row when mask is not given, at least a
+        32nd of the columns that a lane can have (default: C / 32).
+    Returns (mask, positions): int32 (C, words), bit i % 32 of word i / 32 set
+    for column i itself and its ancestors, and int32 (C,).  Rows of columns of
+    no lane are not written.
+    """
+    index = parents.get_device()
+    lanes = _lanes(col_start, lanes, lens)
+    if mask is None or positions is None:
+        import torch
+        C = parents.numel()
+        with _allocate(stream):
+            if mask is None:
+                mask = torch.empty((C, words or (C + 31) // 32), dtype=torch.int32, device=parents.device)
+            if positions is None:
+                positions = torch.empty(C, dtype=torch.int32, device=parents.device)
+    _launch("topk_cols_tree", _round_binding().tree, index, _raw_stream(index, stream), lanes, parents, lens, col_start, mask,
+            positions)
+    return mask, positions
+
+
+def verify_tree(target_values, target_ids, col_start, tokens, parents, uniforms, draft_values=None, draft_ids=None,
+                temperature: float = 1.0, top_p: float = 0.95, lanes: int | None = None, max_tokens: int | None = None,
+                out_tokens=None, out_columns=None, out_count=None, stream=None):
+    """Verify trees of drafts against the target's top-k lists
+    (topk_cols_verify_tree).
+
+    target_values, target_ids: (C, k), as a run on the target's logits wrote
+        them; lane l's columns are col_start[l]..col_start[l+1]-1, the first
+        its anchor (col_start None: the same number for each of `lanes`).
+    tokens, parents: (C,) int32, each column's token and the column that it
+        follows (see tree).
+    uniforms: (C, 2) float32 in [0, 1): the first judges the column's draft, the
+        second draws the token behind the column.
+    draft_values, draft_ids: (C, kq), row c the list that the children of column
+        c were sampled from; without them drafts count as certain.
+    Returns (tokens, columns, count): lane l commits tokens[l, :count[l]], the
+    accepted drafts and one token more; columns[l, :count[l]] are the columns
+    whose keys stay (KeyCache.move), the anchor's first; -1 follows.  max_tokens:
+    the row length when outputs are not given (default: C; pass the deepest path
+    + 1).
+    """
+    index = target_values.get_device()
+    lanes = _lanes(col_start, lanes)
+    if out_tokens is None or out_columns is None or out_count is None:
+        import torch
+        device = target_values.device
+        given = out_tokens if out_tokens is not None else out_columns
+        width = given.shape[-1] if given is not None else max_tokens or target_values.shape[0]
+        with _allocate(stream):
+            if out_tokens is None:
+                out_tokens = torch.empty((lanes, width), dtype=torch.int32, device=device)
+            if out_columns is None:
+                out_columns = torch.empty((lanes, width), dtype=torch.int32, device=device)
+            if out_count is None:
+                out_count = torch.empty(lanes, dtype=torch.int32, device=device)
+    _launch("topk_cols_verify_tree", _round_binding().verify_tree, index, _raw_stream(index, stream), lanes, target_values,
+            target_ids, col_start, tokens, parents, uniforms, draft_values, draft_ids, temperature, top_p, out_tokens,
+            out_columns, out_count)
+    return out_tokens, out_columns, out_count
+
+
+def _lanes(col_start, lanes, per_lane=None) -> int:
+    if lanes is not None:
+        return lanes
+    if col_start is not None:
+        return col_start.numel() - 1
+    if per_lane is not None:
+        return per_lane.numel()
+    raise ValueError("lanes is needed without col_start")
+
+
+class KeyCache:
+    """A paged cache of keys and values (topk_cache), whose slots plan gives out.
+
+    Describes tensors that the caller keeps: the object holds references to
+    them and no state of its own.  All are on one GPU.
+
+    keys, values: (layers, blocks, block_size, heads, dim), or without the
+        first for one layer; bfloat16, or float8_e4m3fn.  Any strides that are
+        multiples of 16 bytes (so heads may also lie outside of a block's
+        slots), the last 1; the same for both.  dim: a multiple of 16, at most
+        256.
+    key_scales, value_scales: with float8_e4m3fn, uint8 (or float8_e8m0fnu) of
+        the shape without dim, any strides, the same for both: a row stands for
+        its elements times 2^(scale - 127).
+    """
+
+    def __init__(self, keys, values, key_scales=None, value_scales=None):
+        import torch
+        formats = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
+        if keys.dim() not in (4, 5) or values.shape != keys.shape or keys.dtype not in formats \
+                or values.dtype != keys.dtype or keys.numel() == 0:
+            raise ValueError("keys and values must be (layers, blocks, block_size, heads, dim) tensors, bfloat16 or "
+                             "float8_e4m3fn")
+        fp8 = keys.dtype == torch.float8_e4m3fn
+        if (key_scales is None) == fp8 or (value_scales is None) == fp8:
+            raise ValueError("float8_e4m3fn needs key_scales and value_scales, bfloat16 has none")
+        self._tensors = tensors = [t for t in (keys, values, key_scales, value_scales) if t is not None]
+        self._index = keys.get_device()
+        if self._index < 0 or any(t.get_device() != self._index for t in tensors):
+            raise ValueError("the cache's tensors must be on one GPU")
+        if fp8 and any(t.shape != keys.shape[:-1] or t.dtype not in (torch.uint8, torch.float8_e8m0fnu)
+                       for t in (key_scales, value_scales)):
+            raise ValueError("scales must be uint8 tensors of the keys' shape without dim")
+        shape = tuple(keys.shape) if keys.dim() == 5 else (1, *keys.shape)
+        self.layers, self.blocks, self.block_size, self.heads, self.dim = shape
+
+        def strides(a, b, what):
+            # (a dimension of one entry has no stride)
+            s, t = ([0 if n == 1 else st for n, st in zip(x.shape, x.stride())] for x in (a, b))
+            if s != t:
+                raise ValueError(f"{what} must have the same strides")
+            return s if a.dim() == len(shape) - (what == "scales") else [0, *s]
+
+        layer, block, slot, head, last = strides(keys, values, "keys and values")
+        unit = 16 // keys.element_size()
+        if last != 1 or any(s % unit for s in (layer, block, slot, head)):
+            raise ValueError("keys and values must have strides of multiples of 16 bytes, the last 1")
+        scale = strides(key_scales, value_scales, "scales") if fp8 else [0, 0, 0, 0]
+        self._args = CacheArgs(
+            layers=self.layers, blocks=self.blocks, block_size=self.block_size, heads=self.heads, dim=self.dim,
+            format=formats[keys.dtype], keys=keys.data_ptr(), values=values.data_ptr(), layer_stride=layer,
+            block_stride=block, slot_stride=slot, head_stride=head,
+            key_scales=key_scales.data_ptr() if fp8 else 0, value_scales=value_scales.data_ptr() if fp8 else 0,
+            scale_layer_stride=scale[0], scale_block_stride=scale[1], scale_slot_stride=scale[2], scale_head_stride=scale[3])
+        self._address = ctypes.addressof(self._args)
+
+    def write(self, k, v, slots, layer: int = 0, stream=None) -> None:
+        """Write the columns' keys and values, (C, heads, dim) bf16 or fp32 with
+        any strides of multiples of 16 bytes (the last 1), into the slots (C,)
+        int64 that plan gave them; negative slots (the padding) are skipped
+        (topk_cols_cache_write)."""
+        _launch("topk_cols_cache_write", _round_binding().cache_write, self._index, _raw_stream(self._index, stream),
+                self._address, self._index, k, v, slots, layer)
+
+    def attend(self, q, lens, table, col_start=None, mask=None, positions=None, window: int = 0, scale=None,
+               layer: int = 0, out=None, stream=None):
+        """Attention of the columns over their lanes' tokens and ancestors
+        (topk_cols_attend); returns out.
+
+        q: (C, query heads, dim) bf16, any strides of multiples of 16 bytes (the
+            last 1); query head h reads key head h / (query heads / heads).
+        lens (lanes,), table (lanes, width): int32, as plan takes them: the
+            tokens before this round's, and the lanes' blocks.
+        col_start (lanes + 1,), or the same number of columns for each lane.
+        mask, positions: as tree gives them.  Without a mask the columns are a
+            chain (or a prompt); without positions column j's is lens + j.
+        window: only this many places up to the column's own, 0 for all.
+        scale: of the products, default dim ** -0.5.
+        out: like q (default: allocated; columns of no lane are then
+            uninitialised).
+        """
+        if scale is None:
+            scale = self.dim ** -0.5
+        if out is None:
+            import torch
+            with _allocate(stream):
+                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        with _allocate(stream):  # (the workspace)
+            _launch("topk_cols_attend", _round_binding().attend, self._index, _raw_stream(self._index, stream),
+                    self._address, self._index, q, lens, table, col_start, mask, positions, window, scale, layer, out)
+        return out
+
+    def move(self, lens, table, columns, stream=None) -> None:
+        """Close up the accepted paths, in all layers (topk_cols_cache_move):
+        what lies at place lens[l] + columns[l, i] of lane l goes to lens[l] + i.
+        columns (lanes, width): int32, as verify_tree gives them; lens (lanes,)
+        and table as for attend (lens without the accepted tokens)."""
+        _launch("topk_cols_cache_move", _round_binding().cache_move, self._index, _raw_stream(self._index, stream),
+                self._address, self._index, lens, table, columns)
 
 
 def topk_cols(x, V: int, C: int, k: int, dtype: str = "bf16", layout: str = "col", ld=None):

@@ -457,6 +457,252 @@ typedef struct {
  */
 int topk_cols_plan(const topk_plan_args *args, hipStream_t stream);
 
+/*
+ * Rounds whose drafts form a tree, and the cache that their keys go to.
+ *
+ * Column 0 of a lane is its anchor, the last committed token; the others are
+ * drafts, and parents[c] gives for column c, the lane's column j, the column
+ * of the lane that its token follows: parents[c] < j.  (A chain of drafts has
+ * parents -1, 0, 1, ...; a column whose entry is outside [0, j) follows none.)
+ * All arrays are packed like the columns (col_start, C).
+ *
+ *   topk_cols_tree         each column's ancestors, as a mask, and its position;
+ *   topk_cols_cache_write  the columns' keys and values into the slots of
+ *                          topk_cols_plan, which reserves them in column order:
+ *                          column j of lane l lies behind the lane's lens[l]
+ *                          tokens, at place lens[l] + j;
+ *   topk_cols_attend       attention of the columns over cache and ancestors;
+ *   topk_cols_verify_tree  the drafts that the target accepts: a path;
+ *   topk_cols_cache_move   the path's keys and values close up behind the
+ *                          lane's tokens.
+ *
+ * What is said above of the steps around the top-k holds for these too.
+ * Lengths below 0 count as 0.
+ */
+
+/*
+ * The tree of a round.
+ *
+ * parents: device, C.  lens: device, lanes, or NULL: 0.
+ * mask: device, C rows of mask_ld >= 1 words.  Bit i % 32 of word i / 32 of
+ *   column j's row is set if i == j or column i is an ancestor of j; all other
+ *   bits of the row are 0.  (Columns from 32*mask_ld on have no bit.)
+ * positions: device, C: lens[l] plus the number of the column's ancestors, the
+ *   place its token has in the text.
+ * Rows and positions of columns that belong to no lane are not written.
+ *
+ * Returns TOPK_ERR_INVALID_ARG for a NULL or misaligned pointer, C < 1, lanes
+ * < 1, mask_ld < 1 or lanes that do not divide C (col_start NULL);
+ * TOPK_ERR_UNSUPPORTED for lanes > TOPK_MAX_LANES or C or mask_ld beyond 2^31
+ * - 1; TOPK_ERR_HIP when the launch fails.
+ */
+int topk_cols_tree(int64_t lanes, int64_t C, const int32_t *col_start, const int32_t *parents, const int32_t *lens,
+                   uint32_t *mask, int64_t mask_ld, int32_t *positions, hipStream_t stream);
+
+typedef enum {
+    TOPK_CACHE_BF16 = 0, /* bfloat16 */
+    TOPK_CACHE_FP8 = 1   /* 8-bit floating point, e4m3 (no infinities), with a power of two for each row */
+} topk_cache_format;
+
+/* Largest head dimension of a cache. */
+#define TOPK_MAX_DIM 256
+
+/*
+ * A cache of keys and values in blocks, described by the caller (who owns its
+ * buffers): element d of head h of slot s in layer y is at
+ *   y*layer_stride + (s / block_size)*block_stride + (s % block_size)*slot_stride + h*head_stride + d
+ * of keys, or of values; in a TOPK_CACHE_FP8 cache a row (a slot's head) stands
+ * for its elements times 2^(b - 127), b being the byte at
+ *   y*scale_layer_stride + (s / block_size)*scale_block_stride + (s % block_size)*scale_slot_stride
+ *   + h*scale_head_stride
+ * of key_scales, or of value_scales.
+ */
+typedef struct {
+    int64_t layers;      /* >= 1 */
+    int64_t blocks;      /* of a layer, >= 1 */
+    int32_t block_size;  /* slots of a block, >= 1 */
+    int32_t heads;       /* key heads, >= 1 */
+    int32_t dim;         /* a multiple of 16, at most TOPK_MAX_DIM */
+    int32_t format;      /* topk_cache_format */
+    void *keys, *values; /* device, 16-byte aligned */
+    /* strides in elements, >= 0 and multiples of 16 bytes */
+    int64_t layer_stride, block_stride, slot_stride, head_stride;
+    uint8_t *key_scales, *value_scales; /* device; unused with TOPK_CACHE_BF16 */
+    int64_t scale_layer_stride, scale_block_stride, scale_slot_stride, scale_head_stride; /* in bytes, >= 0 */
+} topk_cache;
+
+typedef struct {
+    int64_t C;              /* columns, >= 1 */
+    int64_t layer;          /* of the cache, 0 .. layers - 1 */
+    int32_t dtype;          /* topk_dtype of keys and values */
+    const void *keys;       /* device, 16-byte aligned: element d of head h of column c at c*key_stride + h*key_head_stride + d */
+    const void *values;
+    int64_t key_stride, key_head_stride;     /* in elements, >= 0 and multiples of 16 bytes */
+    int64_t value_stride, value_head_stride;
+    const int64_t *slots;   /* device, C: where each column goes; outside the cache: nowhere */
+} topk_cache_write_args;
+
+/*
+ * Write keys and values into a layer of the cache.
+ *
+ * TOPK_CACHE_BF16: elements are rounded to bfloat16 (to nearest, ties to even).
+ * TOPK_CACHE_FP8: with a the largest finite |x_i| of a row (one head of one
+ * column, keys and values apart), e is the smallest whole number with a <=
+ * 448 * 2^e, at least -126; the row keeps x_i * 2^-e rounded to e4m3 (to
+ * nearest, ties to even) and the byte e + 127.  448 is the largest value of
+ * e4m3, so nothing overflows; infinities and NaN become NaN.  Multiplying by a
+ * power of two is exact: reading back rounds no further.
+ *
+ * Slots must differ from each other.
+ *
+ * Returns TOPK_ERR_INVALID_ARG for a NULL or misaligned pointer, or a value or
+ * stride out of the ranges above; TOPK_ERR_UNSUPPORTED for dim >
+ * TOPK_MAX_DIM, blocks*block_size beyond 2^31 - 1, layers*heads beyond 2^20 or
+ * C*heads beyond 2^26;
+ * TOPK_ERR_HIP when the launch fails.
+ */
+int topk_cols_cache_write(const topk_cache *cache, const topk_cache_write_args *args, hipStream_t stream);
+
+typedef struct {
+    int64_t lanes;            /* >= 1 */
+    int64_t C;                /* columns, >= 1 */
+    int64_t layer;            /* of the cache, 0 .. layers - 1 */
+    int32_t heads;            /* query heads, a multiple of the cache's heads: query head h reads head h / (heads / cache heads) */
+    int32_t window;           /* >= 0; 0: none */
+    float scale;              /* finite */
+    const void *q;            /* device, 16-byte aligned, bfloat16: element d of head h of column c at c*q_stride + h*q_head_stride + d */
+    int64_t q_stride, q_head_stride;     /* in elements, >= 0 and multiples of 8 */
+    const int32_t *col_start; /* device, lanes + 1, or NULL */
+    const int32_t *lens;      /* device, lanes: tokens of each lane before its columns */
+    const int32_t *table;     /* device, lanes rows of table_ld block ids */
+    int64_t table_ld;         /* >= 1 */
+    const uint32_t *mask;     /* device, C rows of mask_ld words (topk_cols_tree), or NULL: a chain */
+    int64_t mask_ld;          /* >= 1 with a mask */
+    const int32_t *positions; /* device, C, or NULL: lens[l] + j */
+    void *out;                /* device, 16-byte aligned, bfloat16, laid out like q by the strides below */
+    int64_t out_stride, out_head_stride;
+    void *workspace;          /* device, 256-byte aligned */
+    int64_t workspace_bytes;  /* at least what topk_cols_attend_workspace says */
+} topk_attend_args;
+
+/*
+ * Attention of a round's columns over the cache.
+ *
+ * For column c, column j of lane l (of n columns), and query head h:
+ *   out = sum_p w_p v_p / sum_p w_p,  w_p = exp(s_p - max s),  s_p = scale * (q . k_p)
+ * over the visible places p of the lane, k_p and v_p being the key and value
+ * in slot table[l][p / block_size]*block_size + p % block_size:
+ *   p < lens[l]:               visible, with a window if p > positions[c] - window
+ *                              (positions below lens[l] count as lens[l]);
+ *   lens[l] <= p < lens[l]+n:  visible if bit p - lens[l] of the column's mask is
+ *                              set (columns from 32*mask_ld on are not); without a
+ *                              mask if p - lens[l] <= j, with a window also
+ *                              j - (p - lens[l]) < window.
+ * A column with nothing visible, or whose scores are all -Inf, gets zeros.
+ * What lies in places that are not visible does not matter, NaN and infinities
+ * included.  Places beyond the table's row are not visible; block ids are cut
+ * to the cache's.  Columns that belong to no lane are not written.
+ *
+ * Products are of bfloat16 elements (an e4m3 element times its power of two is
+ * one, except that results below 2^-126 may be 0), sums are binary32; the
+ * weights are rounded to bfloat16 before the sum over values, and the result
+ * once to bfloat16.  The result does not depend on other lanes' contents, and
+ * the same call gives the same bits.
+ *
+ * The workspace holds partial results of places that several workgroups share;
+ * nothing in it is kept between calls.  Calls that may overlap need one each.
+ * out must not overlap q or the cache.
+ *
+ * Returns TOPK_ERR_INVALID_ARG for a NULL or misaligned pointer, a value or
+ * stride out of the ranges above, lanes that do not divide C (col_start NULL)
+ * or a workspace that is too small; TOPK_ERR_UNSUPPORTED for lanes >
+ * TOPK_MAX_LANES, dim > TOPK_MAX_DIM, table_ld, mask_ld or blocks*block_size
+ * beyond 2^31 - 1, layers*heads beyond 2^20 or C*heads beyond 2^26; TOPK_ERR_HIP
+ * when a launch fails.
+ */
+int topk_cols_attend(const topk_cache *cache, const topk_attend_args *args, hipStream_t stream);
+
+/* The bytes of workspace that topk_cols_attend needs for these arguments
+ * (whose pointers are not looked at): they depend on sizes only, not on the
+ * lanes' lengths.  Errors as for topk_cols_attend, bytes is then 0. */
+int topk_cols_attend_workspace(const topk_cache *cache, const topk_attend_args *args, int64_t *bytes);
+
+/*
+ * Close up an accepted path: for i = 0, 1, ..., width - 1 in this order, the
+ * keys and values of place lens[l] + columns[l*width + i] of lane l, in all
+ * layers, go to place lens[l] + i (as topk_cols_attend counts places; rows and
+ * scales are copied as they are).  Entries that are not larger than i, -1
+ * behind the path among them, are left out, and so are places outside the
+ * table's row and blocks outside the cache.  The entries of a lane that are
+ * carried out must increase (a path's do: a parent comes before its child).
+ *
+ * lens: device, lanes.  table: device, lanes rows of table_ld block ids.
+ * columns: device, lanes*width (topk_cols_verify_tree's out_columns).
+ *
+ * Returns TOPK_ERR_INVALID_ARG for a NULL or misaligned pointer, or a value or
+ * stride out of range; TOPK_ERR_UNSUPPORTED for lanes > TOPK_MAX_LANES, dim >
+ * TOPK_MAX_DIM, table_ld, width or blocks*block_size beyond 2^31 - 1, or
+ * layers*heads beyond 2^20; TOPK_ERR_HIP when a launch fails.
+ */
+int topk_cols_cache_move(const topk_cache *cache, int64_t lanes, const int32_t *lens, const int32_t *table,
+                         int64_t table_ld, const int32_t *columns, int64_t width, hipStream_t stream);
+
+typedef struct {
+    int64_t lanes;               /* >= 1 */
+    int32_t dtype;               /* topk_dtype of both lists' values */
+    int32_t k;                   /* entries of a target list, 1 .. TOPK_MAX_K */
+    int32_t kq;                  /* entries of a draft list, 1 .. TOPK_MAX_K (unused without draft lists) */
+    int64_t C;                   /* columns, >= 1 */
+    const int32_t *col_start;    /* device, lanes + 1, or NULL */
+    const void *target_values;   /* device, C*k, as a topk_cols run on the target's logits wrote them */
+    const int32_t *target_ids;   /* device, C*k */
+    const int32_t *tokens;       /* device, C: each column's token (the anchors' are not looked at) */
+    const int32_t *parents;      /* device, C */
+    const void *draft_values;    /* device, C*kq, or NULL: row c is the list that column c's children were sampled from */
+    const int32_t *draft_ids;    /* device, C*kq, or NULL together with draft_values */
+    const float *uniforms;       /* device, C*2, in [0, 1): u judges draft c, u' draws the token that follows column c */
+    double temperature;          /* >= 0, finite */
+    double top_p;                /* in (0, 1] */
+    int64_t max_tokens;          /* >= 1: entries of a lane in out_tokens and out_columns */
+    int32_t *out_tokens;         /* device, lanes*max_tokens */
+    int32_t *out_columns;        /* device, lanes*max_tokens */
+    int32_t *out_count;          /* device, lanes */
+} topk_verify_tree_args;
+
+/*
+ * Verify a tree of drafts against the target's top-k lists, from given random
+ * numbers, so that the tokens are distributed as samples of the target: the
+ * acceptance test of topk_cols_verify, with the siblings of a refused draft
+ * judged against what is left of the target's distribution (each of them
+ * sampled on its own from the same list; Miao and others, 2024).
+ *
+ * Distributions, and a token's probability in them, are those of
+ * topk_cols_verify.  Lane l starts at its column 0.  At column c, with w = p_c
+ * and W = 1, its children x are judged in the order of their columns:
+ *   x is accepted if u_x * q(x) * W < w(x), where q(x) is the probability of
+ *   x's token in column c's draft list (1 without lists) and w(x) the weight of
+ *   the first entry with that token, 0 if there is none; the lane goes on at x;
+ *   otherwise each w_i becomes max(w_i - W * q_i, 0), q_i being the probability
+ *   of entry i's token (without lists 1 for x's token, 0 for others), and W the
+ *   sum of them; if that is 0, w is p_c and W is 1 again.
+ * Where no child is accepted, or max_tokens - 1 are (no further one is judged
+ * then: w = p_c), the lane ends with entry i of column c, the smallest i of
+ * positive weight with R_{i+1} > u'_c * R_k, R_i being the sum of the first i
+ * weights (the last entry of positive weight where rounding leaves none).
+ * out_tokens[l*max_tokens ..] = the t accepted tokens, the last one, then -1;
+ * out_columns[l*max_tokens ..] = column 0, the t accepted columns, then -1;
+ * out_count[l] = t + 1.  A lane without columns gets only -1, and count 0.
+ *
+ * Arithmetic is IEEE double in the order written, exp and running sums as in
+ * topk_cols_verify.  The result is reproducible bit for bit.
+ *
+ * Returns TOPK_ERR_INVALID_ARG for a NULL or misaligned pointer, a value out of
+ * the ranges above, or lanes that do not divide C (col_start NULL);
+ * TOPK_ERR_UNSUPPORTED for lanes > TOPK_MAX_LANES, or C or max_tokens beyond
+ * 2^31 - 1; TOPK_ERR_HIP when the launch fails.
+ */
+int topk_cols_verify_tree(const topk_verify_tree_args *args, hipStream_t stream);
+
 /* A static, human-readable name for a status code.  Never NULL. */
 const char *topk_cols_status_string(int status);
 
