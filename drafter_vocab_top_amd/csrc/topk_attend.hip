@@ -2,131 +2,774 @@
 //
 //   out = sum_p w_p v_p / sum_p w_p,  w_p = exp(s_p - m),  s_p = scale (q . k_p)
 //
-// One wave per column and query head: 64 places at a time, a lane for each
-// place's score, then a lane for each element of the weighted sum; the running
-// maximum m, the sum of the weights and the output are rescaled when m grows.
+// The columns of a lane and the query heads of a key head share that key head's
+// keys and values: together they are the rows of one matrix, cut into items of
+// R = 16 kQueries rows.  An item's places are cut into steps of 128, 32 for
+// each of a workgroup's four waves.
+//
+// Products are 16 x 16 x 32 matrix instructions on transposed operands.
+// S^T = K Q^T has a query in each lane's column and keys in its registers, so
+// the running maximum and sum of a softmax need no other lane, and the weights
+// come out of it as the right operand of O^T = V^T W^T needs them: with lane
+// 16 g + r holding keys 4 g + i and 16 + 4 g + i, i < 4, the contraction just
+// runs over the 32 keys in that order.  Keys go from memory to the registers
+// where the instruction wants them (a lane has 16 bytes of one key), values
+// likewise: lane 16 g + r reads elements 8 r .. 8 r + 7 of its eight keys (rows
+// of 256 contiguous bytes), and byte permutations pair the keys of each element.
+// So nothing passes through LDS until the end.  The next keys are on their way
+// while weights are made and values multiplied, the next values while keys are.
+//
+// The maximum is only raised when a score passes it by more than 2^8 (weights
+// then stay below 2^8, which costs nothing in floating point), so most steps
+// neither exchange maxima nor rescale.
+//
+// The work, items times steps over all lanes, is cut into equal parts for the
+// workgroups of one wave of launches, whatever the lanes' lengths (read on the
+// device).  A part that ends inside an item leaves its partial maximum, sums
+// and output in the workspace, and a second kernel joins them.
+#include <algorithm>
+#include <type_traits>
+
 #include "topk_cache.hpp"
 
 namespace topk {
 
 namespace {
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kNone = -__builtin_inff();
+constexpr uint32_t kStep = 128;  // places of a step
+constexpr uint32_t kTile = 32;   // of one wave
 
-__device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) x = __builtin_fmaxf(x, __shfl_xor(x, s));
+// x, and no reason to compute what depends on it ahead of the loop that asks (the registers
+// would be missed in the loop).
+__device__ __forceinline__ uint32_t opaque(uint32_t x) {
+    asm volatile("" : "+v"(x));
     return x;
 }
 
-__device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) x += __shfl_xor(x, s);
-    return x;
+// What the second kernel needs to know of an item that a part ends in.
+struct Cut {
+    uint32_t more;  // further parts that hold pieces of it; 0: nothing to join
+    uint32_t first_row, rows, first_col, head;
+    uint32_t pad[3];
+};
+
+// Sizes of a launch that do not depend on what the device holds.
+struct Shape {
+    uint32_t workers;  // workgroups, a power of two
+    uint32_t shift;    // its logarithm
+    uint32_t rows;     // of an item
+    Divisor group;     // query heads of a key head
+    Cut* cuts;
+    float* sums;       // [2 workers][rows][2]: maximum and sum
+    float* parts;      // [2 workers][rows][DP]
+};
+
+struct LaneWork {
+    uint32_t cb, n, len, end;  // first column, columns, places before them, places
+    uint32_t first, steps;     // its first step, and how many
+    uint32_t tiles;            // items of a key head
+};
+
+__device__ __forceinline__ LaneWork lane_work(const AttendArgs& args, const Shape& sh, uint32_t l, int32_t b, int32_t e, int32_t len) {
+    LaneWork w;
+    uint32_t ce;
+    args.cols.cut(l, b, e, w.cb, ce);
+    w.n = ce - w.cb;
+    w.len = (uint32_t)max_i32(len, 0);
+    w.end = (uint32_t)min((uint64_t)w.len + w.n, (uint64_t)args.places);
+    const uint32_t all = (w.end + kStep - 1u) / kStep;
+    const uint32_t window = (uint32_t)args.a.window;
+    w.first = 0;
+    if (window && w.len + 1u > window) w.first = min_u32((w.len + 1u - window) / kStep, all - 1u);
+    w.steps = all - w.first;
+    w.tiles = (w.n * sh.group.d + sh.rows - 1u) / sh.rows;
+    if (w.n == 0) w.steps = w.tiles = 0;
+    return w;
 }
 
-__device__ __forceinline__ float scale_of(uint8_t b) { return __builtin_ldexpf(1.0f, (int)b - 127); }
+__device__ __forceinline__ uint64_t shfl_up_u64(uint64_t x, uint32_t by) {
+    return ((uint64_t)(uint32_t)__shfl_up((int)(uint32_t)(x >> 32), by) << 32) | (uint32_t)__shfl_up((int)(uint32_t)x, by);
+}
 
-__device__ __forceinline__ float bf16_value(uint16_t b) { return __builtin_bit_cast(float, (uint32_t)b << 16); }
+__device__ __forceinline__ uint32_t bcast(uint32_t x, uint32_t lane) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)x, (int)lane);
+}
 
-template <bool kFp8>
-__global__ __launch_bounds__(256) void attend_kernel(AttendArgs args) {
-    __shared__ float qs[4][TOPK_MAX_DIM];
-    const topk_attend_args& a = args.a;
-    const topk_cache& c = args.cache.c;
-    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u;
-    const uint32_t h = blockIdx.x;  // query head
-    const uint32_t kh = h / (uint32_t)(a.heads / c.heads);
-    for (int64_t l = blockIdx.y; l < a.lanes; l += gridDim.y) {
-        uint32_t cb, ce;
-        args.cols.range((uint32_t)l, cb, ce);
-        const uint32_t n = ce - cb;
-        const uint32_t len = (uint32_t)max_i32(a.lens[l], 0);
-        const uint32_t end = (uint32_t)min((uint64_t)len + n, (uint64_t)args.places);
-        const int32_t* table = a.table + l * a.table_ld;
-        for (uint32_t j0 = 0; j0 < n; j0 += 4u) {
-            const uint32_t j = j0 + wave;
-            const int64_t col = (int64_t)cb + min_u32(j, n - 1u);
-            __syncthreads();
-            for (uint32_t d = lane; d < (uint32_t)c.dim; d += 64u)
-                qs[wave][d] = bf16_value(static_cast<const uint16_t*>(a.q)[col * a.q_stride + (int64_t)h * a.q_head_stride + d]);
-            __syncthreads();
-            if (j >= n) continue;
-            int64_t lo = 0;  // the first visible place before len
-            if (a.window) lo = (a.positions ? max((int64_t)a.positions[col], (int64_t)len) : (int64_t)len + j) - a.window + 1;
-            float m = -__builtin_inff(), sum = 0.0f, o[4] = {};
-            for (uint32_t p0 = (uint32_t)min(max(lo, (int64_t)0), (int64_t)len) & ~63u; p0 < end; p0 += 64u) {
-                const uint32_t p = min_u32(p0 + lane, end - 1u);
-                bool seen = p0 + lane < end;
-                if (p < len) {
-                    seen = seen && (int64_t)p >= lo;
-                } else {
-                    const uint32_t i = p - len;
-                    if (a.mask) seen = seen && (int64_t)(i >> 5) < a.mask_ld && (a.mask[col * a.mask_ld + (i >> 5)] >> (i & 31u) & 1u);
-                    else seen = seen && i <= j && (!a.window || j - i < (uint32_t)a.window);
-                }
-                const uint32_t b = args.cache.block.div(p);
-                const int32_t id = min_i32(max_i32(table[b], 0), (int32_t)c.blocks - 1);
-                const uint32_t r = p - b * args.cache.block.d;
-                const int64_t at = (int64_t)id * c.block_stride + (int64_t)r * c.slot_stride + (int64_t)kh * c.head_stride;
-                const int64_t sat = (int64_t)id * c.scale_block_stride + (int64_t)r * c.scale_slot_stride + (int64_t)kh * c.scale_head_stride;
-                float s = 0.0f;
-                for (int32_t d = 0; d < c.dim; ++d) {
-                    float k;
-                    if constexpr (kFp8)
-                        k = __builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t*>(c.keys)[at + d], 0);
-                    else
-                        k = bf16_value(static_cast<const uint16_t*>(c.keys)[at + d]);
-                    s += qs[wave][d] * k;
-                }
-                if constexpr (kFp8) s *= scale_of(c.key_scales[sat]);
-                s = seen ? s * (a.scale * kLog2e) : -__builtin_inff();
-                const float top = __builtin_fmaxf(m, wave_max(s));
-                const float zero = top == -__builtin_inff() ? 0.0f : top;
-                const float old = __builtin_amdgcn_exp2f(m - zero);
-                float w = __builtin_amdgcn_exp2f(s - zero);
-                m = top;
-                sum = sum * old + wave_sum(w);
-                w = (float)(__bf16)w;
+__device__ __forceinline__ uint64_t bcast(uint64_t x, uint32_t lane) {
+    return ((uint64_t)bcast((uint32_t)(x >> 32), lane) << 32) | bcast((uint32_t)x, lane);
+}
+
+// The steps of all lanes (the sum), or with `find` the lane that step `at` of
+// them belongs to; `before` gets the steps of the lanes before it.  All of a
+// wave's threads take part, 64 lanes at a time.
+__device__ __forceinline__ uint64_t all_steps(const AttendArgs& args, const Shape& sh, bool find, uint64_t at, uint64_t& before,
+                                              uint32_t& lane, LaneWork& work) {
+    const uint32_t lanes = (uint32_t)args.a.lanes, id = threadIdx.x & 63u;
+    uint64_t sum = 0;
+    for (uint32_t l0 = 0; l0 < lanes; l0 += 64u) {
+        const uint32_t l = min_u32(l0 + id, lanes - 1u);
+        const int32_t* s = args.cols.at(l);
+        const int32_t b = s[0], e = s[args.cols.start ? 1 : 0], len = args.a.lens[l];
+        LaneWork w = lane_work(args, sh, l, b, e, len);
+        if (l0 + id >= lanes) w.steps = 0;
+        const uint64_t own = (uint64_t)w.steps * w.tiles * (uint32_t)args.cache.c.heads;
+        uint64_t run = own;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] *= old;
-                const unsigned long long visible = __ballot(seen);
-                for (int k = 0; k < 64; ++k) {
-                    if (!(visible >> k & 1ull)) continue;
-                    const float wk = __shfl(w, k);
-                    const int64_t ak = __shfl(at, k);
-                    float f = 1.0f;
-                    if constexpr (kFp8) f = scale_of(c.value_scales[__shfl(sat, k)]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int32_t d = (int32_t)lane + 64 * i;
-                        if (d >= c.dim) continue;
-                        if constexpr (kFp8) o[i] += wk * (f * __builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t*>(c.values)[ak + d], 0));
-                        else o[i] += wk * bf16_value(static_cast<const uint16_t*>(c.values)[ak + d]);
-                    }
-                }
+        for (uint32_t d = 1; d < 64u; d <<= 1) {
+            const uint64_t up = shfl_up_u64(run, d);
+            if (id >= d) run += up;
+        }
+        if (find) {
+            const unsigned long long m = __ballot(sum + run > at);
+            if (m) {
+                const uint32_t k = (uint32_t)__builtin_ctzll(m);
+                before = sum + bcast(run, k) - bcast(own, k);
+                lane = l0 + k;
+                work.cb = bcast(w.cb, k);
+                work.n = bcast(w.n, k);
+                work.len = bcast(w.len, k);
+                work.end = bcast(w.end, k);
+                work.first = bcast(w.first, k);
+                work.steps = bcast(w.steps, k);
+                work.tiles = bcast(w.tiles, k);
+                return sum;
             }
-            __bf16* to = static_cast<__bf16*>(a.out) + col * a.out_stride + (int64_t)h * a.out_head_stride;
+        }
+        sum += bcast(run, 63u);
+    }
+    return sum;
+}
+
+// A condition that is the same in all lanes, as the compiler has to know: a matrix
+// instruction takes no notice of lanes that are switched off, so none may
+// stand in a branch that is taken by switching them off.
+__device__ __forceinline__ bool uniform(bool x) { return __builtin_amdgcn_readfirstlane(x ? 1 : 0) != 0; }
+
+__device__ __forceinline__ uint32_t divide(uint64_t a, uint32_t b) {
+    return (a >> 32) == 0 ? (uint32_t)a / b : (uint32_t)(a / b);
+}
+
+// Bits of places [a, b) among the 32 from `base` on.
+__device__ __forceinline__ uint32_t range_bits(int64_t a, int64_t b, int64_t base) {
+    const int64_t lo = min(max(a - base, (int64_t)0), (int64_t)32), hi = min(max(b - base, lo), (int64_t)32);
+    return (uint32_t)((((uint64_t)1 << hi) - 1u) & ~(((uint64_t)1 << lo) - 1u));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    bf16x2 v;
+    v[0] = (__bf16)a;
+    v[1] = (__bf16)b;
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+__device__ __forceinline__ int32_t from_lane(int32_t x, uint32_t lane) { return __builtin_amdgcn_ds_bpermute((int)(lane << 2), x); }
+
+__device__ __forceinline__ float max_over_groups(float x) {
+    x = __builtin_fmaxf(x, __shfl_xor(x, 16));
+    return __builtin_fmaxf(x, __shfl_xor(x, 32));
+}
+
+__device__ __forceinline__ float sum_over_groups(float x) {
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
+}
+
+// Two e4m3 elements times a power of two, as bfloat16.
+template <bool kHigh>
+__device__ __forceinline__ uint32_t widen(uint32_t x, float scale) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, scale, kHigh));
+}
+
+// DP: dim rounded up to 64, 128 or 256; kWhole: dim is DP.
+template <int DP, bool kWhole, bool kFp8, int kQueries>
+struct Item {
+    static constexpr int kSize = kFp8 ? 1 : 2;
+    static constexpr int kKeySteps = DP / 32;                 // products of a score
+    static constexpr int kKeyLoads = kFp8 ? DP / 64 : DP / 32;
+    static constexpr int kHalf = DP < 128 ? DP : 128;         // elements of a value that 16 lanes read at once
+    static constexpr int kHalves = DP / kHalf;
+    static constexpr int kOwn = kHalf / 16;                   // of them one lane's
+    static constexpr int kValueWords = kOwn * kSize / 4;
+    static constexpr int kOut = DP / 16;                      // 16 x 16 tiles of O^T for 16 queries
+    static constexpr uint32_t kRows = 16 * kQueries;
+
+    bf16x8 q[kQueries][kKeySteps];
+    u32x4 k[2][kKeyLoads];
+    uint32_t v[8][kHalves][kValueWords];
+    f32x4 o[kQueries][kOut];
+    float m[kQueries], sum[kQueries];
+    uint32_t scales, next_scales;  // of key lane & 31: lanes 0 - 31 the keys', 32 - 63 the values'
+    // One lane's share of a tile's addresses: place base + (lane & 31).
+    struct Places {
+        uint32_t id, in_block;
+    };
+
+    __device__ __forceinline__ Places lookup(const AttendArgs& a, const int32_t* table, uint32_t base, uint32_t end, uint32_t lane) const {
+        const uint32_t p = min_u32(base + (lane & 31u), end - 1u), b = a.cache.block.div(p);
+        Places s;
+        s.id = (uint32_t)min_i32(max_i32(table[b], 0), (int32_t)a.cache.c.blocks - 1);
+        s.in_block = p - b * a.cache.block.d;
+        return s;
+    }
+
+    // Offset in bytes of the row of the place that lane `key` looked up.
+    struct Rows {
+        int32_t lo, hi;
+        __device__ __forceinline__ int64_t of(uint32_t key) const {
+            return (int64_t)(((uint64_t)(uint32_t)from_lane(hi, key) << 32) | (uint32_t)from_lane(lo, key));
+        }
+    };
+    __device__ __forceinline__ Rows rows_of(const AttendArgs& a, const Places& s) const {
+        const topk_cache& c = a.cache.c;
+        const int64_t at = ((int64_t)s.id * c.block_stride + (int64_t)s.in_block * c.slot_stride) * kSize;
+        return Rows{(int32_t)(uint32_t)at, (int32_t)(uint32_t)((uint64_t)at >> 32)};
+    }
+
+    __device__ __forceinline__ void load_scales(const AttendArgs& a, const Places& s, uint32_t head, uint32_t lane) {
+        if constexpr (kFp8) {
+            const topk_cache& c = a.cache.c;
+            const uint8_t* from = (lane & 32u) ? c.value_scales : c.key_scales;
+            next_scales = from[(int64_t)s.id * c.scale_block_stride + (int64_t)s.in_block * c.scale_slot_stride +
+                               (int64_t)head * c.scale_head_stride];
+        }
+    }
+
+    __device__ __forceinline__ float scale_from(uint32_t lane) const {
+        const uint32_t b = (uint32_t)from_lane((int32_t)scales, lane);
+        return __builtin_bit_cast(float, b ? b << 23 : 0x400000u);
+    }
+
+    __device__ __forceinline__ void load_keys(const AttendArgs& a, const uint8_t* keys, const Rows& at, uint32_t lane) {
+        const uint32_t g = lane >> 4;
+        const int32_t dim = a.cache.c.dim;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int32_t d = (int32_t)lane + 64 * i;
-                if (d < c.dim) to[d] = (__bf16)(m == -__builtin_inff() ? 0.0f : o[i] / sum);
+        for (int t = 0; t < 2; ++t) {
+            const uint8_t* row = keys + at.of((uint32_t)t * 16u + (lane & 15u)) + (kWhole ? g * 16u : 0u);
+#pragma unroll
+            for (int i = 0; i < kKeyLoads; ++i) {
+                // (past the row: its start, cleared below)
+                const int32_t d = i * (64 / kSize) + (kWhole ? 0 : (int32_t)g * (16 / kSize));
+                k[t][i] = *reinterpret_cast<const u32x4*>(row + (kWhole || d < dim ? d * kSize : 0));
             }
         }
     }
+
+    __device__ __forceinline__ void load_values(const AttendArgs& a, const uint8_t* values, const Rows& at, uint32_t lane) {
+        const uint32_t r = lane & 15u, g = lane >> 4;
+        const int32_t dim = a.cache.c.dim;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint8_t* row = values + at.of((uint32_t)(e >> 2) * 16u + g * 4u + (uint32_t)(e & 3)) + (kWhole ? r * (kOwn * kSize) : 0u);
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {
+                const int32_t d = h * kHalf + (kWhole ? 0 : (int32_t)r * kOwn);
+                const uint8_t* p = row + (kWhole || d < dim ? d * kSize : 0);
+                if constexpr (kValueWords == 4) {
+                    const u32x4 x = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[e][h][i] = x[i];
+                } else if constexpr (kValueWords == 2) {
+                    const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+                    v[e][h][0] = x[0];
+                    v[e][h][1] = x[1];
+                } else {
+                    v[e][h][0] = *reinterpret_cast<const uint32_t*>(p);
+                }
+            }
+        }
+    }
+
+    // The left operand of product `step` of keys 16 t .. 16 t + 15.
+    __device__ __forceinline__ bf16x8 key_operand(const AttendArgs& a, int t, int step, float scale, uint32_t lane) const {
+        u32x4 x;
+        int32_t d;  // this lane's first element
+        const int32_t g = (int32_t)(lane >> 4);
+        if constexpr (kFp8) {
+            const u32x4 raw = k[t][step / 2];
+            const uint32_t w0 = raw[2 * (step & 1)], w1 = raw[2 * (step & 1) + 1];
+            x[0] = widen<false>(w0, scale);
+            x[1] = widen<true>(w0, scale);
+            x[2] = widen<false>(w1, scale);
+            x[3] = widen<true>(w1, scale);
+            d = (step / 2) * 64 + g * 16 + (step & 1) * 8;
+        } else {
+            x = k[t][step];
+            d = step * 32 + g * 8;
+        }
+        if (!kWhole && d >= a.cache.c.dim) x = u32x4{0u, 0u, 0u, 0u};
+        return __builtin_bit_cast(bf16x8, x);
+    }
+
+    // The element of a row that this lane's operands of `step` start with.
+    __device__ __forceinline__ static int32_t operand_element(int step, uint32_t lane) {
+        const int32_t g = (int32_t)(lane >> 4);
+        return kFp8 ? (step / 2) * 64 + g * 16 + (step & 1) * 8 : step * 32 + g * 8;
+    }
+
+    // Rows first_row .. of the lane's matrix; a row past the last is the last
+    // again (it is not written).
+    __device__ __forceinline__ void load_queries(const AttendArgs& args, const Shape& sh, const LaneWork& w, uint32_t head, uint32_t first_row, uint32_t lane) {
+        const topk_attend_args& a = args.a;
+        const float c = a.scale;
+#pragma unroll
+        for (int n = 0; n < kQueries; ++n) {
+            const uint32_t row = min_u32(first_row + (uint32_t)n * 16u + (lane & 15u), w.n * sh.group.d - 1u);
+            const uint32_t j = sh.group.div(row), h = head * sh.group.d + (row - j * sh.group.d);
+            const uint16_t* from = static_cast<const uint16_t*>(a.q) + (int64_t)(w.cb + j) * a.q_stride + (int64_t)h * a.q_head_stride;
+#pragma unroll
+            for (int s = 0; s < kKeySteps; ++s) {
+                const int32_t d = operand_element(s, lane);
+                u32x4 x = u32x4{0u, 0u, 0u, 0u};
+                if ((kWhole || d < args.cache.c.dim) && c != 0.0f) x = *reinterpret_cast<const u32x4*>(from + d);
+                if (c < 0.0f) x ^= 0x80008000u;  // so that scores grow with the products
+                q[n][s] = __builtin_bit_cast(bf16x8, x);
+            }
+        }
+    }
+};
+
+template <int DP, bool kWhole, bool kFp8, int kQueries>
+__global__ __launch_bounds__(256, kQueries * DP <= 256 ? 2 : 1) void attend_kernel(AttendArgs args, Shape sh) {
+    using I = Item<DP, kWhole, kFp8, kQueries>;
+    constexpr uint32_t R = I::kRows;
+    constexpr uint32_t kPitch = DP + 4;  // floats of a row in LDS
+    __shared__ float lds_o[4][16][kPitch];
+    __shared__ float lds_m[4][R], lds_l[4][R];
+    const topk_attend_args& a = args.a;
+    const topk_cache& c = args.cache.c;
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    // consecutive parts go to one of the eight dies, whose workgroups share a cache
+    const uint32_t worker = sh.workers >= 8u ? (blockIdx.x & 7u) * (sh.workers >> 3) + (blockIdx.x >> 3) : blockIdx.x;
+    uint64_t before = 0;
+    uint32_t l = 0;
+    LaneWork w = {};
+    const uint64_t total = all_steps(args, sh, false, 0, before, l, w);
+    const uint64_t per = (total + sh.workers - 1u) >> sh.shift;
+    uint64_t at = per * worker;
+    const uint64_t stop = min(at + per, total);
+    uint32_t more = 0;  // parts behind this one that hold the rest of its last item
+    const float factor = a.scale == 0.0f ? 1.0f : __builtin_fabsf(a.scale) * kLog2e;
+    bool found = false;
+    while (at < stop) {
+        if (!found || at >= before + (uint64_t)w.steps * w.tiles * (uint32_t)c.heads) all_steps(args, sh, true, at, before, l, w);
+        found = true;
+        const uint64_t in_lane = at - before;
+        const uint32_t item = divide(in_lane, w.steps), step = (uint32_t)(in_lane - (uint64_t)item * w.steps);
+        const uint32_t head = item / w.tiles, first_row = (item - head * w.tiles) * R;
+        const uint32_t last_step = (uint32_t)min((uint64_t)w.steps, step + (stop - at));
+        const int32_t* table = a.table + (int64_t)l * a.table_ld;
+        const uint32_t rows = w.n * sh.group.d;
+
+        I it;
+        const uint32_t lane = opaque(threadIdx.x) & 63u, r = lane & 15u;
+        it.load_queries(args, sh, w, head, first_row, lane);
+        const uint8_t* keys = static_cast<const uint8_t*>(c.keys) + (int64_t)head * c.head_stride * I::kSize;
+        const uint8_t* values = static_cast<const uint8_t*>(c.values) + (int64_t)head * c.head_stride * I::kSize;
+#pragma unroll
+        for (int n = 0; n < kQueries; ++n) {
+            it.m[n] = kNone;
+            it.sum[n] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < I::kOut; ++i) it.o[n][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        // each row's column, the first place of those before the lane's columns that it sees
+        uint32_t column[kQueries];
+        int64_t low[kQueries];
+        int64_t all_see = 0;  // all rows see the places from here up to the lane's columns
+#pragma unroll
+        for (int n = 0; n < kQueries; ++n) {
+            const uint32_t j = sh.group.div(min_u32(first_row + (uint32_t)n * 16u + r, rows - 1u));
+            column[n] = j;
+            low[n] = 0;
+            if (a.window) {
+                const int64_t position = a.positions ? max((int64_t)a.positions[w.cb + j], (int64_t)w.len) : (int64_t)w.len + j;
+                low[n] = position - a.window + 1;
+                int64_t x = low[n];
+#pragma unroll
+                for (int s = 1; s < 16; s <<= 1) x = max(x, (int64_t)__shfl_xor((long long)x, s));
+                all_see = max(all_see, x);
+            }
+        }
+        all_see = (int64_t)bcast((uint64_t)all_see, 0);
+
+        uint32_t base = (w.first + step) * kStep + wave * kTile;
+        const uint32_t stop_at = min_u32((w.first + last_step) * kStep, w.end);
+        typename I::Places next = {};
+        if (base < stop_at) {
+            const typename I::Places now = it.lookup(args, table, base, w.end, lane);
+            next = it.lookup(args, table, base + kStep, w.end, lane);
+            const typename I::Rows at = it.rows_of(args, now);
+            it.load_scales(args, now, head, lane);
+            it.load_keys(args, keys, at, lane);
+            it.load_values(args, values, at, lane);
+        }
+        // One tile; `masked` where some row may not see some place of it.
+        auto tile = [&](auto masked_tile) __attribute__((always_inline)) {
+            constexpr bool masked = decltype(masked_tile)::value;
+            const uint32_t lane = opaque(threadIdx.x & 63u), r = lane & 15u, g = lane >> 4;
+            it.scales = it.next_scales;
+            // scores of 32 places
+            f32x4 s[kQueries][2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const float scale = kFp8 ? it.scale_from((uint32_t)t * 16u + r) : 1.0f;
+#pragma unroll
+                for (int n = 0; n < kQueries; ++n) s[n][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < I::kKeySteps; ++i) {
+                    const bf16x8 x = it.key_operand(args, t, i, scale, lane);
+#pragma unroll
+                    for (int n = 0; n < kQueries; ++n)
+                        s[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, it.q[n][i], s[n][t], 0, 0, 0);
+                }
+            }
+            // the next keys (past the end: the last place again)
+            __builtin_amdgcn_sched_barrier(0);
+            const typename I::Places now = next;
+            next = it.lookup(args, table, base + 2 * kStep, w.end, lane);
+            const typename I::Rows at = it.rows_of(args, now);
+            it.load_scales(args, now, head, lane);
+            it.load_keys(args, keys, at, lane);
+            __builtin_amdgcn_sched_barrier(0);
+
+            uint32_t seen[kQueries];
+            bf16x8 weights[kQueries];
+#pragma unroll
+            for (int n = 0; n < kQueries; ++n) {
+                if constexpr (masked) {
+                    const int64_t len = w.len, end = w.end, b0 = base;
+                    uint32_t bits = range_bits(low[n], min(len, end), b0);
+                    if (base + kTile > w.len) {
+                        uint32_t own;
+                        if (a.mask) {
+                            const uint32_t* row = a.mask + (int64_t)(w.cb + column[n]) * a.mask_ld;
+                            const uint32_t i0 = base > w.len ? base - w.len : 0u, word = i0 >> 5;
+                            const uint32_t x0 = (int64_t)word < a.mask_ld ? row[word] : 0u;
+                            const uint32_t x1 = (int64_t)word + 1 < a.mask_ld ? row[word + 1] : 0u;
+                            if (base >= w.len) own = (uint32_t)((((uint64_t)x1 << 32) | x0) >> (i0 & 31u));
+                            else own = x0 << (w.len - base);
+                        } else {
+                            const int64_t j = column[n];
+                            own = range_bits(a.window ? len + j - a.window + 1 : len, len + j + 1, b0);
+                        }
+                        bits |= own & range_bits(len, end, b0);
+                    }
+                    seen[n] = bits;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[n][t][e] = (bits >> (t * 16 + (int)g * 4 + e)) & 1u ? s[n][t][e] : kNone;
+                }
+                float top = __builtin_fmaxf(__builtin_fmaxf(s[n][0][0], s[n][0][1]), __builtin_fmaxf(s[n][0][2], s[n][0][3]));
+                top = __builtin_fmaxf(top, __builtin_fmaxf(__builtin_fmaxf(s[n][1][0], s[n][1][1]), __builtin_fmaxf(s[n][1][2], s[n][1][3])));
+                top *= factor;
+                if (__ballot(top > it.m[n] + 8.0f)) {
+                    const float now_m = __builtin_fmaxf(it.m[n], max_over_groups(top));
+                    const float old = __builtin_amdgcn_exp2f(it.m[n] - (now_m == kNone ? 0.0f : now_m));
+                    it.m[n] = now_m;
+                    it.sum[n] *= old;
+#pragma unroll
+                    for (int i = 0; i < I::kOut; ++i) it.o[n][i] *= old;
+                }
+                const float zero = it.m[n] == kNone ? 0.0f : it.m[n];
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][e >> 2][e & 3], factor, -zero));
+                    it.sum[n] += x[e];
+                }
+                u32x4 y;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+                weights[n] = __builtin_bit_cast(bf16x8, y);
+            }
+
+            // values, two elements of a key in each word
+            uint32_t pairs[8][I::kHalves][I::kOwn / 2];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float scale = kFp8 ? it.scale_from(32u + (uint32_t)(e >> 2) * 16u + g * 4u + (uint32_t)(e & 3)) : 1.0f;
+#pragma unroll
+                for (int h = 0; h < I::kHalves; ++h)
+#pragma unroll
+                    for (int i = 0; i < I::kValueWords; ++i) {
+                        const uint32_t x = it.v[e][h][i];
+                        if constexpr (kFp8) {
+                            pairs[e][h][2 * i] = widen<false>(x, scale);
+                            pairs[e][h][2 * i + 1] = widen<true>(x, scale);
+                        } else {
+                            pairs[e][h][i] = x;
+                        }
+                    }
+            }
+            bool odd = false;  // a row may not see a value that is not finite, which a weight of 0 does not remove
+            if constexpr (masked) {
+                bool found_odd = false;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t p = base + (uint32_t)(e >> 2) * 16u + g * 4u + (uint32_t)(e & 3);
+#pragma unroll
+                    for (int h = 0; h < I::kHalves; ++h)
+#pragma unroll
+                        for (int i = 0; i < I::kOwn / 2; ++i) {
+                            if (p >= w.end) pairs[e][h][i] = 0u;
+                            const uint32_t x = pairs[e][h][i];
+                            found_odd |= (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
+                        }
+                }
+                odd = uniform(__ballot(found_odd) != 0ull);
+            }
+#pragma unroll
+            for (int h = 0; h < I::kHalves; ++h)
+#pragma unroll
+                for (int i = 0; i < I::kOwn; ++i) {
+                    u32x4 x;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[e] = __builtin_amdgcn_perm(pairs[2 * e + 1][h][i / 2], pairs[2 * e][h][i / 2], i & 1 ? 0x07060302u : 0x05040100u);
+                    if (!odd) {
+#pragma unroll
+                        for (int n = 0; n < kQueries; ++n)
+                            it.o[n][h * I::kOwn + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), weights[n],
+                                                                                              it.o[n][h * I::kOwn + i], 0, 0, 0);
+                    } else {
+                        // one query after another, with what it does not see taken out of the values
+#pragma unroll
+                        for (int n = 0; n < kQueries; ++n)
+                            for (uint32_t one = 0; one < 16u; ++one) {
+                                const uint32_t bits = bcast(seen[n], one) >> (g * 4u);
+                                u32x4 y;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t two = bits >> ((e >> 1) * 16 + (e & 1) * 2);
+                                    y[e] = x[e] & ((two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u));
+                                }
+                                const f32x4 z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, y), weights[n],
+                                                                                       it.o[n][h * I::kOwn + i], 0, 0, 0);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) it.o[n][h * I::kOwn + i][k] = r == one ? z[k] : it.o[n][h * I::kOwn + i][k];
+                            }
+                    }
+                }
+            __builtin_amdgcn_sched_barrier(0);
+            it.load_values(args, values, at, lane);
+        };
+        for (; base < stop_at; base += kStep) {
+            if (uniform(base + kTile > w.len || (int64_t)base < all_see)) tile(std::true_type());
+            else tile(std::false_type());
+        }
+
+        // the four waves' sums together
+        const uint32_t tid_ = opaque(threadIdx.x), r_ = tid_ & 15u, g_ = (tid_ >> 4) & 3u;
+        const bool direct = step == 0 && last_step == w.steps;
+        const uint32_t slot = 2u * worker + (step == 0 ? 1u : 0u);
+#pragma unroll
+        for (int n = 0; n < kQueries; ++n) {
+            const float sum = sum_over_groups(it.sum[n]);
+            if (g_ == 0) {
+                lds_m[wave][n * 16 + (int)r_] = it.m[n];
+                lds_l[wave][n * 16 + (int)r_] = sum;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < kQueries; ++n) {
+            float top = kNone;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = __builtin_fmaxf(top, lds_m[k][n * 16 + (int)r_]);
+            const float mine = __builtin_amdgcn_exp2f(it.m[n] - (top == kNone ? 0.0f : top));
+#pragma unroll
+            for (int h = 0; h < I::kHalves; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int i = 0; i < I::kOwn; i += 4) {
+                        f32x4 x;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) x[k] = it.o[n][h * I::kOwn + i + k][e] * mine;
+                        *reinterpret_cast<f32x4*>(&lds_o[wave][r_][h * I::kHalf + ((int)g_ * 4 + e) * I::kOwn + i]) = x;
+                    }
+            __syncthreads();
+            // 16 threads a row
+            const uint32_t q = tid_ >> 4, part = tid_ & 15u, row = (uint32_t)n * 16u + q;
+            float all = kNone, sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) all = __builtin_fmaxf(all, lds_m[k][row]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sum += lds_l[k][row] * __builtin_amdgcn_exp2f(lds_m[k][row] - (all == kNone ? 0.0f : all));
+            const uint32_t d0 = part * (DP / 16);
+            float y[DP / 16];
+#pragma unroll
+            for (int i = 0; i < DP / 16; i += 4) {
+                f32x4 x = *reinterpret_cast<const f32x4*>(&lds_o[0][q][d0 + i]);
+#pragma unroll
+                for (int k = 1; k < 4; ++k) x += *reinterpret_cast<const f32x4*>(&lds_o[k][q][d0 + i]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[i + k] = x[k];
+            }
+            if (!direct) {
+                float* to = sh.parts + ((int64_t)slot * R + row) * DP + d0;
+#pragma unroll
+                for (int i = 0; i < DP / 16; i += 4) *reinterpret_cast<f32x4*>(to + i) = f32x4{y[i], y[i + 1], y[i + 2], y[i + 3]};
+                if (part == 0) {
+                    sh.sums[((int64_t)slot * R + row) * 2] = all;
+                    sh.sums[((int64_t)slot * R + row) * 2 + 1] = sum;
+                }
+            } else if (first_row + row < rows && (int32_t)d0 < c.dim) {
+                const uint32_t j = sh.group.div(first_row + row), h = head * sh.group.d + (first_row + row - j * sh.group.d);
+                uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + (int64_t)(w.cb + j) * a.out_stride +
+                                                           (int64_t)h * a.out_head_stride + d0);
+                const float inverse = 1.0f / sum;
+#pragma unroll
+                for (int i = 0; i < DP / 16; i += 2)
+                    if ((int32_t)d0 + i < c.dim) to[i / 2] = sum == 0.0f ? 0u : pack_bf16(y[i] * inverse, y[i + 1] * inverse);
+            }
+            __syncthreads();
+        }
+        at += last_step - step;
+        if (at == stop && step == 0 && last_step < w.steps) {
+            more = (uint32_t)(((uint64_t)(w.steps - last_step) + per - 1u) / per);
+            if (tid_ == 0) sh.cuts[worker] = Cut{more, first_row, rows, w.cb, head, {}};
+        }
+    }
+    if (more == 0 && threadIdx.x == 0) sh.cuts[worker].more = 0;
+}
+
+// Joins the pieces of the items that a part ends in: a workgroup for two rows (DP =
+// 128) of one, its waves share the pieces.
+template <int DP>
+__global__ __launch_bounds__(256) void join_kernel(AttendArgs args, Shape sh) {
+    constexpr uint32_t kThreads = DP / 4;           // of a row
+    constexpr uint32_t kRowsAtOnce = 64 / kThreads; // of a wave
+    __shared__ float lds_m[4][kRowsAtOnce], lds_l[4][kRowsAtOnce];
+    __shared__ f32x4 lds_o[4][64];
+    const uint32_t worker = blockIdx.x, lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+    const Cut cut = sh.cuts[worker];
+    const uint32_t q = lane / kThreads, d = (lane % kThreads) * 4u, row = blockIdx.y * kRowsAtOnce + q;
+    if (cut.more == 0 || cut.first_row + blockIdx.y * kRowsAtOnce >= cut.rows) return;
+    float m = kNone, sum = 0.0f;
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (uint32_t i = wave; i <= cut.more; i += 4u) {
+        const uint32_t slot = i == 0 ? 2u * worker + 1u : 2u * (worker + i);
+        const int64_t at = (int64_t)slot * sh.rows + row;
+        const float m1 = sh.sums[2 * at], l1 = sh.sums[2 * at + 1];
+        const f32x4 o1 = *reinterpret_cast<const f32x4*>(sh.parts + at * DP + d);
+        const float top = __builtin_fmaxf(m, m1), zero = top == kNone ? 0.0f : top;
+        const float f0 = __builtin_amdgcn_exp2f(m - zero), f1 = __builtin_amdgcn_exp2f(m1 - zero);
+        sum = sum * f0 + l1 * f1;
+        o = o * f0 + o1 * f1;
+        m = top;
+    }
+    if (lane % kThreads == 0) {
+        lds_m[wave][q] = m;
+        lds_l[wave][q] = sum;
+    }
+    lds_o[wave][lane] = o;
+    __syncthreads();
+    if (wave != 0 || cut.first_row + row >= cut.rows) return;
+    float top = kNone;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = __builtin_fmaxf(top, lds_m[k][q]);
+    sum = 0.0f;
+    o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float f = __builtin_amdgcn_exp2f(lds_m[k][q] - (top == kNone ? 0.0f : top));
+        sum += lds_l[k][q] * f;
+        o += lds_o[k][lane] * f;
+    }
+    if ((int32_t)d >= args.cache.c.dim) return;
+    const uint32_t j = sh.group.div(cut.first_row + row), h = cut.head * sh.group.d + (cut.first_row + row - j * sh.group.d);
+    uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(args.a.out) + (int64_t)(cut.first_col + j) * args.a.out_stride +
+                                               (int64_t)h * args.a.out_head_stride + d);
+    const float inverse = 1.0f / sum;
+    to[0] = sum == 0.0f ? 0u : pack_bf16(o[0] * inverse, o[1] * inverse);
+    to[1] = sum == 0.0f ? 0u : pack_bf16(o[2] * inverse, o[3] * inverse);
+}
+
+int padded_dim(const AttendArgs& a) { return a.cache.c.dim <= 64 ? 64 : a.cache.c.dim <= 128 ? 128 : 256; }
+
+// 16 rows for each of these.
+int queries_of(const AttendArgs& a) {
+    const int64_t rows = (a.a.C + a.a.lanes - 1) / a.a.lanes * (a.a.heads / a.cache.c.heads);
+    if (rows <= 16) return 1;
+    if (rows <= 32 || padded_dim(a) == 256) return 2;
+    return 4;
+}
+
+Shape shape_of(const AttendArgs& a, int64_t* bytes) {
+    Shape s = {};
+    const int queries = queries_of(a), dp = padded_dim(a);
+    s.rows = 16u * (uint32_t)queries;
+    s.group = Divisor::of((uint32_t)(a.a.heads / a.cache.c.heads));
+    // at most so many parts as workgroups run at once, and as there are steps
+    const int64_t most = queries * dp <= 256 ? 512 : 256;
+    const int64_t items = a.cache.c.heads * ((a.a.C * s.group.d + s.rows - 1) / s.rows + a.a.lanes);
+    const int64_t span = a.a.window ? std::min<int64_t>(a.places, (int64_t)a.a.window + a.a.C + kStep) : a.places;
+    const int64_t steps = std::min<int64_t>(most, (span + kStep - 1) / kStep + 1);
+    while ((int64_t)1 << s.shift < std::min(most, items * steps)) ++s.shift;
+    s.workers = 1u << s.shift;
+    const int64_t cuts = (sizeof(Cut) * s.workers + 255) / 256 * 256;
+    const int64_t sums = (int64_t)2 * s.workers * s.rows * 2 * sizeof(float);
+    const int64_t parts = (int64_t)2 * s.workers * s.rows * dp * sizeof(float);
+    *bytes = cuts + sums + parts;
+    uint8_t* p = static_cast<uint8_t*>(a.a.workspace);
+    s.cuts = reinterpret_cast<Cut*>(p);
+    s.sums = reinterpret_cast<float*>(p + cuts);
+    s.parts = reinterpret_cast<float*>(p + cuts + sums);
+    return s;
+}
+
+template <int DP, bool kWhole, bool kFp8, int kQueries>
+hipError_t launch(const AttendArgs& a, hipStream_t stream) {
+    int64_t bytes;
+    const Shape s = shape_of(a, &bytes);
+    hipLaunchKernelGGL((attend_kernel<DP, kWhole, kFp8, kQueries>), dim3(s.workers), dim3(256), 0, stream, a, s);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    hipLaunchKernelGGL((join_kernel<DP>), dim3(s.workers, s.rows * DP / 256), dim3(256), 0, stream, a, s);
+    return hipGetLastError();
+}
+
+template <int DP, bool kWhole, bool kFp8>
+hipError_t launch_queries(const AttendArgs& a, hipStream_t stream) {
+    const int n = queries_of(a);
+    if (n == 1) return launch<DP, kWhole, kFp8, 1>(a, stream);
+    if (n == 2) return launch<DP, kWhole, kFp8, 2>(a, stream);
+    if constexpr (DP <= 128) return launch<DP, kWhole, kFp8, 4>(a, stream);
+    return hipErrorInvalidValue;
+}
+
+template <int DP, bool kFp8>
+hipError_t launch_whole(const AttendArgs& a, hipStream_t stream) {
+    return a.cache.c.dim == DP ? launch_queries<DP, true, kFp8>(a, stream) : launch_queries<DP, false, kFp8>(a, stream);
+}
+
+template <bool kFp8>
+hipError_t launch_dim(const AttendArgs& a, hipStream_t stream) {
+    const int dp = padded_dim(a);
+    if (dp == 64) return launch_whole<64, kFp8>(a, stream);
+    if (dp == 128) return launch_whole<128, kFp8>(a, stream);
+    return launch_whole<256, kFp8>(a, stream);
 }
 
 }  // namespace
 
-int64_t attend_workspace(const AttendArgs&) { return 0; }
+int64_t attend_workspace(const AttendArgs& a) {
+    int64_t bytes;
+    shape_of(a, &bytes);
+    return bytes;
+}
 
 hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
-    const dim3 grid((uint32_t)a.a.heads, (uint32_t)(a.a.lanes < kGridY ? a.a.lanes : kGridY));
-    if (a.cache.c.format == TOPK_CACHE_FP8) hipLaunchKernelGGL(attend_kernel<true>, grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL(attend_kernel<false>, grid, dim3(256), 0, stream, a);
-    return hipGetLastError();
+    return a.cache.c.format == TOPK_CACHE_FP8 ? launch_dim<true>(a, stream) : launch_dim<false>(a, stream);
 }
 
 }  // namespace topk
