@@ -314,6 +314,56 @@ struct Item {
         return kFp8 ? (step / 2) * 64 + g * 16 + (step & 1) * 8 : step * 32 + g * 8;
     }
 
+    // Adds the values that are not finite, each to the rows that see it.
+    __device__ __forceinline__ void add_odd(const AttendArgs& a, const int32_t* table, const uint8_t* values, uint32_t head, uint32_t base,
+                                            uint32_t end, const uint32_t (&seen)[kQueries], const bf16x8 (&weights)[kQueries], uint32_t lane) {
+        const uint32_t r = lane & 15u, g = lane >> 4;
+        const Places s = lookup(a, table, base, end, lane);
+        const Rows at = rows_of(a, s);
+        uint32_t scale_bits = 0;
+        if constexpr (kFp8) {
+            const topk_cache& c = a.cache.c;
+            scale_bits = c.value_scales[(int64_t)s.id * c.scale_block_stride + (int64_t)s.in_block * c.scale_slot_stride +
+                                        (int64_t)head * c.scale_head_stride];
+            scale_bits = scale_bits ? scale_bits << 23 : 0x400000u;
+        }
+        for (uint32_t key = 0; key < kTile && base + key < end; ++key) {
+            const uint8_t* row = values + at.of(key);
+            const float scale = __builtin_bit_cast(float, from_lane((int32_t)scale_bits, key));
+            float weight[kQueries];
+            bool sees[kQueries];
+#pragma unroll
+            for (int n = 0; n < kQueries; ++n) {
+                const u32x4 y = __builtin_bit_cast(u32x4, weights[n]);
+                const uint32_t at_word = (key >> 4) * 2u + ((key >> 1) & 1u);  // keys 16 t + 4 g + i: word 2 t + i / 2 of group g
+                const uint32_t both = at_word == 0 ? y[0] : at_word == 1 ? y[1] : at_word == 2 ? y[2] : y[3];
+                const uint32_t x = (uint32_t)from_lane((int32_t)both, r + 16u * ((key >> 2) & 3u));
+                weight[n] = __builtin_bit_cast(float, key & 1u ? x & 0xFFFF0000u : x << 16);
+                sees[n] = seen[n] >> key & 1u;
+            }
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int32_t d = h * kHalf + ((int32_t)g * 4 + e) * kOwn;
+                    const uint8_t* from = row + (kWhole || d < a.cache.c.dim ? d * kSize : 0);
+#pragma unroll
+                    for (int i = 0; i < kOwn; i += 2) {
+                        uint32_t x;
+                        if constexpr (kFp8) x = widen<false>(*reinterpret_cast<const uint16_t*>(from + i), scale);
+                        else x = *reinterpret_cast<const uint32_t*>(from + 2 * i);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float v1 = __builtin_bit_cast(float, k ? x & 0xFFFF0000u : x << 16);
+#pragma unroll
+                            for (int n = 0; n < kQueries; ++n)
+                                if (sees[n] && !__builtin_isfinite(v1)) o[n][h * kOwn + i + k][e] += weight[n] * v1;
+                        }
+                    }
+                }
+        }
+    }
+
     // Rows first_row .. of the lane's matrix; a row past the last is the last
     // again (it is not written).
     __device__ __forceinline__ void load_queries(const AttendArgs& args, const Shape& sh, const LaneWork& w, uint32_t head, uint32_t first_row, uint32_t lane) {
@@ -337,7 +387,7 @@ struct Item {
 };
 
 template <int DP, bool kWhole, bool kFp8, int kQueries>
-__global__ __launch_bounds__(256, kQueries * DP <= 256 ? 2 : 1) void attend_kernel(AttendArgs args, Shape sh) {
+__global__ __launch_bounds__(256, DP < 256 && kQueries * DP <= 256 ? 2 : 1) void attend_kernel(AttendArgs args, Shape sh) {
     using I = Item<DP, kWhole, kFp8, kQueries>;
     constexpr uint32_t R = I::kRows;
     constexpr uint32_t kPitch = DP + 4;  // floats of a row in LDS
@@ -413,7 +463,7 @@ __global__ __launch_bounds__(256, kQueries * DP <= 256 ? 2 : 1) void attend_kern
         }
         // One tile; `masked` where some row may not see some place of it.
         auto tile = [&](auto masked_tile) __attribute__((always_inline)) {
-            constexpr bool masked = decltype(masked_tile)::value;
+            const bool masked = masked_tile;
             const uint32_t lane = opaque(threadIdx.x & 63u), r = lane & 15u, g = lane >> 4;
             it.scales = it.next_scales;
             // scores of 32 places
@@ -440,11 +490,11 @@ __global__ __launch_bounds__(256, kQueries * DP <= 256 ? 2 : 1) void attend_kern
             it.load_keys(args, keys, at, lane);
             __builtin_amdgcn_sched_barrier(0);
 
-            uint32_t seen[kQueries];
+            uint32_t seen[kQueries] = {};
             bf16x8 weights[kQueries];
 #pragma unroll
             for (int n = 0; n < kQueries; ++n) {
-                if constexpr (masked) {
+                if (masked) {
                     const int64_t len = w.len, end = w.end, b0 = base;
                     uint32_t bits = range_bits(low[n], min(len, end), b0);
                     if (base + kTile > w.len) {
@@ -510,22 +560,24 @@ __global__ __launch_bounds__(256, kQueries * DP <= 256 ? 2 : 1) void attend_kern
                         }
                     }
             }
-            bool odd = false;  // a row may not see a value that is not finite, which a weight of 0 does not remove
-            if constexpr (masked) {
-                bool found_odd = false;
+            // A row may not see a value that is not finite, which a weight of 0 does not
+            // remove: such values count as 0 here and are added below, one by one.
+            bool odd = false;
+            if (masked) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const uint32_t p = base + (uint32_t)(e >> 2) * 16u + g * 4u + (uint32_t)(e & 3);
+                    const bool past = base + (uint32_t)(e >> 2) * 16u + g * 4u + (uint32_t)(e & 3) >= w.end;
 #pragma unroll
                     for (int h = 0; h < I::kHalves; ++h)
 #pragma unroll
                         for (int i = 0; i < I::kOwn / 2; ++i) {
-                            if (p >= w.end) pairs[e][h][i] = 0u;
-                            const uint32_t x = pairs[e][h][i];
-                            found_odd |= (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
+                            uint32_t x = past ? 0u : pairs[e][h][i];
+                            const bool low_odd = (x & 0x7F80u) == 0x7F80u, high_odd = (x & 0x7F800000u) == 0x7F800000u;
+                            odd |= low_odd || high_odd;
+                            x &= low_odd ? 0xFFFF0000u : ~0u;
+                            pairs[e][h][i] = x & (high_odd ? 0xFFFFu : ~0u);
                         }
                 }
-                odd = uniform(__ballot(found_odd) != 0ull);
             }
 #pragma unroll
             for (int h = 0; h < I::kHalves; ++h)
@@ -535,36 +587,17 @@ __global__ __launch_bounds__(256, kQueries * DP <= 256 ? 2 : 1) void attend_kern
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         x[e] = __builtin_amdgcn_perm(pairs[2 * e + 1][h][i / 2], pairs[2 * e][h][i / 2], i & 1 ? 0x07060302u : 0x05040100u);
-                    if (!odd) {
 #pragma unroll
-                        for (int n = 0; n < kQueries; ++n)
-                            it.o[n][h * I::kOwn + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), weights[n],
-                                                                                              it.o[n][h * I::kOwn + i], 0, 0, 0);
-                    } else {
-                        // one query after another, with what it does not see taken out of the values
-#pragma unroll
-                        for (int n = 0; n < kQueries; ++n)
-                            for (uint32_t one = 0; one < 16u; ++one) {
-                                const uint32_t bits = bcast(seen[n], one) >> (g * 4u);
-                                u32x4 y;
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const uint32_t two = bits >> ((e >> 1) * 16 + (e & 1) * 2);
-                                    y[e] = x[e] & ((two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u));
-                                }
-                                const f32x4 z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, y), weights[n],
-                                                                                       it.o[n][h * I::kOwn + i], 0, 0, 0);
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) it.o[n][h * I::kOwn + i][k] = r == one ? z[k] : it.o[n][h * I::kOwn + i][k];
-                            }
-                    }
+                    for (int n = 0; n < kQueries; ++n)
+                        it.o[n][h * I::kOwn + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), weights[n],
+                                                                                          it.o[n][h * I::kOwn + i], 0, 0, 0);
                 }
+            if (uniform(masked && __ballot(odd) != 0ull)) it.add_odd(args, table, values, head, base, w.end, seen, weights, lane);
             __builtin_amdgcn_sched_barrier(0);
             it.load_values(args, values, at, lane);
         };
         for (; base < stop_at; base += kStep) {
-            if (uniform(base + kTile > w.len || (int64_t)base < all_see)) tile(std::true_type());
-            else tile(std::false_type());
+            tile(uniform(base + kTile > w.len || (int64_t)base < all_see));
         }
 
         // the four waves' sums together
@@ -711,7 +744,7 @@ Shape shape_of(const AttendArgs& a, int64_t* bytes) {
     s.rows = 16u * (uint32_t)queries;
     s.group = Divisor::of((uint32_t)(a.a.heads / a.cache.c.heads));
     // at most so many parts as workgroups run at once, and as there are steps
-    const int64_t most = queries * dp <= 256 ? 512 : 256;
+    const int64_t most = dp < 256 && queries * dp <= 256 ? 512 : 256;
     const int64_t items = a.cache.c.heads * ((a.a.C * s.group.d + s.rows - 1) / s.rows + a.a.lanes);
     const int64_t span = a.a.window ? std::min<int64_t>(a.places, (int64_t)a.a.window + a.a.C + kStep) : a.places;
     const int64_t steps = std::min<int64_t>(most, (span + kStep - 1) / kStep + 1);
