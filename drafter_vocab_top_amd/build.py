@@ -21,7 +21,7 @@ LIBRARY = os.path.join(HERE, "libtopk_cols.so")
 SOURCES = [os.path.join(CSRC, n) for n in ("topk_col.hip", "topk_row.hip", "topk_onewave.hip",
                                             "topk_sample.hip", "topk_noalloc.hip", "topk_cols_api.cpp",
                                             "topk_adjust.hip", "topk_count.hip", "topk_verify.hip", "topk_plan.hip",
-                                            "topk_round_api.cpp", "topk_tree.hip", "topk_cache.hip", "topk_attend.hip",
+                                            "topk_round_api.cpp", "topk_tree.hip", "topk_cache.hip", "topk_attend.hip", "topk_attend_rows.hip",
                                             "topk_verify_tree.hip", "topk_cache_api.cpp")]
 OBJDIR = os.path.join(ROOT, "_build")
 # Per-source flags.  The column kernel takes its ticket before ranking and
@@ -39,7 +39,7 @@ EXTRA_FLAGS = {"topk_col.hip": ["-mllvm", "-amdgpu-atomic-optimizer-strategy=Non
 STREAM_SOURCE = os.path.join(CSRC, "stream_read.hip")
 STREAM_LIBRARY = os.path.join(HERE, "libstream_read.so")
 HEADERS = [os.path.join(CSRC, n) for n in ("topk_device.hpp", "topk_col_common.hpp", "topk_internal.hpp", "topk_draw.hpp",
-                                            "topk_round.hpp", "topk_lists.hpp", "topk_cache.hpp")] + \
+                                            "topk_round.hpp", "topk_lists.hpp", "topk_cache.hpp", "topk_attend.hpp")] + \
           [os.path.join(INCLUDE, "topk_cols.h")]
 # The compiled part of the Python binding (host code against torch's headers).
 # It holds what it was built for, since it fits no other torch or Python.

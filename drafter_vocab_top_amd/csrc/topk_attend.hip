@@ -28,165 +28,15 @@
 // device).  A part that ends inside an item leaves its partial maximum, sums
 // and output in the workspace, and a second kernel joins them.
 #include <algorithm>
-#include <type_traits>
 
-#include "topk_cache.hpp"
+#include "topk_attend.hpp"
 
 namespace topk {
 
 namespace {
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kNone = -__builtin_inff();
 constexpr uint32_t kStep = 128;  // places of a step
 constexpr uint32_t kTile = 32;   // of one wave
-
-// x, and no reason to compute what depends on it ahead of the loop that asks (the registers
-// would be missed in the loop).
-__device__ __forceinline__ uint32_t opaque(uint32_t x) {
-    asm volatile("" : "+v"(x));
-    return x;
-}
-
-// What the second kernel needs to know of an item that a part ends in.
-struct Cut {
-    uint32_t more;  // further parts that hold pieces of it; 0: nothing to join
-    uint32_t first_row, rows, first_col, head;
-    uint32_t pad[3];
-};
-
-// Sizes of a launch that do not depend on what the device holds.
-struct Shape {
-    uint32_t workers;  // workgroups, a power of two
-    uint32_t shift;    // its logarithm
-    uint32_t rows;     // of an item
-    Divisor group;     // query heads of a key head
-    Cut* cuts;
-    float* sums;       // [2 workers][rows][2]: maximum and sum
-    float* parts;      // [2 workers][rows][DP]
-};
-
-struct LaneWork {
-    uint32_t cb, n, len, end;  // first column, columns, places before them, places
-    uint32_t first, steps;     // its first step, and how many
-    uint32_t tiles;            // items of a key head
-};
-
-__device__ __forceinline__ LaneWork lane_work(const AttendArgs& args, const Shape& sh, uint32_t l, int32_t b, int32_t e, int32_t len) {
-    LaneWork w;
-    uint32_t ce;
-    args.cols.cut(l, b, e, w.cb, ce);
-    w.n = ce - w.cb;
-    w.len = (uint32_t)max_i32(len, 0);
-    w.end = (uint32_t)min((uint64_t)w.len + w.n, (uint64_t)args.places);
-    const uint32_t all = (w.end + kStep - 1u) / kStep;
-    const uint32_t window = (uint32_t)args.a.window;
-    w.first = 0;
-    if (window && w.len + 1u > window) w.first = min_u32((w.len + 1u - window) / kStep, all - 1u);
-    w.steps = all - w.first;
-    w.tiles = (w.n * sh.group.d + sh.rows - 1u) / sh.rows;
-    if (w.n == 0) w.steps = w.tiles = 0;
-    return w;
-}
-
-__device__ __forceinline__ uint64_t shfl_up_u64(uint64_t x, uint32_t by) {
-    return ((uint64_t)(uint32_t)__shfl_up((int)(uint32_t)(x >> 32), by) << 32) | (uint32_t)__shfl_up((int)(uint32_t)x, by);
-}
-
-__device__ __forceinline__ uint32_t bcast(uint32_t x, uint32_t lane) {
-    return (uint32_t)__builtin_amdgcn_readlane((int)x, (int)lane);
-}
-
-__device__ __forceinline__ uint64_t bcast(uint64_t x, uint32_t lane) {
-    return ((uint64_t)bcast((uint32_t)(x >> 32), lane) << 32) | bcast((uint32_t)x, lane);
-}
-
-// The steps of all lanes (the sum), or with `find` the lane that step `at` of
-// them belongs to; `before` gets the steps of the lanes before it.  All of a
-// wave's threads take part, 64 lanes at a time.
-__device__ __forceinline__ uint64_t all_steps(const AttendArgs& args, const Shape& sh, bool find, uint64_t at, uint64_t& before,
-                                              uint32_t& lane, LaneWork& work) {
-    const uint32_t lanes = (uint32_t)args.a.lanes, id = threadIdx.x & 63u;
-    uint64_t sum = 0;
-    for (uint32_t l0 = 0; l0 < lanes; l0 += 64u) {
-        const uint32_t l = min_u32(l0 + id, lanes - 1u);
-        const int32_t* s = args.cols.at(l);
-        const int32_t b = s[0], e = s[args.cols.start ? 1 : 0], len = args.a.lens[l];
-        LaneWork w = lane_work(args, sh, l, b, e, len);
-        if (l0 + id >= lanes) w.steps = 0;
-        const uint64_t own = (uint64_t)w.steps * w.tiles * (uint32_t)args.cache.c.heads;
-        uint64_t run = own;
-#pragma unroll
-        for (uint32_t d = 1; d < 64u; d <<= 1) {
-            const uint64_t up = shfl_up_u64(run, d);
-            if (id >= d) run += up;
-        }
-        if (find) {
-            const unsigned long long m = __ballot(sum + run > at);
-            if (m) {
-                const uint32_t k = (uint32_t)__builtin_ctzll(m);
-                before = sum + bcast(run, k) - bcast(own, k);
-                lane = l0 + k;
-                work.cb = bcast(w.cb, k);
-                work.n = bcast(w.n, k);
-                work.len = bcast(w.len, k);
-                work.end = bcast(w.end, k);
-                work.first = bcast(w.first, k);
-                work.steps = bcast(w.steps, k);
-                work.tiles = bcast(w.tiles, k);
-                return sum;
-            }
-        }
-        sum += bcast(run, 63u);
-    }
-    return sum;
-}
-
-// A condition that is the same in all lanes, as the compiler has to know: a matrix
-// instruction takes no notice of lanes that are switched off, so none may
-// stand in a branch that is taken by switching them off.
-__device__ __forceinline__ bool uniform(bool x) { return __builtin_amdgcn_readfirstlane(x ? 1 : 0) != 0; }
-
-__device__ __forceinline__ uint32_t divide(uint64_t a, uint32_t b) {
-    return (a >> 32) == 0 ? (uint32_t)a / b : (uint32_t)(a / b);
-}
-
-// Bits of places [a, b) among the 32 from `base` on.
-__device__ __forceinline__ uint32_t range_bits(int64_t a, int64_t b, int64_t base) {
-    const int64_t lo = min(max(a - base, (int64_t)0), (int64_t)32), hi = min(max(b - base, lo), (int64_t)32);
-    return (uint32_t)((((uint64_t)1 << hi) - 1u) & ~(((uint64_t)1 << lo) - 1u));
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    bf16x2 v;
-    v[0] = (__bf16)a;
-    v[1] = (__bf16)b;
-    return __builtin_bit_cast(uint32_t, v);
-}
-
-__device__ __forceinline__ int32_t from_lane(int32_t x, uint32_t lane) { return __builtin_amdgcn_ds_bpermute((int)(lane << 2), x); }
-
-__device__ __forceinline__ float max_over_groups(float x) {
-    x = __builtin_fmaxf(x, __shfl_xor(x, 16));
-    return __builtin_fmaxf(x, __shfl_xor(x, 32));
-}
-
-__device__ __forceinline__ float sum_over_groups(float x) {
-    x += __shfl_xor(x, 16);
-    return x + __shfl_xor(x, 32);
-}
-
-// Two e4m3 elements times a power of two, as bfloat16.
-template <bool kHigh>
-__device__ __forceinline__ uint32_t widen(uint32_t x, float scale) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, scale, kHigh));
-}
 
 // DP: dim rounded up to 64, 128 or 256; kWhole: dim is DP.
 template <int DP, bool kWhole, bool kFp8, int kQueries>
@@ -243,8 +93,7 @@ struct Item {
     }
 
     __device__ __forceinline__ float scale_from(uint32_t lane) const {
-        const uint32_t b = (uint32_t)from_lane((int32_t)scales, lane);
-        return __builtin_bit_cast(float, b ? b << 23 : 0x400000u);
+        return power_of((uint32_t)from_lane((int32_t)scales, lane));
     }
 
     __device__ __forceinline__ void load_keys(const AttendArgs& a, const uint8_t* keys, const Rows& at, uint32_t lane) {
@@ -320,25 +169,20 @@ struct Item {
         const uint32_t r = lane & 15u, g = lane >> 4;
         const Places s = lookup(a, table, base, end, lane);
         const Rows at = rows_of(a, s);
-        uint32_t scale_bits = 0;
+        uint32_t scale_byte = 0;
         if constexpr (kFp8) {
             const topk_cache& c = a.cache.c;
-            scale_bits = c.value_scales[(int64_t)s.id * c.scale_block_stride + (int64_t)s.in_block * c.scale_slot_stride +
+            scale_byte = c.value_scales[(int64_t)s.id * c.scale_block_stride + (int64_t)s.in_block * c.scale_slot_stride +
                                         (int64_t)head * c.scale_head_stride];
-            scale_bits = scale_bits ? scale_bits << 23 : 0x400000u;
-        }
+                    }
         for (uint32_t key = 0; key < kTile && base + key < end; ++key) {
             const uint8_t* row = values + at.of(key);
-            const float scale = __builtin_bit_cast(float, from_lane((int32_t)scale_bits, key));
+            const float scale = power_of((uint32_t)from_lane((int32_t)scale_byte, key));
             float weight[kQueries];
             bool sees[kQueries];
 #pragma unroll
             for (int n = 0; n < kQueries; ++n) {
-                const u32x4 y = __builtin_bit_cast(u32x4, weights[n]);
-                const uint32_t at_word = (key >> 4) * 2u + ((key >> 1) & 1u);  // keys 16 t + 4 g + i: word 2 t + i / 2 of group g
-                const uint32_t both = at_word == 0 ? y[0] : at_word == 1 ? y[1] : at_word == 2 ? y[2] : y[3];
-                const uint32_t x = (uint32_t)from_lane((int32_t)both, r + 16u * ((key >> 2) & 3u));
-                weight[n] = __builtin_bit_cast(float, key & 1u ? x & 0xFFFF0000u : x << 16);
+                weight[n] = weight_of(weights[n], key, r);
                 sees[n] = seen[n] >> key & 1u;
             }
 #pragma unroll
@@ -387,7 +231,7 @@ struct Item {
 };
 
 template <int DP, bool kWhole, bool kFp8, int kQueries>
-__global__ __launch_bounds__(256, DP < 256 && kQueries * DP <= 256 ? 2 : 1) void attend_kernel(AttendArgs args, Shape sh) {
+__global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_kernel(AttendArgs args, Shape sh) {
     using I = Item<DP, kWhole, kFp8, kQueries>;
     constexpr uint32_t R = I::kRows;
     constexpr uint32_t kPitch = DP + 4;  // floats of a row in LDS
@@ -401,7 +245,7 @@ __global__ __launch_bounds__(256, DP < 256 && kQueries * DP <= 256 ? 2 : 1) void
     uint64_t before = 0;
     uint32_t l = 0;
     LaneWork w = {};
-    const uint64_t total = all_steps(args, sh, false, 0, before, l, w);
+    const uint64_t total = all_steps<kStep>(args, sh, false, 0, before, l, w);
     const uint64_t per = (total + sh.workers - 1u) >> sh.shift;
     uint64_t at = per * worker;
     const uint64_t stop = min(at + per, total);
@@ -409,7 +253,7 @@ __global__ __launch_bounds__(256, DP < 256 && kQueries * DP <= 256 ? 2 : 1) void
     const float factor = a.scale == 0.0f ? 1.0f : __builtin_fabsf(a.scale) * kLog2e;
     bool found = false;
     while (at < stop) {
-        if (!found || at >= before + (uint64_t)w.steps * w.tiles * (uint32_t)c.heads) all_steps(args, sh, true, at, before, l, w);
+        if (!found || at >= before + (uint64_t)w.steps * w.tiles * (uint32_t)c.heads) all_steps<kStep>(args, sh, true, at, before, l, w);
         found = true;
         const uint64_t in_lane = at - before;
         const uint32_t item = divide(in_lane, w.steps), step = (uint32_t)(in_lane - (uint64_t)item * w.steps);
@@ -438,10 +282,8 @@ __global__ __launch_bounds__(256, DP < 256 && kQueries * DP <= 256 ? 2 : 1) void
         for (int n = 0; n < kQueries; ++n) {
             const uint32_t j = sh.group.div(min_u32(first_row + (uint32_t)n * 16u + r, rows - 1u));
             column[n] = j;
-            low[n] = 0;
+            low[n] = first_seen(args, w, j);
             if (a.window) {
-                const int64_t position = a.positions ? max((int64_t)a.positions[w.cb + j], (int64_t)w.len) : (int64_t)w.len + j;
-                low[n] = position - a.window + 1;
                 int64_t x = low[n];
 #pragma unroll
                 for (int s = 1; s < 16; s <<= 1) x = max(x, (int64_t)__shfl_xor((long long)x, s));
@@ -461,9 +303,8 @@ __global__ __launch_bounds__(256, DP < 256 && kQueries * DP <= 256 ? 2 : 1) void
             it.load_keys(args, keys, at, lane);
             it.load_values(args, values, at, lane);
         }
-        // One tile; `masked` where some row may not see some place of it.
-        auto tile = [&](auto masked_tile) __attribute__((always_inline)) {
-            const bool masked = masked_tile;
+        for (; base < stop_at; base += kStep) {
+            const bool masked = uniform(base + kTile > w.len || (int64_t)base < all_see);  // some row may not see all
             const uint32_t lane = opaque(threadIdx.x & 63u), r = lane & 15u, g = lane >> 4;
             it.scales = it.next_scales;
             // scores of 32 places
@@ -494,52 +335,8 @@ __global__ __launch_bounds__(256, DP < 256 && kQueries * DP <= 256 ? 2 : 1) void
             bf16x8 weights[kQueries];
 #pragma unroll
             for (int n = 0; n < kQueries; ++n) {
-                if (masked) {
-                    const int64_t len = w.len, end = w.end, b0 = base;
-                    uint32_t bits = range_bits(low[n], min(len, end), b0);
-                    if (base + kTile > w.len) {
-                        uint32_t own;
-                        if (a.mask) {
-                            const uint32_t* row = a.mask + (int64_t)(w.cb + column[n]) * a.mask_ld;
-                            const uint32_t i0 = base > w.len ? base - w.len : 0u, word = i0 >> 5;
-                            const uint32_t x0 = (int64_t)word < a.mask_ld ? row[word] : 0u;
-                            const uint32_t x1 = (int64_t)word + 1 < a.mask_ld ? row[word + 1] : 0u;
-                            if (base >= w.len) own = (uint32_t)((((uint64_t)x1 << 32) | x0) >> (i0 & 31u));
-                            else own = x0 << (w.len - base);
-                        } else {
-                            const int64_t j = column[n];
-                            own = range_bits(a.window ? len + j - a.window + 1 : len, len + j + 1, b0);
-                        }
-                        bits |= own & range_bits(len, end, b0);
-                    }
-                    seen[n] = bits;
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[n][t][e] = (bits >> (t * 16 + (int)g * 4 + e)) & 1u ? s[n][t][e] : kNone;
-                }
-                float top = __builtin_fmaxf(__builtin_fmaxf(s[n][0][0], s[n][0][1]), __builtin_fmaxf(s[n][0][2], s[n][0][3]));
-                top = __builtin_fmaxf(top, __builtin_fmaxf(__builtin_fmaxf(s[n][1][0], s[n][1][1]), __builtin_fmaxf(s[n][1][2], s[n][1][3])));
-                top *= factor;
-                if (__ballot(top > it.m[n] + 8.0f)) {
-                    const float now_m = __builtin_fmaxf(it.m[n], max_over_groups(top));
-                    const float old = __builtin_amdgcn_exp2f(it.m[n] - (now_m == kNone ? 0.0f : now_m));
-                    it.m[n] = now_m;
-                    it.sum[n] *= old;
-#pragma unroll
-                    for (int i = 0; i < I::kOut; ++i) it.o[n][i] *= old;
-                }
-                const float zero = it.m[n] == kNone ? 0.0f : it.m[n];
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][e >> 2][e & 3], factor, -zero));
-                    it.sum[n] += x[e];
-                }
-                u32x4 y;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
-                weights[n] = __builtin_bit_cast(bf16x8, y);
+                if (masked) seen[n] = seen_bits(args, w, column[n], low[n], base);
+                weights[n] = weigh<true>(s[n], masked, seen[n], factor, g, it.m[n], it.sum[n], it.o[n]);
             }
 
             // values, two elements of a key in each word
@@ -570,13 +367,8 @@ __global__ __launch_bounds__(256, DP < 256 && kQueries * DP <= 256 ? 2 : 1) void
 #pragma unroll
                     for (int h = 0; h < I::kHalves; ++h)
 #pragma unroll
-                        for (int i = 0; i < I::kOwn / 2; ++i) {
-                            uint32_t x = past ? 0u : pairs[e][h][i];
-                            const bool low_odd = (x & 0x7F80u) == 0x7F80u, high_odd = (x & 0x7F800000u) == 0x7F800000u;
-                            odd |= low_odd || high_odd;
-                            x &= low_odd ? 0xFFFF0000u : ~0u;
-                            pairs[e][h][i] = x & (high_odd ? 0xFFFFu : ~0u);
-                        }
+                        for (int i = 0; i < I::kOwn / 2; ++i)
+                            pairs[e][h][i] = only_finite(past ? 0u : pairs[e][h][i], odd);
                 }
             }
 #pragma unroll
@@ -595,9 +387,6 @@ __global__ __launch_bounds__(256, DP < 256 && kQueries * DP <= 256 ? 2 : 1) void
             if (uniform(masked && __ballot(odd) != 0ull)) it.add_odd(args, table, values, head, base, w.end, seen, weights, lane);
             __builtin_amdgcn_sched_barrier(0);
             it.load_values(args, values, at, lane);
-        };
-        for (; base < stop_at; base += kStep) {
-            tile(uniform(base + kTile > w.len || (int64_t)base < all_see));
         }
 
         // the four waves' sums together
@@ -728,26 +517,26 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs args, Shape sh) {
     to[1] = sum == 0.0f ? 0u : pack_bf16(o[2] * inverse, o[3] * inverse);
 }
 
-int padded_dim(const AttendArgs& a) { return a.cache.c.dim <= 64 ? 64 : a.cache.c.dim <= 128 ? 128 : 256; }
-
-// 16 rows for each of these.
-int queries_of(const AttendArgs& a) {
+// Rows of an item: those of an average lane's columns and a key head's queries, rounded up.  Up to 32 the
+// waves of a workgroup share the places, beyond that the rows (topk_attend_rows.hip).
+uint32_t rows_of(const AttendArgs& a) {
     const int64_t rows = (a.a.C + a.a.lanes - 1) / a.a.lanes * (a.a.heads / a.cache.c.heads);
-    if (rows <= 16) return 1;
-    if (rows <= 32 || padded_dim(a) == 256) return 2;
-    return 4;
+    if (rows <= 16) return 16;
+    if (rows <= 32 && padded_dim(a) < 256) return 32;
+    return rows <= 64 || padded_dim(a) == 256 ? 64 : 128;
 }
 
 Shape shape_of(const AttendArgs& a, int64_t* bytes) {
     Shape s = {};
-    const int queries = queries_of(a), dp = padded_dim(a);
-    s.rows = 16u * (uint32_t)queries;
+    const int dp = padded_dim(a);
+    s.rows = rows_of(a);
     s.group = Divisor::of((uint32_t)(a.a.heads / a.cache.c.heads));
+    const int64_t step = s.rows <= 32 ? kStep : kRowsStep;
     // at most so many parts as workgroups run at once, and as there are steps
-    const int64_t most = dp < 256 && queries * dp <= 256 ? 512 : 256;
+    const int64_t most = dp < 256 ? 512 : 256;
     const int64_t items = a.cache.c.heads * ((a.a.C * s.group.d + s.rows - 1) / s.rows + a.a.lanes);
-    const int64_t span = a.a.window ? std::min<int64_t>(a.places, (int64_t)a.a.window + a.a.C + kStep) : a.places;
-    const int64_t steps = std::min<int64_t>(most, (span + kStep - 1) / kStep + 1);
+    const int64_t span = a.a.window ? std::min<int64_t>(a.places, (int64_t)a.a.window + a.a.C + step) : a.places;
+    const int64_t steps = std::min<int64_t>(most, (span + step - 1) / step + 1);
     while ((int64_t)1 << s.shift < std::min(most, items * steps)) ++s.shift;
     s.workers = 1u << s.shift;
     const int64_t cuts = (sizeof(Cut) * s.workers + 255) / 256 * 256;
@@ -762,22 +551,21 @@ Shape shape_of(const AttendArgs& a, int64_t* bytes) {
 }
 
 template <int DP, bool kWhole, bool kFp8, int kQueries>
-hipError_t launch(const AttendArgs& a, hipStream_t stream) {
-    int64_t bytes;
-    const Shape s = shape_of(a, &bytes);
+void launch(const AttendArgs& a, const Shape& s, hipStream_t stream) {
     hipLaunchKernelGGL((attend_kernel<DP, kWhole, kFp8, kQueries>), dim3(s.workers), dim3(256), 0, stream, a, s);
-    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    hipLaunchKernelGGL((join_kernel<DP>), dim3(s.workers, s.rows * DP / 256), dim3(256), 0, stream, a, s);
-    return hipGetLastError();
 }
 
 template <int DP, bool kWhole, bool kFp8>
 hipError_t launch_queries(const AttendArgs& a, hipStream_t stream) {
-    const int n = queries_of(a);
-    if (n == 1) return launch<DP, kWhole, kFp8, 1>(a, stream);
-    if (n == 2) return launch<DP, kWhole, kFp8, 2>(a, stream);
-    if constexpr (DP <= 128) return launch<DP, kWhole, kFp8, 4>(a, stream);
-    return hipErrorInvalidValue;
+    int64_t bytes;
+    const Shape s = shape_of(a, &bytes);
+    if (s.rows == 16) launch<DP, kWhole, kFp8, 1>(a, s, stream);
+    else if (s.rows > 32) launch_attend_rows(a, s, stream);
+    if constexpr (DP < 256)
+        if (s.rows == 32) launch<DP, kWhole, kFp8, 2>(a, s, stream);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    hipLaunchKernelGGL((join_kernel<DP>), dim3(s.workers, s.rows * DP / 256), dim3(256), 0, stream, a, s);
+    return hipGetLastError();
 }
 
 template <int DP, bool kFp8>

@@ -1,0 +1,250 @@
+// What the kernels of topk_cols_attend share: how the work of all lanes is cut
+// into parts, which places a row sees, and the weights of a softmax.
+#pragma once
+
+#include "topk_cache.hpp"
+
+namespace topk {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kNone = -__builtin_inff();
+// x, and no reason to compute what depends on it ahead of the loop that asks (the registers
+// would be missed in the loop).
+__device__ __forceinline__ uint32_t opaque(uint32_t x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// What the second kernel needs to know of an item that a part ends in.
+struct Cut {
+    uint32_t more;  // further parts that hold pieces of it; 0: nothing to join
+    uint32_t first_row, rows, first_col, head;
+    uint32_t pad[3];
+};
+
+// Sizes of a launch that do not depend on what the device holds.
+struct Shape {
+    uint32_t workers;  // workgroups, a power of two
+    uint32_t shift;    // its logarithm
+    uint32_t rows;     // of an item
+    Divisor group;     // query heads of a key head
+    Cut* cuts;
+    float* sums;       // [2 workers][rows][2]: maximum and sum
+    float* parts;      // [2 workers][rows][DP]
+};
+
+struct LaneWork {
+    uint32_t cb, n, len, end;  // first column, columns, places before them, places
+    uint32_t first, steps;     // its first step, and how many
+    uint32_t tiles;            // items of a key head
+};
+
+template <uint32_t kStep>
+__device__ __forceinline__ LaneWork lane_work(const AttendArgs& args, const Shape& sh, uint32_t l, int32_t b, int32_t e, int32_t len) {
+    LaneWork w;
+    uint32_t ce;
+    args.cols.cut(l, b, e, w.cb, ce);
+    w.n = ce - w.cb;
+    w.len = (uint32_t)max_i32(len, 0);
+    w.end = (uint32_t)min((uint64_t)w.len + w.n, (uint64_t)args.places);
+    const uint32_t all = (w.end + kStep - 1u) / kStep;
+    const uint32_t window = (uint32_t)args.a.window;
+    w.first = 0;
+    if (window && w.len + 1u > window) w.first = min_u32((w.len + 1u - window) / kStep, all - 1u);
+    w.steps = all - w.first;
+    w.tiles = (w.n * sh.group.d + sh.rows - 1u) / sh.rows;
+    if (w.n == 0) w.steps = w.tiles = 0;
+    return w;
+}
+
+__device__ __forceinline__ uint64_t shfl_up_u64(uint64_t x, uint32_t by) {
+    return ((uint64_t)(uint32_t)__shfl_up((int)(uint32_t)(x >> 32), by) << 32) | (uint32_t)__shfl_up((int)(uint32_t)x, by);
+}
+
+__device__ __forceinline__ uint32_t bcast(uint32_t x, uint32_t lane) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)x, (int)lane);
+}
+
+__device__ __forceinline__ uint64_t bcast(uint64_t x, uint32_t lane) {
+    return ((uint64_t)bcast((uint32_t)(x >> 32), lane) << 32) | bcast((uint32_t)x, lane);
+}
+
+// The steps of all lanes (the sum), or with `find` the lane that step `at` of
+// them belongs to; `before` gets the steps of the lanes before it.  All of a
+// wave's threads take part, 64 lanes at a time.
+template <uint32_t kStep>
+__device__ __forceinline__ uint64_t all_steps(const AttendArgs& args, const Shape& sh, bool find, uint64_t at, uint64_t& before,
+                                              uint32_t& lane, LaneWork& work) {
+    const uint32_t lanes = (uint32_t)args.a.lanes, id = threadIdx.x & 63u;
+    uint64_t sum = 0;
+    for (uint32_t l0 = 0; l0 < lanes; l0 += 64u) {
+        const uint32_t l = min_u32(l0 + id, lanes - 1u);
+        const int32_t* s = args.cols.at(l);
+        const int32_t b = s[0], e = s[args.cols.start ? 1 : 0], len = args.a.lens[l];
+        LaneWork w = lane_work<kStep>(args, sh, l, b, e, len);
+        if (l0 + id >= lanes) w.steps = 0;
+        const uint64_t own = (uint64_t)w.steps * w.tiles * (uint32_t)args.cache.c.heads;
+        uint64_t run = own;
+#pragma unroll
+        for (uint32_t d = 1; d < 64u; d <<= 1) {
+            const uint64_t up = shfl_up_u64(run, d);
+            if (id >= d) run += up;
+        }
+        if (find) {
+            const unsigned long long m = __ballot(sum + run > at);
+            if (m) {
+                const uint32_t k = (uint32_t)__builtin_ctzll(m);
+                before = sum + bcast(run, k) - bcast(own, k);
+                lane = l0 + k;
+                work.cb = bcast(w.cb, k);
+                work.n = bcast(w.n, k);
+                work.len = bcast(w.len, k);
+                work.end = bcast(w.end, k);
+                work.first = bcast(w.first, k);
+                work.steps = bcast(w.steps, k);
+                work.tiles = bcast(w.tiles, k);
+                return sum;
+            }
+        }
+        sum += bcast(run, 63u);
+    }
+    return sum;
+}
+
+// A condition that is the same in all lanes, as the compiler has to know: a matrix
+// instruction takes no notice of lanes that are switched off, so none may
+// stand in a branch that is taken by switching them off.
+__device__ __forceinline__ bool uniform(bool x) { return __builtin_amdgcn_readfirstlane(x ? 1 : 0) != 0; }
+
+__device__ __forceinline__ uint32_t divide(uint64_t a, uint32_t b) {
+    return (a >> 32) == 0 ? (uint32_t)a / b : (uint32_t)(a / b);
+}
+
+// Bits of places [a, b) among the 32 from `base` on.
+__device__ __forceinline__ uint32_t range_bits(int64_t a, int64_t b, int64_t base) {
+    const int64_t lo = min(max(a - base, (int64_t)0), (int64_t)32), hi = min(max(b - base, lo), (int64_t)32);
+    return (uint32_t)((((uint64_t)1 << hi) - 1u) & ~(((uint64_t)1 << lo) - 1u));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    bf16x2 v;
+    v[0] = (__bf16)a;
+    v[1] = (__bf16)b;
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+__device__ __forceinline__ int32_t from_lane(int32_t x, uint32_t lane) { return __builtin_amdgcn_ds_bpermute((int)(lane << 2), x); }
+
+__device__ __forceinline__ float max_over_groups(float x) {
+    x = __builtin_fmaxf(x, __shfl_xor(x, 16));
+    return __builtin_fmaxf(x, __shfl_xor(x, 32));
+}
+
+__device__ __forceinline__ float sum_over_groups(float x) {
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
+}
+
+// Two e4m3 elements times a power of two, as bfloat16.
+template <bool kHigh>
+__device__ __forceinline__ uint32_t widen(uint32_t x, float scale) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, scale, kHigh));
+}
+
+// The places that a row sees among the 32 from `base` on, as bits: `column` is
+// the row's, `low` the first place that it sees of those before the columns.
+__device__ __forceinline__ uint32_t seen_bits(const AttendArgs& args, const LaneWork& w, uint32_t column, int64_t low, uint32_t base) {
+    const topk_attend_args& a = args.a;
+    const int64_t len = w.len, end = w.end, b0 = base;
+    uint32_t bits = range_bits(low, min(len, end), b0);
+    if (base + 32u > w.len) {
+        uint32_t own;
+        if (a.mask) {
+            const uint32_t* row = a.mask + (int64_t)(w.cb + column) * a.mask_ld;
+            const uint32_t i0 = base > w.len ? base - w.len : 0u, word = i0 >> 5;
+            const uint32_t x0 = (int64_t)word < a.mask_ld ? row[word] : 0u;
+            const uint32_t x1 = (int64_t)word + 1 < a.mask_ld ? row[word + 1] : 0u;
+            if (base >= w.len) own = (uint32_t)((((uint64_t)x1 << 32) | x0) >> (i0 & 31u));
+            else own = x0 << (w.len - base);
+        } else {
+            const int64_t j = column;
+            own = range_bits(a.window ? len + j - a.window + 1 : len, len + j + 1, b0);
+        }
+        bits |= own & range_bits(len, end, b0);
+    }
+    return bits;
+}
+
+// The first place that column j of the lane sees of those before the columns.
+__device__ __forceinline__ int64_t first_seen(const AttendArgs& args, const LaneWork& w, uint32_t j) {
+    const topk_attend_args& a = args.a;
+    if (!a.window) return 0;
+    return (a.positions ? max((int64_t)a.positions[w.cb + j], (int64_t)w.len) : (int64_t)w.len + j) - a.window + 1;
+}
+
+// Scores of 16 queries against 32 places become weights: lane 16 g + r has query r and places 4 g + i and 16 +
+// 4 g + i.  m, sum and o (16 x 16 tiles, a query in each column) are the running maximum, sum and output.
+template <bool kMaybeMasked, int kOut>
+__device__ __forceinline__ bf16x8 weigh(f32x4 (&s)[2], bool masked, uint32_t bits, float factor, uint32_t g, float& m, float& sum, f32x4 (&o)[kOut]) {
+    if (kMaybeMasked && masked) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[t][e] = (bits >> (t * 16 + (int)g * 4 + e)) & 1u ? s[t][e] : kNone;
+    }
+    float top = __builtin_fmaxf(__builtin_fmaxf(s[0][0], s[0][1]), __builtin_fmaxf(s[0][2], s[0][3]));
+    top = __builtin_fmaxf(top, __builtin_fmaxf(__builtin_fmaxf(s[1][0], s[1][1]), __builtin_fmaxf(s[1][2], s[1][3])));
+    top *= factor;
+    if (__ballot(top > m + 8.0f)) {
+        const float now = __builtin_fmaxf(m, max_over_groups(top));
+        const float old = __builtin_amdgcn_exp2f(m - (now == kNone ? 0.0f : now));
+        m = now;
+        sum *= old;
+#pragma unroll
+        for (int i = 0; i < kOut; ++i) o[i] *= old;
+    }
+    const float zero = m == kNone ? 0.0f : m;
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e >> 2][e & 3], factor, -zero));
+        sum += x[e];
+    }
+    u32x4 y;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+    return __builtin_bit_cast(bf16x8, y);
+}
+
+__device__ __forceinline__ float power_of(uint32_t byte) { return __builtin_bit_cast(float, byte ? byte << 23 : 0x400000u); }
+
+// Clears what is not finite of two bfloat16 values; `odd` tells whether there was any.
+__device__ __forceinline__ uint32_t only_finite(uint32_t x, bool& odd) {
+    const bool low_odd = (x & 0x7F80u) == 0x7F80u, high_odd = (x & 0x7F800000u) == 0x7F800000u;
+    odd |= low_odd || high_odd;
+    x &= low_odd ? 0xFFFF0000u : ~0u;
+    return x & (high_odd ? 0xFFFFu : ~0u);
+}
+
+// The weight of place `key` of 32 for this lane's query.
+__device__ __forceinline__ float weight_of(const bf16x8& weights, uint32_t key, uint32_t r) {
+    const u32x4 y = __builtin_bit_cast(u32x4, weights);
+    const uint32_t word = (key >> 4) * 2u + ((key >> 1) & 1u);  // places 16 t + 4 g + i: word 2 t + i / 2 of group g
+    const uint32_t both = word == 0 ? y[0] : word == 1 ? y[1] : word == 2 ? y[2] : y[3];
+    const uint32_t x = (uint32_t)from_lane((int32_t)both, r + 16u * ((key >> 2) & 3u));
+    return __builtin_bit_cast(float, key & 1u ? x & 0xFFFF0000u : x << 16);
+}
+
+// DP of the kernels: dim rounded up.
+inline int padded_dim(const AttendArgs& a) { return a.cache.c.dim <= 64 ? 64 : a.cache.c.dim <= 128 ? 128 : 256; }
+
+constexpr uint32_t kRowsStep = 64;  // places of a step where a workgroup's waves share the rows
+void launch_attend_rows(const AttendArgs& a, const Shape& s, hipStream_t stream);
+
+}  // namespace topk

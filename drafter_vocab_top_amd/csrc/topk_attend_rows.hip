@@ -1,0 +1,326 @@
+// Attention over the paged cache where a key head has many rows (see
+// topk_attend.hip for the mathematics and how the work is cut).
+//
+// The four waves of a workgroup share keys and values through LDS, 64 places at
+// a time, and have 16 kQueries rows each: the products' operands are read from
+// LDS once for each wave instead of coming through memory once for each 32
+// rows.  The next 64 places are on their way to registers while these are worked
+// on (an e4m3 cache is widened between registers and LDS, once for all rows).
+//
+// LDS holds rows of elements in chunks of 8, swapped so that 16 lanes that read a
+// chunk of 16 keys, or four keys' 16 elements of a transposed read, meet 16 (8)
+// different parts of the 64 banks.  Values are read transposed: lane 16 g + r
+// gets element r of places 4 g .. 4 g + 3.
+#include "topk_attend.hpp"
+
+namespace topk {
+
+namespace {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+template <int DP, bool kWhole, bool kFp8, int kQueries>
+struct Rows {
+    static constexpr int kSize = kFp8 ? 1 : 2;
+    static constexpr uint32_t kStep = kRowsStep;
+    static constexpr int kChunks = DP / 8;                       // 16-byte chunks of a row in LDS
+    static constexpr int kVectors = DP * kSize / 16;             // 16-byte vectors of a row in memory
+    static constexpr int kLoads = kStep * kVectors / 256;        // of keys (and of values) for each thread
+    static constexpr int kKeySteps = DP / 32;
+    static constexpr int kOut = DP / 16;
+    static constexpr uint32_t kRows = 4 * 16 * kQueries;
+
+    // Where chunk `c` of place `key` lies, in 16-byte units.
+    __device__ __forceinline__ static uint32_t key_chunk(uint32_t key, uint32_t c) {
+        return key * kChunks + (c ^ (DP == 64 ? (key >> 1) & 7u : key & 15u));
+    }
+    __device__ __forceinline__ static uint32_t value_chunk(uint32_t key, uint32_t c) {
+        return key * kChunks + (c ^ (2u * (DP == 64 ? (key >> 1) & 3u : key & 7u)));
+    }
+
+    u32x4 k[kLoads], v[kLoads];  // on their way
+    uint32_t scales;             // lane's place: byte of the keys, byte of the values
+
+    // Place base + lane of the step: block and slot in it.
+    __device__ __forceinline__ static void lookup(const AttendArgs& a, const int32_t* table, uint32_t base, uint32_t end, uint32_t lane, uint32_t& id,
+                                                  uint32_t& in_block) {
+        const uint32_t p = min_u32(base + lane, end - 1u), b = a.cache.block.div(p);
+        id = (uint32_t)min_i32(max_i32(table[b], 0), (int32_t)a.cache.c.blocks - 1);
+        in_block = p - b * a.cache.block.d;
+    }
+
+    __device__ __forceinline__ void load(const AttendArgs& a, const uint8_t* keys, const uint8_t* values, uint32_t head, uint32_t id,
+                                         uint32_t in_block, uint32_t tid) {
+        const topk_cache& c = a.cache.c;
+        const int64_t at = ((int64_t)id * c.block_stride + (int64_t)in_block * c.slot_stride) * kSize;
+        if constexpr (kFp8) {
+            const int64_t s = (int64_t)id * c.scale_block_stride + (int64_t)in_block * c.scale_slot_stride + (int64_t)head * c.scale_head_stride;
+            scales = (uint32_t)c.key_scales[s] | ((uint32_t)c.value_scales[s] << 8);
+        }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint32_t x = (uint32_t)i * 256u + tid, key = x / kVectors, part = x % kVectors;
+            const int64_t row = (int64_t)(((uint64_t)(uint32_t)from_lane((int32_t)(uint32_t)((uint64_t)at >> 32), key) << 32) |
+                                          (uint32_t)from_lane((int32_t)(uint32_t)at, key));
+            const int64_t off = row + (kWhole || (int32_t)(part * 16u) < c.dim * kSize ? part * 16u : 0u);
+            k[i] = *reinterpret_cast<const u32x4*>(keys + off);
+            v[i] = *reinterpret_cast<const u32x4*>(values + off);
+        }
+    }
+
+    // What has arrived goes to LDS; places past the end and elements past the row as zeros.
+    __device__ __forceinline__ void store(const AttendArgs& a, u32x4* lds_k, u32x4* lds_v, uint32_t base, uint32_t end, uint32_t tid) const {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint32_t x = (uint32_t)i * 256u + tid, key = x / kVectors, part = x % kVectors;
+            const bool in_row = kWhole || (int32_t)(part * 16u) < a.cache.c.dim * kSize;
+            const u32x4 zero = {0u, 0u, 0u, 0u};
+            if constexpr (kFp8) {
+                const uint32_t both = (uint32_t)from_lane((int32_t)scales, key);
+                const float ks = power_of(both & 0xFFu), vs = power_of(both >> 8);
+                u32x4 y[2], z[2];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    y[h >> 1][2 * (h & 1)] = widen<false>(k[i][h], ks);
+                    y[h >> 1][2 * (h & 1) + 1] = widen<true>(k[i][h], ks);
+                    z[h >> 1][2 * (h & 1)] = widen<false>(v[i][h], vs);
+                    z[h >> 1][2 * (h & 1) + 1] = widen<true>(v[i][h], vs);
+                }
+#pragma unroll
+                for (uint32_t h = 0; h < 2; ++h) {
+                    lds_k[key_chunk(key, 2u * part + h)] = in_row ? y[h] : zero;
+                    lds_v[value_chunk(key, 2u * part + h)] = in_row && base + key < end ? z[h] : zero;
+                }
+            } else {
+                lds_k[key_chunk(key, part)] = in_row ? k[i] : zero;
+                lds_v[value_chunk(key, part)] = in_row && base + key < end ? v[i] : zero;
+            }
+        }
+    }
+};
+
+template <int DP, bool kWhole, bool kFp8, int kQueries>
+__global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_rows_kernel(AttendArgs args, Shape sh) {
+    using I = Rows<DP, kWhole, kFp8, kQueries>;
+    constexpr uint32_t R = I::kRows, kStep = kRowsStep;
+    __shared__ u32x4 lds_k[2][kStep * I::kChunks], lds_v[2][kStep * I::kChunks];
+    const topk_attend_args& a = args.a;
+    const topk_cache& c = args.cache.c;
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    // consecutive parts go to one of the eight dies, whose workgroups share a cache
+    const uint32_t worker = sh.workers >= 8u ? (blockIdx.x & 7u) * (sh.workers >> 3) + (blockIdx.x >> 3) : blockIdx.x;
+    uint64_t before = 0;
+    uint32_t l = 0;
+    LaneWork w = {};
+    const uint64_t total = all_steps<kStep>(args, sh, false, 0, before, l, w);
+    const uint64_t per = (total + sh.workers - 1u) >> sh.shift;
+    uint64_t at = per * worker;
+    const uint64_t stop = min(at + per, total);
+    uint32_t more = 0;  // parts behind this one that hold the rest of its last item
+    const float factor = a.scale == 0.0f ? 1.0f : __builtin_fabsf(a.scale) * kLog2e;
+    bool found = false;
+    while (at < stop) {
+        if (!found || at >= before + (uint64_t)w.steps * w.tiles * (uint32_t)c.heads) all_steps<kStep>(args, sh, true, at, before, l, w);
+        found = true;
+        const uint64_t in_lane = at - before;
+        const uint32_t item = divide(in_lane, w.steps), step = (uint32_t)(in_lane - (uint64_t)item * w.steps);
+        const uint32_t head = item / w.tiles, first_row = (item - head * w.tiles) * R;
+        const uint32_t last_step = (uint32_t)min((uint64_t)w.steps, step + (stop - at));
+        const int32_t* table = a.table + (int64_t)l * a.table_ld;
+        const uint32_t rows = w.n * sh.group.d, wave_row = first_row + wave * 16u * kQueries;
+        const uint8_t* keys = static_cast<const uint8_t*>(c.keys) + (int64_t)head * c.head_stride * I::kSize;
+        const uint8_t* values = static_cast<const uint8_t*>(c.values) + (int64_t)head * c.head_stride * I::kSize;
+
+        bf16x8 q[kQueries][I::kKeySteps];
+        f32x4 o[kQueries][I::kOut];
+        float m[kQueries], sum[kQueries];
+        uint32_t column[kQueries];
+        int64_t low[kQueries], all_see = 0;
+        {
+            const uint32_t lane = opaque(threadIdx.x) & 63u, r = lane & 15u, g = lane >> 4;
+#pragma unroll
+            for (int n = 0; n < kQueries; ++n) {
+                m[n] = kNone;
+                sum[n] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < I::kOut; ++i) o[n][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                // (a row past the last is the last again; it is not written)
+                const uint32_t row = min_u32(wave_row + (uint32_t)n * 16u + r, rows - 1u);
+                const uint32_t j = sh.group.div(row), h = head * sh.group.d + (row - j * sh.group.d);
+                column[n] = j;
+                low[n] = first_seen(args, w, j);
+                if (a.window) {
+                    int64_t x = low[n];
+#pragma unroll
+                    for (int s = 1; s < 16; s <<= 1) x = max(x, (int64_t)__shfl_xor((long long)x, s));
+                    all_see = max(all_see, x);
+                }
+                const uint16_t* from = static_cast<const uint16_t*>(a.q) + (int64_t)(w.cb + j) * a.q_stride + (int64_t)h * a.q_head_stride;
+#pragma unroll
+                for (int s = 0; s < I::kKeySteps; ++s) {
+                    const int32_t d = s * 32 + (int32_t)g * 8;
+                    u32x4 x = u32x4{0u, 0u, 0u, 0u};
+                    if ((kWhole || d < c.dim) && a.scale != 0.0f) x = *reinterpret_cast<const u32x4*>(from + d);
+                    if (a.scale < 0.0f) x ^= 0x80008000u;  // so that scores grow with the products
+                    q[n][s] = __builtin_bit_cast(bf16x8, x);
+                }
+            }
+        }
+        all_see = (int64_t)bcast((uint64_t)all_see, 0);
+
+        uint32_t base = (w.first + step) * kStep;
+        const uint32_t stop_at = min_u32((w.first + last_step) * kStep, w.end);
+        I it;
+        uint32_t id, in_block;
+        {
+            const uint32_t tid = opaque(threadIdx.x);
+            I::lookup(args, table, base, w.end, tid & 63u, id, in_block);
+            it.load(args, keys, values, head, id, in_block, tid);
+            I::lookup(args, table, base + kStep, w.end, tid & 63u, id, in_block);
+            it.store(args, lds_k[0], lds_v[0], base, w.end, tid);
+        }
+        __syncthreads();
+        for (uint32_t buffer = 0; base < stop_at; base += kStep, buffer ^= 1u) {
+            {
+                // the next places (past the end: the last one again)
+                const uint32_t tid = opaque(threadIdx.x);
+                it.load(args, keys, values, head, id, in_block, tid);
+                I::lookup(args, table, base + 2 * kStep, w.end, tid & 63u, id, in_block);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            const u32x4 *ks = lds_k[buffer], *vs = lds_v[buffer];
+            for (uint32_t half = 0; half < 2u; ++half) {
+                const uint32_t lane = opaque(threadIdx.x & 63u), r = lane & 15u, g = lane >> 4;
+                const uint32_t b0 = base + half * 32u;
+                const bool masked = uniform(b0 + 32u > w.len || (int64_t)b0 < all_see);  // some row may not see all
+                f32x4 s[kQueries][2];
+#pragma unroll
+                for (uint32_t t = 0; t < 2; ++t) {
+#pragma unroll
+                    for (int n = 0; n < kQueries; ++n) s[n][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (uint32_t i = 0; i < (uint32_t)I::kKeySteps; ++i) {
+                        const bf16x8 x = __builtin_bit_cast(bf16x8, ks[I::key_chunk(half * 32u + t * 16u + r, i * 4u + g)]);
+#pragma unroll
+                        for (int n = 0; n < kQueries; ++n) s[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, q[n][i], s[n][t], 0, 0, 0);
+                    }
+                }
+                uint32_t seen[kQueries] = {};
+                bf16x8 weights[kQueries];
+#pragma unroll
+                for (int n = 0; n < kQueries; ++n) {
+                    if (masked) seen[n] = seen_bits(args, w, column[n], low[n], b0);
+                    weights[n] = weigh<true>(s[n], masked, seen[n], factor, g, m[n], sum[n], o[n]);
+                }
+                // A row may not see a value that is not finite, which a weight of 0 does not
+                // remove: such values count as 0 here and are added below, one by one.
+                bool odd = false;
+#pragma unroll
+                for (uint32_t i = 0; i < (uint32_t)I::kOut; ++i) {
+                    u32x4 x;
+#pragma unroll
+                    for (uint32_t t = 0; t < 2; ++t) {
+                        const uint32_t key = half * 32u + t * 16u + g * 4u + (r >> 2);
+                        const u32x4* from = &vs[I::value_chunk(key, 2u * i + ((r & 3u) >> 1))];
+                        const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            (__attribute__((address_space(3))) s16x4*)(reinterpret_cast<const uint8_t*>(from) + (r & 1u) * 8u));
+                        const u32x2 z = __builtin_bit_cast(u32x2, y);
+                        x[2 * t] = z[0];
+                        x[2 * t + 1] = z[1];
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[e] = only_finite(x[e], odd);
+                    }
+#pragma unroll
+                    for (int n = 0; n < kQueries; ++n)
+                        o[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), weights[n], o[n][i], 0, 0, 0);
+                }
+                if (uniform(masked && __ballot(odd) != 0ull)) {
+                    for (uint32_t key = 0; key < 32u; ++key) {
+                        float weight[kQueries];
+#pragma unroll
+                        for (int n = 0; n < kQueries; ++n) weight[n] = weight_of(weights[n], key, r);
+#pragma unroll
+                        for (uint32_t i = 0; i < (uint32_t)I::kOut; ++i) {
+                            const uint32_t d = i * 16u + g * 4u;
+                            const uint8_t* from = reinterpret_cast<const uint8_t*>(&vs[I::value_chunk(half * 32u + key, d / 8u)]) + (d & 7u) * 2u;
+                            const u32x2 x = *reinterpret_cast<const u32x2*>(from);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float v1 = __builtin_bit_cast(float, e & 1 ? x[e / 2] & 0xFFFF0000u : x[e / 2] << 16);
+#pragma unroll
+                                for (int n = 0; n < kQueries; ++n)
+                                    if ((seen[n] >> key & 1u) && !__builtin_isfinite(v1)) o[n][i][e] += weight[n] * v1;
+                            }
+                        }
+                    }
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            it.store(args, lds_k[buffer ^ 1u], lds_v[buffer ^ 1u], base + kStep, w.end, opaque(threadIdx.x));
+            __syncthreads();
+        }
+
+        const bool direct = step == 0 && last_step == w.steps;
+        const uint32_t slot = 2u * worker + (step == 0 ? 1u : 0u);
+        const uint32_t lane = opaque(threadIdx.x) & 63u, r = lane & 15u, g = lane >> 4;
+#pragma unroll
+        for (int n = 0; n < kQueries; ++n) {
+            const float all = sum_over_groups(sum[n]);
+            const uint32_t row = wave * 16u * kQueries + (uint32_t)n * 16u + r;
+            if (!direct) {
+                float* to = sh.parts + ((int64_t)slot * R + row) * DP + g * 4u;
+#pragma unroll
+                for (int i = 0; i < I::kOut; ++i) *reinterpret_cast<f32x4*>(to + i * 16) = o[n][i];
+                if (g == 0) {
+                    sh.sums[((int64_t)slot * R + row) * 2] = m[n];
+                    sh.sums[((int64_t)slot * R + row) * 2 + 1] = all;
+                }
+            } else if (first_row + row < rows) {
+                const uint32_t j = sh.group.div(first_row + row), h = head * sh.group.d + (first_row + row - j * sh.group.d);
+                uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + (int64_t)(w.cb + j) * a.out_stride +
+                                                           (int64_t)h * a.out_head_stride + g * 4u);
+                const float inverse = 1.0f / all;
+#pragma unroll
+                for (int i = 0; i < I::kOut; ++i) {
+                    u32x2 y;
+                    y[0] = all == 0.0f ? 0u : pack_bf16(o[n][i][0] * inverse, o[n][i][1] * inverse);
+                    y[1] = all == 0.0f ? 0u : pack_bf16(o[n][i][2] * inverse, o[n][i][3] * inverse);
+                    if (kWhole || i * 16 < c.dim) *reinterpret_cast<u32x2*>(to + i * 8) = y;
+                }
+            }
+        }
+        at += last_step - step;
+        if (at == stop && step == 0 && last_step < w.steps) {
+            more = (uint32_t)(((uint64_t)(w.steps - last_step) + per - 1u) / per);
+            if (threadIdx.x == 0) sh.cuts[worker] = Cut{more, first_row, rows, w.cb, head, {}};
+        }
+    }
+    if (more == 0 && threadIdx.x == 0) sh.cuts[worker].more = 0;
+}
+
+template <int DP, bool kWhole, bool kFp8>
+void launch_rows(const AttendArgs& a, const Shape& s, hipStream_t stream) {
+    if (s.rows == 64) hipLaunchKernelGGL((attend_rows_kernel<DP, kWhole, kFp8, 1>), dim3(s.workers), dim3(256), 0, stream, a, s);
+    if constexpr (DP < 256)
+        if (s.rows == 128) hipLaunchKernelGGL((attend_rows_kernel<DP, kWhole, kFp8, 2>), dim3(s.workers), dim3(256), 0, stream, a, s);
+}
+
+template <int DP>
+void launch_format(const AttendArgs& a, const Shape& s, hipStream_t stream) {
+    const bool whole = a.cache.c.dim == DP;
+    if (a.cache.c.format == TOPK_CACHE_FP8) whole ? launch_rows<DP, true, true>(a, s, stream) : launch_rows<DP, false, true>(a, s, stream);
+    else whole ? launch_rows<DP, true, false>(a, s, stream) : launch_rows<DP, false, false>(a, s, stream);
+}
+
+}  // namespace
+
+void launch_attend_rows(const AttendArgs& a, const Shape& s, hipStream_t stream) {
+    const int dp = padded_dim(a);
+    if (dp == 64) launch_format<64>(a, s, stream);
+    else if (dp == 128) launch_format<128>(a, s, stream);
+    else launch_format<256>(a, s, stream);
+}
+
+}  // namespace topk
