@@ -55,7 +55,8 @@ struct Item {
     u32x4 k[2][kKeyLoads];
     uint32_t v[8][kHalves][kValueWords];
     f32x4 o[kQueries][kOut];
-    float m[kQueries], sum[kQueries];
+    float m[kQueries];
+    f32x4 sum[kQueries];
     uint32_t scales, next_scales;  // of key lane & 31: lanes 0 - 31 the keys', 32 - 63 the values'
     // One lane's share of a tile's addresses: place base + (lane & 31).
     struct Places {
@@ -270,7 +271,7 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_kernel(AttendArg
 #pragma unroll
         for (int n = 0; n < kQueries; ++n) {
             it.m[n] = kNone;
-            it.sum[n] = 0.0f;
+            it.sum[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < I::kOut; ++i) it.o[n][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
@@ -395,10 +396,9 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_kernel(AttendArg
         const uint32_t slot = 2u * worker + (step == 0 ? 1u : 0u);
 #pragma unroll
         for (int n = 0; n < kQueries; ++n) {
-            const float sum = sum_over_groups(it.sum[n]);
             if (g_ == 0) {
                 lds_m[wave][n * 16 + (int)r_] = it.m[n];
-                lds_l[wave][n * 16 + (int)r_] = sum;
+                lds_l[wave][n * 16 + (int)r_] = it.sum[n][0];
             }
         }
         __syncthreads();

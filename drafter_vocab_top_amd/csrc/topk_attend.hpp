@@ -146,11 +146,6 @@ __device__ __forceinline__ float max_over_groups(float x) {
     return __builtin_fmaxf(x, __shfl_xor(x, 32));
 }
 
-__device__ __forceinline__ float sum_over_groups(float x) {
-    x += __shfl_xor(x, 16);
-    return x + __shfl_xor(x, 32);
-}
-
 // Two e4m3 elements times a power of two, as bfloat16.
 template <bool kHigh>
 __device__ __forceinline__ uint32_t widen(uint32_t x, float scale) {
@@ -189,9 +184,10 @@ __device__ __forceinline__ int64_t first_seen(const AttendArgs& args, const Lane
 }
 
 // Scores of 16 queries against 32 places become weights: lane 16 g + r has query r and places 4 g + i and 16 +
-// 4 g + i.  m, sum and o (16 x 16 tiles, a query in each column) are the running maximum, sum and output.
+// 4 g + i.  m, sum and o (16 x 16 tiles, a query in each column) are the running maximum, sum and output.  The sum
+// is a product with ones: it is of the weights as they are rounded for the products with values.
 template <bool kMaybeMasked, int kOut>
-__device__ __forceinline__ bf16x8 weigh(f32x4 (&s)[2], bool masked, uint32_t bits, float factor, uint32_t g, float& m, float& sum, f32x4 (&o)[kOut]) {
+__device__ __forceinline__ bf16x8 weigh(f32x4 (&s)[2], bool masked, uint32_t bits, float factor, uint32_t g, float& m, f32x4& sum, f32x4 (&o)[kOut]) {
     if (kMaybeMasked && masked) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -205,20 +201,19 @@ __device__ __forceinline__ bf16x8 weigh(f32x4 (&s)[2], bool masked, uint32_t bit
         const float now = __builtin_fmaxf(m, max_over_groups(top));
         const float old = __builtin_amdgcn_exp2f(m - (now == kNone ? 0.0f : now));
         m = now;
-        sum *= old;
+        sum[0] *= old;  // (the product's rows are alike, and the first is the one that is read)
 #pragma unroll
         for (int i = 0; i < kOut; ++i) o[i] *= old;
     }
     const float zero = m == kNone ? 0.0f : m;
     float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e >> 2][e & 3], factor, -zero));
-        sum += x[e];
-    }
+    for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e >> 2][e & 3], factor, -zero));
     u32x4 y;
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+    const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+    sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, ones), __builtin_bit_cast(bf16x8, y), sum, 0, 0, 0);
     return __builtin_bit_cast(bf16x8, y);
 }
 

@@ -2,9 +2,9 @@
 // topk_attend.hip for the mathematics and how the work is cut).
 //
 // The four waves of a workgroup share keys and values through LDS, 64 places at
-// a time, and have 16 kQueries rows each: the products' operands are read from
-// LDS once for each wave instead of coming through memory once for each 32
-// rows.  The next 64 places are on their way to registers while these are worked
+// a time.  kGroups groups of 16 kQueries rows each have a wave, or two that take
+// 32 of the places each and add up at the end (64 rows: four waves of 16 rows
+// would read every operand from LDS for half as many products).  The next 64 places are on their way to registers while these are worked
 // on (an e4m3 cache is widened between registers and LDS, once for all rows).
 //
 // LDS holds rows of elements in chunks of 8, swapped so that 16 lanes that read a
@@ -19,7 +19,7 @@ namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-template <int DP, bool kWhole, bool kFp8, int kQueries>
+template <int DP, bool kWhole, bool kFp8, int kQueries, int kGroups>
 struct Rows {
     static constexpr int kSize = kFp8 ? 1 : 2;
     static constexpr uint32_t kStep = kRowsStep;
@@ -28,7 +28,8 @@ struct Rows {
     static constexpr int kLoads = kStep * kVectors / 256;        // of keys (and of values) for each thread
     static constexpr int kKeySteps = DP / 32;
     static constexpr int kOut = DP / 16;
-    static constexpr uint32_t kRows = 4 * 16 * kQueries;
+    static constexpr uint32_t kRows = 16 * kQueries * kGroups;
+    static constexpr uint32_t kSplits = 4 / kGroups;
 
     // Where chunk `c` of place `key` lies, in 16-byte units.
     __device__ __forceinline__ static uint32_t key_chunk(uint32_t key, uint32_t c) {
@@ -70,9 +71,13 @@ struct Rows {
 
     // What has arrived goes to LDS; places past the end and elements past the row as zeros.
     __device__ __forceinline__ void store(const AttendArgs& a, u32x4* lds_k, u32x4* lds_v, uint32_t base, uint32_t end, uint32_t tid) const {
+        constexpr uint32_t kApart = 256 / kVectors;  // of a thread's places
+        const uint32_t first = tid / kVectors, part = tid % kVectors;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const uint32_t x = (uint32_t)i * 256u + tid, key = x / kVectors, part = x % kVectors;
+            const uint32_t key = (uint32_t)i * kApart + first;
+            // (places 16 apart have their chunks swapped alike)
+            const uint32_t like = (uint32_t)i * kApart % 16u + first, whole = (uint32_t)i * kApart / 16u * 16u * kChunks;
             const bool in_row = kWhole || (int32_t)(part * 16u) < a.cache.c.dim * kSize;
             const u32x4 zero = {0u, 0u, 0u, 0u};
             if constexpr (kFp8) {
@@ -88,25 +93,37 @@ struct Rows {
                 }
 #pragma unroll
                 for (uint32_t h = 0; h < 2; ++h) {
-                    lds_k[key_chunk(key, 2u * part + h)] = in_row ? y[h] : zero;
-                    lds_v[value_chunk(key, 2u * part + h)] = in_row && base + key < end ? z[h] : zero;
+                    lds_k[key_chunk(like, 2u * part + h) + whole] = in_row ? y[h] : zero;
+                    lds_v[value_chunk(like, 2u * part + h) + whole] = in_row && base + key < end ? z[h] : zero;
                 }
             } else {
-                lds_k[key_chunk(key, part)] = in_row ? k[i] : zero;
-                lds_v[value_chunk(key, part)] = in_row && base + key < end ? v[i] : zero;
+                lds_k[key_chunk(like, part) + whole] = in_row ? k[i] : zero;
+                lds_v[value_chunk(like, part) + whole] = in_row && base + key < end ? v[i] : zero;
             }
         }
     }
 };
 
-template <int DP, bool kWhole, bool kFp8, int kQueries>
+template <int DP, bool kWhole, bool kFp8, int kQueries, int kGroups>
 __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_rows_kernel(AttendArgs args, Shape sh) {
-    using I = Rows<DP, kWhole, kFp8, kQueries>;
-    constexpr uint32_t R = I::kRows, kStep = kRowsStep;
+    using I = Rows<DP, kWhole, kFp8, kQueries, kGroups>;
+    constexpr uint32_t R = I::kRows, kStep = kRowsStep, kSplits = I::kSplits;
+    static_assert(kSplits <= 2, "");
     __shared__ u32x4 lds_k[2][kStep * I::kChunks], lds_v[2][kStep * I::kChunks];
     const topk_attend_args& a = args.a;
     const topk_cache& c = args.cache.c;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const uint32_t split = wave % kSplits, group_row = wave / kSplits * 16u * kQueries;  // its places, its rows
+    // where this lane reads: chunk i of key r, and element 16 i of value 4 g + r / 4 (the other places lie whole rows further)
+    uint32_t key_at[I::kKeySteps], value_at[I::kOut];
+    {
+        const uint32_t r = threadIdx.x & 15u, g = (threadIdx.x >> 4) & 3u;
+#pragma unroll
+        for (uint32_t i = 0; i < (uint32_t)I::kKeySteps; ++i) key_at[i] = I::key_chunk(r, i * 4u + g) * 16u;
+#pragma unroll
+        for (uint32_t i = 0; i < (uint32_t)I::kOut; ++i)
+            value_at[i] = I::value_chunk(g * 4u + (r >> 2), 2u * i + ((r & 3u) >> 1)) * 16u + (r & 1u) * 8u;
+    }
     // consecutive parts go to one of the eight dies, whose workgroups share a cache
     const uint32_t worker = sh.workers >= 8u ? (blockIdx.x & 7u) * (sh.workers >> 3) + (blockIdx.x >> 3) : blockIdx.x;
     uint64_t before = 0;
@@ -127,13 +144,14 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_rows_kernel(Atte
         const uint32_t head = item / w.tiles, first_row = (item - head * w.tiles) * R;
         const uint32_t last_step = (uint32_t)min((uint64_t)w.steps, step + (stop - at));
         const int32_t* table = a.table + (int64_t)l * a.table_ld;
-        const uint32_t rows = w.n * sh.group.d, wave_row = first_row + wave * 16u * kQueries;
+        const uint32_t rows = w.n * sh.group.d, wave_row = first_row + group_row;
         const uint8_t* keys = static_cast<const uint8_t*>(c.keys) + (int64_t)head * c.head_stride * I::kSize;
         const uint8_t* values = static_cast<const uint8_t*>(c.values) + (int64_t)head * c.head_stride * I::kSize;
 
         bf16x8 q[kQueries][I::kKeySteps];
         f32x4 o[kQueries][I::kOut];
-        float m[kQueries], sum[kQueries];
+        f32x4 sum[kQueries];
+        float m[kQueries];
         uint32_t column[kQueries];
         int64_t low[kQueries], all_see = 0;
         {
@@ -141,7 +159,7 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_rows_kernel(Atte
 #pragma unroll
             for (int n = 0; n < kQueries; ++n) {
                 m[n] = kNone;
-                sum[n] = 0.0f;
+                sum[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int i = 0; i < I::kOut; ++i) o[n][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                 // (a row past the last is the last again; it is not written)
@@ -188,8 +206,11 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_rows_kernel(Atte
                 I::lookup(args, table, base + 2 * kStep, w.end, tid & 63u, id, in_block);
             }
             __builtin_amdgcn_sched_barrier(0);
-            const u32x4 *ks = lds_k[buffer], *vs = lds_v[buffer];
-            for (uint32_t half = 0; half < 2u; ++half) {
+            const uint8_t* ks = reinterpret_cast<const uint8_t*>(lds_k[buffer]);
+            const uint8_t* vs = reinterpret_cast<const uint8_t*>(lds_v[buffer]);
+#pragma unroll
+            for (uint32_t u = 0; u < 2u / kSplits; ++u) {
+                const uint32_t half = kSplits == 1u ? u : split;
                 const uint32_t lane = opaque(threadIdx.x & 63u), r = lane & 15u, g = lane >> 4;
                 const uint32_t b0 = base + half * 32u;
                 const bool masked = uniform(b0 + 32u > w.len || (int64_t)b0 < all_see);  // some row may not see all
@@ -200,7 +221,7 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_rows_kernel(Atte
                     for (int n = 0; n < kQueries; ++n) s[n][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (uint32_t i = 0; i < (uint32_t)I::kKeySteps; ++i) {
-                        const bf16x8 x = __builtin_bit_cast(bf16x8, ks[I::key_chunk(half * 32u + t * 16u + r, i * 4u + g)]);
+                        const bf16x8 x = *reinterpret_cast<const bf16x8*>(ks + key_at[i] + (half * 32u + t * 16u) * I::kChunks * 16u);
 #pragma unroll
                         for (int n = 0; n < kQueries; ++n) s[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, q[n][i], s[n][t], 0, 0, 0);
                     }
@@ -220,10 +241,8 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_rows_kernel(Atte
                     u32x4 x;
 #pragma unroll
                     for (uint32_t t = 0; t < 2; ++t) {
-                        const uint32_t key = half * 32u + t * 16u + g * 4u + (r >> 2);
-                        const u32x4* from = &vs[I::value_chunk(key, 2u * i + ((r & 3u) >> 1))];
                         const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                            (__attribute__((address_space(3))) s16x4*)(reinterpret_cast<const uint8_t*>(from) + (r & 1u) * 8u));
+                            (__attribute__((address_space(3))) s16x4*)(vs + value_at[i] + (half * 32u + t * 16u) * I::kChunks * 16u));
                         const u32x2 z = __builtin_bit_cast(u32x2, y);
                         x[2 * t] = z[0];
                         x[2 * t + 1] = z[1];
@@ -244,7 +263,7 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_rows_kernel(Atte
 #pragma unroll
                         for (uint32_t i = 0; i < (uint32_t)I::kOut; ++i) {
                             const uint32_t d = i * 16u + g * 4u;
-                            const uint8_t* from = reinterpret_cast<const uint8_t*>(&vs[I::value_chunk(half * 32u + key, d / 8u)]) + (d & 7u) * 2u;
+                            const uint8_t* from = vs + I::value_chunk(half * 32u + key, d / 8u) * 16u + (d & 7u) * 2u;
                             const u32x2 x = *reinterpret_cast<const u32x2*>(from);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
@@ -265,10 +284,39 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_rows_kernel(Atte
         const bool direct = step == 0 && last_step == w.steps;
         const uint32_t slot = 2u * worker + (step == 0 ? 1u : 0u);
         const uint32_t lane = opaque(threadIdx.x) & 63u, r = lane & 15u, g = lane >> 4;
+        if constexpr (kSplits == 2) {
+            // the second half of the places joins the first, through the keys' LDS (all have left the loop)
+            static_assert(sizeof(lds_k) >= kQueries * 64 * (I::kOut * 16 + 8), "");
+            f32x4* to = reinterpret_cast<f32x4*>(group_row == 0 ? lds_k : lds_v);
+            float* ml = reinterpret_cast<float*>(to + kQueries * I::kOut * 64);
+            if (split == 1) {
+#pragma unroll
+                for (int n = 0; n < kQueries; ++n) {
+#pragma unroll
+                    for (int i = 0; i < I::kOut; ++i) to[(n * I::kOut + i) * 64 + (int)lane] = o[n][i];
+                    ml[(2 * n) * 64 + (int)lane] = m[n];
+                    ml[(2 * n + 1) * 64 + (int)lane] = sum[n][0];
+                }
+            }
+            __syncthreads();
+            if (split == 0) {
+#pragma unroll
+                for (int n = 0; n < kQueries; ++n) {
+                    const float other = ml[(2 * n) * 64 + (int)lane], top = __builtin_fmaxf(m[n], other), zero = top == kNone ? 0.0f : top;
+                    const float f0 = __builtin_amdgcn_exp2f(m[n] - zero), f1 = __builtin_amdgcn_exp2f(other - zero);
+                    m[n] = top;
+                    sum[n][0] = sum[n][0] * f0 + ml[(2 * n + 1) * 64 + (int)lane] * f1;
+#pragma unroll
+                    for (int i = 0; i < I::kOut; ++i) o[n][i] = o[n][i] * f0 + to[(n * I::kOut + i) * 64 + (int)lane] * f1;
+                }
+            }
+            __syncthreads();  // the next item's keys come here
+        }
 #pragma unroll
         for (int n = 0; n < kQueries; ++n) {
-            const float all = sum_over_groups(sum[n]);
-            const uint32_t row = wave * 16u * kQueries + (uint32_t)n * 16u + r;
+            if (split != 0) break;
+            const float all = sum[n][0];
+            const uint32_t row = group_row + (uint32_t)n * 16u + r;
             if (!direct) {
                 float* to = sh.parts + ((int64_t)slot * R + row) * DP + g * 4u;
 #pragma unroll
@@ -302,9 +350,13 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_rows_kernel(Atte
 
 template <int DP, bool kWhole, bool kFp8>
 void launch_rows(const AttendArgs& a, const Shape& s, hipStream_t stream) {
-    if (s.rows == 64) hipLaunchKernelGGL((attend_rows_kernel<DP, kWhole, kFp8, 1>), dim3(s.workers), dim3(256), 0, stream, a, s);
-    if constexpr (DP < 256)
-        if (s.rows == 128) hipLaunchKernelGGL((attend_rows_kernel<DP, kWhole, kFp8, 2>), dim3(s.workers), dim3(256), 0, stream, a, s);
+    const dim3 grid(s.workers), block(256);
+    if constexpr (DP == 256) {
+        hipLaunchKernelGGL((attend_rows_kernel<DP, kWhole, kFp8, 1, 4>), grid, block, 0, stream, a, s);
+    } else {
+        if (s.rows == 64) hipLaunchKernelGGL((attend_rows_kernel<DP, kWhole, kFp8, 2, 2>), grid, block, 0, stream, a, s);
+        else hipLaunchKernelGGL((attend_rows_kernel<DP, kWhole, kFp8, 2, 4>), grid, block, 0, stream, a, s);
+    }
 }
 
 template <int DP>
