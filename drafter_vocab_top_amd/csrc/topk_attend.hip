@@ -334,11 +334,11 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_kernel(AttendArg
 
             uint32_t seen[kQueries] = {};
             bf16x8 weights[kQueries];
+            if (masked) {
 #pragma unroll
-            for (int n = 0; n < kQueries; ++n) {
-                if (masked) seen[n] = seen_bits(args, w, column[n], low[n], base);
-                weights[n] = weigh<true>(s[n], masked, seen[n], factor, g, it.m[n], it.sum[n], it.o[n]);
+                for (int n = 0; n < kQueries; ++n) seen[n] = seen_bits(args, w, column[n], low[n], base);
             }
+            weigh(s, masked, seen, factor, g, it.m, it.sum, it.o, weights);
 
             // values, two elements of a key in each word
             uint32_t pairs[8][I::kHalves][I::kOwn / 2];
@@ -360,7 +360,7 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_kernel(AttendArg
             }
             // A row may not see a value that is not finite, which a weight of 0 does not
             // remove: such values count as 0 here and are added below, one by one.
-            bool odd = false;
+            uint32_t odd = 0;
             if (masked) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -385,7 +385,7 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_kernel(AttendArg
                         it.o[n][h * I::kOwn + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), weights[n],
                                                                                           it.o[n][h * I::kOwn + i], 0, 0, 0);
                 }
-            if (uniform(masked && __ballot(odd) != 0ull)) it.add_odd(args, table, values, head, base, w.end, seen, weights, lane);
+            if (uniform(masked && __ballot(odd != 0u) != 0ull)) it.add_odd(args, table, values, head, base, w.end, seen, weights, lane);
             __builtin_amdgcn_sched_barrier(0);
             it.load_values(args, values, at, lane);
         }

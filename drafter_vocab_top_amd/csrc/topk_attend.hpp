@@ -156,6 +156,7 @@ __device__ __forceinline__ uint32_t widen(uint32_t x, float scale) {
 // the row's, `low` the first place that it sees of those before the columns.
 __device__ __forceinline__ uint32_t seen_bits(const AttendArgs& args, const LaneWork& w, uint32_t column, int64_t low, uint32_t base) {
     const topk_attend_args& a = args.a;
+    asm volatile("" : "+s"(base));  // (nothing of this is computed where no row asks for it)
     const int64_t len = w.len, end = w.end, b0 = base;
     uint32_t bits = range_bits(low, min(len, end), b0);
     if (base + 32u > w.len) {
@@ -183,48 +184,64 @@ __device__ __forceinline__ int64_t first_seen(const AttendArgs& args, const Lane
     return (a.positions ? max((int64_t)a.positions[w.cb + j], (int64_t)w.len) : (int64_t)w.len + j) - a.window + 1;
 }
 
-// Scores of 16 queries against 32 places become weights: lane 16 g + r has query r and places 4 g + i and 16 +
-// 4 g + i.  m, sum and o (16 x 16 tiles, a query in each column) are the running maximum, sum and output.  The sum
-// is a product with ones: it is of the weights as they are rounded for the products with values.
-template <bool kMaybeMasked, int kOut>
-__device__ __forceinline__ bf16x8 weigh(f32x4 (&s)[2], bool masked, uint32_t bits, float factor, uint32_t g, float& m, f32x4& sum, f32x4 (&o)[kOut]) {
-    if (kMaybeMasked && masked) {
+// Scores of 16 kQueries queries against 32 places become weights: lane 16 g + r has query r of each 16 and places
+// 4 g + i and 16 + 4 g + i.  m, sum and o (16 x 16 tiles, a query in each column) are the running maximum, sum and
+// output.  The sum is a product with ones: it is of the weights as they are rounded for the products with values.
+// `seen`: with `masked`, the places that each query sees.
+template <int kQueries, int kOut>
+__device__ __forceinline__ void weigh(f32x4 (&s)[kQueries][2], bool masked, const uint32_t (&seen)[kQueries], float factor, uint32_t g,
+                                      float (&m)[kQueries], f32x4 (&sum)[kQueries], f32x4 (&o)[kQueries][kOut], bf16x8 (&weights)[kQueries]) {
+    if (masked) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int n = 0; n < kQueries; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[t][e] = (bits >> (t * 16 + (int)g * 4 + e)) & 1u ? s[t][e] : kNone;
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][t][e] = (seen[n] >> (t * 16 + (int)g * 4 + e)) & 1u ? s[n][t][e] : kNone;
     }
-    float top = __builtin_fmaxf(__builtin_fmaxf(s[0][0], s[0][1]), __builtin_fmaxf(s[0][2], s[0][3]));
-    top = __builtin_fmaxf(top, __builtin_fmaxf(__builtin_fmaxf(s[1][0], s[1][1]), __builtin_fmaxf(s[1][2], s[1][3])));
-    top *= factor;
-    if (__ballot(top > m + 8.0f)) {
-        const float now = __builtin_fmaxf(m, max_over_groups(top));
-        const float old = __builtin_amdgcn_exp2f(m - (now == kNone ? 0.0f : now));
-        m = now;
-        sum[0] *= old;  // (the product's rows are alike, and the first is the one that is read)
+    float top[kQueries];
+    bool grown = false;
 #pragma unroll
-        for (int i = 0; i < kOut; ++i) o[i] *= old;
+    for (int n = 0; n < kQueries; ++n) {
+        top[n] = __builtin_fmaxf(__builtin_fmaxf(s[n][0][0], s[n][0][1]), __builtin_fmaxf(s[n][0][2], s[n][0][3]));
+        top[n] = __builtin_fmaxf(top[n], __builtin_fmaxf(__builtin_fmaxf(s[n][1][0], s[n][1][1]), __builtin_fmaxf(s[n][1][2], s[n][1][3])));
+        top[n] *= factor;
+        grown |= top[n] > m[n] + 8.0f;
     }
-    const float zero = m == kNone ? 0.0f : m;
-    float x[8];
+    if (__ballot(grown)) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e >> 2][e & 3], factor, -zero));
-    u32x4 y;
+        for (int n = 0; n < kQueries; ++n) {
+            const float now = __builtin_fmaxf(m[n], max_over_groups(top[n]));
+            const float old = __builtin_amdgcn_exp2f(m[n] - (now == kNone ? 0.0f : now));
+            m[n] = now;
+            sum[n][0] *= old;  // (the product's rows are alike, and the first is the one that is read)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+            for (int i = 0; i < kOut; ++i) o[n][i] *= old;
+        }
+    }
     const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-    sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, ones), __builtin_bit_cast(bf16x8, y), sum, 0, 0, 0);
-    return __builtin_bit_cast(bf16x8, y);
+#pragma unroll
+    for (int n = 0; n < kQueries; ++n) {
+        const float zero = m[n] == kNone ? 0.0f : m[n];
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][e >> 2][e & 3], factor, -zero));
+        u32x4 y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+        weights[n] = __builtin_bit_cast(bf16x8, y);
+        sum[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, ones), weights[n], sum[n], 0, 0, 0);
+    }
 }
 
 __device__ __forceinline__ float power_of(uint32_t byte) { return __builtin_bit_cast(float, byte ? byte << 23 : 0x400000u); }
 
-// Clears what is not finite of two bfloat16 values; `odd` tells whether there was any.
-__device__ __forceinline__ uint32_t only_finite(uint32_t x, bool& odd) {
-    const bool low_odd = (x & 0x7F80u) == 0x7F80u, high_odd = (x & 0x7F800000u) == 0x7F800000u;
-    odd |= low_odd || high_odd;
-    x &= low_odd ? 0xFFFF0000u : ~0u;
-    return x & (high_odd ? 0xFFFFu : ~0u);
+// Clears what is not finite of two bfloat16 values; `odd` gets a bit where there is any.
+__device__ __forceinline__ uint32_t only_finite(uint32_t x, uint32_t& odd) {
+    // an exponent of ones and one more carry into the sign's place
+    const uint32_t b = ((x & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+    odd |= b;
+    return x & ~((b << 1) - (b >> 15));
 }
 
 // The weight of place `key` of 32 for this lane's query.

@@ -69,8 +69,12 @@ struct Rows {
         }
     }
 
-    // What has arrived goes to LDS; places past the end and elements past the row as zeros.
-    __device__ __forceinline__ void store(const AttendArgs& a, u32x4* lds_k, u32x4* lds_v, uint32_t base, uint32_t end, uint32_t tid) const {
+    // What has arrived goes to LDS; places past the end and elements past the row as zeros.  With `masked` (some row
+    // may not see some place) values that are not finite go there as zeros too: a weight of 0 would not remove
+    // them.  They are added one by one (add_odd), where `odd` says that there are any: it gets `base`.
+    __device__ __forceinline__ void store(const AttendArgs& a, u32x4* lds_k, u32x4* lds_v, uint32_t base, uint32_t end, bool masked, uint32_t* odd,
+                                          uint32_t tid) const {
+        uint32_t found = 0;
         constexpr uint32_t kApart = 256 / kVectors;  // of a thread's places
         const uint32_t first = tid / kVectors, part = tid % kVectors;
 #pragma unroll
@@ -80,6 +84,7 @@ struct Rows {
             const uint32_t like = (uint32_t)i * kApart % 16u + first, whole = (uint32_t)i * kApart / 16u * 16u * kChunks;
             const bool in_row = kWhole || (int32_t)(part * 16u) < a.cache.c.dim * kSize;
             const u32x4 zero = {0u, 0u, 0u, 0u};
+            const bool has_value = in_row && base + key < end;
             if constexpr (kFp8) {
                 const uint32_t both = (uint32_t)from_lane((int32_t)scales, key);
                 const float ks = power_of(both & 0xFFu), vs = power_of(both >> 8);
@@ -94,11 +99,62 @@ struct Rows {
 #pragma unroll
                 for (uint32_t h = 0; h < 2; ++h) {
                     lds_k[key_chunk(like, 2u * part + h) + whole] = in_row ? y[h] : zero;
-                    lds_v[value_chunk(like, 2u * part + h) + whole] = in_row && base + key < end ? z[h] : zero;
+                    z[h] = has_value ? z[h] : zero;
+                    if (masked) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) z[h][e] = only_finite(z[h][e], found);
+                    }
+                    lds_v[value_chunk(like, 2u * part + h) + whole] = z[h];
                 }
             } else {
                 lds_k[key_chunk(like, part) + whole] = in_row ? k[i] : zero;
-                lds_v[value_chunk(like, part) + whole] = in_row && base + key < end ? v[i] : zero;
+                u32x4 z = has_value ? v[i] : zero;
+                if (masked) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[e] = only_finite(z[e], found);
+                }
+                lds_v[value_chunk(like, part) + whole] = z;
+            }
+        }
+        if (found) *odd = base;
+    }
+
+    // Adds the values that are not finite of the 32 places from `base` on, each to the rows that see it.
+    __device__ __forceinline__ static void add_odd(const AttendArgs& a, const int32_t* table, const uint8_t* values, uint32_t head, uint32_t base,
+                                                   uint32_t end, const uint32_t (&seen)[kQueries], const bf16x8 (&weights)[kQueries],
+                                                   f32x4 (&o)[kQueries][kOut], uint32_t lane) {
+        const topk_cache& c = a.cache.c;
+        const uint32_t r = lane & 15u, g = lane >> 4;
+        for (uint32_t key = 0; key < 32u && base + key < end; ++key) {
+            uint32_t id, in_block;
+            lookup(a, table, base + key, end, 0u, id, in_block);
+            const uint8_t* row = values + ((int64_t)id * c.block_stride + (int64_t)in_block * c.slot_stride) * kSize;
+            float scale = 1.0f;
+            if constexpr (kFp8)
+                scale = power_of(c.value_scales[(int64_t)id * c.scale_block_stride + (int64_t)in_block * c.scale_slot_stride +
+                                                (int64_t)head * c.scale_head_stride]);
+            float weight[kQueries];
+#pragma unroll
+            for (int n = 0; n < kQueries; ++n) weight[n] = weight_of(weights[n], key, r);
+#pragma unroll
+            for (int i = 0; i < kOut; ++i) {
+                const int32_t d = i * 16 + (int32_t)g * 4;
+                const uint8_t* from = row + (kWhole || d < c.dim ? d * kSize : 0);
+                u32x2 x;
+                if constexpr (kFp8) {
+                    const uint32_t y = *reinterpret_cast<const uint32_t*>(from);
+                    x[0] = widen<false>(y, scale);
+                    x[1] = widen<true>(y, scale);
+                } else {
+                    x = *reinterpret_cast<const u32x2*>(from);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v1 = __builtin_bit_cast(float, e & 1 ? x[e / 2] & 0xFFFF0000u : x[e / 2] << 16);
+#pragma unroll
+                    for (int n = 0; n < kQueries; ++n)
+                        if ((seen[n] >> key & 1u) && !__builtin_isfinite(v1)) o[n][i][e] += weight[n] * v1;
+                }
             }
         }
     }
@@ -110,6 +166,9 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_rows_kernel(Atte
     constexpr uint32_t R = I::kRows, kStep = kRowsStep, kSplits = I::kSplits;
     static_assert(kSplits <= 2, "");
     __shared__ u32x4 lds_k[2][kStep * I::kChunks], lds_v[2][kStep * I::kChunks];
+    __shared__ uint32_t lds_odd[2];
+    __shared__ int64_t lds_see[4];
+    if (threadIdx.x < 2u) lds_odd[threadIdx.x] = ~0u;
     const topk_attend_args& a = args.a;
     const topk_cache& c = args.cache.c;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -185,6 +244,12 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_rows_kernel(Atte
             }
         }
         all_see = (int64_t)bcast((uint64_t)all_see, 0);
+        if (threadIdx.x % 64u == 0u) lds_see[wave] = all_see;
+        __syncthreads();
+        // all rows of the item see the places from here up to the lane's columns
+        all_see = max(max(lds_see[0], lds_see[1]), max(lds_see[2], lds_see[3]));
+        all_see = (int64_t)bcast((uint64_t)all_see, 0);
+        auto masked_from = [&](uint32_t first, uint32_t places) { return uniform(first + places > w.len || (int64_t)first < all_see); };
 
         uint32_t base = (w.first + step) * kStep;
         const uint32_t stop_at = min_u32((w.first + last_step) * kStep, w.end);
@@ -195,7 +260,7 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_rows_kernel(Atte
             I::lookup(args, table, base, w.end, tid & 63u, id, in_block);
             it.load(args, keys, values, head, id, in_block, tid);
             I::lookup(args, table, base + kStep, w.end, tid & 63u, id, in_block);
-            it.store(args, lds_k[0], lds_v[0], base, w.end, tid);
+            it.store(args, lds_k[0], lds_v[0], base, w.end, masked_from(base, kStep), &lds_odd[0], tid);
         }
         __syncthreads();
         for (uint32_t buffer = 0; base < stop_at; base += kStep, buffer ^= 1u) {
@@ -211,9 +276,9 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_rows_kernel(Atte
 #pragma unroll
             for (uint32_t u = 0; u < 2u / kSplits; ++u) {
                 const uint32_t half = kSplits == 1u ? u : split;
-                const uint32_t lane = opaque(threadIdx.x & 63u), r = lane & 15u, g = lane >> 4;
+                const uint32_t lane = opaque(threadIdx.x & 63u), g = lane >> 4;
                 const uint32_t b0 = base + half * 32u;
-                const bool masked = uniform(b0 + 32u > w.len || (int64_t)b0 < all_see);  // some row may not see all
+                const bool masked = masked_from(b0, 32u);  // some row may not see all
                 f32x4 s[kQueries][2];
 #pragma unroll
                 for (uint32_t t = 0; t < 2; ++t) {
@@ -228,14 +293,11 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_rows_kernel(Atte
                 }
                 uint32_t seen[kQueries] = {};
                 bf16x8 weights[kQueries];
+                if (masked) {
 #pragma unroll
-                for (int n = 0; n < kQueries; ++n) {
-                    if (masked) seen[n] = seen_bits(args, w, column[n], low[n], b0);
-                    weights[n] = weigh<true>(s[n], masked, seen[n], factor, g, m[n], sum[n], o[n]);
+                    for (int n = 0; n < kQueries; ++n) seen[n] = seen_bits(args, w, column[n], low[n], b0);
                 }
-                // A row may not see a value that is not finite, which a weight of 0 does not
-                // remove: such values count as 0 here and are added below, one by one.
-                bool odd = false;
+                weigh(s, masked, seen, factor, g, m, sum, o, weights);
 #pragma unroll
                 for (uint32_t i = 0; i < (uint32_t)I::kOut; ++i) {
                     u32x4 x;
@@ -247,37 +309,15 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_rows_kernel(Atte
                         x[2 * t] = z[0];
                         x[2 * t + 1] = z[1];
                     }
-                    if (masked) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) x[e] = only_finite(x[e], odd);
-                    }
 #pragma unroll
                     for (int n = 0; n < kQueries; ++n)
                         o[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), weights[n], o[n][i], 0, 0, 0);
                 }
-                if (uniform(masked && __ballot(odd) != 0ull)) {
-                    for (uint32_t key = 0; key < 32u; ++key) {
-                        float weight[kQueries];
-#pragma unroll
-                        for (int n = 0; n < kQueries; ++n) weight[n] = weight_of(weights[n], key, r);
-#pragma unroll
-                        for (uint32_t i = 0; i < (uint32_t)I::kOut; ++i) {
-                            const uint32_t d = i * 16u + g * 4u;
-                            const uint8_t* from = vs + I::value_chunk(half * 32u + key, d / 8u) * 16u + (d & 7u) * 2u;
-                            const u32x2 x = *reinterpret_cast<const u32x2*>(from);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float v1 = __builtin_bit_cast(float, e & 1 ? x[e / 2] & 0xFFFF0000u : x[e / 2] << 16);
-#pragma unroll
-                                for (int n = 0; n < kQueries; ++n)
-                                    if ((seen[n] >> key & 1u) && !__builtin_isfinite(v1)) o[n][i][e] += weight[n] * v1;
-                            }
-                        }
-                    }
-                }
+                if (masked && uniform(lds_odd[buffer] == base)) I::add_odd(args, table, values, head, b0, w.end, seen, weights, o, lane);
             }
             __builtin_amdgcn_sched_barrier(0);
-            it.store(args, lds_k[buffer ^ 1u], lds_v[buffer ^ 1u], base + kStep, w.end, opaque(threadIdx.x));
+            it.store(args, lds_k[buffer ^ 1u], lds_v[buffer ^ 1u], base + kStep, w.end, masked_from(base + kStep, kStep), &lds_odd[buffer ^ 1u],
+                     opaque(threadIdx.x));
             __syncthreads();
         }
 
