@@ -523,7 +523,8 @@ uint32_t rows_of(const AttendArgs& a) {
     const int64_t rows = (a.a.C + a.a.lanes - 1) / a.a.lanes * (a.a.heads / a.cache.c.heads);
     if (rows <= 16) return 16;
     if (rows <= 32 && padded_dim(a) < 256) return 32;
-    return rows <= 64 || padded_dim(a) == 256 ? 64 : 128;
+    if (rows <= 64 || padded_dim(a) == 256) return 64;
+    return rows <= 128 ? 128 : 256;
 }
 
 Shape shape_of(const AttendArgs& a, int64_t* bytes) {
@@ -533,7 +534,7 @@ Shape shape_of(const AttendArgs& a, int64_t* bytes) {
     s.group = Divisor::of((uint32_t)(a.a.heads / a.cache.c.heads));
     const int64_t step = s.rows <= 32 ? kStep : kRowsStep;
     // at most so many parts as workgroups run at once, and as there are steps
-    const int64_t most = dp < 256 ? 512 : 256;
+    const int64_t most = dp < 256 && s.rows < 256 ? 512 : 256;
     const int64_t items = a.cache.c.heads * ((a.a.C * s.group.d + s.rows - 1) / s.rows + a.a.lanes);
     const int64_t span = a.a.window ? std::min<int64_t>(a.places, (int64_t)a.a.window + a.a.C + step) : a.places;
     const int64_t steps = std::min<int64_t>(most, (span + step - 1) / step + 1);

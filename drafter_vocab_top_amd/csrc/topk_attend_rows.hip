@@ -1,8 +1,8 @@
 // Attention over the paged cache where a key head has many rows (see
 // topk_attend.hip for the mathematics and how the work is cut).
 //
-// The four waves of a workgroup share keys and values through LDS, 64 places at
-// a time.  kGroups groups of 16 kQueries rows each have a wave, or two that take
+// The waves of a workgroup share keys and values through LDS, 64 places at a
+// time.  kGroups groups of 16 kQueries rows each have a wave, or two that take
 // 32 of the places each and add up at the end (64 rows: four waves of 16 rows
 // would read every operand from LDS for half as many products).  The next 64 places are on their way to registers while these are worked
 // on (an e4m3 cache is widened between registers and LDS, once for all rows).
@@ -25,11 +25,12 @@ struct Rows {
     static constexpr uint32_t kStep = kRowsStep;
     static constexpr int kChunks = DP / 8;                       // 16-byte chunks of a row in LDS
     static constexpr int kVectors = DP * kSize / 16;             // 16-byte vectors of a row in memory
-    static constexpr int kLoads = kStep * kVectors / 256;        // of keys (and of values) for each thread
+    static constexpr uint32_t kWaves = kGroups < 4 ? 4 : kGroups, kThreads = 64 * kWaves;
+    static constexpr int kLoads = kStep * kVectors / kThreads;   // of keys (and of values) for each thread
     static constexpr int kKeySteps = DP / 32;
     static constexpr int kOut = DP / 16;
     static constexpr uint32_t kRows = 16 * kQueries * kGroups;
-    static constexpr uint32_t kSplits = 4 / kGroups;
+    static constexpr uint32_t kSplits = kWaves / kGroups;
 
     // Where chunk `c` of place `key` lies, in 16-byte units.
     __device__ __forceinline__ static uint32_t key_chunk(uint32_t key, uint32_t c) {
@@ -60,7 +61,7 @@ struct Rows {
         }
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const uint32_t x = (uint32_t)i * 256u + tid, key = x / kVectors, part = x % kVectors;
+            const uint32_t x = (uint32_t)i * kThreads + tid, key = x / kVectors, part = x % kVectors;
             const int64_t row = (int64_t)(((uint64_t)(uint32_t)from_lane((int32_t)(uint32_t)((uint64_t)at >> 32), key) << 32) |
                                           (uint32_t)from_lane((int32_t)(uint32_t)at, key));
             const int64_t off = row + (kWhole || (int32_t)(part * 16u) < c.dim * kSize ? part * 16u : 0u);
@@ -69,13 +70,20 @@ struct Rows {
         }
     }
 
-    // What has arrived goes to LDS; places past the end and elements past the row as zeros.  With `masked` (some row
+    // What has arrived goes to LDS; values past the end and keys' elements past the row as zeros.  With `masked` (some row
     // may not see some place) values that are not finite go there as zeros too: a weight of 0 would not remove
     // them.  They are added one by one (add_odd), where `odd` says that there are any: it gets `base`.
     __device__ __forceinline__ void store(const AttendArgs& a, u32x4* lds_k, u32x4* lds_v, uint32_t base, uint32_t end, bool masked, uint32_t* odd,
                                           uint32_t tid) const {
+        if (masked) store_as<true>(a, lds_k, lds_v, base, end, odd, tid);  // (so is every step with places past the end)
+        else store_as<false>(a, lds_k, lds_v, base, end, odd, tid);
+    }
+
+    template <bool kMasked>
+    __device__ __forceinline__ void store_as(const AttendArgs& a, u32x4* lds_k, u32x4* lds_v, uint32_t base, uint32_t end, uint32_t* odd,
+                                             uint32_t tid) const {
         uint32_t found = 0;
-        constexpr uint32_t kApart = 256 / kVectors;  // of a thread's places
+        constexpr uint32_t kApart = kThreads / kVectors;  // of a thread's places
         const uint32_t first = tid / kVectors, part = tid % kVectors;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
@@ -84,7 +92,6 @@ struct Rows {
             const uint32_t like = (uint32_t)i * kApart % 16u + first, whole = (uint32_t)i * kApart / 16u * 16u * kChunks;
             const bool in_row = kWhole || (int32_t)(part * 16u) < a.cache.c.dim * kSize;
             const u32x4 zero = {0u, 0u, 0u, 0u};
-            const bool has_value = in_row && base + key < end;
             if constexpr (kFp8) {
                 const uint32_t both = (uint32_t)from_lane((int32_t)scales, key);
                 const float ks = power_of(both & 0xFFu), vs = power_of(both >> 8);
@@ -99,19 +106,18 @@ struct Rows {
 #pragma unroll
                 for (uint32_t h = 0; h < 2; ++h) {
                     lds_k[key_chunk(like, 2u * part + h) + whole] = in_row ? y[h] : zero;
-                    z[h] = has_value ? z[h] : zero;
-                    if (masked) {
+                    if constexpr (kMasked) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) z[h][e] = only_finite(z[h][e], found);
+                        for (int e = 0; e < 4; ++e) z[h][e] = base + key < end ? only_finite(z[h][e], found) : 0u;
                     }
                     lds_v[value_chunk(like, 2u * part + h) + whole] = z[h];
                 }
             } else {
                 lds_k[key_chunk(like, part) + whole] = in_row ? k[i] : zero;
-                u32x4 z = has_value ? v[i] : zero;
-                if (masked) {
+                u32x4 z = v[i];
+                if constexpr (kMasked) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) z[e] = only_finite(z[e], found);
+                    for (int e = 0; e < 4; ++e) z[e] = base + key < end ? only_finite(z[e], found) : 0u;
                 }
                 lds_v[value_chunk(like, part) + whole] = z;
             }
@@ -161,13 +167,14 @@ struct Rows {
 };
 
 template <int DP, bool kWhole, bool kFp8, int kQueries, int kGroups>
-__global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_rows_kernel(AttendArgs args, Shape sh) {
+__global__ __launch_bounds__(64 * (kGroups < 4 ? 4 : kGroups), DP < 256 ? 2 : 1) void attend_rows_kernel(AttendArgs args, Shape sh) {
     using I = Rows<DP, kWhole, kFp8, kQueries, kGroups>;
     constexpr uint32_t R = I::kRows, kStep = kRowsStep, kSplits = I::kSplits;
+    constexpr uint32_t kAhead = 4;  // tiles of values read ahead
     static_assert(kSplits <= 2, "");
     __shared__ u32x4 lds_k[2][kStep * I::kChunks], lds_v[2][kStep * I::kChunks];
     __shared__ uint32_t lds_odd[2];
-    __shared__ int64_t lds_see[4];
+    __shared__ int64_t lds_see[I::kWaves];
     if (threadIdx.x < 2u) lds_odd[threadIdx.x] = ~0u;
     const topk_attend_args& a = args.a;
     const topk_cache& c = args.cache.c;
@@ -247,7 +254,8 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_rows_kernel(Atte
         if (threadIdx.x % 64u == 0u) lds_see[wave] = all_see;
         __syncthreads();
         // all rows of the item see the places from here up to the lane's columns
-        all_see = max(max(lds_see[0], lds_see[1]), max(lds_see[2], lds_see[3]));
+#pragma unroll
+        for (uint32_t i = 0; i < I::kWaves; ++i) all_see = max(all_see, lds_see[i]);
         all_see = (int64_t)bcast((uint64_t)all_see, 0);
         auto masked_from = [&](uint32_t first, uint32_t places) { return uniform(first + places > w.len || (int64_t)first < all_see); };
 
@@ -261,16 +269,11 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_rows_kernel(Atte
             it.load(args, keys, values, head, id, in_block, tid);
             I::lookup(args, table, base + kStep, w.end, tid & 63u, id, in_block);
             it.store(args, lds_k[0], lds_v[0], base, w.end, masked_from(base, kStep), &lds_odd[0], tid);
+            it.load(args, keys, values, head, id, in_block, tid);
+            I::lookup(args, table, base + 2 * kStep, w.end, tid & 63u, id, in_block);
         }
         __syncthreads();
         for (uint32_t buffer = 0; base < stop_at; base += kStep, buffer ^= 1u) {
-            {
-                // the next places (past the end: the last one again)
-                const uint32_t tid = opaque(threadIdx.x);
-                it.load(args, keys, values, head, id, in_block, tid);
-                I::lookup(args, table, base + 2 * kStep, w.end, tid & 63u, id, in_block);
-            }
-            __builtin_amdgcn_sched_barrier(0);
             const uint8_t* ks = reinterpret_cast<const uint8_t*>(lds_k[buffer]);
             const uint8_t* vs = reinterpret_cast<const uint8_t*>(lds_v[buffer]);
 #pragma unroll
@@ -280,17 +283,39 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_rows_kernel(Atte
                 const uint32_t b0 = base + half * 32u;
                 const bool masked = masked_from(b0, 32u);  // some row may not see all
                 f32x4 s[kQueries][2];
+                // (operands are read ahead of their products: left to itself the compiler waits for each)
+                bf16x8 x[2][I::kKeySteps];
 #pragma unroll
-                for (uint32_t t = 0; t < 2; ++t) {
+                for (uint32_t i = 0; i < (uint32_t)I::kKeySteps; ++i)
 #pragma unroll
-                    for (int n = 0; n < kQueries; ++n) s[n][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    for (uint32_t t = 0; t < 2; ++t)
+                        x[t][i] = *reinterpret_cast<const bf16x8*>(ks + key_at[i] + (half * 32u + t * 16u) * I::kChunks * 16u);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (uint32_t i = 0; i < (uint32_t)I::kKeySteps; ++i) {
-                        const bf16x8 x = *reinterpret_cast<const bf16x8*>(ks + key_at[i] + (half * 32u + t * 16u) * I::kChunks * 16u);
+                for (int n = 0; n < kQueries; ++n) s[n][0] = s[n][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                        for (int n = 0; n < kQueries; ++n) s[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, q[n][i], s[n][t], 0, 0, 0);
+                for (uint32_t i = 0; i < (uint32_t)I::kKeySteps; ++i)
+#pragma unroll
+                    for (uint32_t t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int n = 0; n < kQueries; ++n) s[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[t][i], q[n][i], s[n][t], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+                // the first values are read while weights are made
+                u32x4 y[kAhead];
+                auto read_values = [&](uint32_t i) __attribute__((always_inline)) {
+                    u32x4 z;
+#pragma unroll
+                    for (uint32_t t = 0; t < 2; ++t) {
+                        const s16x4 z1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            (__attribute__((address_space(3))) s16x4*)(vs + value_at[i] + (half * 32u + t * 16u) * I::kChunks * 16u));
+                        const u32x2 z2 = __builtin_bit_cast(u32x2, z1);
+                        z[2 * t] = z2[0];
+                        z[2 * t + 1] = z2[1];
                     }
-                }
+                    return z;
+                };
+#pragma unroll
+                for (uint32_t i = 0; i < kAhead; ++i) y[i] = read_values(i);
                 uint32_t seen[kQueries] = {};
                 bf16x8 weights[kQueries];
                 if (masked) {
@@ -300,24 +325,22 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_rows_kernel(Atte
                 weigh(s, masked, seen, factor, g, m, sum, o, weights);
 #pragma unroll
                 for (uint32_t i = 0; i < (uint32_t)I::kOut; ++i) {
-                    u32x4 x;
+                    const bf16x8 v1 = __builtin_bit_cast(bf16x8, y[i % kAhead]);
+                    if (i + kAhead < (uint32_t)I::kOut) y[i % kAhead] = read_values(i + kAhead);
 #pragma unroll
-                    for (uint32_t t = 0; t < 2; ++t) {
-                        const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                            (__attribute__((address_space(3))) s16x4*)(vs + value_at[i] + (half * 32u + t * 16u) * I::kChunks * 16u));
-                        const u32x2 z = __builtin_bit_cast(u32x2, y);
-                        x[2 * t] = z[0];
-                        x[2 * t + 1] = z[1];
-                    }
-#pragma unroll
-                    for (int n = 0; n < kQueries; ++n)
-                        o[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), weights[n], o[n][i], 0, 0, 0);
+                    for (int n = 0; n < kQueries; ++n) o[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, weights[n], o[n][i], 0, 0, 0);
                 }
                 if (masked && uniform(lds_odd[buffer] == base)) I::add_odd(args, table, values, head, b0, w.end, seen, weights, o, lane);
             }
             __builtin_amdgcn_sched_barrier(0);
             it.store(args, lds_k[buffer ^ 1u], lds_v[buffer ^ 1u], base + kStep, w.end, masked_from(base + kStep, kStep), &lds_odd[buffer ^ 1u],
                      opaque(threadIdx.x));
+            {
+                // the places behind them (past the end: the last one again)
+                const uint32_t tid = opaque(threadIdx.x);
+                it.load(args, keys, values, head, id, in_block, tid);
+                I::lookup(args, table, base + 3 * kStep, w.end, tid & 63u, id, in_block);
+            }
             __syncthreads();
         }
 
@@ -390,12 +413,13 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_rows_kernel(Atte
 
 template <int DP, bool kWhole, bool kFp8>
 void launch_rows(const AttendArgs& a, const Shape& s, hipStream_t stream) {
-    const dim3 grid(s.workers), block(256);
+    const dim3 grid(s.workers), block(s.rows == 256 ? 512 : 256);
     if constexpr (DP == 256) {
         hipLaunchKernelGGL((attend_rows_kernel<DP, kWhole, kFp8, 1, 4>), grid, block, 0, stream, a, s);
     } else {
         if (s.rows == 64) hipLaunchKernelGGL((attend_rows_kernel<DP, kWhole, kFp8, 2, 2>), grid, block, 0, stream, a, s);
-        else hipLaunchKernelGGL((attend_rows_kernel<DP, kWhole, kFp8, 2, 4>), grid, block, 0, stream, a, s);
+        else if (s.rows == 128) hipLaunchKernelGGL((attend_rows_kernel<DP, kWhole, kFp8, 2, 4>), grid, block, 0, stream, a, s);
+        else hipLaunchKernelGGL((attend_rows_kernel<DP, kWhole, kFp8, 2, 8>), grid, block, 0, stream, a, s);
     }
 }
 
