@@ -71,25 +71,18 @@ struct Item {
         return s;
     }
 
-    // Offset in bytes of the row of the place that lane `key` looked up.
+    // Offset in 16 bytes of the row of the place that lane `key` looked up.
     struct Rows {
-        int32_t lo, hi;
-        __device__ __forceinline__ int64_t of(uint32_t key) const {
-            return (int64_t)(((uint64_t)(uint32_t)from_lane(hi, key) << 32) | (uint32_t)from_lane(lo, key));
-        }
+        uint32_t own;
+        __device__ __forceinline__ uint32_t of(uint32_t key) const { return (uint32_t)from_lane((int32_t)own, key); }
     };
-    __device__ __forceinline__ Rows rows_of(const AttendArgs& a, const Places& s) const {
-        const topk_cache& c = a.cache.c;
-        const int64_t at = ((int64_t)s.id * c.block_stride + (int64_t)s.in_block * c.slot_stride) * kSize;
-        return Rows{(int32_t)(uint32_t)at, (int32_t)(uint32_t)((uint64_t)at >> 32)};
-    }
+    __device__ __forceinline__ Rows rows_of(const AttendArgs& a, const Places& s) const { return Rows{a.cache.row16(s.id, s.in_block)}; }
 
     __device__ __forceinline__ void load_scales(const AttendArgs& a, const Places& s, uint32_t head, uint32_t lane) {
         if constexpr (kFp8) {
             const topk_cache& c = a.cache.c;
             const uint8_t* from = (lane & 32u) ? c.value_scales : c.key_scales;
-            next_scales = from[(int64_t)s.id * c.scale_block_stride + (int64_t)s.in_block * c.scale_slot_stride +
-                               (int64_t)head * c.scale_head_stride];
+            next_scales = (from + (int64_t)head * c.scale_head_stride)[a.cache.scale_row(s.id, s.in_block)];
         }
     }
 
@@ -102,7 +95,7 @@ struct Item {
         const int32_t dim = a.cache.c.dim;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const uint8_t* row = keys + at.of((uint32_t)t * 16u + (lane & 15u)) + (kWhole ? g * 16u : 0u);
+            const uint8_t* row = past16(keys, at.of((uint32_t)t * 16u + (lane & 15u))) + (kWhole ? g * 16u : 0u);
 #pragma unroll
             for (int i = 0; i < kKeyLoads; ++i) {
                 // (past the row: its start, cleared below)
@@ -117,7 +110,7 @@ struct Item {
         const int32_t dim = a.cache.c.dim;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const uint8_t* row = values + at.of((uint32_t)(e >> 2) * 16u + g * 4u + (uint32_t)(e & 3)) + (kWhole ? r * (kOwn * kSize) : 0u);
+            const uint8_t* row = past16(values, at.of((uint32_t)(e >> 2) * 16u + g * 4u + (uint32_t)(e & 3))) + (kWhole ? r * (kOwn * kSize) : 0u);
 #pragma unroll
             for (int h = 0; h < kHalves; ++h) {
                 const int32_t d = h * kHalf + (kWhole ? 0 : (int32_t)r * kOwn);
@@ -173,11 +166,10 @@ struct Item {
         uint32_t scale_byte = 0;
         if constexpr (kFp8) {
             const topk_cache& c = a.cache.c;
-            scale_byte = c.value_scales[(int64_t)s.id * c.scale_block_stride + (int64_t)s.in_block * c.scale_slot_stride +
-                                        (int64_t)head * c.scale_head_stride];
+            scale_byte = c.value_scales[(int64_t)head * c.scale_head_stride + a.cache.scale_row(s.id, s.in_block)];
                     }
         for (uint32_t key = 0; key < kTile && base + key < end; ++key) {
-            const uint8_t* row = values + at.of(key);
+            const uint8_t* row = past16(values, at.of(key));
             const float scale = power_of((uint32_t)from_lane((int32_t)scale_byte, key));
             float weight[kQueries];
             bool sees[kQueries];

@@ -41,7 +41,7 @@ struct Rows {
     }
 
     u32x4 k[kLoads], v[kLoads];  // on their way
-    uint32_t scales;             // lane's place: byte of the keys, byte of the values
+    uint32_t key_scale, value_scale;  // of the lane's place, as binary32
 
     // Place base + lane of the step: block and slot in it.
     __device__ __forceinline__ static void lookup(const AttendArgs& a, const int32_t* table, uint32_t base, uint32_t end, uint32_t lane, uint32_t& id,
@@ -54,19 +54,19 @@ struct Rows {
     __device__ __forceinline__ void load(const AttendArgs& a, const uint8_t* keys, const uint8_t* values, uint32_t head, uint32_t id,
                                          uint32_t in_block, uint32_t tid) {
         const topk_cache& c = a.cache.c;
-        const int64_t at = ((int64_t)id * c.block_stride + (int64_t)in_block * c.slot_stride) * kSize;
+        const uint32_t at = a.cache.row16(id, in_block);
         if constexpr (kFp8) {
-            const int64_t s = (int64_t)id * c.scale_block_stride + (int64_t)in_block * c.scale_slot_stride + (int64_t)head * c.scale_head_stride;
-            scales = (uint32_t)c.key_scales[s] | ((uint32_t)c.value_scales[s] << 8);
+            const uint32_t s = a.cache.scale_row(id, in_block);
+            const int64_t h = (int64_t)head * c.scale_head_stride;
+            key_scale = (c.key_scales + h)[s];
+            value_scale = (c.value_scales + h)[s];
         }
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const uint32_t x = (uint32_t)i * kThreads + tid, key = x / kVectors, part = x % kVectors;
-            const int64_t row = (int64_t)(((uint64_t)(uint32_t)from_lane((int32_t)(uint32_t)((uint64_t)at >> 32), key) << 32) |
-                                          (uint32_t)from_lane((int32_t)(uint32_t)at, key));
-            const int64_t off = row + (kWhole || (int32_t)(part * 16u) < c.dim * kSize ? part * 16u : 0u);
-            k[i] = *reinterpret_cast<const u32x4*>(keys + off);
-            v[i] = *reinterpret_cast<const u32x4*>(values + off);
+            const uint32_t off = (uint32_t)from_lane((int32_t)at, key) + (kWhole || (int32_t)(part * 16u) < c.dim * kSize ? part : 0u);
+            k[i] = *reinterpret_cast<const u32x4*>(past16(keys, off));
+            v[i] = *reinterpret_cast<const u32x4*>(past16(values, off));
         }
     }
 
@@ -83,6 +83,7 @@ struct Rows {
     __device__ __forceinline__ void store_as(const AttendArgs& a, u32x4* lds_k, u32x4* lds_v, uint32_t base, uint32_t end, uint32_t* odd,
                                              uint32_t tid) const {
         uint32_t found = 0;
+        const int32_t ks_bits = __builtin_bit_cast(int32_t, power_of(key_scale)), vs_bits = __builtin_bit_cast(int32_t, power_of(value_scale));
         constexpr uint32_t kApart = kThreads / kVectors;  // of a thread's places
         const uint32_t first = tid / kVectors, part = tid % kVectors;
 #pragma unroll
@@ -93,8 +94,7 @@ struct Rows {
             const bool in_row = kWhole || (int32_t)(part * 16u) < a.cache.c.dim * kSize;
             const u32x4 zero = {0u, 0u, 0u, 0u};
             if constexpr (kFp8) {
-                const uint32_t both = (uint32_t)from_lane((int32_t)scales, key);
-                const float ks = power_of(both & 0xFFu), vs = power_of(both >> 8);
+                const float ks = __builtin_bit_cast(float, from_lane(ks_bits, key)), vs = __builtin_bit_cast(float, from_lane(vs_bits, key));
                 u32x4 y[2], z[2];
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
@@ -134,11 +134,10 @@ struct Rows {
         for (uint32_t key = 0; key < 32u && base + key < end; ++key) {
             uint32_t id, in_block;
             lookup(a, table, base + key, end, 0u, id, in_block);
-            const uint8_t* row = values + ((int64_t)id * c.block_stride + (int64_t)in_block * c.slot_stride) * kSize;
+            const uint8_t* row = past16(values, a.cache.row16(id, in_block));
             float scale = 1.0f;
             if constexpr (kFp8)
-                scale = power_of(c.value_scales[(int64_t)id * c.scale_block_stride + (int64_t)in_block * c.scale_slot_stride +
-                                                (int64_t)head * c.scale_head_stride]);
+                scale = power_of(c.value_scales[(int64_t)head * c.scale_head_stride + a.cache.scale_row(id, in_block)]);
             float weight[kQueries];
 #pragma unroll
             for (int n = 0; n < kQueries; ++n) weight[n] = weight_of(weights[n], key, r);
@@ -334,7 +333,7 @@ __global__ __launch_bounds__(64 * (kGroups < 4 ? 4 : kGroups), DP < 256 ? 2 : 1)
             }
             __builtin_amdgcn_sched_barrier(0);
             it.store(args, lds_k[buffer ^ 1u], lds_v[buffer ^ 1u], base + kStep, w.end, masked_from(base + kStep, kStep), &lds_odd[buffer ^ 1u],
-                     opaque(threadIdx.x));
+                     threadIdx.x);
             {
                 // the places behind them (past the end: the last one again)
                 const uint32_t tid = opaque(threadIdx.x);

@@ -57,8 +57,9 @@ __global__ __launch_bounds__(256) void write_kernel(CacheWriteArgs a) {
         load8<DT>(values ? a.w.values : a.w.keys,
                   (int64_t)col * (values ? a.w.value_stride : a.w.key_stride) +
                       (int64_t)head * (values ? a.w.value_head_stride : a.w.key_head_stride) + part * 8u, x);
-    const int64_t at = live ? a.cache.row((uint32_t)slot) + (int64_t)head * c.head_stride + part * 8u : 0;
-    void* to = values ? c.values : c.keys;
+    const uint32_t block = a.cache.block.div(live ? (uint32_t)slot : 0u), in_block = (live ? (uint32_t)slot : 0u) - block * a.cache.block.d;
+    void* to = past16(values ? c.values : c.keys, a.cache.row16(block, in_block));
+    const int64_t at = (int64_t)head * c.head_stride + part * 8u;
     if constexpr (!kFp8) {
         if (!live) return;
         u32x4 v;
@@ -88,7 +89,7 @@ __global__ __launch_bounds__(256) void write_kernel(CacheWriteArgs a) {
         }
         *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(to) + at) = v;
         if (part == 0)
-            (values ? c.value_scales : c.key_scales)[a.cache.scale_row((uint32_t)slot) + (int64_t)head * c.scale_head_stride] =
+            (values ? c.value_scales : c.key_scales)[a.cache.scale_row(block, in_block) + (int64_t)head * c.scale_head_stride] =
                 (uint8_t)(e + 127);
     }
 }

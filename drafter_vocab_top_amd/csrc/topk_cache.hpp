@@ -42,16 +42,18 @@ struct Divisor {
 struct Cache {
     topk_cache c;
     Divisor block;
-    // Element offset of a slot's first head in layer 0.
-    __device__ __forceinline__ int64_t row(uint32_t slot) const {
-        const uint32_t b = block.div(slot), r = slot - b * block.d;
-        return (int64_t)b * c.block_stride + (int64_t)r * c.slot_stride;
-    }
-    __device__ __forceinline__ int64_t scale_row(uint32_t slot) const {
-        const uint32_t b = block.div(slot), r = slot - b * block.d;
-        return (int64_t)b * c.scale_block_stride + (int64_t)r * c.scale_slot_stride;
-    }
+    // Strides in 16 bytes, and of the scales in bytes: no offset within a layer passes 32 bits then (a layer has less
+    // than 64 GiB, its scales less than 4).
+    uint32_t block16, slot16, scale_block, scale_slot;
+    // Offset of slot r of block b (its first head), in 16 bytes; and of its scale.
+    __device__ __forceinline__ uint32_t row16(uint32_t b, uint32_t r) const { return b * block16 + r * slot16; }
+    __device__ __forceinline__ uint32_t scale_row(uint32_t b, uint32_t r) const { return b * scale_block + r * scale_slot; }
 };
+
+template <class T>
+__device__ __forceinline__ T* past16(T* base, uint32_t offset16) {
+    return reinterpret_cast<T*>((uintptr_t)base + ((uint64_t)offset16 << 4));
+}
 
 struct CacheWriteArgs {
     Cache cache;  // of the layer

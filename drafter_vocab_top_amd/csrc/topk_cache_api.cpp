@@ -24,6 +24,11 @@ int make_parts(topk::Parts* parts, const int32_t* start, int64_t total, int64_t 
     return TOPK_OK;
 }
 
+// Offset of the last slot of a layer.
+unsigned __int128 last_slot(const topk_cache& c, int64_t block_stride, int64_t slot_stride) {
+    return (unsigned __int128)(c.blocks - 1) * (uint64_t)block_stride + (unsigned __int128)(c.block_size - 1) * (uint64_t)slot_stride;
+}
+
 int check_cache(const topk_cache* c) {
     if (!c || c->layers < 1 || c->blocks < 1 || c->block_size < 1 || c->heads < 1 || c->dim < 16 || c->dim % 16 != 0)
         return TOPK_ERR_INVALID_ARG;
@@ -39,13 +44,18 @@ int check_cache(const topk_cache* c) {
         return TOPK_ERR_INVALID_ARG;
     if (c->dim > TOPK_MAX_DIM || c->blocks > kMax32 / c->block_size || c->layers > kMaxPlanes / c->heads)
         return TOPK_ERR_UNSUPPORTED;
+    // offsets within a layer are computed in 32 bits, of rows in units of 16 bytes
+    if (last_slot(*c, c->block_stride / unit, c->slot_stride / unit) >> 32 ||
+        (c->format == TOPK_CACHE_FP8 && last_slot(*c, c->scale_block_stride, c->scale_slot_stride) >> 32))
+        return TOPK_ERR_UNSUPPORTED;
     return TOPK_OK;
 }
 
 // The cache from `layer` on.
 topk::Cache cache_at(const topk_cache& c, int64_t layer) {
-    topk::Cache a = {c, topk::Divisor::of((uint32_t)c.block_size)};
     const int64_t size = c.format == TOPK_CACHE_BF16 ? 2 : 1;
+    topk::Cache a = {c, topk::Divisor::of((uint32_t)c.block_size), (uint32_t)(c.block_stride * size / 16), (uint32_t)(c.slot_stride * size / 16),
+                     (uint32_t)c.scale_block_stride, (uint32_t)c.scale_slot_stride};
     a.c.keys = static_cast<uint8_t*>(c.keys) + layer * c.layer_stride * size;
     a.c.values = static_cast<uint8_t*>(c.values) + layer * c.layer_stride * size;
     if (c.format == TOPK_CACHE_FP8) {

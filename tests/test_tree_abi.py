@@ -37,7 +37,8 @@ BAD_CACHES += [dict(FP8, **kw) for kw in (
     dict(key_scales=None), dict(value_scales=None), dict(scale_layer_stride=-1), dict(scale_block_stride=-1),
     dict(scale_slot_stride=-1), dict(scale_head_stride=-1), dict(head_stride=8))]
 LARGE_CACHES = [dict(CACHE, **kw) for kw in (
-    dict(dim=272), dict(blocks=1 << 27), dict(blocks=1 << 31, block_size=1), dict(layers=1 << 20))]
+    dict(dim=272), dict(blocks=1 << 27), dict(blocks=1 << 31, block_size=1), dict(layers=1 << 20),
+    dict(block_stride=1 << 34), dict(slot_stride=1 << 33))] + [dict(FP8, scale_block_stride=1 << 29), dict(FP8, block_stride=1 << 33)]
 
 WRITE = dict(C=8, layer=0, dtype=0, keys=P, values=P, key_stride=128, key_head_stride=64, value_stride=128,
              value_head_stride=64, slots=P)
