@@ -301,18 +301,18 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_kernel(AttendArg
             const uint32_t lane = opaque(threadIdx.x & 63u), r = lane & 15u, g = lane >> 4;
             it.scales = it.next_scales;
             // scores of 32 places
-            f32x4 s[kQueries][2];
+            f32x4 s[1][kQueries][2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const float scale = kFp8 ? it.scale_from((uint32_t)t * 16u + r) : 1.0f;
 #pragma unroll
-                for (int n = 0; n < kQueries; ++n) s[n][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int n = 0; n < kQueries; ++n) s[0][n][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int i = 0; i < I::kKeySteps; ++i) {
                     const bf16x8 x = it.key_operand(args, t, i, scale, lane);
 #pragma unroll
                     for (int n = 0; n < kQueries; ++n)
-                        s[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, it.q[n][i], s[n][t], 0, 0, 0);
+                        s[0][n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, it.q[n][i], s[0][n][t], 0, 0, 0);
                 }
             }
             // the next keys (past the end: the last place again)
@@ -324,11 +324,11 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_kernel(AttendArg
             it.load_keys(args, keys, at, lane);
             __builtin_amdgcn_sched_barrier(0);
 
-            uint32_t seen[kQueries] = {};
-            bf16x8 weights[kQueries];
+            uint32_t seen[1][kQueries] = {};
+            bf16x8 weights[1][kQueries];
             if (masked) {
 #pragma unroll
-                for (int n = 0; n < kQueries; ++n) seen[n] = seen_bits(args, w, column[n], low[n], base);
+                for (int n = 0; n < kQueries; ++n) seen[0][n] = seen_bits(args, w, column[n], low[n], base);
             }
             weigh(s, masked, seen, factor, g, it.m, it.sum, it.o, weights);
 
@@ -374,10 +374,10 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_kernel(AttendArg
                         x[e] = __builtin_amdgcn_perm(pairs[2 * e + 1][h][i / 2], pairs[2 * e][h][i / 2], i & 1 ? 0x07060302u : 0x05040100u);
 #pragma unroll
                     for (int n = 0; n < kQueries; ++n)
-                        it.o[n][h * I::kOwn + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), weights[n],
+                        it.o[n][h * I::kOwn + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), weights[0][n],
                                                                                           it.o[n][h * I::kOwn + i], 0, 0, 0);
                 }
-            if (uniform(masked && __ballot(odd != 0u) != 0ull)) it.add_odd(args, table, values, head, base, w.end, seen, weights, lane);
+            if (uniform(masked && __ballot(odd != 0u) != 0ull)) it.add_odd(args, table, values, head, base, w.end, seen[0], weights[0], lane);
             __builtin_amdgcn_sched_barrier(0);
             it.load_values(args, values, at, lane);
         }

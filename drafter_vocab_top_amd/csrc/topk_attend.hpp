@@ -184,27 +184,34 @@ __device__ __forceinline__ int64_t first_seen(const AttendArgs& args, const Lane
     return (a.positions ? max((int64_t)a.positions[w.cb + j], (int64_t)w.len) : (int64_t)w.len + j) - a.window + 1;
 }
 
-// Scores of 16 kQueries queries against 32 places become weights: lane 16 g + r has query r of each 16 and places
-// 4 g + i and 16 + 4 g + i.  m, sum and o (16 x 16 tiles, a query in each column) are the running maximum, sum and
-// output.  The sum is a product with ones: it is of the weights as they are rounded for the products with values.
-// `seen`: with `masked`, the places that each query sees.
-template <int kQueries, int kOut>
-__device__ __forceinline__ void weigh(f32x4 (&s)[kQueries][2], bool masked, const uint32_t (&seen)[kQueries], float factor, uint32_t g,
-                                      float (&m)[kQueries], f32x4 (&sum)[kQueries], f32x4 (&o)[kQueries][kOut], bf16x8 (&weights)[kQueries]) {
+// Scores of 16 kQueries queries against 32 kTiles places become weights: lane 16 g + r has query r of each 16 and
+// places 4 g + i and 16 + 4 g + i of each 32.  m, sum and o (16 x 16 tiles, a query in each column) are the running
+// maximum, sum and output.  The sum is a product with ones: it is of the weights as they are rounded for the products
+// with values.  `seen`: with `masked`, the places that each query sees.
+template <int kTiles, int kQueries, int kOut>
+__device__ __forceinline__ void weigh(f32x4 (&s)[kTiles][kQueries][2], bool masked, const uint32_t (&seen)[kTiles][kQueries], float factor,
+                                      uint32_t g, float (&m)[kQueries], f32x4 (&sum)[kQueries], f32x4 (&o)[kQueries][kOut],
+                                      bf16x8 (&weights)[kTiles][kQueries]) {
     if (masked) {
 #pragma unroll
-        for (int n = 0; n < kQueries; ++n)
+        for (int u = 0; u < kTiles; ++u)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int n = 0; n < kQueries; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][t][e] = (seen[n] >> (t * 16 + (int)g * 4 + e)) & 1u ? s[n][t][e] : kNone;
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[u][n][t][e] = (seen[u][n] >> (t * 16 + (int)g * 4 + e)) & 1u ? s[u][n][t][e] : kNone;
     }
     float top[kQueries];
     bool grown = false;
 #pragma unroll
     for (int n = 0; n < kQueries; ++n) {
-        top[n] = __builtin_fmaxf(__builtin_fmaxf(s[n][0][0], s[n][0][1]), __builtin_fmaxf(s[n][0][2], s[n][0][3]));
-        top[n] = __builtin_fmaxf(top[n], __builtin_fmaxf(__builtin_fmaxf(s[n][1][0], s[n][1][1]), __builtin_fmaxf(s[n][1][2], s[n][1][3])));
+        top[n] = kNone;
+#pragma unroll
+        for (int u = 0; u < kTiles; ++u)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                top[n] = __builtin_fmaxf(top[n], __builtin_fmaxf(__builtin_fmaxf(s[u][n][t][0], s[u][n][t][1]), __builtin_fmaxf(s[u][n][t][2], s[u][n][t][3])));
         top[n] *= factor;
         grown |= top[n] > m[n] + 8.0f;
     }
@@ -221,17 +228,19 @@ __device__ __forceinline__ void weigh(f32x4 (&s)[kQueries][2], bool masked, cons
     }
     const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 #pragma unroll
-    for (int n = 0; n < kQueries; ++n) {
-        const float zero = m[n] == kNone ? 0.0f : m[n];
-        float x[8];
+    for (int u = 0; u < kTiles; ++u)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][e >> 2][e & 3], factor, -zero));
-        u32x4 y;
+        for (int n = 0; n < kQueries; ++n) {
+            const float zero = m[n] == kNone ? 0.0f : m[n];
+            float x[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
-        weights[n] = __builtin_bit_cast(bf16x8, y);
-        sum[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, ones), weights[n], sum[n], 0, 0, 0);
-    }
+            for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][n][e >> 2][e & 3], factor, -zero));
+            u32x4 y;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+            weights[u][n] = __builtin_bit_cast(bf16x8, y);
+            sum[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, ones), weights[u][n], sum[n], 0, 0, 0);
+        }
 }
 
 __device__ __forceinline__ float power_of(uint32_t byte) { return __builtin_bit_cast(float, byte ? byte << 23 : 0x400000u); }

@@ -169,7 +169,8 @@ template <int DP, bool kWhole, bool kFp8, int kQueries, int kGroups>
 __global__ __launch_bounds__(64 * (kGroups < 4 ? 4 : kGroups), DP < 256 ? 2 : 1) void attend_rows_kernel(AttendArgs args, Shape sh) {
     using I = Rows<DP, kWhole, kFp8, kQueries, kGroups>;
     constexpr uint32_t R = I::kRows, kStep = kRowsStep, kSplits = I::kSplits;
-    constexpr uint32_t kAhead = 4;  // tiles of values read ahead
+    constexpr uint32_t kAhead = 4;             // operands of values read ahead
+    constexpr uint32_t kTiles = 2u / kSplits;  // times 32 places of a wave
     static_assert(kSplits <= 2, "");
     __shared__ u32x4 lds_k[2][kStep * I::kChunks], lds_v[2][kStep * I::kChunks];
     __shared__ uint32_t lds_odd[2];
@@ -275,61 +276,69 @@ __global__ __launch_bounds__(64 * (kGroups < 4 ? 4 : kGroups), DP < 256 ? 2 : 1)
         for (uint32_t buffer = 0; base < stop_at; base += kStep, buffer ^= 1u) {
             const uint8_t* ks = reinterpret_cast<const uint8_t*>(lds_k[buffer]);
             const uint8_t* vs = reinterpret_cast<const uint8_t*>(lds_v[buffer]);
+            const uint32_t lane = opaque(threadIdx.x & 63u), g = lane >> 4;
+            const uint32_t b0 = base + split * 32u;                             // this wave's places: kTiles times 32
+            const bool masked = masked_from(b0, 32u * kTiles);                  // some row may not see all
+            const uint32_t own = split * 32u * I::kChunks * 16u;
+            // Operands are read ahead of their products (left to itself the compiler waits for each).
+            f32x4 s[kTiles][kQueries][2];
+            bf16x8 x[2][I::kKeySteps];
+            auto read_keys = [&](uint32_t t) __attribute__((always_inline)) {
 #pragma unroll
-            for (uint32_t u = 0; u < 2u / kSplits; ++u) {
-                const uint32_t half = kSplits == 1u ? u : split;
-                const uint32_t lane = opaque(threadIdx.x & 63u), g = lane >> 4;
-                const uint32_t b0 = base + half * 32u;
-                const bool masked = masked_from(b0, 32u);  // some row may not see all
-                f32x4 s[kQueries][2];
-                // (operands are read ahead of their products: left to itself the compiler waits for each)
-                bf16x8 x[2][I::kKeySteps];
+                for (uint32_t i = 0; i < (uint32_t)I::kKeySteps; ++i)
+                    x[t & 1u][i] = *reinterpret_cast<const bf16x8*>(ks + key_at[i] + own + t * 16u * I::kChunks * 16u);
+            };
+            read_keys(0);
+#pragma unroll
+            for (uint32_t t = 0; t < 2u * kTiles; ++t) {
+                if (t + 1u < 2u * kTiles) read_keys(t + 1u);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int n = 0; n < kQueries; ++n) s[t / 2][n][t & 1u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (uint32_t i = 0; i < (uint32_t)I::kKeySteps; ++i)
 #pragma unroll
-                    for (uint32_t t = 0; t < 2; ++t)
-                        x[t][i] = *reinterpret_cast<const bf16x8*>(ks + key_at[i] + (half * 32u + t * 16u) * I::kChunks * 16u);
+                    for (int n = 0; n < kQueries; ++n)
+                        s[t / 2][n][t & 1u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[t & 1u][i], q[n][i], s[t / 2][n][t & 1u], 0, 0, 0);
                 __builtin_amdgcn_sched_barrier(0);
+            }
+            // the first values are read while weights are made: tile i of the output for places 32 u .. 32 u + 31
+            u32x4 y[kAhead];
+            auto read_values = [&](uint32_t iu) __attribute__((always_inline)) {
+                const uint32_t i = iu / kTiles, u = iu % kTiles;
+                u32x4 z;
 #pragma unroll
-                for (int n = 0; n < kQueries; ++n) s[n][0] = s[n][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (uint32_t i = 0; i < (uint32_t)I::kKeySteps; ++i)
-#pragma unroll
-                    for (uint32_t t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int n = 0; n < kQueries; ++n) s[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[t][i], q[n][i], s[n][t], 0, 0, 0);
-                __builtin_amdgcn_sched_barrier(0);
-                // the first values are read while weights are made
-                u32x4 y[kAhead];
-                auto read_values = [&](uint32_t i) __attribute__((always_inline)) {
-                    u32x4 z;
-#pragma unroll
-                    for (uint32_t t = 0; t < 2; ++t) {
-                        const s16x4 z1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                            (__attribute__((address_space(3))) s16x4*)(vs + value_at[i] + (half * 32u + t * 16u) * I::kChunks * 16u));
-                        const u32x2 z2 = __builtin_bit_cast(u32x2, z1);
-                        z[2 * t] = z2[0];
-                        z[2 * t + 1] = z2[1];
-                    }
-                    return z;
-                };
-#pragma unroll
-                for (uint32_t i = 0; i < kAhead; ++i) y[i] = read_values(i);
-                uint32_t seen[kQueries] = {};
-                bf16x8 weights[kQueries];
-                if (masked) {
-#pragma unroll
-                    for (int n = 0; n < kQueries; ++n) seen[n] = seen_bits(args, w, column[n], low[n], b0);
+                for (uint32_t t = 0; t < 2; ++t) {
+                    const s16x4 z1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        (__attribute__((address_space(3))) s16x4*)(vs + value_at[i] + own + (u * 32u + t * 16u) * I::kChunks * 16u));
+                    const u32x2 z2 = __builtin_bit_cast(u32x2, z1);
+                    z[2 * t] = z2[0];
+                    z[2 * t + 1] = z2[1];
                 }
-                weigh(s, masked, seen, factor, g, m, sum, o, weights);
+                return z;
+            };
 #pragma unroll
-                for (uint32_t i = 0; i < (uint32_t)I::kOut; ++i) {
-                    const bf16x8 v1 = __builtin_bit_cast(bf16x8, y[i % kAhead]);
-                    if (i + kAhead < (uint32_t)I::kOut) y[i % kAhead] = read_values(i + kAhead);
+            for (uint32_t i = 0; i < kAhead; ++i) y[i] = read_values(i);
+            uint32_t seen[kTiles][kQueries] = {};
+            bf16x8 weights[kTiles][kQueries];
+            if (masked) {
 #pragma unroll
-                    for (int n = 0; n < kQueries; ++n) o[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, weights[n], o[n][i], 0, 0, 0);
-                }
-                if (masked && uniform(lds_odd[buffer] == base)) I::add_odd(args, table, values, head, b0, w.end, seen, weights, o, lane);
+                for (uint32_t u = 0; u < kTiles; ++u)
+#pragma unroll
+                    for (int n = 0; n < kQueries; ++n) seen[u][n] = seen_bits(args, w, column[n], low[n], b0 + u * 32u);
+            }
+            weigh(s, masked, seen, factor, g, m, sum, o, weights);
+#pragma unroll
+            for (uint32_t iu = 0; iu < I::kOut * kTiles; ++iu) {
+                const uint32_t i = iu / kTiles, u = iu % kTiles;
+                const bf16x8 v1 = __builtin_bit_cast(bf16x8, y[iu % kAhead]);
+                if (iu + kAhead < I::kOut * kTiles) y[iu % kAhead] = read_values(iu + kAhead);
+#pragma unroll
+                for (int n = 0; n < kQueries; ++n) o[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, weights[u][n], o[n][i], 0, 0, 0);
+            }
+            if (masked && uniform(lds_odd[buffer] == base)) {
+#pragma unroll
+                for (uint32_t u = 0; u < kTiles; ++u) I::add_odd(args, table, values, head, b0 + u * 32u, w.end, seen[u], weights[u], o, lane);
             }
             __builtin_amdgcn_sched_barrier(0);
             it.store(args, lds_k[buffer ^ 1u], lds_v[buffer ^ 1u], base + kStep, w.end, masked_from(base + kStep, kStep), &lds_odd[buffer ^ 1u],
