@@ -238,15 +238,15 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_kernel(AttendArg
     uint64_t before = 0;
     uint32_t l = 0;
     LaneWork w = {};
-    const uint64_t total = all_steps<kStep>(args, sh, false, 0, before, l, w);
-    const uint64_t per = (total + sh.workers - 1u) >> sh.shift;
+    const Steps<kStep> steps(args, sh);
+    const uint64_t total = steps.total, per = (total + sh.workers - 1u) >> sh.shift;
     uint64_t at = per * worker;
     const uint64_t stop = min(at + per, total);
     uint32_t more = 0;  // parts behind this one that hold the rest of its last item
     const float factor = a.scale == 0.0f ? 1.0f : __builtin_fabsf(a.scale) * kLog2e;
     bool found = false;
     while (at < stop) {
-        if (!found || at >= before + (uint64_t)w.steps * w.tiles * (uint32_t)c.heads) all_steps<kStep>(args, sh, true, at, before, l, w);
+        if (!found || at >= before + (uint64_t)w.steps * w.tiles * (uint32_t)c.heads) steps.find(args, sh, at, before, l, w);
         found = true;
         const uint64_t in_lane = at - before;
         const uint32_t item = divide(in_lane, w.steps), step = (uint32_t)(in_lane - (uint64_t)item * w.steps);
@@ -257,7 +257,6 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_kernel(AttendArg
 
         I it;
         const uint32_t lane = opaque(threadIdx.x) & 63u, r = lane & 15u;
-        it.load_queries(args, sh, w, head, first_row, lane);
         const uint8_t* keys = static_cast<const uint8_t*>(c.keys) + (int64_t)head * c.head_stride * I::kSize;
         const uint8_t* values = static_cast<const uint8_t*>(c.values) + (int64_t)head * c.head_stride * I::kSize;
 #pragma unroll
@@ -267,37 +266,30 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_kernel(AttendArg
 #pragma unroll
             for (int i = 0; i < I::kOut; ++i) it.o[n][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        // each row's column, the first place of those before the lane's columns that it sees
-        uint32_t column[kQueries];
-        int64_t low[kQueries];
-        int64_t all_see = 0;  // all rows see the places from here up to the lane's columns
-#pragma unroll
-        for (int n = 0; n < kQueries; ++n) {
-            const uint32_t j = sh.group.div(min_u32(first_row + (uint32_t)n * 16u + r, rows - 1u));
-            column[n] = j;
-            low[n] = first_seen(args, w, j);
-            if (a.window) {
-                int64_t x = low[n];
-#pragma unroll
-                for (int s = 1; s < 16; s <<= 1) x = max(x, (int64_t)__shfl_xor((long long)x, s));
-                all_see = max(all_see, x);
-            }
-        }
-        all_see = (int64_t)bcast((uint64_t)all_see, 0);
-
+        // (in the order in which they are waited for)
         uint32_t base = (w.first + step) * kStep + wave * kTile;
         const uint32_t stop_at = min_u32((w.first + last_step) * kStep, w.end);
-        typename I::Places next = {};
+        const typename I::Places now = it.lookup(args, table, base, w.end, lane);
+        typename I::Places next = it.lookup(args, table, base + kStep, w.end, lane);
+        it.load_queries(args, sh, w, head, first_row, lane);
         if (base < stop_at) {
-            const typename I::Places now = it.lookup(args, table, base, w.end, lane);
-            next = it.lookup(args, table, base + kStep, w.end, lane);
             const typename I::Rows at = it.rows_of(args, now);
             it.load_scales(args, now, head, lane);
             it.load_keys(args, keys, at, lane);
             it.load_values(args, values, at, lane);
         }
+        // each row's column, the first place of those before the lane's columns that it sees
+        uint32_t column[kQueries], low[kQueries];
+        uint32_t all_see = 0;  // all rows see the places from here up to the lane's columns
+#pragma unroll
+        for (int n = 0; n < kQueries; ++n) {
+            column[n] = sh.group.div(min_u32(first_row + (uint32_t)n * 16u + r, rows - 1u));
+            low[n] = first_seen(args, w, column[n]);
+            if (a.window) all_see = max_u32(all_see, max_of_16(low[n]));
+        }
+
         for (; base < stop_at; base += kStep) {
-            const bool masked = uniform(base + kTile > w.len || (int64_t)base < all_see);  // some row may not see all
+            const bool masked = uniform(base + kTile > w.len || base < all_see);  // some row may not see all
             const uint32_t lane = opaque(threadIdx.x & 63u), r = lane & 15u, g = lane >> 4;
             it.scales = it.next_scales;
             // scores of 32 places

@@ -117,6 +117,63 @@ __device__ __forceinline__ uint64_t all_steps(const AttendArgs& args, const Shap
     return sum;
 }
 
+// x of lane - N of the same 16 lanes, or of the end of an earlier 16 (0 where there is none).
+template <int kCtrl, int kRowMask>
+__device__ __forceinline__ uint32_t dpp_add(uint32_t x) {
+    return x + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, kCtrl, kRowMask, 0xF, true);
+}
+
+// The lanes' steps, read once where a wave's threads can keep them: up to 64 lanes with less than 2^26 each.
+template <uint32_t kStep>
+struct Steps {
+    LaneWork own;  // of the lane of this thread
+    uint32_t run;  // steps up to its end
+    bool kept;
+    uint64_t total;
+
+    __device__ __forceinline__ Steps(const AttendArgs& args, const Shape& sh) {
+        kept = false;
+        uint64_t before;
+        uint32_t lane;
+        const uint32_t lanes = (uint32_t)args.a.lanes, id = threadIdx.x & 63u;
+        if (lanes <= 64u) {
+            const uint32_t l = min_u32(id, lanes - 1u);
+            const int32_t* s = args.cols.at(l);
+            own = lane_work<kStep>(args, sh, l, s[0], s[args.cols.start ? 1 : 0], args.a.lens[l]);
+            const uint64_t all = id < lanes ? (uint64_t)own.steps * own.tiles * (uint32_t)args.cache.c.heads : 0u;
+            if (!__ballot(all >> 26)) {
+                run = (uint32_t)all;
+                run = dpp_add<0x111, 0xF>(run);  // row_shr:1
+                run = dpp_add<0x112, 0xF>(run);
+                run = dpp_add<0x114, 0xF>(run);
+                run = dpp_add<0x118, 0xF>(run);
+                run = dpp_add<0x142, 0xA>(run);  // row_bcast:15
+                run = dpp_add<0x143, 0xC>(run);  // row_bcast:31
+                kept = true;
+                total = bcast(run, 63u);
+            }
+        }
+        if (!kept) total = all_steps<kStep>(args, sh, false, 0, before, lane, own);
+    }
+
+    // The lane that step `at` belongs to, and the steps of those before it.
+    __device__ __forceinline__ void find(const AttendArgs& args, const Shape& sh, uint64_t at, uint64_t& before, uint32_t& lane, LaneWork& w) const {
+        if (!kept) {
+            all_steps<kStep>(args, sh, true, at, before, lane, w);
+            return;
+        }
+        lane = (uint32_t)__builtin_ctzll(__ballot(run > (uint32_t)at));
+        w.cb = bcast(own.cb, lane);
+        w.n = bcast(own.n, lane);
+        w.len = bcast(own.len, lane);
+        w.end = bcast(own.end, lane);
+        w.first = bcast(own.first, lane);
+        w.steps = bcast(own.steps, lane);
+        w.tiles = bcast(own.tiles, lane);
+        before = bcast(run, lane) - w.steps * w.tiles * (uint32_t)args.cache.c.heads;
+    }
+};
+
 // A condition that is the same in all lanes, as the compiler has to know: a matrix
 // instruction takes no notice of lanes that are switched off, so none may
 // stand in a branch that is taken by switching them off.
@@ -127,9 +184,9 @@ __device__ __forceinline__ uint32_t divide(uint64_t a, uint32_t b) {
 }
 
 // Bits of places [a, b) among the 32 from `base` on.
-__device__ __forceinline__ uint32_t range_bits(int64_t a, int64_t b, int64_t base) {
-    const int64_t lo = min(max(a - base, (int64_t)0), (int64_t)32), hi = min(max(b - base, lo), (int64_t)32);
-    return (uint32_t)((((uint64_t)1 << hi) - 1u) & ~(((uint64_t)1 << lo) - 1u));
+__device__ __forceinline__ uint32_t range_bits(uint32_t a, uint32_t b, uint32_t base) {
+    const uint32_t lo = a > base ? min_u32(a - base, 32u) : 0u, hi = b > base ? min_u32(b - base, 32u) : 0u;
+    return lo < hi ? (~0u >> (32u - hi)) & (~0u << lo) : 0u;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -154,34 +211,40 @@ __device__ __forceinline__ uint32_t widen(uint32_t x, float scale) {
 
 // The places that a row sees among the 32 from `base` on, as bits: `column` is
 // the row's, `low` the first place that it sees of those before the columns.
-__device__ __forceinline__ uint32_t seen_bits(const AttendArgs& args, const LaneWork& w, uint32_t column, int64_t low, uint32_t base) {
+__device__ __forceinline__ uint32_t seen_bits(const AttendArgs& args, const LaneWork& w, uint32_t column, uint32_t low, uint32_t base) {
     const topk_attend_args& a = args.a;
     asm volatile("" : "+s"(base));  // (nothing of this is computed where no row asks for it)
-    const int64_t len = w.len, end = w.end, b0 = base;
-    uint32_t bits = range_bits(low, min(len, end), b0);
+    uint32_t bits = range_bits(low, min_u32(w.len, w.end), base);
     if (base + 32u > w.len) {
         uint32_t own;
         if (a.mask) {
             const uint32_t* row = a.mask + (int64_t)(w.cb + column) * a.mask_ld;
-            const uint32_t i0 = base > w.len ? base - w.len : 0u, word = i0 >> 5;
-            const uint32_t x0 = (int64_t)word < a.mask_ld ? row[word] : 0u;
-            const uint32_t x1 = (int64_t)word + 1 < a.mask_ld ? row[word + 1] : 0u;
-            if (base >= w.len) own = (uint32_t)((((uint64_t)x1 << 32) | x0) >> (i0 & 31u));
-            else own = x0 << (w.len - base);
+            const uint32_t i0 = base > w.len ? base - w.len : 0u, word = i0 >> 5, words = (uint32_t)a.mask_ld;
+            const uint32_t x0 = word < words ? row[word] : 0u;
+            const uint32_t x1 = word + 1u < words ? row[word + 1u] : 0u;
+            own = base >= w.len ? (uint32_t)((((uint64_t)x1 << 32) | x0) >> (i0 & 31u)) : x0 << (w.len - base);
         } else {
-            const int64_t j = column;
-            own = range_bits(a.window ? len + j - a.window + 1 : len, len + j + 1, b0);
+            const uint32_t window = (uint32_t)a.window;
+            own = range_bits(window && column + 1u > window ? w.len + (column + 1u - window) : w.len, w.len + column + 1u, base);
         }
-        bits |= own & range_bits(len, end, b0);
+        bits |= own & range_bits(w.len, w.end, base);
     }
     return bits;
 }
 
 // The first place that column j of the lane sees of those before the columns.
-__device__ __forceinline__ int64_t first_seen(const AttendArgs& args, const LaneWork& w, uint32_t j) {
+__device__ __forceinline__ uint32_t first_seen(const AttendArgs& args, const LaneWork& w, uint32_t j) {
     const topk_attend_args& a = args.a;
     if (!a.window) return 0;
-    return (a.positions ? max((int64_t)a.positions[w.cb + j], (int64_t)w.len) : (int64_t)w.len + j) - a.window + 1;
+    const uint32_t position = a.positions ? (uint32_t)max_i32(a.positions[w.cb + j], (int32_t)w.len) : w.len + j;
+    return position + 1u > (uint32_t)a.window ? position + 1u - (uint32_t)a.window : 0u;
+}
+
+// The largest of a wave's values, of which each 16 lanes have all.
+__device__ __forceinline__ uint32_t max_of_16(uint32_t x) {
+#pragma unroll
+    for (int s = 1; s < 16; s <<= 1) x = max_u32(x, (uint32_t)__shfl_xor((int)x, s));
+    return bcast(x, 0u);
 }
 
 // Scores of 16 kQueries queries against 32 kTiles places become weights: lane 16 g + r has query r of each 16 and

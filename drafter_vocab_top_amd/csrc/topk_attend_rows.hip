@@ -174,8 +174,9 @@ __global__ __launch_bounds__(64 * (kGroups < 4 ? 4 : kGroups), DP < 256 ? 2 : 1)
     static_assert(kSplits <= 2, "");
     __shared__ u32x4 lds_k[2][kStep * I::kChunks], lds_v[2][kStep * I::kChunks];
     __shared__ uint32_t lds_odd[2];
-    __shared__ int64_t lds_see[I::kWaves];
+    __shared__ uint32_t lds_see[I::kWaves];
     if (threadIdx.x < 2u) lds_odd[threadIdx.x] = ~0u;
+    __syncthreads();
     const topk_attend_args& a = args.a;
     const topk_cache& c = args.cache.c;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -195,15 +196,15 @@ __global__ __launch_bounds__(64 * (kGroups < 4 ? 4 : kGroups), DP < 256 ? 2 : 1)
     uint64_t before = 0;
     uint32_t l = 0;
     LaneWork w = {};
-    const uint64_t total = all_steps<kStep>(args, sh, false, 0, before, l, w);
-    const uint64_t per = (total + sh.workers - 1u) >> sh.shift;
+    const Steps<kStep> steps(args, sh);
+    const uint64_t total = steps.total, per = (total + sh.workers - 1u) >> sh.shift;
     uint64_t at = per * worker;
     const uint64_t stop = min(at + per, total);
     uint32_t more = 0;  // parts behind this one that hold the rest of its last item
     const float factor = a.scale == 0.0f ? 1.0f : __builtin_fabsf(a.scale) * kLog2e;
     bool found = false;
     while (at < stop) {
-        if (!found || at >= before + (uint64_t)w.steps * w.tiles * (uint32_t)c.heads) all_steps<kStep>(args, sh, true, at, before, l, w);
+        if (!found || at >= before + (uint64_t)w.steps * w.tiles * (uint32_t)c.heads) steps.find(args, sh, at, before, l, w);
         found = true;
         const uint64_t in_lane = at - before;
         const uint32_t item = divide(in_lane, w.steps), step = (uint32_t)(in_lane - (uint64_t)item * w.steps);
@@ -218,8 +219,7 @@ __global__ __launch_bounds__(64 * (kGroups < 4 ? 4 : kGroups), DP < 256 ? 2 : 1)
         f32x4 o[kQueries][I::kOut];
         f32x4 sum[kQueries];
         float m[kQueries];
-        uint32_t column[kQueries];
-        int64_t low[kQueries], all_see = 0;
+        uint32_t column[kQueries], low[kQueries], all_see = 0;
         {
             const uint32_t lane = opaque(threadIdx.x) & 63u, r = lane & 15u, g = lane >> 4;
 #pragma unroll
@@ -233,12 +233,7 @@ __global__ __launch_bounds__(64 * (kGroups < 4 ? 4 : kGroups), DP < 256 ? 2 : 1)
                 const uint32_t j = sh.group.div(row), h = head * sh.group.d + (row - j * sh.group.d);
                 column[n] = j;
                 low[n] = first_seen(args, w, j);
-                if (a.window) {
-                    int64_t x = low[n];
-#pragma unroll
-                    for (int s = 1; s < 16; s <<= 1) x = max(x, (int64_t)__shfl_xor((long long)x, s));
-                    all_see = max(all_see, x);
-                }
+                if (a.window) all_see = max_u32(all_see, max_of_16(low[n]));
                 const uint16_t* from = static_cast<const uint16_t*>(a.q) + (int64_t)(w.cb + j) * a.q_stride + (int64_t)h * a.q_head_stride;
 #pragma unroll
                 for (int s = 0; s < I::kKeySteps; ++s) {
@@ -250,14 +245,14 @@ __global__ __launch_bounds__(64 * (kGroups < 4 ? 4 : kGroups), DP < 256 ? 2 : 1)
                 }
             }
         }
-        all_see = (int64_t)bcast((uint64_t)all_see, 0);
-        if (threadIdx.x % 64u == 0u) lds_see[wave] = all_see;
-        __syncthreads();
-        // all rows of the item see the places from here up to the lane's columns
+        if (a.window) {  // all rows of the item see the places from here up to the lane's columns
+            if (threadIdx.x % 64u == 0u) lds_see[wave] = all_see;
+            __syncthreads();
 #pragma unroll
-        for (uint32_t i = 0; i < I::kWaves; ++i) all_see = max(all_see, lds_see[i]);
-        all_see = (int64_t)bcast((uint64_t)all_see, 0);
-        auto masked_from = [&](uint32_t first, uint32_t places) { return uniform(first + places > w.len || (int64_t)first < all_see); };
+            for (uint32_t i = 0; i < I::kWaves; ++i) all_see = max_u32(all_see, lds_see[i]);
+            all_see = bcast(all_see, 0u);
+        }
+        auto masked_from = [&](uint32_t first, uint32_t places) { return uniform(first + places > w.len || first < all_see); };
 
         uint32_t base = (w.first + step) * kStep;
         const uint32_t stop_at = min_u32((w.first + last_step) * kStep, w.end);
