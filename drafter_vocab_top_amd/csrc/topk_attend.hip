@@ -35,8 +35,9 @@ namespace topk {
 
 namespace {
 
-constexpr uint32_t kStep = 128;  // places of a step
-constexpr uint32_t kTile = 32;   // of one wave
+constexpr uint32_t kStep = 128;       // places of a step
+constexpr uint32_t kTile = 32;        // of one wave
+constexpr uint32_t kJoinGroups = 64;  // workgroups that share the parts to join, for each two rows (DP = 128) of an item
 
 // DP: dim rounded up to 64, 128 or 256; kWhole: dim is DP.
 template <int DP, bool kWhole, bool kFp8, int kQueries>
@@ -228,7 +229,7 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_kernel(AttendArg
     using I = Item<DP, kWhole, kFp8, kQueries>;
     constexpr uint32_t R = I::kRows;
     constexpr uint32_t kPitch = DP + 4;  // floats of a row in LDS
-    __shared__ float lds_o[4][16][kPitch];
+    __shared__ float lds_o[4][R][kPitch];
     __shared__ float lds_m[4][R], lds_l[4][R];
     const topk_attend_args& a = args.a;
     const topk_cache& c = args.cache.c;
@@ -401,10 +402,13 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_kernel(AttendArg
                         f32x4 x;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) x[k] = it.o[n][h * I::kOwn + i + k][e] * mine;
-                        *reinterpret_cast<f32x4*>(&lds_o[wave][r_][h * I::kHalf + ((int)g_ * 4 + e) * I::kOwn + i]) = x;
+                        *reinterpret_cast<f32x4*>(&lds_o[wave][n * 16 + (int)r_][h * I::kHalf + ((int)g_ * 4 + e) * I::kOwn + i]) = x;
                     }
-            __syncthreads();
-            // 16 threads a row
+        }
+        __syncthreads();
+        // 16 threads a row
+#pragma unroll
+        for (int n = 0; n < kQueries; ++n) {
             const uint32_t q = tid_ >> 4, part = tid_ & 15u, row = (uint32_t)n * 16u + q;
             float all = kNone, sum = 0.0f;
 #pragma unroll
@@ -415,9 +419,9 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_kernel(AttendArg
             float y[DP / 16];
 #pragma unroll
             for (int i = 0; i < DP / 16; i += 4) {
-                f32x4 x = *reinterpret_cast<const f32x4*>(&lds_o[0][q][d0 + i]);
+                f32x4 x = *reinterpret_cast<const f32x4*>(&lds_o[0][row][d0 + i]);
 #pragma unroll
-                for (int k = 1; k < 4; ++k) x += *reinterpret_cast<const f32x4*>(&lds_o[k][q][d0 + i]);
+                for (int k = 1; k < 4; ++k) x += *reinterpret_cast<const f32x4*>(&lds_o[k][row][d0 + i]);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) y[i + k] = x[k];
             }
@@ -438,8 +442,8 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_kernel(AttendArg
                 for (int i = 0; i < DP / 16; i += 2)
                     if ((int32_t)d0 + i < c.dim) to[i / 2] = sum == 0.0f ? 0u : pack_bf16(y[i] * inverse, y[i + 1] * inverse);
             }
-            __syncthreads();
         }
+        __syncthreads();  // (the next item's maxima come here)
         at += last_step - step;
         if (at == stop && step == 0 && last_step < w.steps) {
             more = (uint32_t)(((uint64_t)(w.steps - last_step) + per - 1u) / per);
@@ -450,55 +454,73 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_kernel(AttendArg
 }
 
 // Joins the pieces of the items that a part ends in: a workgroup for two rows (DP =
-// 128) of one, its waves share the pieces.
+// 128) of one after another, its waves share the pieces.
 template <int DP>
 __global__ __launch_bounds__(256) void join_kernel(AttendArgs args, Shape sh) {
     constexpr uint32_t kThreads = DP / 4;           // of a row
     constexpr uint32_t kRowsAtOnce = 64 / kThreads; // of a wave
+    constexpr uint32_t kAhead = 4;                  // pieces in flight
     __shared__ float lds_m[4][kRowsAtOnce], lds_l[4][kRowsAtOnce];
     __shared__ f32x4 lds_o[4][64];
-    const uint32_t worker = blockIdx.x, lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
-    const Cut cut = sh.cuts[worker];
-    const uint32_t q = lane / kThreads, d = (lane % kThreads) * 4u, row = blockIdx.y * kRowsAtOnce + q;
-    if (cut.more == 0 || cut.first_row + blockIdx.y * kRowsAtOnce >= cut.rows) return;
-    float m = kNone, sum = 0.0f;
-    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (uint32_t i = wave; i <= cut.more; i += 4u) {
-        const uint32_t slot = i == 0 ? 2u * worker + 1u : 2u * (worker + i);
-        const int64_t at = (int64_t)slot * sh.rows + row;
-        const float m1 = sh.sums[2 * at], l1 = sh.sums[2 * at + 1];
-        const f32x4 o1 = *reinterpret_cast<const f32x4*>(sh.parts + at * DP + d);
-        const float top = __builtin_fmaxf(m, m1), zero = top == kNone ? 0.0f : top;
-        const float f0 = __builtin_amdgcn_exp2f(m - zero), f1 = __builtin_amdgcn_exp2f(m1 - zero);
-        sum = sum * f0 + l1 * f1;
-        o = o * f0 + o1 * f1;
-        m = top;
-    }
-    if (lane % kThreads == 0) {
-        lds_m[wave][q] = m;
-        lds_l[wave][q] = sum;
-    }
-    lds_o[wave][lane] = o;
-    __syncthreads();
-    if (wave != 0 || cut.first_row + row >= cut.rows) return;
-    float top = kNone;
+    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+    const uint32_t q = lane / kThreads, d = (lane % kThreads) * 4u, first = blockIdx.y * kRowsAtOnce, row = first + q;
+    // every gridDim.x-th part is this workgroup's, at most 64 of them
+    const uint32_t candidate = blockIdx.x + gridDim.x * lane;
+    const uint32_t parts_of_it = candidate < sh.workers ? sh.cuts[candidate].more : 0u;
+    for (unsigned long long todo = __ballot(parts_of_it != 0u); todo; todo &= todo - 1ull) {
+        const uint32_t worker = blockIdx.x + gridDim.x * (uint32_t)__builtin_ctzll(todo);
+        const Cut cut = sh.cuts[worker];
+        if (cut.first_row + first >= cut.rows) continue;
+        float m = kNone, sum = 0.0f;
+        f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (uint32_t i0 = wave; i0 <= cut.more; i0 += 4u * kAhead) {
+            float m1[kAhead], l1[kAhead];
+            f32x4 o1[kAhead];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) top = __builtin_fmaxf(top, lds_m[k][q]);
-    sum = 0.0f;
-    o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (uint32_t u = 0; u < kAhead; ++u) {
+                const uint32_t i = min_u32(i0 + 4u * u, cut.more), slot = i == 0 ? 2u * worker + 1u : 2u * (worker + i);
+                const int64_t at = (int64_t)slot * sh.rows + row;
+                m1[u] = sh.sums[2 * at];
+                l1[u] = sh.sums[2 * at + 1];
+                o1[u] = *reinterpret_cast<const f32x4*>(sh.parts + at * DP + d);
+            }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float f = __builtin_amdgcn_exp2f(lds_m[k][q] - (top == kNone ? 0.0f : top));
-        sum += lds_l[k][q] * f;
-        o += lds_o[k][lane] * f;
+            for (uint32_t u = 0; u < kAhead; ++u) {
+                if (i0 + 4u * u > cut.more) break;
+                const float top = __builtin_fmaxf(m, m1[u]), zero = top == kNone ? 0.0f : top;
+                const float f0 = __builtin_amdgcn_exp2f(m - zero), f1 = __builtin_amdgcn_exp2f(m1[u] - zero);
+                sum = sum * f0 + l1[u] * f1;
+                o = o * f0 + o1[u] * f1;
+                m = top;
+            }
+        }
+        if (lane % kThreads == 0) {
+            lds_m[wave][q] = m;
+            lds_l[wave][q] = sum;
+        }
+        lds_o[wave][lane] = o;
+        __syncthreads();
+        if (wave == 0 && cut.first_row + row < cut.rows && (int32_t)d < args.cache.c.dim) {
+            float top = kNone;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = __builtin_fmaxf(top, lds_m[k][q]);
+            sum = 0.0f;
+            o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float f = __builtin_amdgcn_exp2f(lds_m[k][q] - (top == kNone ? 0.0f : top));
+                sum += lds_l[k][q] * f;
+                o += lds_o[k][lane] * f;
+            }
+            const uint32_t j = sh.group.div(cut.first_row + row), h = cut.head * sh.group.d + (cut.first_row + row - j * sh.group.d);
+            uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(args.a.out) + (int64_t)(cut.first_col + j) * args.a.out_stride +
+                                                       (int64_t)h * args.a.out_head_stride + d);
+            const float inverse = 1.0f / sum;
+            to[0] = sum == 0.0f ? 0u : pack_bf16(o[0] * inverse, o[1] * inverse);
+            to[1] = sum == 0.0f ? 0u : pack_bf16(o[2] * inverse, o[3] * inverse);
+        }
+        __syncthreads();  // the next part's sums come here
     }
-    if ((int32_t)d >= args.cache.c.dim) return;
-    const uint32_t j = sh.group.div(cut.first_row + row), h = cut.head * sh.group.d + (cut.first_row + row - j * sh.group.d);
-    uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(args.a.out) + (int64_t)(cut.first_col + j) * args.a.out_stride +
-                                               (int64_t)h * args.a.out_head_stride + d);
-    const float inverse = 1.0f / sum;
-    to[0] = sum == 0.0f ? 0u : pack_bf16(o[0] * inverse, o[1] * inverse);
-    to[1] = sum == 0.0f ? 0u : pack_bf16(o[2] * inverse, o[3] * inverse);
 }
 
 // Rows of an item: those of an average lane's columns and a key head's queries, rounded up.  Up to 32 the
@@ -519,7 +541,7 @@ Shape shape_of(const AttendArgs& a, int64_t* bytes) {
     const int64_t step = s.rows <= 32 ? kStep : kRowsStep;
     // at most so many parts as workgroups run at once, and as there are steps
     const int64_t most = dp < 256 && s.rows < 256 ? 512 : 256;
-    const int64_t items = a.cache.c.heads * ((a.a.C * s.group.d + s.rows - 1) / s.rows + a.a.lanes);
+    const int64_t items = a.cache.c.heads * ((a.a.C * s.group.d + a.a.lanes * (s.rows - 1)) / s.rows);
     const int64_t span = a.a.window ? std::min<int64_t>(a.places, (int64_t)a.a.window + a.a.C + step) : a.places;
     const int64_t steps = std::min<int64_t>(most, (span + step - 1) / step + 1);
     while ((int64_t)1 << s.shift < std::min(most, items * steps)) ++s.shift;
@@ -549,7 +571,7 @@ hipError_t launch_queries(const AttendArgs& a, hipStream_t stream) {
     if constexpr (DP < 256)
         if (s.rows == 32) launch<DP, kWhole, kFp8, 2>(a, s, stream);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    hipLaunchKernelGGL((join_kernel<DP>), dim3(s.workers, s.rows * DP / 256), dim3(256), 0, stream, a, s);
+    hipLaunchKernelGGL((join_kernel<DP>), dim3(std::min(s.workers, kJoinGroups), s.rows * DP / 256), dim3(256), 0, stream, a, s);
     return hipGetLastError();
 }
 
