@@ -110,15 +110,19 @@ hipError_t write_dim(const CacheWriteArgs& a, hipStream_t stream) {
     return write_grid<DT, kFp8, 32>(a, stream);
 }
 
-// One thread for 16 bytes of a row (of every slot that moves), or one scale.  A thread
-// reads kAhead places before it writes the first of them: place i comes from a
-// later one, and what a batch reads lies behind all that was written before it.
+// One thread for 16 bytes of a row (of every slot that moves), or one scale.  A
+// workgroup first lists the moves of its lane: threads look up one entry of the
+// path each, so the reads that hang on each other (path, table) are made once
+// and not once for every few rows.  Then a thread reads kAhead places before it
+// writes the first of them: place i comes from a later one, and what a batch
+// reads lies behind all that was written before it.
 template <bool kFp8>
 __global__ __launch_bounds__(256) void move_kernel(CacheMoveArgs a, uint32_t row_vectors, uint32_t vectors, uint32_t scales, uint32_t first_lane) {
     constexpr uint32_t kAhead = 8;
+    __shared__ uint32_t from16[256], to16[256], scale_from[256], scale_to[256], counts[4];
     const topk_cache& c = a.cache.c;
     constexpr int32_t size = kFp8 ? 1 : 2;
-    const uint32_t t = blockIdx.x * 256u + threadIdx.x;
+    const uint32_t tid = threadIdx.x, wave = tid >> 6, t = blockIdx.x * 256u + tid;
     const uint32_t l = first_lane + blockIdx.y;
     const bool vector = t < vectors, scale = kFp8 && !vector && t - vectors < scales;
     // layer, keys or values, head and vector of the head's row
@@ -126,48 +130,63 @@ __global__ __launch_bounds__(256) void move_kernel(CacheMoveArgs a, uint32_t row
     const uint32_t head = item % (uint32_t)c.heads, both = item / (uint32_t)c.heads;
     const int64_t layer = both >> 1;
     const bool values = both & 1u;
-    const int64_t len = max_i32(a.lens[l], 0);
+    uint8_t* base = scale ? (values ? c.value_scales : c.key_scales) + layer * c.scale_layer_stride + (int64_t)head * c.scale_head_stride
+                          : static_cast<uint8_t*>(values ? c.values : c.keys) + (layer * c.layer_stride + (int64_t)head * c.head_stride) * size + part * 16u;
+    const int64_t len = max_i32(a.lens[l], 0), places = a.table_ld * c.block_size;
     const int32_t* table = a.table + (int64_t)l * a.table_ld;
     const int32_t* columns = a.columns + (int64_t)l * a.width;
-    const int64_t places = a.table_ld * c.block_size;
-    uint8_t* base;
-    int64_t block_stride, slot_stride;
-    if (scale) {
-        base = (values ? c.value_scales : c.key_scales) + layer * c.scale_layer_stride + (int64_t)head * c.scale_head_stride;
-        block_stride = c.scale_block_stride;
-        slot_stride = c.scale_slot_stride;
-    } else {
-        base = static_cast<uint8_t*>(values ? c.values : c.keys) +
-               (layer * c.layer_stride + (int64_t)head * c.head_stride) * size + part * 16u;
-        block_stride = c.block_stride * size;
-        slot_stride = c.slot_stride * size;
-    }
-    for (uint32_t i0 = 0; i0 < a.width; i0 += kAhead) {
-        u32x4 v[kAhead];
-        uint8_t b[kAhead];
-        int64_t to[kAhead];
-#pragma unroll
-        for (uint32_t u = 0; u < kAhead; ++u) {
-            const uint32_t i = i0 + u;
-            to[u] = -1;
-            if (i >= a.width) continue;
-            const int32_t from = columns[i];
-            if (from <= (int32_t)i) continue;
-            const int64_t src = len + from, dst = len + i;
-            if (src >= places) continue;
-            const uint32_t sb = a.cache.block.div((uint32_t)src), db = a.cache.block.div((uint32_t)dst);
-            const int64_t s = table[sb], d = table[db];
-            if (s < 0 || s >= c.blocks || d < 0 || d >= c.blocks) continue;
-            const uint8_t* at = base + s * block_stride + (int64_t)((uint32_t)src - sb * a.cache.block.d) * slot_stride;
-            to[u] = d * block_stride + (int64_t)((uint32_t)dst - db * a.cache.block.d) * slot_stride;
-            if (vector) v[u] = *reinterpret_cast<const u32x4*>(at);
-            else if (scale) b[u] = *at;
+    for (uint32_t first = 0; first < a.width; first += 256u) {
+        const uint32_t i = first + tid;
+        const int32_t from = i < a.width ? columns[i] : -1;
+        const int64_t src = len + from, dst = len + i;
+        bool moves = from > (int32_t)i && src < places;
+        uint32_t sb = 0, db = 0;
+        int32_t s = -1, d = -1;
+        if (moves) {
+            sb = a.cache.block.div((uint32_t)src);
+            db = a.cache.block.div((uint32_t)dst);
+            s = table[sb];
+            d = table[db];
         }
+        moves = moves && s >= 0 && s < c.blocks && d >= 0 && d < c.blocks;
+        const unsigned long long mask = __ballot(moves);
+        if (first) __syncthreads();  // (the list before is done with)
+        if ((tid & 63u) == 0) counts[wave] = (uint32_t)__builtin_popcountll(mask);
+        __syncthreads();
+        uint32_t at = lanes_below(mask), n = 0;
 #pragma unroll
-        for (uint32_t u = 0; u < kAhead; ++u) {
-            if (to[u] < 0) continue;
-            if (vector) *reinterpret_cast<u32x4*>(base + to[u]) = v[u];
-            else if (scale) base[to[u]] = b[u];
+        for (uint32_t k = 0; k < 4; ++k) {
+            at += k < wave ? counts[k] : 0u;
+            n += counts[k];
+        }
+        if (moves) {
+            const uint32_t sr = (uint32_t)src - sb * a.cache.block.d, dr = (uint32_t)dst - db * a.cache.block.d;
+            from16[at] = a.cache.row16((uint32_t)s, sr);
+            to16[at] = a.cache.row16((uint32_t)d, dr);
+            if constexpr (kFp8) {
+                scale_from[at] = a.cache.scale_row((uint32_t)s, sr);
+                scale_to[at] = a.cache.scale_row((uint32_t)d, dr);
+            }
+        }
+        __syncthreads();
+        if (vector) {
+            for (uint32_t k = 0; k < n; k += kAhead) {
+                u32x4 v[kAhead];
+#pragma unroll
+                for (uint32_t u = 0; u < kAhead; ++u) v[u] = *reinterpret_cast<const u32x4*>(past16(base, from16[min_u32(k + u, n - 1u)]));
+#pragma unroll
+                for (uint32_t u = 0; u < kAhead; ++u)
+                    if (k + u < n) *reinterpret_cast<u32x4*>(past16(base, to16[k + u])) = v[u];
+            }
+        } else if (scale) {
+            for (uint32_t k = 0; k < n; k += kAhead) {
+                uint8_t v[kAhead];
+#pragma unroll
+                for (uint32_t u = 0; u < kAhead; ++u) v[u] = base[scale_from[min_u32(k + u, n - 1u)]];
+#pragma unroll
+                for (uint32_t u = 0; u < kAhead; ++u)
+                    if (k + u < n) base[scale_to[k + u]] = v[u];
+            }
         }
     }
 }

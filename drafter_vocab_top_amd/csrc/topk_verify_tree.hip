@@ -8,9 +8,9 @@
 // token is drawn from what is left.
 //
 // One workgroup per lane, one wave per column: what a column's children meet does
-// not depend on the other columns, so the waves judge the columns that follow
-// the current one at once, and the path through them is then a walk in LDS.
-// Parents come before their children, so the walk only goes forward.
+// not depend on the other columns, so the waves judge the current column, its
+// children and columns behind them at once, and the path through them is then a
+// walk in LDS.
 //
 // The decisions are integers made by floating point, so every step is IEEE
 // double in a fixed order with no contraction.
@@ -32,10 +32,32 @@ __device__ __forceinline__ double probability_at(int32_t id, double q, int32_t q
     return at;
 }
 
+// The column that a wave judges when the path stands at column `now`: that for
+// wave 0, its children for the next ones (one of them comes next), the columns
+// behind it for the rest.  Where the waves can judge all columns they take them
+// in order.  A column past the last: none.
+template <uint32_t kWaves>
+__device__ __forceinline__ uint32_t column_of_wave(const int32_t* parents, uint32_t cb, uint32_t n, uint32_t now, uint32_t wave) {
+    if (n - now <= kWaves || wave == 0) return now + wave;
+    const uint32_t x = now + 1u + (threadIdx.x & 63u);
+    const bool in = x < n;
+    const int32_t parent = parents[(int64_t)cb + (in ? x : n - 1u)];
+    unsigned long long kids = __ballot(in && parent == (int32_t)now), rest = __ballot(in && parent != (int32_t)now);
+    uint32_t skip = wave - 1u;
+    const uint32_t many = (uint32_t)__builtin_popcountll(kids);
+    if (skip >= many) {
+        skip -= many;
+        kids = rest;
+    }
+    for (uint32_t i = 0; i < skip; ++i) kids &= kids - 1ull;
+    return kids ? now + 1u + first_lane(kids) : n;
+}
+
 template <class DT, uint32_t kWaves>
 __global__ __launch_bounds__(kWaves * 64) void verify_tree_kernel(VerifyTreeArgs args) {
 #pragma clang fp contract(off)
-    __shared__ int32_t chosen[kWaves];  // the accepted child of each column, or -1
+    __shared__ int32_t chosen[kWaves];   // the accepted child of each column, or -1
+    __shared__ uint32_t judged[kWaves];  // the columns
     const topk_verify_tree_args& a = args.v;
     const uint32_t l = blockIdx.x, tid = threadIdx.x;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(tid >> 6));
@@ -50,7 +72,7 @@ __global__ __launch_bounds__(kWaves * 64) void verify_tree_kernel(VerifyTreeArgs
     bool some = n > 0;
     uint32_t now = 0;  // the column where the path stands
     while (some) {
-        const uint32_t first = now, j = first + wave;
+        const uint32_t j = column_of_wave<kWaves>(a.parents, cb, n, now, wave);
         double w = 0.0, p = 0.0;
         int32_t id = 0;
         if (j < n) {  // wave-uniform
@@ -106,19 +128,23 @@ __global__ __launch_bounds__(kWaves * 64) void verify_tree_kernel(VerifyTreeArgs
             }
             if (lane == 0) chosen[wave] = accepted;
         }
+        if (lane == 0) judged[wave] = j;
         __syncthreads();
         bool last = false;
-        while (!last && now - first < kWaves) {
-            const int32_t down = chosen[now - first];
+        uint32_t slot = 0;  // of the column where the path stands (the first is judged)
+        while (slot < kWaves) {
+            const int32_t down = chosen[slot];
             if (tid == 0) columns[t] = (int32_t)now;
             last = down < 0 || t + 1u == most;
             if (last) break;
             if (tid == 0) tokens[t] = a.tokens[(int64_t)cb + (uint32_t)down];
             ++t;
             now = (uint32_t)down;
+            slot = 0;
+            while (slot < kWaves && judged[slot] != now) ++slot;
         }
         if (last) {
-            if (wave == now - first) {
+            if (wave == slot) {
                 if (t + 1u == most) w = p;  // no child was judged
                 const double sums = running_sum(w);
                 const double target = (double)a.uniforms[2 * ((int64_t)cb + now) + 1] * lane_value(sums, a.k - 1);
