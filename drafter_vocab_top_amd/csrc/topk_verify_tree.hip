@@ -24,25 +24,39 @@ namespace {
 // The probabilities in a draft list of this lane's target token (0 where it has
 // none, and past the target list): that of the first entry with its id.
 __device__ __forceinline__ double probability_at(int32_t id, double q, int32_t qid, int32_t nq) {
-    double at = 0.0;
-    for (int32_t i = nq - 1; i >= 0; --i) {  // from the last, so that the first entry of an id stays
-        const double qi = lane_value(q, i);
-        if (__builtin_amdgcn_readlane(qid, i) == id) at = qi;
-    }
-    return at;
+    int32_t at = -1;
+    for (int32_t i = nq - 1; i >= 0; --i)  // from the last, so that the first entry of an id stays
+        at = __builtin_amdgcn_readlane(qid, i) == id ? i : at;
+    const uint64_t b = __builtin_bit_cast(uint64_t, q);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(at << 2, (int)(uint32_t)b);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute(at << 2, (int)(uint32_t)(b >> 32));
+    return at < 0 ? 0.0 : __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
+
+// 64 columns of a lane, one for each thread of a wave: those from 64 q on.
+struct Columns {
+    int32_t parent, token;
+    float u;
+    __device__ __forceinline__ void load(const topk_verify_tree_args& a, uint32_t cb, uint32_t n, uint32_t q) {
+        const uint32_t x = q * 64u + (threadIdx.x & 63u);
+        const int64_t c = (int64_t)cb + min_u32(x, n - 1u);
+        parent = x < n ? a.parents[c] : -1;
+        token = a.tokens[c];
+        u = a.uniforms[2 * c];
+    }
+};
 
 // The column that a wave judges when the path stands at column `now`: that for
 // wave 0, its children for the next ones (one of them comes next), the columns
-// behind it for the rest.  Where the waves can judge all columns they take them
-// in order.  A column past the last: none.
+// behind it for the rest, all among the 64 that `now` is one of.  Where the
+// waves can judge all columns they take them in order.  n: none.
 template <uint32_t kWaves>
-__device__ __forceinline__ uint32_t column_of_wave(const int32_t* parents, uint32_t cb, uint32_t n, uint32_t now, uint32_t wave) {
+__device__ __forceinline__ uint32_t column_of_wave(const Columns& c, uint32_t n, uint32_t now, uint32_t wave) {
     if (n - now <= kWaves || wave == 0) return now + wave;
-    const uint32_t x = now + 1u + (threadIdx.x & 63u);
-    const bool in = x < n;
-    const int32_t parent = parents[(int64_t)cb + (in ? x : n - 1u)];
-    unsigned long long kids = __ballot(in && parent == (int32_t)now), rest = __ballot(in && parent != (int32_t)now);
+    const uint32_t x = (now & ~63u) + (threadIdx.x & 63u);
+    const bool behind = x > now && x < n;
+    unsigned long long kids = __ballot(behind && c.parent == (int32_t)now);
+    const unsigned long long rest = __ballot(behind && c.parent != (int32_t)now);
     uint32_t skip = wave - 1u;
     const uint32_t many = (uint32_t)__builtin_popcountll(kids);
     if (skip >= many) {
@@ -50,7 +64,7 @@ __device__ __forceinline__ uint32_t column_of_wave(const int32_t* parents, uint3
         kids = rest;
     }
     for (uint32_t i = 0; i < skip; ++i) kids &= kids - 1ull;
-    return kids ? now + 1u + first_lane(kids) : n;
+    return kids ? (now & ~63u) + first_lane(kids) : n;
 }
 
 template <class DT, uint32_t kWaves>
@@ -71,8 +85,12 @@ __global__ __launch_bounds__(kWaves * 64) void verify_tree_kernel(VerifyTreeArgs
     uint32_t t = 0;  // accepted drafts
     bool some = n > 0;
     uint32_t now = 0;  // the column where the path stands
+    Columns first64;  // (most trees have no more)
+    if (some) first64.load(a, cb, n, 0);
     while (some) {
-        const uint32_t j = column_of_wave<kWaves>(a.parents, cb, n, now, wave);
+        Columns near = first64;
+        if (now >= 64u && n - now > kWaves) near.load(a, cb, n, now >> 6);
+        const uint32_t j = column_of_wave<kWaves>(near, n, now, wave);
         double w = 0.0, p = 0.0;
         int32_t id = 0;
         if (j < n) {  // wave-uniform
@@ -91,12 +109,12 @@ __global__ __launch_bounds__(kWaves * 64) void verify_tree_kernel(VerifyTreeArgs
             double W = 1.0, q = 0.0, q_at = 0.0;
             bool have_q = false, have_at = false;
             int32_t accepted = -1;
-            for (uint32_t x0 = j + 1u; x0 < n && accepted < 0; x0 += 64u) {
-                const uint32_t x = x0 + (uint32_t)lane;
-                const int64_t cx = (int64_t)cb + min_u32(x, n - 1u);
-                const int32_t parent = a.parents[cx], token = a.tokens[cx];
-                const float u = a.uniforms[2 * cx];
-                unsigned long long kids = __ballot(x < n && parent == (int32_t)j);
+            for (uint32_t x0 = (j + 1u) & ~63u; x0 < n && accepted < 0; x0 += 64u) {
+                Columns columns_of = first64;
+                if (x0) columns_of.load(a, cb, n, x0 >> 6);
+                const int32_t token = columns_of.token;
+                const float u = columns_of.u;
+                unsigned long long kids = __ballot(x0 + (uint32_t)lane > j && columns_of.parent == (int32_t)j);
                 while (kids) {
                     const uint32_t i = first_lane(kids);
                     kids &= kids - 1ull;
