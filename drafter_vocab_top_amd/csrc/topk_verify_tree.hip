@@ -187,7 +187,12 @@ __global__ __launch_bounds__(kWaves * 64) void verify_tree_kernel(VerifyTreeArgs
 
 template <class DT>
 hipError_t launch_dt(const VerifyTreeArgs& a, hipStream_t stream) {
-    hipLaunchKernelGGL((verify_tree_kernel<DT, 8>), dim3((uint32_t)a.v.lanes), dim3(512), 0, stream, a);
+    const dim3 grid((uint32_t)a.v.lanes);
+    // Eight waves while the card has room for them (256 lanes of 8 columns with two levels 4.2 us, with four waves
+    // 5.3; a chain of 8 accepted drafts 6.0 and 6.9), four where more lanes than that share it (1,024 lanes: 7.2 and
+    // 9.2 us, with eight waves 7.4 and 11.2).
+    if (a.v.lanes <= 256) hipLaunchKernelGGL((verify_tree_kernel<DT, 8>), grid, dim3(512), 0, stream, a);
+    else hipLaunchKernelGGL((verify_tree_kernel<DT, 4>), grid, dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
