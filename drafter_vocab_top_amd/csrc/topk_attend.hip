@@ -168,7 +168,7 @@ struct Item {
         if constexpr (kFp8) {
             const topk_cache& c = a.cache.c;
             scale_byte = c.value_scales[(int64_t)head * c.scale_head_stride + a.cache.scale_row(s.id, s.in_block)];
-                    }
+        }
         for (uint32_t key = 0; key < kTile && base + key < end; ++key) {
             const uint8_t* row = past16(values, at.of(key));
             const float scale = power_of((uint32_t)from_lane((int32_t)scale_byte, key));
@@ -467,18 +467,23 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs args, Shape sh) {
     // every gridDim.x-th part is this workgroup's, at most 64 of them
     const uint32_t candidate = blockIdx.x + gridDim.x * lane;
     const uint32_t parts_of_it = candidate < sh.workers ? sh.cuts[candidate].more : 0u;
-    for (unsigned long long todo = __ballot(parts_of_it != 0u); todo; todo &= todo - 1ull) {
+    // where no item has more pieces than a wave keeps in flight, each wave joins items of its own
+    const bool alone = !__ballot(parts_of_it >= kAhead);
+    const uint32_t apart = alone ? 1u : 4u;
+    uint32_t count = 0;
+    for (unsigned long long todo = __ballot(parts_of_it != 0u); todo; todo &= todo - 1ull, ++count) {
+        if (alone && (count & 3u) != wave) continue;
         const uint32_t worker = blockIdx.x + gridDim.x * (uint32_t)__builtin_ctzll(todo);
         const Cut cut = sh.cuts[worker];
         if (cut.first_row + first >= cut.rows) continue;
         float m = kNone, sum = 0.0f;
         f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (uint32_t i0 = wave; i0 <= cut.more; i0 += 4u * kAhead) {
+        for (uint32_t i0 = alone ? 0u : wave; i0 <= cut.more; i0 += apart * kAhead) {
             float m1[kAhead], l1[kAhead];
             f32x4 o1[kAhead];
 #pragma unroll
             for (uint32_t u = 0; u < kAhead; ++u) {
-                const uint32_t i = min_u32(i0 + 4u * u, cut.more), slot = i == 0 ? 2u * worker + 1u : 2u * (worker + i);
+                const uint32_t i = min_u32(i0 + apart * u, cut.more), slot = i == 0 ? 2u * worker + 1u : 2u * (worker + i);
                 const int64_t at = (int64_t)slot * sh.rows + row;
                 m1[u] = sh.sums[2 * at];
                 l1[u] = sh.sums[2 * at + 1];
@@ -486,7 +491,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs args, Shape sh) {
             }
 #pragma unroll
             for (uint32_t u = 0; u < kAhead; ++u) {
-                if (i0 + 4u * u > cut.more) break;
+                if (i0 + apart * u > cut.more) break;
                 const float top = __builtin_fmaxf(m, m1[u]), zero = top == kNone ? 0.0f : top;
                 const float f0 = __builtin_amdgcn_exp2f(m - zero), f1 = __builtin_amdgcn_exp2f(m1[u] - zero);
                 sum = sum * f0 + l1[u] * f1;
@@ -494,13 +499,13 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs args, Shape sh) {
                 m = top;
             }
         }
-        if (lane % kThreads == 0) {
-            lds_m[wave][q] = m;
-            lds_l[wave][q] = sum;
-        }
-        lds_o[wave][lane] = o;
-        __syncthreads();
-        if (wave == 0 && cut.first_row + row < cut.rows && (int32_t)d < args.cache.c.dim) {
+        if (!alone) {
+            if (lane % kThreads == 0) {
+                lds_m[wave][q] = m;
+                lds_l[wave][q] = sum;
+            }
+            lds_o[wave][lane] = o;
+            __syncthreads();
             float top = kNone;
 #pragma unroll
             for (int k = 0; k < 4; ++k) top = __builtin_fmaxf(top, lds_m[k][q]);
@@ -512,6 +517,9 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs args, Shape sh) {
                 sum += lds_l[k][q] * f;
                 o += lds_o[k][lane] * f;
             }
+            __syncthreads();  // the next part's sums come here
+        }
+        if ((alone || wave == 0) && cut.first_row + row < cut.rows && (int32_t)d < args.cache.c.dim) {
             const uint32_t j = sh.group.div(cut.first_row + row), h = cut.head * sh.group.d + (cut.first_row + row - j * sh.group.d);
             uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(args.a.out) + (int64_t)(cut.first_col + j) * args.a.out_stride +
                                                        (int64_t)h * args.a.out_head_stride + d);
@@ -519,7 +527,6 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs args, Shape sh) {
             to[0] = sum == 0.0f ? 0u : pack_bf16(o[0] * inverse, o[1] * inverse);
             to[1] = sum == 0.0f ? 0u : pack_bf16(o[2] * inverse, o[3] * inverse);
         }
-        __syncthreads();  // the next part's sums come here
     }
 }
 

@@ -220,8 +220,10 @@ __device__ __forceinline__ uint32_t seen_bits(const AttendArgs& args, const Lane
         if (a.mask) {
             const uint32_t* row = a.mask + (int64_t)(w.cb + column) * a.mask_ld;
             const uint32_t i0 = base > w.len ? base - w.len : 0u, word = i0 >> 5, words = (uint32_t)a.mask_ld;
-            const uint32_t x0 = word < words ? row[word] : 0u;
-            const uint32_t x1 = word + 1u < words ? row[word + 1u] : 0u;
+            uint32_t x0 = word < words ? row[word] : 0u;
+            uint32_t x1 = word + 1u < words ? row[word + 1u] : 0u;
+            // (both are waited for here: a wait behind the branch would be one for keys and values too, in every step)
+            asm volatile("" : "+v"(x0), "+v"(x1));
             own = base >= w.len ? (uint32_t)((((uint64_t)x1 << 32) | x0) >> (i0 & 31u)) : x0 << (w.len - base);
         } else {
             const uint32_t window = (uint32_t)a.window;
@@ -274,7 +276,7 @@ __device__ __forceinline__ void weigh(f32x4 (&s)[kTiles][kQueries][2], bool mask
         for (int u = 0; u < kTiles; ++u)
 #pragma unroll
             for (int t = 0; t < 2; ++t)
-                top[n] = __builtin_fmaxf(top[n], __builtin_fmaxf(__builtin_fmaxf(s[u][n][t][0], s[u][n][t][1]), __builtin_fmaxf(s[u][n][t][2], s[u][n][t][3])));
+                top[n] = __builtin_fmaxf(__builtin_fmaxf(__builtin_fmaxf(__builtin_fmaxf(top[n], s[u][n][t][0]), s[u][n][t][1]), s[u][n][t][2]), s[u][n][t][3]);
         top[n] *= factor;
         grown |= top[n] > m[n] + 8.0f;
     }

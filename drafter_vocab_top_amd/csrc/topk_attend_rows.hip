@@ -47,13 +47,18 @@ struct Rows {
     __device__ __forceinline__ static void lookup(const AttendArgs& a, const int32_t* table, uint32_t base, uint32_t end, uint32_t lane, uint32_t& id,
                                                   uint32_t& in_block) {
         const uint32_t p = min_u32(base + lane, end - 1u), b = a.cache.block.div(p);
-        id = (uint32_t)min_i32(max_i32(table[b], 0), (int32_t)a.cache.c.blocks - 1);
+        id = (uint32_t)table[b];  // (as it stands there: nothing waits for it before it is asked for)
         in_block = p - b * a.cache.block.d;
+    }
+
+    __device__ __forceinline__ static uint32_t valid(const AttendArgs& a, uint32_t id) {
+        return (uint32_t)min_i32(max_i32((int32_t)id, 0), (int32_t)a.cache.c.blocks - 1);
     }
 
     __device__ __forceinline__ void load(const AttendArgs& a, const uint8_t* keys, const uint8_t* values, uint32_t head, uint32_t id,
                                          uint32_t in_block, uint32_t tid) {
         const topk_cache& c = a.cache.c;
+        id = valid(a, id);
         const uint32_t at = a.cache.row16(id, in_block);
         if constexpr (kFp8) {
             const uint32_t s = a.cache.scale_row(id, in_block);
@@ -134,6 +139,7 @@ struct Rows {
         for (uint32_t key = 0; key < 32u && base + key < end; ++key) {
             uint32_t id, in_block;
             lookup(a, table, base + key, end, 0u, id, in_block);
+            id = valid(a, id);
             const uint8_t* row = past16(values, a.cache.row16(id, in_block));
             float scale = 1.0f;
             if constexpr (kFp8)
@@ -383,7 +389,7 @@ __global__ __launch_bounds__(64 * (kGroups < 4 ? 4 : kGroups), DP < 256 ? 2 : 1)
             if (split != 0) break;
             const float all = sum[n][0];
             const uint32_t row = group_row + (uint32_t)n * 16u + r;
-            if (!direct) {
+            if (!direct && first_row + row < rows) {
                 float* to = sh.parts + ((int64_t)slot * R + row) * DP + g * 4u;
 #pragma unroll
                 for (int i = 0; i < I::kOut; ++i) *reinterpret_cast<f32x4*>(to + i * 16) = o[n][i];
@@ -391,7 +397,7 @@ __global__ __launch_bounds__(64 * (kGroups < 4 ? 4 : kGroups), DP < 256 ? 2 : 1)
                     sh.sums[((int64_t)slot * R + row) * 2] = m[n];
                     sh.sums[((int64_t)slot * R + row) * 2 + 1] = all;
                 }
-            } else if (first_row + row < rows) {
+            } else if (direct && first_row + row < rows) {
                 const uint32_t j = sh.group.div(first_row + row), h = head * sh.group.d + (first_row + row - j * sh.group.d);
                 uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + (int64_t)(w.cb + j) * a.out_stride +
                                                            (int64_t)h * a.out_head_stride + g * 4u);

@@ -52,7 +52,7 @@ struct Cache {
 
 template <class T>
 __device__ __forceinline__ T* past16(T* base, uint32_t offset16) {
-    return reinterpret_cast<T*>((uintptr_t)base + ((uint64_t)offset16 << 4));
+    return reinterpret_cast<T*>(const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(base)) + ((uint64_t)offset16 << 4));
 }
 
 struct CacheWriteArgs {
