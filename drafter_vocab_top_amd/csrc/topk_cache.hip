@@ -132,7 +132,7 @@ __global__ __launch_bounds__(256) void move_kernel(CacheMoveArgs a, uint32_t row
     const bool values = both & 1u;
     uint8_t* base = scale ? (values ? c.value_scales : c.key_scales) + layer * c.scale_layer_stride + (int64_t)head * c.scale_head_stride
                           : static_cast<uint8_t*>(values ? c.values : c.keys) + (layer * c.layer_stride + (int64_t)head * c.head_stride) * size + part * 16u;
-    const int64_t len = max_i32(a.lens[l], 0), places = a.table_ld * c.block_size;
+    const int64_t len = max_i32(a.lens[l], 0), places = min(a.table_ld * c.block_size, (int64_t)0x7FFFFFFF);
     const int32_t* table = a.table + (int64_t)l * a.table_ld;
     const int32_t* columns = a.columns + (int64_t)l * a.width;
     for (uint32_t first = 0; first < a.width; first += 256u) {

@@ -477,7 +477,8 @@ int topk_cols_plan(const topk_plan_args *args, hipStream_t stream);
  *                          lane's tokens.
  *
  * What is said above of the steps around the top-k holds for these too.
- * Lengths below 0 count as 0.
+ * Lengths below 0 count as 0; a lane has at most 2^31 - 1 places, and no more
+ * than its row of the table has slots for.
  */
 
 /*
@@ -606,8 +607,10 @@ typedef struct {
  * Products are of bfloat16 elements (an e4m3 element times its power of two is
  * one, except that results below 2^-126 may be 0), sums are binary32; the
  * weights are rounded to bfloat16 before the sum over values, and the result
- * once to bfloat16.  The result does not depend on other lanes' contents, and
- * the same call gives the same bits.
+ * once to bfloat16.  The same call gives the same bits.  What other lanes'
+ * columns hold does not matter; how many they have, and how long those lanes
+ * are, decides how a lane's places are shared out among workgroups, so its sums
+ * may be rounded differently next to other lanes.
  *
  * The workspace holds partial results of places that several workgroups share;
  * nothing in it is kept between calls.  Calls that may overlap need one each.
