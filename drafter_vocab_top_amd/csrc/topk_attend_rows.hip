@@ -26,7 +26,8 @@ struct Rows {
     static constexpr int kChunks = DP / 8;                       // 16-byte chunks of a row in LDS
     static constexpr int kVectors = DP * kSize / 16;             // 16-byte vectors of a row in memory
     static constexpr uint32_t kWaves = kGroups < 4 ? 4 : kGroups, kThreads = 64 * kWaves;
-    static constexpr int kLoads = kStep * kVectors / kThreads;   // of keys (and of values) for each thread
+    static constexpr bool kAll = kStep * kVectors >= kThreads;   // (256 rows, dim 64, e4m3: half of the threads bring a step)
+    static constexpr int kLoads = kAll ? kStep * kVectors / kThreads : 1;  // of keys (and of values) for each thread
     static constexpr int kKeySteps = DP / 32;
     static constexpr int kOut = DP / 16;
     static constexpr uint32_t kRows = 16 * kQueries * kGroups;
@@ -66,6 +67,7 @@ struct Rows {
             key_scale = (c.key_scales + h)[s];
             value_scale = (c.value_scales + h)[s];
         }
+        if (!kAll && tid >= kStep * kVectors) return;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const uint32_t x = (uint32_t)i * kThreads + tid, key = x / kVectors, part = x % kVectors;
@@ -87,6 +89,7 @@ struct Rows {
     template <bool kMasked>
     __device__ __forceinline__ void store_as(const AttendArgs& a, u32x4* lds_k, u32x4* lds_v, uint32_t base, uint32_t end, uint32_t* odd,
                                              uint32_t tid) const {
+        if (!kAll && tid >= kStep * kVectors) return;
         uint32_t found = 0;
         const int32_t ks_bits = __builtin_bit_cast(int32_t, power_of(key_scale)), vs_bits = __builtin_bit_cast(int32_t, power_of(value_scale));
         constexpr uint32_t kApart = kThreads / kVectors;  // of a thread's places

@@ -235,6 +235,42 @@ def test_cache_move(gpu, c):
         assert np.array_equal(whole(torch, t), w)
 
 
+def test_cache_move_long_paths(gpu):
+    """More entries than a workgroup has threads, an entry twice, and lanes without any."""
+    torch, T = gpu
+    rng = np.random.default_rng(18)
+    cache, tensors = make_cache(gpu, rng, True, 2, 200, 16, 2, 64)
+    table = rng.permutation(200)[:180].reshape(3, 60).astype(np.int32)
+    lens = np.array([5, 100, 30], np.int32)
+    columns = np.full((3, 600), -1, np.int32)
+    for l, n in enumerate((600, 0, 300)):
+        path = np.sort(rng.permutation(900)[:n])
+        columns[l, :n] = path
+    columns[2, 7] = columns[2, 8]
+    want = [whole(torch, t) for t in tensors]
+    cache.move(dev(torch, lens), dev(torch, table), dev(torch, columns))
+    for w, t in zip(want, tensors):
+        R.move(w, lens, table, columns, 16)
+        assert np.array_equal(whole(torch, t), w)
+
+
+def test_cache_move_the_last_places(gpu):
+    """Places up to 2^31 - 2 are places; those from 2^31 - 1 on are none, whatever the table has room for."""
+    torch, T = gpu
+    bs = 1 << 20
+    keys = torch.zeros(1, 2, bs, 1, 16, dtype=torch.bfloat16, device="cuda")
+    values = torch.zeros_like(keys)
+    cache = T.KeyCache(keys, values)
+    table = torch.full((1, 4096), -1, dtype=torch.int32, device="cuda")
+    table[0, 2047], table[0, 2048] = 0, 1  # places 2^31 - 2^20 .. 2^31 + 2^20 - 1
+    keys[0, 0, bs - 2], keys[0, 1, 2] = 3.0, 5.0
+    before = keys.clone()
+    cache.move(torch.tensor([2**31 - 3], dtype=torch.int32, device="cuda"), table,
+               torch.tensor([[1, 5]], dtype=torch.int32, device="cuda"))
+    before[0, 0, bs - 3] = 3.0
+    assert torch.equal(keys, before)
+
+
 # ----------------------------------------------------------------- attend ---
 
 def attend_case(gpu, c, seed=0):
@@ -248,6 +284,8 @@ def attend_case(gpu, c, seed=0):
     spans = R.spans_of(cs, L, C)
     ctx = c["ctx"]
     lens = rng.integers(c.get("ctx_min", 0), ctx + 1, L).astype(np.int32)
+    if "lens" in c:
+        lens = np.resize(np.array(c["lens"], np.int32), L)
     width = (ctx + most) // bs + 1
     blocks = L * width + 2
     table = rng.permutation(blocks)[:L * width].reshape(L, width).astype(np.int32)
@@ -264,6 +302,9 @@ def attend_case(gpu, c, seed=0):
             else:
                 tensors[n][where] = dev(torch, rng.standard_normal((len(p), H, D)).astype(np.float32)).to(torch.bfloat16)
     q = dev(torch, (rng.standard_normal((C, H * G, D)) * c.get("sharp", 1.0)).astype(np.float32)).to(torch.bfloat16)
+    if c.get("odd_queries"):
+        for x in (np.nan, np.inf, -np.inf):
+            q[int(rng.integers(0, C)), int(rng.integers(0, H * G)), int(rng.integers(0, D))] = x
     mask = positions = None
     if not c.get("chain"):
         parents = random_parents(rng, spans, C)
@@ -347,6 +388,83 @@ ATTENDS = [
 def test_attend(gpu, c, fp8):
     got, want, bound, spans = attend_case(gpu, dict(c, fp8=fp8))
     check(got, want, bound)
+
+
+# Every size class of an item's rows (columns times query heads of a key head: 16, 32, 64, 128, 256), at dims that fill
+# a kernel's 64, 128 or 256 and dims that do not, with steps that all rows see whole and steps that they do not.
+CLASSES = [dict(rows=rows, dim=dim) for rows in (16, 32, 64, 128, 256) for dim in (64, 48, 128, 112, 256, 208)]
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("c", CLASSES, ids=str)
+def test_attend_sizes(gpu, c, fp8):
+    rows, dim = c["rows"], c["dim"]
+    for i, extra in enumerate((dict(), dict(window=90), dict(poison=True), dict(chain=True, odd_queries=True))):
+        got, want, bound, _ = attend_case(gpu, dict(lanes=2, most=rows // 4, ctx=420, ctx_min=250, heads=1, group=4, dim=dim, bs=16,
+                                                    ragged=False, fp8=fp8, **extra), seed=i)
+        check(got, want, bound)
+
+
+MIXES = [dict(lanes=70, most=16, ctx=150, heads=1, group=4, dim=64, bs=16),              # more lanes than a wave has threads
+         dict(lanes=70, most=64, ctx=90, heads=1, group=1, dim=128, bs=32),
+         dict(lanes=1, most=64, ctx=4000, ctx_min=4000, heads=1, group=2, dim=64, bs=16),  # one item in many pieces
+         dict(lanes=1, most=48, ctx=3000, ctx_min=3000, heads=1, group=4, dim=128, bs=64),
+         dict(lanes=24, most=3, ctx=12000, heads=1, group=2, dim=64, bs=64, lens=[12000] + [5] * 23),  # pieces few and many
+         dict(lanes=24, most=24, ctx=9000, heads=1, group=2, dim=64, bs=64, lens=[3, 9000, 700, 0]),
+         dict(lanes=600, most=2, ctx=300, heads=1, group=1, dim=16, bs=16, lens=[1, 300, 20]),
+         dict(lanes=6, most=20, ctx=40, heads=2, group=8, dim=64, bs=16, words=3, odd_queries=True)]
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("c", MIXES, ids=str)
+def test_attend_mixed_lengths(gpu, c, fp8):
+    got, want, bound, _ = attend_case(gpu, dict(c, fp8=fp8))
+    check(got, want, bound)
+
+
+@pytest.mark.parametrize("most", [4, 24], ids=["few rows", "many rows"])
+def test_attend_captured(gpu, most):
+    """Two captured calls replayed in turn, with other lengths, queries and cache contents each time and eager work
+    between: each replay gives the eager call's bits."""
+    torch, T = gpu
+    rng = np.random.default_rng(31)
+    cache, tensors = make_cache(gpu, rng, True, 1, 260, 16, 2, 128)
+    table = torch.randperm(260, device="cuda").int()[:240].view(3, 80)
+    states, graphs = [], []
+    parents = dev(torch, random_parents(rng, R.spans_of(None, 3, 3 * most), 3 * most))
+    for _ in range(2):
+        s = dict(q=torch.randn(3 * most, 8, 128, device="cuda").to(torch.bfloat16), lens=torch.zeros(3, dtype=torch.int32, device="cuda"))
+        call = lambda s=s: cache.attend(s["q"], s["lens"], table, None, *T.tree(parents, s["lens"], lanes=3))  # noqa: E731
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            s["out"] = call()
+        states.append(dict(s, call=call))
+        graphs.append(graph)
+    for i in range(5):
+        tensors[2].copy_(dev(torch, rng.integers(120, 128, tuple(tensors[2].shape)).astype(np.uint8)))
+        for s in states:
+            s["lens"].copy_(dev(torch, rng.integers(0, 1200, 3).astype(np.int32)))
+            s["q"].copy_(torch.randn(3 * most, 8, 128, device="cuda").to(torch.bfloat16))
+        want = [s["call"]() for s in states]
+        for g in graphs if i % 2 else graphs[::-1]:
+            g.replay()
+        assert torch.randn(500, 500, device="cuda").sum().isfinite()
+        for s, w in zip(states, want):
+            assert torch.equal(s["out"], w), i
+
+
+def test_attend_nothing_to_do(gpu):
+    """No lane has a column: nothing is written."""
+    torch, T = gpu
+    cache, _ = make_cache(gpu, np.random.default_rng(1), False, 1, 4, 16, 2, 64)
+    for C in (1, 100):
+        q = torch.randn(C, 4, 64, device="cuda").to(torch.bfloat16)
+        out = q.clone()
+        lens, table = torch.tensor([9, 3], dtype=torch.int32, device="cuda"), torch.zeros(2, 2, dtype=torch.int32, device="cuda")
+        cache.attend(q, lens, table, col_start=torch.zeros(3, dtype=torch.int32, device="cuda"), out=out)
+        assert torch.equal(q, out)
 
 
 def test_attend_repeats_bit_for_bit_and_lanes_do_not_matter(gpu):
@@ -437,7 +555,10 @@ VERIFIES = [dict(lanes=1, most=1, k=1, kq=1), dict(lanes=1, most=8, k=20, kq=20)
             dict(lanes=40, most=12, k=10, kq=7, temperature=0.0), dict(lanes=40, most=12, k=10, kq=0, temperature=0.0),
             dict(lanes=25, most=9, k=12, kq=9, top_p=0.4, temperature=0.6), dict(lanes=25, most=30, k=4, kq=4, same=True),
             dict(lanes=300, most=6, k=3, kq=3, empty=0.4, gap=9), dict(lanes=10, most=20, k=6, kq=6, chain=True, cut=4, same=True),
-            dict(lanes=10, most=20, k=6, kq=0, cut=1), dict(lanes=30, most=33, k=7, kq=7, top_p=1.0, special=True)]
+            dict(lanes=10, most=20, k=6, kq=0, cut=1), dict(lanes=300, most=90, k=4, kq=4, bushy=True, same=True),
+            dict(lanes=260, most=150, k=3, kq=3, chain=True, same=True), dict(lanes=4, most=150, k=3, kq=3, chain=True, same=True),
+            dict(lanes=256, most=70, k=5, kq=0, bushy=True), dict(lanes=12, most=200, k=4, kq=4, wide=True),
+            dict(lanes=270, most=130, k=4, kq=2, wide=True), dict(lanes=30, most=33, k=7, kq=7, top_p=1.0, special=True)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -454,6 +575,11 @@ def test_verify_tree(gpu, c, dtype):
         for b, e in spans:
             for j in range(1, e - b):
                 parents[b + j] = (j - 1) // 5
+    elif c.get("wide"):  # children of a column far behind it
+        parents = np.full(C, -1, np.int32)
+        for b, e in spans:
+            for j in range(1, e - b):
+                parents[b + j] = j % 3 if j > 2 else 0
     else:
         parents = random_parents(rng, spans, C, c.get("chain"))
     universe = max(k, kq) + 3
