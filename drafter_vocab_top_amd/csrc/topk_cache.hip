@@ -41,63 +41,65 @@ __device__ __forceinline__ uint32_t bf16_of(float x) {
     return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x);
 }
 
-// Eight elements of a row for each thread, kGroup threads (a power of two) for
-// each row; the row's last threads have none where dim / 8 is no power of two.
+// Eight elements of a key and of its value for each thread, kGroup threads (a
+// power of two) for each row; the row's last threads have none where dim / 8 is
+// no power of two.
 template <class DT, bool kFp8, int kGroup>
 __global__ __launch_bounds__(256) void write_kernel(CacheWriteArgs a) {
     const topk_cache& c = a.cache.c;
     const uint32_t part = threadIdx.x % kGroup;
     const uint32_t row = blockIdx.x * (256u / kGroup) + threadIdx.x / kGroup, rows = (uint32_t)(a.w.C * c.heads);
-    const bool values = blockIdx.y != 0;
     const uint32_t col = row < rows ? row / (uint32_t)c.heads : 0u, head = row < rows ? row % (uint32_t)c.heads : 0u;
     const int64_t slot = a.w.slots[col];
     const bool live = row < rows && (int32_t)(part * 8u) < c.dim && slot >= 0 && slot < c.blocks * c.block_size;
-    float x[8] = {};
-    if (live)
-        load8<DT>(values ? a.w.values : a.w.keys,
-                  (int64_t)col * (values ? a.w.value_stride : a.w.key_stride) +
-                      (int64_t)head * (values ? a.w.value_head_stride : a.w.key_head_stride) + part * 8u, x);
+    float x[2][8] = {};
+    if (live) {
+        load8<DT>(a.w.keys, (int64_t)col * a.w.key_stride + (int64_t)head * a.w.key_head_stride + part * 8u, x[0]);
+        load8<DT>(a.w.values, (int64_t)col * a.w.value_stride + (int64_t)head * a.w.value_head_stride + part * 8u, x[1]);
+    }
     const uint32_t block = a.cache.block.div(live ? (uint32_t)slot : 0u), in_block = (live ? (uint32_t)slot : 0u) - block * a.cache.block.d;
-    void* to = past16(values ? c.values : c.keys, a.cache.row16(block, in_block));
+    const uint32_t row16 = a.cache.row16(block, in_block);
     const int64_t at = (int64_t)head * c.head_stride + part * 8u;
-    if constexpr (!kFp8) {
-        if (!live) return;
-        u32x4 v;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = bf16_of(x[2 * i]) | (bf16_of(x[2 * i + 1]) << 16);
-        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(to) + at) = v;
-    } else {
-        uint32_t largest = 0;  // of the finite magnitudes, as patterns
+    for (int n = 0; n < 2; ++n) {
+        void* to = past16(n ? c.values : c.keys, row16);
+        if constexpr (!kFp8) {
+            u32x4 v;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t m = __builtin_bit_cast(uint32_t, x[i]) & 0x7FFFFFFFu;
-            if (m < 0x7F800000u) largest = max_u32(largest, m);
+            for (int i = 0; i < 4; ++i) v[i] = bf16_of(x[n][2 * i]) | (bf16_of(x[n][2 * i + 1]) << 16);
+            if (live) *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(to) + at) = v;
+        } else {
+            uint32_t largest = 0;  // of the finite magnitudes, as patterns
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t m = __builtin_bit_cast(uint32_t, x[n][i]) & 0x7FFFFFFFu;
+                if (m < 0x7F800000u) largest = max_u32(largest, m);
+            }
+#pragma unroll
+            for (int s = 1; s < kGroup; s <<= 1) largest = max_u32(largest, (uint32_t)__shfl_xor((int)largest, s));
+            const int32_t e = max_i32((int32_t)(largest >> 23) - 135 + ((largest & 0x7FFFFFu) > 0x600000u ? 1 : 0), -126);
+            u32x2 v = {0u, 0u};
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                float y[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    y[k] = __builtin_isfinite(x[n][i + k]) ? __builtin_ldexpf(x[n][i + k], -e) : __builtin_nanf("");
+                if (i % 4 == 0) v[i / 4] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], (int)v[i / 4], false);
+                else v[i / 4] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], (int)v[i / 4], true);
+            }
+            if (live) *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(to) + at) = v;
+            if (live && part == 0)
+                (n ? c.value_scales : c.key_scales)[a.cache.scale_row(block, in_block) + (int64_t)head * c.scale_head_stride] =
+                    (uint8_t)(e + 127);
         }
-#pragma unroll
-        for (int s = 1; s < kGroup; s <<= 1) largest = max_u32(largest, (uint32_t)__shfl_xor((int)largest, s));
-        if (!live) return;
-        const int32_t e = max_i32((int32_t)(largest >> 23) - 135 + ((largest & 0x7FFFFFu) > 0x600000u ? 1 : 0), -126);
-        u32x2 v = {0u, 0u};
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            float y[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                y[k] = __builtin_isfinite(x[i + k]) ? __builtin_ldexpf(x[i + k], -e) : __builtin_nanf("");
-            if (i % 4 == 0) v[i / 4] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], (int)v[i / 4], false);
-            else v[i / 4] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], (int)v[i / 4], true);
-        }
-        *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(to) + at) = v;
-        if (part == 0)
-            (values ? c.value_scales : c.key_scales)[a.cache.scale_row(block, in_block) + (int64_t)head * c.scale_head_stride] =
-                (uint8_t)(e + 127);
     }
 }
 
 template <class DT, bool kFp8, int kGroup>
 hipError_t write_grid(const CacheWriteArgs& a, hipStream_t stream) {
     const int64_t rows = a.w.C * a.cache.c.heads;
-    const dim3 grid((uint32_t)((rows + 256 / kGroup - 1) / (256 / kGroup)), 2);
+    const dim3 grid((uint32_t)((rows + 256 / kGroup - 1) / (256 / kGroup)));
     hipLaunchKernelGGL((write_kernel<DT, kFp8, kGroup>), grid, dim3(256), 0, stream, a);
     return hipGetLastError();
 }
