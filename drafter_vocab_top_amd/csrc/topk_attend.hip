@@ -27,6 +27,15 @@
 // workgroups of one wave of launches, whatever the lanes' lengths (read on the
 // device).  A part that ends inside an item leaves its partial maximum, sums
 // and output in the workspace, and a second kernel joins them.
+//
+// Memory bounds it: 2 lanes of 6 columns over 98,304 bfloat16 places of 8 key
+// heads of 128 are 806 MB in 156 us, 5.2 TB/s where a large copy makes 5.4 (146
+// us of it in this kernel, 10 in the join).  An e4m3 cache, whose rows are 128
+// bytes, is read at 4.1 TB/s (64 lanes of 6 columns over 6,144 places: 826 MB in
+// 200 us; the same with every block in cache 111 us); twice as many places in
+// flight did not change that.  One lane over 2,048 places is a chain of
+// latencies: 16 us, 12 of them here (lengths, table, keys, and the sums of four
+// waves).
 #include <algorithm>
 
 #include "topk_attend.hpp"
@@ -37,7 +46,9 @@ namespace {
 
 constexpr uint32_t kStep = 128;       // places of a step
 constexpr uint32_t kTile = 32;        // of one wave
-constexpr uint32_t kJoinGroups = 64;  // workgroups that share the parts to join, for each two rows (DP = 128) of an item
+// Workgroups that share the parts to join, for each two rows (DP = 128) of an item.  With 16, 64 and 256 of them one
+// lane's columns over 2,048 places take 15.9, 16.1 and 17.2 us, 64 lanes of 64 rows 217, 208 and 216.
+constexpr uint32_t kJoinGroups = 64;
 
 // DP: dim rounded up to 64, 128 or 256; kWhole: dim is DP.
 template <int DP, bool kWhole, bool kFp8, int kQueries>
@@ -531,7 +542,10 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs args, Shape sh) {
 }
 
 // Rows of an item: those of an average lane's columns and a key head's queries, rounded up.  Up to 32 the
-// waves of a workgroup share the places, beyond that the rows (topk_attend_rows.hip).
+// waves of a workgroup share the places, beyond that the rows (topk_attend_rows.hip).  Fewer rows than there are mean
+// that keys and values are read again: 64 lanes over 6,144 places of 8 key heads of 128, e4m3 and bfloat16, 32 rows
+// 216 and 348 us (in items of 16: 362 and 555), 64 rows 231 and 356 (of 32: 354 and 594), 128 rows 305 and 380 (of
+// 64: 409 and 631), 256 rows 471 (of 128: 561).  Of dim 256 the registers hold 16 and 64 rows.
 uint32_t rows_of(const AttendArgs& a) {
     const int64_t rows = (a.a.C + a.a.lanes - 1) / a.a.lanes * (a.a.heads / a.cache.c.heads);
     if (rows <= 16) return 16;
@@ -546,7 +560,8 @@ Shape shape_of(const AttendArgs& a, int64_t* bytes) {
     s.rows = rows_of(a);
     s.group = Divisor::of((uint32_t)(a.a.heads / a.cache.c.heads));
     const int64_t step = s.rows <= 32 ? kStep : kRowsStep;
-    // at most so many parts as workgroups run at once, and as there are steps
+    // at most so many parts as workgroups run at once (two on a compute unit, where 256 registers for each thread allow
+    // it: with one, 64 lanes of 64 rows take 260 us instead of 208), and as there are steps
     const int64_t most = dp < 256 && s.rows < 256 ? 512 : 256;
     const int64_t items = a.cache.c.heads * ((a.a.C * s.group.d + a.a.lanes * (s.rows - 1)) / s.rows);
     const int64_t span = a.a.window ? std::min<int64_t>(a.places, (int64_t)a.a.window + a.a.C + step) : a.places;

@@ -43,7 +43,10 @@ __device__ __forceinline__ uint32_t bf16_of(float x) {
 
 // Eight elements of a key and of its value for each thread, kGroup threads (a
 // power of two) for each row; the row's last threads have none where dim / 8 is
-// no power of two.
+// no power of two.  Memory bounds long calls: 98,304 rows of 128 bfloat16
+// elements into an e4m3 cache are 76 MB in 18 us (with keys and values in
+// threads of their own 22; two rows for each thread 18), short ones the chain
+// slot, row, store: 384 rows 3 us.
 template <class DT, bool kFp8, int kGroup>
 __global__ __launch_bounds__(256) void write_kernel(CacheWriteArgs a) {
     const topk_cache& c = a.cache.c;
@@ -117,7 +120,9 @@ hipError_t write_dim(const CacheWriteArgs& a, hipStream_t stream) {
 // path each, so the reads that hang on each other (path, table) are made once
 // and not once for every few rows.  Then a thread reads kAhead places before it
 // writes the first of them: place i comes from a later one, and what a batch
-// reads lies behind all that was written before it.
+// reads lies behind all that was written before it.  64 lanes' paths of 13 in 32
+// layers of 4 heads of 128 (54 MB): 14.7 us, 3.7 TB/s (kAhead 2: 15.7); one lane's
+// 3.4 (kAhead 16: 3.8).
 template <bool kFp8>
 __global__ __launch_bounds__(256) void move_kernel(CacheMoveArgs a, uint32_t row_vectors, uint32_t vectors, uint32_t scales, uint32_t first_lane) {
     constexpr uint32_t kAhead = 8;
