@@ -412,7 +412,11 @@ MIXES = [dict(lanes=70, most=16, ctx=150, heads=1, group=4, dim=64, bs=16),     
          dict(lanes=24, most=3, ctx=12000, heads=1, group=2, dim=64, bs=64, lens=[12000] + [5] * 23),  # pieces few and many
          dict(lanes=24, most=24, ctx=9000, heads=1, group=2, dim=64, bs=64, lens=[3, 9000, 700, 0]),
          dict(lanes=600, most=2, ctx=300, heads=1, group=1, dim=16, bs=16, lens=[1, 300, 20]),
-         dict(lanes=6, most=20, ctx=40, heads=2, group=8, dim=64, bs=16, words=3, odd_queries=True)]
+         dict(lanes=6, most=20, ctx=40, heads=2, group=8, dim=64, bs=16, words=3, odd_queries=True),
+         dict(lanes=3, most=5, ctx=300, heads=2, group=4, dim=128, bs=16, gap=300),       # a padded batch: few rows in large items
+         dict(lanes=3, most=2, ctx=300, heads=1, group=1, dim=64, bs=16, gap=150, window=40),
+         dict(lanes=9, most=150, ctx=120, heads=1, group=3, dim=128, bs=16, empty=0.8),    # many rows in small items
+         dict(lanes=70, most=90, ctx=60, heads=1, group=1, dim=64, bs=16, empty=0.95)]
 
 
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
@@ -467,7 +471,7 @@ def test_attend_nothing_to_do(gpu):
         assert torch.equal(q, out)
 
 
-def test_attend_repeats_bit_for_bit_and_lanes_do_not_matter(gpu):
+def test_attend_repeats_bit_for_bit(gpu):
     torch, T = gpu
     rng = np.random.default_rng(3)
     cache, _ = make_cache(gpu, rng, False, 1, 600, 16, 2, 128)
