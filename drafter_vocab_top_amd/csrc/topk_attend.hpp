@@ -252,10 +252,11 @@ __device__ __forceinline__ uint32_t max_of_16(uint32_t x) {
 // Scores of 16 kQueries queries against 32 kTiles places become weights: lane 16 g + r has query r of each 16 and
 // places 4 g + i and 16 + 4 g + i of each 32.  m, sum and o (16 x 16 tiles, a query in each column) are the running
 // maximum, sum and output.  The sum is a product with ones: it is of the weights as they are rounded for the products
-// with values.  `seen`: with `masked`, the places that each query sees.
-template <int kTiles, int kQueries, int kOut>
+// with values.  `seen`: with `masked`, the places that each query sees.  (m, sum and o may be of more queries: the first
+// ones are these.)
+template <int kTiles, int kQueries, int kOut, int kAll>
 __device__ __forceinline__ void weigh(f32x4 (&s)[kTiles][kQueries][2], bool masked, const uint32_t (&seen)[kTiles][kQueries], float factor,
-                                      uint32_t g, float (&m)[kQueries], f32x4 (&sum)[kQueries], f32x4 (&o)[kQueries][kOut],
+                                      uint32_t g, float (&m)[kAll], f32x4 (&sum)[kAll], f32x4 (&o)[kAll][kOut],
                                       bf16x8 (&weights)[kTiles][kQueries]) {
     if (masked) {
 #pragma unroll

@@ -5,15 +5,22 @@
 // time.  kGroups groups of 16 kQueries rows each have a wave, or two that take
 // 32 of the places each and add up at the end (64 rows: four waves of 16 rows
 // would read every operand from LDS for half as many products).  The next 64
-// places are on their way to registers while these are worked on (an e4m3 cache is widened between registers and LDS, once for all rows).
+// places are on their way to registers while these are worked on (an e4m3 cache
+// is widened between registers and LDS, once for all rows).
 //
-// 64 lanes of 48 rows over 6,144 e4m3 places of 8 key heads of 128: 826 MB in 208
-// us, 4.0 TB/s (a large copy makes 5.4).  16 lanes of 192 rows, bfloat16: 418 MB
-// and 78 GFLOP in 150 us.  Neither memory nor the matrix cores (24 and 41 % of
+// A batch's columns may be fewer than it has room for, which is what an item's size
+// goes by.  A wave's rows are every kGroups-th 16 of an item, so that few rows are
+// many waves' alike, and a wave leaves out what it has no rows for: 64 lanes of
+// 32 rows in items of 256 take 267 us (442 with all products made), 16 lanes of
+// 64 rows, bfloat16, 106 (137), full items of 128 rows 2 % longer.
+//
+// 64 lanes of 48 rows over 6,144 e4m3 places of 8 key heads of 128: 826 MB in 210
+// us, 3.9 TB/s (a large copy makes 5.4).  16 lanes of 192 rows, bfloat16: 418 MB
+// and 78 GFLOP in 144 us.  Neither memory nor the matrix cores (24 and 41 % of
 // the time) bound it: a wave's products, weights and staging follow one another,
 // and two waves on a SIMD overlap them in part.  Priorities for one of the two,
 // and scores of the next places made among the weights of these (which takes
-// all registers), did not help (153 and 164 us).
+// all registers), did not help (153 and 164 us where it was 150).
 //
 // LDS holds rows of elements in chunks of 8, swapped so that 16 lanes that read a
 // chunk of 16 keys, or four keys' 16 elements of a transposed read, meet 16 (8)
@@ -22,6 +29,8 @@
 // (without that 30 % of an e4m3 cache's LDS cycles were conflicts: 64 lanes of 64
 // rows over 8192 places 231 and 221 us).  Values are read transposed: lane 16 g + r
 // gets element r of places 4 g .. 4 g + 3.
+#include <type_traits>
+
 #include "topk_attend.hpp"
 
 namespace topk {
@@ -145,8 +154,9 @@ struct Rows {
     }
 
     // Adds the values that are not finite of the 32 places from `base` on, each to the rows that see it.
+    template <int N>
     __device__ __forceinline__ static void add_odd(const AttendArgs& a, const int32_t* table, const uint8_t* values, uint32_t head, uint32_t base,
-                                                   uint32_t end, const uint32_t (&seen)[kQueries], const bf16x8 (&weights)[kQueries],
+                                                   uint32_t end, const uint32_t (&seen)[N], const bf16x8 (&weights)[N],
                                                    f32x4 (&o)[kQueries][kOut], uint32_t lane) {
         const topk_cache& c = a.cache.c;
         const uint32_t r = lane & 15u, g = lane >> 4;
@@ -158,9 +168,9 @@ struct Rows {
             float scale = 1.0f;
             if constexpr (kFp8)
                 scale = power_of(c.value_scales[(int64_t)head * c.scale_head_stride + a.cache.scale_row(id, in_block)]);
-            float weight[kQueries];
+            float weight[N];
 #pragma unroll
-            for (int n = 0; n < kQueries; ++n) weight[n] = weight_of(weights[n], key, r);
+            for (int n = 0; n < N; ++n) weight[n] = weight_of(weights[n], key, r);
 #pragma unroll
             for (int i = 0; i < kOut; ++i) {
                 const int32_t d = i * 16 + (int32_t)g * 4;
@@ -177,7 +187,7 @@ struct Rows {
                 for (int e = 0; e < 4; ++e) {
                     const float v1 = __builtin_bit_cast(float, e & 1 ? x[e / 2] & 0xFFFF0000u : x[e / 2] << 16);
 #pragma unroll
-                    for (int n = 0; n < kQueries; ++n)
+                    for (int n = 0; n < N; ++n)
                         if ((seen[n] >> key & 1u) && !__builtin_isfinite(v1)) o[n][i][e] += weight[n] * v1;
                 }
             }
@@ -200,7 +210,7 @@ __global__ __launch_bounds__(64 * (kGroups < 4 ? 4 : kGroups), DP < 256 ? 2 : 1)
     const topk_attend_args& a = args.a;
     const topk_cache& c = args.cache.c;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const uint32_t split = wave % kSplits, group_row = wave / kSplits * 16u * kQueries;  // its places, its rows
+    const uint32_t split = wave % kSplits, group = wave / kSplits;  // its places, its rows: every kGroups-th 16
     // where this lane reads: chunk i of key r, and element 16 i of value 4 g + r / 4 (the other places lie whole rows further)
     uint32_t key_at[I::kKeySteps], value_at[I::kOut];
     {
@@ -231,7 +241,7 @@ __global__ __launch_bounds__(64 * (kGroups < 4 ? 4 : kGroups), DP < 256 ? 2 : 1)
         const uint32_t head = item / w.tiles, first_row = (item - head * w.tiles) * R;
         const uint32_t last_step = (uint32_t)min((uint64_t)w.steps, step + (stop - at));
         const int32_t* table = a.table + (int64_t)l * a.table_ld;
-        const uint32_t rows = w.n * sh.group.d, wave_row = first_row + group_row;
+        const uint32_t rows = w.n * sh.group.d, wave_row = first_row + group * 16u;
         const uint8_t* keys = static_cast<const uint8_t*>(c.keys) + (int64_t)head * c.head_stride * I::kSize;
         const uint8_t* values = static_cast<const uint8_t*>(c.values) + (int64_t)head * c.head_stride * I::kSize;
 
@@ -249,7 +259,7 @@ __global__ __launch_bounds__(64 * (kGroups < 4 ? 4 : kGroups), DP < 256 ? 2 : 1)
 #pragma unroll
                 for (int i = 0; i < I::kOut; ++i) o[n][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                 // (a row past the last is the last again; it is not written)
-                const uint32_t row = min_u32(wave_row + (uint32_t)n * 16u + r, rows - 1u);
+                const uint32_t row = min_u32(wave_row + (uint32_t)n * 16u * kGroups + r, rows - 1u);
                 const uint32_t j = sh.group.div(row), h = head * sh.group.d + (row - j * sh.group.d);
                 column[n] = j;
                 low[n] = first_seen(args, w, j);
@@ -276,6 +286,8 @@ __global__ __launch_bounds__(64 * (kGroups < 4 ? 4 : kGroups), DP < 256 ? 2 : 1)
 
         uint32_t base = (w.first + step) * kStep;
         const uint32_t stop_at = min_u32((w.first + last_step) * kStep, w.end);
+        // (which of this wave's 16 rows there are)
+        const bool one = uniform(wave_row < rows), two = uniform(wave_row + 16u * kGroups < rows);
         I it;
         uint32_t id, in_block;
         {
@@ -295,66 +307,71 @@ __global__ __launch_bounds__(64 * (kGroups < 4 ? 4 : kGroups), DP < 256 ? 2 : 1)
             const uint32_t b0 = base + split * 32u;                             // this wave's places: kTiles times 32
             const bool masked = masked_from(b0, 32u * kTiles);                  // some row may not see all
             const uint32_t own = split * 32u * I::kChunks * 16u;
-            // Operands are read ahead of their products (left to itself the compiler waits for each).
-            f32x4 s[kTiles][kQueries][2];
-            bf16x8 x[2][I::kKeySteps];
-            auto read_keys = [&](uint32_t t) __attribute__((always_inline)) {
+            auto work = [&](auto count) __attribute__((always_inline)) {
+                constexpr int N = decltype(count)::value;  // of the wave's kQueries 16 rows
+                // Operands are read ahead of their products (left to itself the compiler waits for each).
+                f32x4 s[kTiles][N][2];
+                bf16x8 x[2][I::kKeySteps];
+                auto read_keys = [&](uint32_t t) __attribute__((always_inline)) {
 #pragma unroll
-                for (uint32_t i = 0; i < (uint32_t)I::kKeySteps; ++i)
-                    x[t & 1u][i] = *reinterpret_cast<const bf16x8*>(ks + key_at[i] + own + t * 16u * I::kChunks * 16u);
-            };
-            read_keys(0);
+                    for (uint32_t i = 0; i < (uint32_t)I::kKeySteps; ++i)
+                        x[t & 1u][i] = *reinterpret_cast<const bf16x8*>(ks + key_at[i] + own + t * 16u * I::kChunks * 16u);
+                };
+                read_keys(0);
 #pragma unroll
-            for (uint32_t t = 0; t < 2u * kTiles; ++t) {
-                if (t + 1u < 2u * kTiles) read_keys(t + 1u);
-                __builtin_amdgcn_sched_barrier(0);
+                for (uint32_t t = 0; t < 2u * kTiles; ++t) {
+                    if (t + 1u < 2u * kTiles) read_keys(t + 1u);
+                    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int n = 0; n < kQueries; ++n) s[t / 2][n][t & 1u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int n = 0; n < N; ++n) s[t / 2][n][t & 1u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (uint32_t i = 0; i < (uint32_t)I::kKeySteps; ++i)
+                    for (uint32_t i = 0; i < (uint32_t)I::kKeySteps; ++i)
 #pragma unroll
-                    for (int n = 0; n < kQueries; ++n)
-                        s[t / 2][n][t & 1u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[t & 1u][i], q[n][i], s[t / 2][n][t & 1u], 0, 0, 0);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            // the first values are read while weights are made: tile i of the output for places 32 u .. 32 u + 31
-            u32x4 y[kAhead];
-            auto read_values = [&](uint32_t iu) __attribute__((always_inline)) {
-                const uint32_t i = iu / kTiles, u = iu % kTiles;
-                u32x4 z;
-#pragma unroll
-                for (uint32_t t = 0; t < 2; ++t) {
-                    const s16x4 z1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                        (__attribute__((address_space(3))) s16x4*)(vs + value_at[i] + own + (u * 32u + t * 16u) * I::kChunks * 16u));
-                    const u32x2 z2 = __builtin_bit_cast(u32x2, z1);
-                    z[2 * t] = z2[0];
-                    z[2 * t + 1] = z2[1];
+                        for (int n = 0; n < N; ++n)
+                            s[t / 2][n][t & 1u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[t & 1u][i], q[n][i], s[t / 2][n][t & 1u], 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                return z;
+                // the first values are read while weights are made: tile i of the output for places 32 u .. 32 u + 31
+                u32x4 y[kAhead];
+                auto read_values = [&](uint32_t iu) __attribute__((always_inline)) {
+                    const uint32_t i = iu / kTiles, u = iu % kTiles;
+                    u32x4 z;
+#pragma unroll
+                    for (uint32_t t = 0; t < 2; ++t) {
+                        const s16x4 z1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            (__attribute__((address_space(3))) s16x4*)(vs + value_at[i] + own + (u * 32u + t * 16u) * I::kChunks * 16u));
+                        const u32x2 z2 = __builtin_bit_cast(u32x2, z1);
+                        z[2 * t] = z2[0];
+                        z[2 * t + 1] = z2[1];
+                    }
+                    return z;
+                };
+#pragma unroll
+                for (uint32_t i = 0; i < kAhead; ++i) y[i] = read_values(i);
+                uint32_t seen[kTiles][N] = {};
+                bf16x8 weights[kTiles][N];
+                if (masked) {
+#pragma unroll
+                    for (uint32_t u = 0; u < kTiles; ++u)
+#pragma unroll
+                        for (int n = 0; n < N; ++n) seen[u][n] = seen_bits(args, w, column[n], low[n], b0 + u * 32u);
+                }
+                weigh(s, masked, seen, factor, g, m, sum, o, weights);
+#pragma unroll
+                for (uint32_t iu = 0; iu < I::kOut * kTiles; ++iu) {
+                    const uint32_t i = iu / kTiles, u = iu % kTiles;
+                    const bf16x8 v1 = __builtin_bit_cast(bf16x8, y[iu % kAhead]);
+                    if (iu + kAhead < I::kOut * kTiles) y[iu % kAhead] = read_values(iu + kAhead);
+#pragma unroll
+                    for (int n = 0; n < N; ++n) o[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, weights[u][n], o[n][i], 0, 0, 0);
+                }
+                if (masked && uniform(lds_odd[buffer] == base)) {
+#pragma unroll
+                    for (uint32_t u = 0; u < kTiles; ++u) I::add_odd(args, table, values, head, b0 + u * 32u, w.end, seen[u], weights[u], o, lane);
+                }
             };
-#pragma unroll
-            for (uint32_t i = 0; i < kAhead; ++i) y[i] = read_values(i);
-            uint32_t seen[kTiles][kQueries] = {};
-            bf16x8 weights[kTiles][kQueries];
-            if (masked) {
-#pragma unroll
-                for (uint32_t u = 0; u < kTiles; ++u)
-#pragma unroll
-                    for (int n = 0; n < kQueries; ++n) seen[u][n] = seen_bits(args, w, column[n], low[n], b0 + u * 32u);
-            }
-            weigh(s, masked, seen, factor, g, m, sum, o, weights);
-#pragma unroll
-            for (uint32_t iu = 0; iu < I::kOut * kTiles; ++iu) {
-                const uint32_t i = iu / kTiles, u = iu % kTiles;
-                const bf16x8 v1 = __builtin_bit_cast(bf16x8, y[iu % kAhead]);
-                if (iu + kAhead < I::kOut * kTiles) y[iu % kAhead] = read_values(iu + kAhead);
-#pragma unroll
-                for (int n = 0; n < kQueries; ++n) o[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, weights[u][n], o[n][i], 0, 0, 0);
-            }
-            if (masked && uniform(lds_odd[buffer] == base)) {
-#pragma unroll
-                for (uint32_t u = 0; u < kTiles; ++u) I::add_odd(args, table, values, head, b0 + u * 32u, w.end, seen[u], weights[u], o, lane);
-            }
+            if (kQueries == 2 && two) work(std::integral_constant<int, kQueries>());
+            else if (one) work(std::integral_constant<int, 1>());
             __builtin_amdgcn_sched_barrier(0);
             it.store(args, lds_k[buffer ^ 1u], lds_v[buffer ^ 1u], base + kStep, w.end, masked_from(base + kStep, kStep), &lds_odd[buffer ^ 1u],
                      threadIdx.x);
@@ -373,7 +390,7 @@ __global__ __launch_bounds__(64 * (kGroups < 4 ? 4 : kGroups), DP < 256 ? 2 : 1)
         if constexpr (kSplits == 2) {
             // the second half of the places joins the first, through the keys' LDS (all have left the loop)
             static_assert(sizeof(lds_k) >= kQueries * 64 * (I::kOut * 16 + 8), "");
-            f32x4* to = reinterpret_cast<f32x4*>(group_row == 0 ? lds_k : lds_v);
+            f32x4* to = reinterpret_cast<f32x4*>(group == 0 ? lds_k : lds_v);
             float* ml = reinterpret_cast<float*>(to + kQueries * I::kOut * 64);
             if (split == 1) {
 #pragma unroll
@@ -402,7 +419,7 @@ __global__ __launch_bounds__(64 * (kGroups < 4 ? 4 : kGroups), DP < 256 ? 2 : 1)
         for (int n = 0; n < kQueries; ++n) {
             if (split != 0) break;
             const float all = sum[n][0];
-            const uint32_t row = group_row + (uint32_t)n * 16u + r;
+            const uint32_t row = group * 16u + (uint32_t)n * 16u * kGroups + r;
             if (!direct && first_row + row < rows) {
                 float* to = sh.parts + ((int64_t)slot * R + row) * DP + g * 4u;
 #pragma unroll
