@@ -16,7 +16,7 @@
 //
 // 64 lanes of 48 rows over 6,144 e4m3 places of 8 key heads of 128: 826 MB in 210
 // us, 3.9 TB/s (a large copy makes 5.4).  16 lanes of 192 rows, bfloat16: 418 MB
-// and 78 GFLOP in 144 us.  Neither memory nor the matrix cores (24 and 41 % of
+// and 78 GFLOP in 144 us.  Neither memory nor the matrix cores (20 and 32 % of
 // the time) bound it: a wave's products, weights and staging follow one another,
 // and two waves on a SIMD overlap them in part.  Priorities for one of the two,
 // and scores of the next places made among the weights of these (which takes
