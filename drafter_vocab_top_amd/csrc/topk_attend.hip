@@ -541,15 +541,25 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs args, Shape sh) {
     }
 }
 
+// Places of a lane that are read, at most.
+int64_t span_of(const AttendArgs& a) {
+    return a.a.window ? std::min<int64_t>(a.places, (int64_t)a.a.window + a.a.C + 128) : a.places;
+}
+
 // Rows of an item: those of an average lane's columns and a key head's queries, rounded up.  Up to 32 the
 // waves of a workgroup share the places, beyond that the rows (topk_attend_rows.hip).  Fewer rows than there are mean
 // that keys and values are read again: 64 lanes over 6,144 places of 8 key heads of 128, e4m3 and bfloat16, 32 rows
 // 216 and 348 us (in items of 16: 362 and 555), 64 rows 231 and 356 (of 32: 354 and 594), 128 rows 305 and 380 (of
 // 64: 409 and 631), 256 rows 471 (of 128: 561).  Of dim 256 the registers hold 16 and 64 rows.
+// Little work is done sooner in more and smaller items, whose parts take less time each and leave smaller pieces:
+// 4 lanes of 256 rows over 300 places 17 us in items of 16, 20 of 32, 27 of 256; 8 lanes of 64 rows over 1,024 places 23,
+// 25 and (of 64) 28; one lane of 256 rows over 2,048 places 21, 22 and 27, over 8,192 33, 30 and 36, over 32,768 82, 59
+// and 58.  The limits are of the bytes that are then read (from cache, but for the first time).
 uint32_t rows_of(const AttendArgs& a) {
     const int64_t rows = (a.a.C + a.a.lanes - 1) / a.a.lanes * (a.a.heads / a.cache.c.heads);
-    if (rows <= 16) return 16;
-    if (rows <= 32 && padded_dim(a) < 256) return 32;
+    const double once = 2.0 * (a.cache.c.format == TOPK_CACHE_FP8 ? 1 : 2) * a.cache.c.dim * a.cache.c.heads * (double)a.a.lanes * (double)span_of(a);
+    if (rows <= 16 || once * (double)((rows + 15) / 16) <= 150e6) return 16;
+    if (padded_dim(a) < 256 && (rows <= 32 || once * (double)((rows + 31) / 32) <= 300e6)) return 32;
     if (rows <= 64 || padded_dim(a) == 256) return 64;
     return rows <= 128 ? 128 : 256;
 }
@@ -564,8 +574,7 @@ Shape shape_of(const AttendArgs& a, int64_t* bytes) {
     // it: with one, 64 lanes of 64 rows take 260 us instead of 208), and as there are steps
     const int64_t most = dp < 256 && s.rows < 256 ? 512 : 256;
     const int64_t items = a.cache.c.heads * ((a.a.C * s.group.d + a.a.lanes * (s.rows - 1)) / s.rows);
-    const int64_t span = a.a.window ? std::min<int64_t>(a.places, (int64_t)a.a.window + a.a.C + step) : a.places;
-    const int64_t steps = std::min<int64_t>(most, (span + step - 1) / step + 1);
+    const int64_t steps = std::min<int64_t>(most, (span_of(a) + step - 1) / step + 1);
     while ((int64_t)1 << s.shift < std::min(most, items * steps)) ++s.shift;
     s.workers = 1u << s.shift;
     const int64_t cuts = (sizeof(Cut) * s.workers + 255) / 256 * 256;

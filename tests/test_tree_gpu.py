@@ -289,6 +289,8 @@ def attend_case(gpu, c, seed=0):
     width = (ctx + most) // bs + 1
     blocks = L * width + 2
     table = rng.permutation(blocks)[:L * width].reshape(L, width).astype(np.int32)
+    if c.get("room"):  # for more places, which decides how the work is cut
+        table = np.concatenate([table, np.full((L, c["room"] // bs), -1, np.int32)], axis=1)
     cache, tensors = make_cache(gpu, rng, c["fp8"], 2, blocks, bs, H, D, c.get("layout", "slots"), fill="nan")
     # what lies in the lanes' places; everywhere else there is NaN
     for l, (b, e) in enumerate(spans):
@@ -386,13 +388,16 @@ ATTENDS = [
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
 @pytest.mark.parametrize("c", ATTENDS, ids=str)
 def test_attend(gpu, c, fp8):
-    got, want, bound, spans = attend_case(gpu, dict(c, fp8=fp8))
-    check(got, want, bound)
+    for room in (0, 4000000 // c["lanes"]):
+        got, want, bound, spans = attend_case(gpu, dict(c, fp8=fp8, room=room))
+        check(got, want, bound)
 
 
 # Every size class of an item's rows (columns times query heads of a key head: 16, 32, 64, 128, 256), at dims that fill
-# a kernel's 64, 128 or 256 and dims that do not, with steps that all rows see whole and steps that they do not.
-CLASSES = [dict(rows=rows, dim=dim) for rows in (16, 32, 64, 128, 256) for dim in (64, 48, 128, 112, 256, 208)]
+# a kernel's 64, 128 or 256 and dims that do not, with steps that all rows see whole and steps that they do not.  Little
+# work is cut into small items, so the table has room for 4,000,000 places (384 MB of one e4m3 head of dim 48).
+CLASSES = [dict(rows=rows, dim=dim, room=room) for rows in (16, 32, 64, 128, 256) for dim in (64, 48, 128, 112, 256, 208)
+           for room in (0, 2000000)]
 
 
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
@@ -401,7 +406,7 @@ def test_attend_sizes(gpu, c, fp8):
     rows, dim = c["rows"], c["dim"]
     for i, extra in enumerate((dict(), dict(window=90), dict(poison=True), dict(chain=True, odd_queries=True))):
         got, want, bound, _ = attend_case(gpu, dict(lanes=2, most=rows // 4, ctx=420, ctx_min=250, heads=1, group=4, dim=dim, bs=16,
-                                                    ragged=False, fp8=fp8, **extra), seed=i)
+                                                    room=c["room"], ragged=False, fp8=fp8, **extra), seed=i)
         check(got, want, bound)
 
 
@@ -422,8 +427,9 @@ MIXES = [dict(lanes=70, most=16, ctx=150, heads=1, group=4, dim=64, bs=16),     
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
 @pytest.mark.parametrize("c", MIXES, ids=str)
 def test_attend_mixed_lengths(gpu, c, fp8):
-    got, want, bound, _ = attend_case(gpu, dict(c, fp8=fp8))
-    check(got, want, bound)
+    for room in (0, 4000000 // c["lanes"]):
+        got, want, bound, _ = attend_case(gpu, dict(c, fp8=fp8, room=room))
+        check(got, want, bound)
 
 
 @pytest.mark.parametrize("most", [4, 24], ids=["few rows", "many rows"])
