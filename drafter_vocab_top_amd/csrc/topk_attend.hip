@@ -34,7 +34,7 @@
 // bytes, is read at 4.1 TB/s (64 lanes of 6 columns over 6,144 places: 826 MB in
 // 200 us; the same with every block in cache 111 us); twice as many places in
 // flight did not change that.  One lane over 2,048 places is a chain of
-// latencies: 16 us, 12 of them here (lengths, table, keys, and the sums of four
+// latencies: 15 us, 12 of them here (lengths, table, keys, and the sums of four
 // waves).
 #include <algorithm>
 
