@@ -301,7 +301,7 @@ __global__ __launch_bounds__(256, DP < 256 ? 2 : 1) void attend_kernel(AttendArg
         }
 
         for (; base < stop_at; base += kStep) {
-            const bool masked = uniform(base + kTile > w.len || base < all_see);  // some row may not see all
+            const bool masked = uniform(base + kTile > w.open() || base < all_see);  // some row may not see all
             const uint32_t lane = opaque(threadIdx.x & 63u), r = lane & 15u, g = lane >> 4;
             it.scales = it.next_scales;
             // scores of 32 places

@@ -43,6 +43,10 @@ struct LaneWork {
     uint32_t cb, n, len, end;  // first column, columns, places before them, places
     uint32_t first, steps;     // its first step, and how many
     uint32_t tiles;            // items of a key head
+
+    // Some row may not see places from here on: the lane's columns, and what lies past the table's row (where the
+    // lane's tokens do not fit in it, this is before len).
+    __device__ __forceinline__ uint32_t open() const { return min_u32(len, end); }
 };
 
 template <uint32_t kStep>
@@ -214,7 +218,7 @@ __device__ __forceinline__ uint32_t widen(uint32_t x, float scale) {
 __device__ __forceinline__ uint32_t seen_bits(const AttendArgs& args, const LaneWork& w, uint32_t column, uint32_t low, uint32_t base) {
     const topk_attend_args& a = args.a;
     asm volatile("" : "+s"(base));  // (nothing of this is computed where no row asks for it)
-    uint32_t bits = range_bits(low, min_u32(w.len, w.end), base);
+    uint32_t bits = range_bits(low, w.open(), base);
     if (base + 32u > w.len) {
         uint32_t own;
         if (a.mask) {

@@ -282,7 +282,7 @@ __global__ __launch_bounds__(64 * (kGroups < 4 ? 4 : kGroups), DP < 256 ? 2 : 1)
             for (uint32_t i = 0; i < I::kWaves; ++i) all_see = max_u32(all_see, lds_see[i]);
             all_see = bcast(all_see, 0u);
         }
-        auto masked_from = [&](uint32_t first, uint32_t places) { return uniform(first + places > w.len || first < all_see); };
+        auto masked_from = [&](uint32_t first, uint32_t places) { return uniform(first + places > w.open() || first < all_see); };
 
         uint32_t base = (w.first + step) * kStep;
         const uint32_t stop_at = min_u32((w.first + last_step) * kStep, w.end);

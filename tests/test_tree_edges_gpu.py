@@ -1,0 +1,114 @@
+"""GPU tests of attention over the paged cache where a step of places is seen in
+part, in every size class of an item's rows, against the definition in 64 bits."""
+import math
+
+import pytest
+
+import tree_reference as R
+
+pytestmark = pytest.mark.gpu
+
+
+def stored(torch, shape, fp8, g):
+    """Ordinary random keys or values of a cache: (elements, scale bytes or None, the float64 values they stand for)."""
+    if not fp8:
+        x = torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16)
+        return x, None, x.double()
+    sign = torch.randint(0, 2, shape, generator=g, device="cuda") << 7
+    bits = sign | torch.randint(9, 14, shape, generator=g, device="cuda") << 3 | torch.randint(0, 8, shape, generator=g, device="cuda")
+    scales = torch.randint(121, 127, shape[:-1], generator=g, device="cuda").to(torch.uint8)
+    return bits.to(torch.uint8).view(torch.float8_e4m3fn), scales, worth(torch, bits, scales)
+
+
+def worth(torch, bits, scales):
+    return torch.from_numpy(R.E4M3).cuda()[bits.long()] * torch.exp2(scales.double() - 127)[..., None]
+
+
+def dense(torch, q, k, v, see, scale):
+    """The columns q (n, heads, group, dim) of one lane over its places k, v (places, heads, dim), all float64; see
+    (n, places).  Returns out and, for each element, what roundings move it by at most: a weight is rounded to bfloat16
+    (half a step, 2^-8), its score is a binary32 sum of dim products, scaled, less a maximum; then exponentials, the
+    sums over places in binary32, and the result's own rounding."""
+    n, heads, group, dim = q.shape
+    eps = 2.0**-8
+    s = scale * torch.matmul(q.permute(1, 0, 2, 3).reshape(heads, n * group, dim), k.permute(1, 2, 0)).view(heads, n, group, -1)
+    spread = abs(scale) * torch.matmul(q.abs().permute(1, 0, 2, 3).reshape(heads, n * group, dim), k.abs().permute(1, 2, 0)).view_as(s)
+    seen = see[None, :, None, :]
+    s = torch.where(seen, s, -math.inf)
+    top = s.amax(-1, keepdim=True)
+    w = torch.exp(s - torch.where(top == -math.inf, 0.0, top))
+    total = w.sum(-1, keepdim=True)
+    # (a weight of 0 of a place that is not visible removes it, whatever the value)
+    values = v.permute(1, 0, 2)[:, None].expand(heads, n, -1, dim)
+    values = torch.where(see[None, :, :, None], values, 0.0)
+    out = torch.matmul(w, values) / total
+    rel = eps + (dim + 8) * 2.0**-24 * (spread + s.abs()) + 2.0**-22 * top.abs() + 2.0**-20
+    rel = torch.where(s == -math.inf, eps, rel)
+    moved = torch.matmul(w * rel, values.abs()) / total + out.abs() * ((w * (rel - eps)).sum(-1, keepdim=True) / total)
+    sums = (see.sum(-1)[None, :, None, None] + 16) * 2.0**-23 * torch.matmul(w, values.abs()) / total
+    bound = moved + sums + (out.abs() + moved + sums) * eps
+    none = total == 0
+    back = lambda x: torch.where(none, 0.0, x).permute(1, 0, 2, 3).reshape(n, heads * group, dim)  # noqa: E731
+    return back(out), back(bound)
+
+
+def check(torch, got, want, bound, what):
+    got = got.double()
+    nan, inf = want.isnan(), want.isinf()
+    assert torch.equal(got.isnan(), nan), f"{what}: {int((got.isnan() != nan).sum())} of {nan.numel()} are NaN on one side only"
+    assert torch.equal(got[inf], want[inf]), what
+    fine = ~nan & ~inf
+    off = ((got - want).abs() - bound)[fine]
+    assert not (off > 0).any(), f"{what}: {int((off > 0).sum())} of {off.numel()} off, the worst by {float(off.max())} more than {float(bound[fine][off.argmax()])}"
+
+
+def words_of(torch, bits):
+    """Rows of truth values (C, n) as rows of 32-bit words."""
+    C, n = bits.shape
+    b = torch.nn.functional.pad(bits, (0, -n % 32)).view(C, -1, 32).long()
+    w = (b << torch.arange(32, device="cuda")).sum(-1)
+    return torch.where(w >= 1 << 31, w - (1 << 32), w).to(torch.int32)
+
+
+ROWS = (16, 32, 64, 128, 256)
+
+
+def lanes_for(rows, dim, fp8, heads, places):
+    """So many lanes that items get `rows` rows: little work goes to smaller items, the limits are 150 MB of keys and
+    values read for more than 16 rows and 300 MB for more than 32."""
+    each = 2 * (1 if fp8 else 2) * dim * heads * places
+    return max(6, math.ceil(1.2 * 300e6 / each / math.ceil(rows / 32)) if rows > 32 else math.ceil(1.2 * 150e6 / each / 2) if rows > 16 else 0)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("dim", [64, 112, 128, 256])
+@pytest.mark.parametrize("rows", ROWS)
+def test_attend_lengths_beyond_the_tables_row(gpu, rows, dim, fp8):
+    """The table's row ends inside a step of places; lengths go on far behind it."""
+    torch, T = gpu
+    g = torch.Generator(device="cuda").manual_seed(rows + dim)
+    H, group = 64, 2
+    n = rows // group
+    for bs, width in ((13, 3), (13, 5), (16, 5), (100, 1)):
+        places = bs * width
+        L = lanes_for(rows, dim, fp8, H, places)
+        blocks = L * width
+        shape = (blocks, bs, H, dim)
+        (k, ks, kd), (v, vs, vd) = (stored(torch, shape, fp8, g) for _ in range(2))
+        cache = T.KeyCache(k, v, *([ks, vs] if fp8 else []))
+        table = torch.randperm(blocks, generator=g, device="cuda").view(L, width).int()
+        some = [places + 64, 5 * places, places - n // 2, places, places + 1, 2**31 - 1, 0, places - n]
+        lens = torch.tensor([some[l % len(some)] for l in range(L)], dtype=torch.int64, device="cuda").clamp(min=0)
+        q = torch.randn(L * n, H * group, dim, generator=g, device="cuda").to(torch.bfloat16)
+        tree = torch.randint(0, 2, (L * n, n), generator=g, device="cuda").bool()
+        for mask in (None, words_of(torch, tree)):
+            out = torch.full_like(q, 7.0)
+            cache.attend(q, lens.int(), table, mask=mask, out=out)
+            for l in list(range(min(L, 16))) + [L - 1]:
+                at, own = table[l].long(), slice(l * n, (l + 1) * n)
+                lane_k, lane_v = (x[at].view(places, H, dim) for x in (kd, vd))
+                p, j = torch.arange(places, device="cuda")[None], torch.arange(n, device="cuda")[:, None]
+                i = (p - lens[l]).expand(n, -1)
+                seen = i <= j if mask is None else (i < 0) | ((i < n) & tree[own].gather(1, i.clamp(0, n - 1)))
+                want, bound = dense(torch, q[own].double().view(n, H, group, dim), lane_k, lane_v, seen, dim**-0.5)
+                check(torch, out[own], want, bound, f"blocks of {bs}, {width} of them, length {int(lens[l])}, mask {mask is not None}")
