@@ -305,7 +305,8 @@ __global__ __launch_bounds__(64 * (kGroups < 4 ? 4 : kGroups), DP < 256 ? 2 : 1)
             const uint8_t* vs = reinterpret_cast<const uint8_t*>(lds_v[buffer]);
             const uint32_t lane = opaque(threadIdx.x & 63u), g = lane >> 4;
             const uint32_t b0 = base + split * 32u;                             // this wave's places: kTiles times 32
-            const bool masked = masked_from(b0, 32u * kTiles);                  // some row may not see all
+            // (of the whole step, as its values went to LDS: what was cleared there is added by the wave whose places it is of)
+            const bool masked = masked_from(base, kStep);
             const uint32_t own = split * 32u * I::kChunks * 16u;
             auto work = [&](auto count) __attribute__((always_inline)) {
                 constexpr int N = decltype(count)::value;  // of the wave's kQueries 16 rows

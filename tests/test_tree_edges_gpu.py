@@ -112,3 +112,53 @@ def test_attend_lengths_beyond_the_tables_row(gpu, rows, dim, fp8):
                 seen = i <= j if mask is None else (i < 0) | ((i < n) & tree[own].gather(1, i.clamp(0, n - 1)))
                 want, bound = dense(torch, q[own].double().view(n, H, group, dim), lane_k, lane_v, seen, dim**-0.5)
                 check(torch, out[own], want, bound, f"blocks of {bs}, {width} of them, length {int(lens[l])}, mask {mask is not None}")
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("dim", [64, 48, 128, 112, 256, 208])
+@pytest.mark.parametrize("rows", ROWS)
+def test_attend_values_that_are_not_finite_before_the_columns(gpu, rows, dim, fp8):
+    """NaN and infinities in places that are seen by all rows of an item or, at a window's edge, by some: for lengths at
+    every offset of a step."""
+    torch, T = gpu
+    g = torch.Generator(device="cuda").manual_seed(rows + dim)
+    L, bs, group, H = 64, 16, 4, 1
+    n = rows // group
+    lens = 128 + torch.arange(L, device="cuda")
+    width = (128 + L + n) // bs + 1
+    blocks = L * width
+    room = 4_000_000 // L // bs  # decides the items' sizes
+    table = torch.full((L, room), -1, dtype=torch.int32, device="cuda")
+    table[:, :width] = torch.randperm(blocks, generator=g, device="cuda").view(L, width)
+    (k, ks, kd), (v, vs, vd) = (stored(torch, (blocks, bs, H, dim), fp8, g) for _ in range(2))
+    cache = T.KeyCache(k, v, *([ks, vs] if fp8 else []))
+    # one value that is not finite in every eighth place of a lane, each in a dim of its own
+    flat = (v.view(torch.uint8) if fp8 else v.view(torch.int16)).view(-1, dim)
+    kinds = [0x7F, 0xFF] if fp8 else [0x7FC0, 0x7F80, -0x80]
+    for l in range(L):
+        p = torch.arange(l % 8, int(lens[l]), 8, device="cuda")
+        d = torch.randperm(dim, generator=g, device="cuda")[:len(p)]
+        at = table[l, p // bs].long() * bs + p % bs
+        kind = torch.tensor(kinds, device="cuda")[torch.randint(0, len(kinds), (len(p),), generator=g, device="cuda")]
+        flat[at, d] = kind.to(flat.dtype)
+    vd = worth(torch, v.view(torch.uint8), vs) if fp8 else v.double()
+    q = torch.randn(L * n, H * group, dim, generator=g, device="cuda").to(torch.bfloat16)
+    tree = torch.randint(0, 2, (L * n, n), generator=g, device="cuda").bool()
+    depth = torch.randint(0, n, (L * n,), generator=g, device="cuda")
+    for window, mask in ((0, None), (0, words_of(torch, tree)), (70, None), (100, words_of(torch, tree)), (33, None)):
+        positions = None if mask is None else (lens.repeat_interleave(n) + depth).int()
+        out = cache.attend(q, lens.int(), table, mask=mask, positions=positions, window=window)
+        for l in range(L):
+            own, places = slice(l * n, (l + 1) * n), int(lens[l]) + n
+            p, j = torch.arange(places, device="cuda"), torch.arange(n, device="cuda")[:, None]
+            at = table[l, p // bs].long() * bs + p % bs
+            lane_k, lane_v = (x.reshape(-1, H, dim)[at] for x in (kd, vd))
+            i = (p[None] - lens[l]).expand(n, -1)
+            position = (lens[l] + j) if positions is None else positions[own].long()[:, None]
+            before = (i < 0) & ((p[None] > position - window) if window else True)
+            if mask is None:
+                seen = before | ((i >= 0) & (i <= j) & ((j - i < window) if window else True))
+            else:
+                seen = before | ((i >= 0) & tree[own].gather(1, i.clamp(0, n - 1)))
+            want, bound = dense(torch, q[own].double().view(n, H, group, dim), lane_k, lane_v, seen, dim**-0.5)
+            check(torch, out[own], want, bound, f"length {int(lens[l])}, window {window}, mask {mask is not None}")
