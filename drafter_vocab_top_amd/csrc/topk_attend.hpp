@@ -313,6 +313,7 @@ __device__ __forceinline__ void weigh(f32x4 (&s)[kTiles][kQueries][2], bool mask
         }
 }
 
+// 2^(byte - 127); of 255 an infinity, whose exponent the widening takes as NaN.
 __device__ __forceinline__ float power_of(uint32_t byte) { return __builtin_bit_cast(float, byte ? byte << 23 : 0x400000u); }
 
 // Clears what is not finite of two bfloat16 values; `odd` gets a bit where there is any.

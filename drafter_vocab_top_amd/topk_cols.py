@@ -697,7 +697,7 @@ class KeyCache:
         256.
     key_scales, value_scales: with float8_e4m3fn, uint8 (or float8_e8m0fnu) of
         the shape without dim, any strides, the same for both: a row stands for
-        its elements times 2^(scale - 127).
+        its elements times 2^(scale - 127), with 255 for NaN.
     """
 
     def __init__(self, keys, values, key_scales=None, value_scales=None):

@@ -516,7 +516,8 @@ typedef enum {
  * for its elements times 2^(b - 127), b being the byte at
  *   y*scale_layer_stride + (s / block_size)*scale_block_stride + (s % block_size)*scale_slot_stride
  *   + h*scale_head_stride
- * of key_scales, or of value_scales.
+ * of key_scales, or of value_scales.  (b = 255 stands for NaN in all of the row;
+ * topk_cols_cache_write never writes it.)
  */
 typedef struct {
     int64_t layers;      /* >= 1 */

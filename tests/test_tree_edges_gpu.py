@@ -162,3 +162,33 @@ def test_attend_values_that_are_not_finite_before_the_columns(gpu, rows, dim, fp
                 seen = before | ((i >= 0) & tree[own].gather(1, i.clamp(0, n - 1)))
             want, bound = dense(torch, q[own].double().view(n, H, group, dim), lane_k, lane_v, seen, dim**-0.5)
             check(torch, out[own], want, bound, f"length {int(lens[l])}, window {window}, mask {mask is not None}")
+
+
+@pytest.mark.parametrize("group", [1, 2, 4, 8, 16])
+@pytest.mark.parametrize("dim", [16, 64, 128, 256])
+def test_attend_reads_every_pattern_and_scale(gpu, dim, group):
+    """Each of the 256 e4m3 patterns with each of the 256 scale bytes: a place that is alone has weight 1, so its value
+    comes out as it stands for (times below 2^-126 may be 0; a byte of 255 stands for NaN)."""
+    torch, T = gpu
+    H, bs = 256 // dim, 16
+    patterns = torch.arange(256, device="cuda").to(torch.uint8).view(1, 1, H, dim).expand(256, bs, H, dim).contiguous()
+    scales = torch.arange(256, device="cuda").to(torch.uint8).view(256, 1, 1).expand(256, bs, H).contiguous()
+    cache = T.KeyCache(torch.zeros_like(patterns).view(torch.float8_e4m3fn), patterns.view(torch.float8_e4m3fn),
+                       torch.full_like(scales, 127), scales)
+    table = torch.full((256, 40000), -1, dtype=torch.int32, device="cuda")  # (the room decides the items' sizes)
+    table[:, 0] = torch.arange(256, device="cuda").int()
+    want = worth(torch, patterns[:, 0], scales[:, 0])
+    want[255] = math.nan
+    # all rows of an item see the place; or only the columns before the last do, which leave it out as if it were masked
+    lens = torch.zeros(256, dtype=torch.int32, device="cuda")
+    for n, bits in ((1, [1]), (16, [1] * 16), (16, [1] * 15 + [0])):
+        mask = torch.tensor(bits, dtype=torch.int32, device="cuda").repeat(256).view(-1, 1)
+        q = torch.randn(256 * n, H * group, dim, device="cuda").to(torch.bfloat16)
+        out = cache.attend(q, lens, table, mask=mask).view(256, n, H, group, dim)
+        for j in range(n):
+            for h in range(group):
+                got = out[:, j, :, h].double()
+                value = want if bits[j] else torch.zeros_like(want)
+                rounded = value.float().to(torch.bfloat16).double()
+                same = (got == rounded) | (got.isnan() & rounded.isnan()) | ((value.abs() < 2.0**-126) & (got == 0))
+                assert same.all(), (n, j, h, (~same).nonzero()[:5].tolist())
