@@ -164,6 +164,53 @@ def test_attend_values_that_are_not_finite_before_the_columns(gpu, rows, dim, fp
             check(torch, out[own], want, bound, f"length {int(lens[l])}, window {window}, mask {mask is not None}")
 
 
+PROMPTS = [dict(n=[700, 0, 1, 333], lens=[0, 40, 300, 65], heads=2, group=4, dim=128, bs=16),
+           dict(n=[513, 2, 64], lens=[1, 64, 0], heads=1, group=2, dim=64, bs=13),
+           dict(n=[1100], lens=[900], heads=1, group=8, dim=96, bs=64),
+           dict(n=[300, 5], lens=[77, 200], heads=1, group=5, dim=256, bs=7),
+           dict(n=[1, 1, 600] + [1] * 70, lens=[400, 0, 33] + [129] * 70, heads=1, group=1, dim=80, bs=32)]
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("c", PROMPTS, ids=lambda c: f"{len(c['n'])} lanes to {max(c['n'])} columns, dim {c['dim']}")
+def test_attend_prompts(gpu, c, fp8):
+    """Hundreds of columns in a lane, next to lanes that decode: as chains, with windows that are shorter than the
+    prompt, and under masks of many words."""
+    torch, T = gpu
+    g = torch.Generator(device="cuda").manual_seed(3)
+    H, group, dim, bs = c["heads"], c["group"], c["dim"], c["bs"]
+    n, lens = c["n"], torch.tensor(c["lens"], device="cuda")
+    cs = torch.zeros(len(n) + 1, dtype=torch.int32, device="cuda")
+    cs[1:] = torch.cumsum(torch.tensor(n, device="cuda"), 0)
+    L, C, most = len(n), sum(n), max(n)
+    width = max(a + b for a, b in zip(n, c["lens"])) // bs + 1
+    blocks = L * width
+    (k, ks, kd), (v, vs, vd) = (stored(torch, (blocks, bs, H, dim), fp8, g) for _ in range(2))
+    cache = T.KeyCache(k, v, *([ks, vs] if fp8 else []))
+    q = torch.randn(C + 3, H * group, dim, generator=g, device="cuda").to(torch.bfloat16)
+    tree = torch.randint(0, 2, (C + 3, most), generator=g, device="cuda").bool()
+    for room in (0, 4_000_000 // L // bs):  # decides the items' sizes
+        table = torch.full((L, width + room), -1, dtype=torch.int32, device="cuda")
+        table[:, :width] = torch.randperm(blocks, generator=g, device="cuda").view(L, width)
+        for window, mask in ((0, None), (45, None), (300, None), (0, words_of(torch, tree))):
+            out = torch.full_like(q, 7.0)
+            cache.attend(q, lens.int(), table, cs, mask=mask, window=window, out=out)
+            assert (out[C:] == 7).all()
+            for l in range(L):
+                if n[l] == 0:
+                    continue
+                own, p = slice(int(cs[l]), int(cs[l + 1])), torch.arange(int(lens[l]) + n[l], device="cuda")
+                j, at = torch.arange(n[l], device="cuda")[:, None], table[l, p // bs].long() * bs + p % bs
+                lane_k, lane_v = (x.reshape(-1, H, dim)[at] for x in (kd, vd))
+                i = (p[None] - lens[l]).expand(n[l], -1)
+                if mask is None:
+                    seen = (i <= j) & ((j - i < window) if window else True)
+                else:
+                    seen = (i < 0) | tree[own].gather(1, i.clamp(0, most - 1))
+                want, bound = dense(torch, q[own].double().view(n[l], H, group, dim), lane_k, lane_v, seen, dim**-0.5)
+                check(torch, out[own], want, bound, f"lane {l}, window {window}, mask {mask is not None}, room {room}")
+
+
 @pytest.mark.parametrize("group", [1, 2, 4, 8, 16])
 @pytest.mark.parametrize("dim", [16, 64, 128, 256])
 def test_attend_reads_every_pattern_and_scale(gpu, dim, group):
