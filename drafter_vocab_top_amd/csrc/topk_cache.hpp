@@ -42,8 +42,8 @@ struct Divisor {
 struct Cache {
     topk_cache c;
     Divisor block;
-    // Strides in 16 bytes, and of the scales in bytes: no offset within a layer passes 32 bits then (a layer has less
-    // than 64 GiB, its scales less than 4).
+    // Strides in 16 bytes, and of the scales in bytes: no offset of a row's parts passes 32 bits then (the last slot's row
+    // ends within 64 GiB of the layer's start, its scale within 4).
     uint32_t block16, slot16, scale_block, scale_slot;
     // Offset of slot r of block b (its first head), in 16 bytes; and of its scale.
     __device__ __forceinline__ uint32_t row16(uint32_t b, uint32_t r) const { return b * block16 + r * slot16; }

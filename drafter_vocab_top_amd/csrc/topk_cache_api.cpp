@@ -44,8 +44,8 @@ int check_cache(const topk_cache* c) {
         return TOPK_ERR_INVALID_ARG;
     if (c->dim > TOPK_MAX_DIM || c->blocks > kMax32 / c->block_size || c->layers > kMaxPlanes / c->heads)
         return TOPK_ERR_UNSUPPORTED;
-    // offsets within a layer are computed in 32 bits, of rows in units of 16 bytes
-    if (last_slot(*c, c->block_stride / unit, c->slot_stride / unit) >> 32 ||
+    // offsets within a layer are computed in 32 bits, of rows' 16-byte parts in units of those: the last one has to fit
+    if ((last_slot(*c, c->block_stride / unit, c->slot_stride / unit) + (uint64_t)(c->dim / unit - 1)) >> 32 ||
         (c->format == TOPK_CACHE_FP8 && last_slot(*c, c->scale_block_stride, c->scale_slot_stride) >> 32))
         return TOPK_ERR_UNSUPPORTED;
     return TOPK_OK;

@@ -559,8 +559,9 @@ typedef struct {
  *
  * Returns TOPK_ERR_INVALID_ARG for a NULL or misaligned pointer, or a value or
  * stride out of the ranges above; TOPK_ERR_UNSUPPORTED for dim >
- * TOPK_MAX_DIM, blocks*block_size beyond 2^31 - 1, a layer of 64 GiB (its scales:
- * 4 GiB) or more, layers*heads beyond 2^20 or C*heads beyond 2^26;
+ * TOPK_MAX_DIM, blocks*block_size beyond 2^31 - 1, a layer whose last slot ends
+ * more than 64 GiB (its scale: 4 GiB) from the layer's start, layers*heads beyond
+ * 2^20 or C*heads beyond 2^26;
  * TOPK_ERR_HIP when the launch fails.
  */
 int topk_cols_cache_write(const topk_cache *cache, const topk_cache_write_args *args, hipStream_t stream);
@@ -621,7 +622,7 @@ typedef struct {
  * stride out of the ranges above, lanes that do not divide C (col_start NULL)
  * or a workspace that is too small; TOPK_ERR_UNSUPPORTED for lanes >
  * TOPK_MAX_LANES, dim > TOPK_MAX_DIM, table_ld, mask_ld or blocks*block_size
- * beyond 2^31 - 1, a layer of 64 GiB (its scales: 4 GiB) or more, layers*heads
+ * beyond 2^31 - 1, a layer larger than topk_cols_cache_write takes, layers*heads
  * beyond 2^20 or C*heads beyond 2^26; TOPK_ERR_HIP when a launch fails.
  */
 int topk_cols_attend(const topk_cache *cache, const topk_attend_args *args, hipStream_t stream);
@@ -645,8 +646,9 @@ int topk_cols_attend_workspace(const topk_cache *cache, const topk_attend_args *
  *
  * Returns TOPK_ERR_INVALID_ARG for a NULL or misaligned pointer, or a value or
  * stride out of range; TOPK_ERR_UNSUPPORTED for lanes > TOPK_MAX_LANES, dim >
- * TOPK_MAX_DIM, table_ld, width or blocks*block_size beyond 2^31 - 1, a layer of
- * 64 GiB (its scales: 4 GiB) or more, or layers*heads beyond 2^20; TOPK_ERR_HIP when a launch fails.
+ * TOPK_MAX_DIM, table_ld, width or blocks*block_size beyond 2^31 - 1, a layer
+ * larger than topk_cols_cache_write takes, or layers*heads beyond 2^20;
+ * TOPK_ERR_HIP when a launch fails.
  */
 int topk_cols_cache_move(const topk_cache *cache, int64_t lanes, const int32_t *lens, const int32_t *table,
                          int64_t table_ld, const int32_t *columns, int64_t width, hipStream_t stream);
