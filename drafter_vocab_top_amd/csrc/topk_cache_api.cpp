@@ -70,7 +70,7 @@ int make_attend(topk::AttendArgs* to, const topk_cache* c, const topk_attend_arg
     if (!a || a->lanes < 1 || a->C < 1 || a->table_ld < 1 || a->window < 0) return TOPK_ERR_INVALID_ARG;
     if (const int bad = check_cache(c)) return bad;
     if (a->layer < 0 || a->layer >= c->layers || a->heads < 1 || a->heads % c->heads != 0) return TOPK_ERR_INVALID_ARG;
-    if (!(a->scale >= -3.4028234e38f && a->scale <= 3.4028234e38f)) return TOPK_ERR_INVALID_ARG;
+    if (!(a->scale >= -0x1p127f && a->scale <= 0x1p127f)) return TOPK_ERR_INVALID_ARG;  // (its product with log2(e) is finite)
     if (bad_stride(a->q_stride, 8) || bad_stride(a->q_head_stride, 8) || bad_stride(a->out_stride, 8) ||
         bad_stride(a->out_head_stride, 8))
         return TOPK_ERR_INVALID_ARG;

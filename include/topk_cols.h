@@ -572,7 +572,7 @@ typedef struct {
     int64_t layer;            /* of the cache, 0 .. layers - 1 */
     int32_t heads;            /* query heads, a multiple of the cache's heads: query head h reads head h / (heads / cache heads) */
     int32_t window;           /* >= 0; 0: none */
-    float scale;              /* finite */
+    float scale;              /* at most 2^127 in magnitude */
     const void *q;            /* device, 16-byte aligned, bfloat16: element d of head h of column c at c*q_stride + h*q_head_stride + d */
     int64_t q_stride, q_head_stride;     /* in elements, >= 0 and multiples of 8 */
     const int32_t *col_start; /* device, lanes + 1, or NULL */

@@ -24,3 +24,12 @@ def test_the_last_row_ends_within_64_gib(lib, base):  # noqa: F811
     for kw in (dict(blocks=2, block_size=1, block_stride=((1 << 32) - row) * each),
                dict(blocks=1, block_size=2, slot_stride=((1 << 32) - row) * each)):
         assert workspace(lib, dict(base, **kw))[0] == T.TOPK_OK, kw
+
+
+def test_scales_beyond_2_127_are_refused(lib):  # noqa: F811
+    """Scores are multiplied by scale * log2(e) in binary32: where that overflows, a score of 0 would become NaN."""
+    for scale in (2.0**127 * (1 + 2**-23), 3.4e38, -2.0**127 * (1 + 2**-23), math.inf, -math.inf):
+        assert attend(lib, scale=scale) == BAD, scale
+        assert workspace(lib, scale=scale) == (BAD, 0), scale
+    for scale in (2.0**127, -2.0**127, 0.0, 1e-45):
+        assert workspace(lib, scale=scale)[0] == T.TOPK_OK, scale
