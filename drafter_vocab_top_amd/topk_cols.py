@@ -760,10 +760,14 @@ class KeyCache:
         col_start (lanes + 1,), or the same number of columns for each lane.
         mask, positions: as tree gives them.  Without a mask the columns are a
             chain (or a prompt); without positions column j's is lens + j.
-        window: only this many places up to the column's own, 0 for all.
+        window: only this many places up to the column's own, 0 for all: of the
+            lane's tokens those less than window before its position, and
+            without a mask of the columns likewise.  A mask says by itself
+            which columns are seen: ancestors whose bits are set are, at any
+            distance.
         scale: of the products, default dim ** -0.5.
-        out: like q (default: allocated; columns of no lane are then
-            uninitialised).
+        out: like q, overlapping neither q nor the cache (default: allocated;
+            columns of no lane are then uninitialised).
         """
         if scale is None:
             scale = self.dim ** -0.5

@@ -598,9 +598,9 @@ typedef struct {
  *   p < lens[l]:               visible, with a window if p > positions[c] - window
  *                              (positions below lens[l] count as lens[l]);
  *   lens[l] <= p < lens[l]+n:  visible if bit p - lens[l] of the column's mask is
- *                              set (columns from 32*mask_ld on are not); without a
- *                              mask if p - lens[l] <= j, with a window also
- *                              j - (p - lens[l]) < window.
+ *                              set (columns from 32*mask_ld on are not), whatever
+ *                              the window; without a mask if p - lens[l] <= j,
+ *                              with a window also j - (p - lens[l]) < window.
  * A column with nothing visible, or whose scores are all -Inf, gets zeros.
  * What lies in places that are not visible does not matter, NaN and infinities
  * included.  Places beyond the table's row are not visible; block ids are cut

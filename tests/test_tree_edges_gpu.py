@@ -239,3 +239,34 @@ def test_attend_reads_every_pattern_and_scale(gpu, dim, group):
                 rounded = value.float().to(torch.bfloat16).double()
                 same = (got == rounded) | (got.isnan() & rounded.isnan()) | ((value.abs() < 2.0**-126) & (got == 0))
                 assert same.all(), (n, j, h, (~same).nonzero()[:5].tolist())
+
+
+@pytest.mark.parametrize("group", [1, 4, 16])
+def test_attend_windows_and_masks(gpu, group):
+    """A window cuts the lane's tokens by the column's position, and a chain's columns; a mask says by itself which
+    columns are seen.  So a chain's mask whose far ancestors are cleared gives the chain's bits, and as tree makes it
+    shows all ancestors."""
+    torch, T = gpu
+    g = torch.Generator(device="cuda").manual_seed(1)
+    n, H, dim, bs = 12, 2, 64, 16
+    lens = torch.tensor([100, 3, 0], device="cuda")
+    L = len(lens)
+    (k, _, kd), (v, _, vd) = (stored(torch, (L * 8, bs, H, dim), False, g) for _ in range(2))
+    cache, table = T.KeyCache(k, v), torch.randperm(L * 8, generator=g, device="cuda").view(L, 8).int()
+    q = torch.randn(L * n, H * group, dim, generator=g, device="cuda").to(torch.bfloat16)
+    parents = (torch.arange(L * n, device="cuda") % n - 1).int()
+    mask, positions = T.tree(parents, lens.int(), lanes=L, words=1)
+    i, j = torch.arange(n, device="cuda")[None], torch.arange(n, device="cuda")[:, None]
+    for window in (1, 2, 5, 11, 12, 40):
+        chain = cache.attend(q, lens.int(), table, window=window)
+        cut = words_of(torch, ((i <= j) & (j - i < window)).repeat(L, 1))
+        assert torch.equal(cache.attend(q, lens.int(), table, mask=cut, positions=positions, window=window), chain)
+        whole = cache.attend(q, lens.int(), table, mask=mask, positions=positions, window=window)
+        for l in range(L):
+            own, p = slice(l * n, (l + 1) * n), torch.arange(int(lens[l]) + n, device="cuda")
+            lane_k, lane_v = (x.reshape(-1, H, dim)[table[l, p // bs].long() * bs + p % bs] for x in (kd, vd))
+            column = (p[None] - lens[l]).expand(n, -1)
+            near = j - column < window
+            for out, seen in ((chain, (column <= j) & near), (whole, (column <= j) & (near | (column >= 0)))):
+                want, bound = dense(torch, q[own].double().view(n, H, group, dim), lane_k, lane_v, seen, dim**-0.5)
+                check(torch, out[own], want, bound, f"lane {l}, window {window}")
