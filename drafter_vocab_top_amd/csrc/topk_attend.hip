@@ -217,7 +217,6 @@ struct Item {
     // again (it is not written).
     __device__ __forceinline__ void load_queries(const AttendArgs& args, const Shape& sh, const LaneWork& w, uint32_t head, uint32_t first_row, uint32_t lane) {
         const topk_attend_args& a = args.a;
-        const float c = a.scale;
 #pragma unroll
         for (int n = 0; n < kQueries; ++n) {
             const uint32_t row = min_u32(first_row + (uint32_t)n * 16u + (lane & 15u), w.n * sh.group.d - 1u);
@@ -227,9 +226,8 @@ struct Item {
             for (int s = 0; s < kKeySteps; ++s) {
                 const int32_t d = operand_element(s, lane);
                 u32x4 x = u32x4{0u, 0u, 0u, 0u};
-                if ((kWhole || d < args.cache.c.dim) && c != 0.0f) x = *reinterpret_cast<const u32x4*>(from + d);
-                if (c < 0.0f) x ^= 0x80008000u;  // so that scores grow with the products
-                q[n][s] = __builtin_bit_cast(bf16x8, x);
+                if (kWhole || d < args.cache.c.dim) x = *reinterpret_cast<const u32x4*>(from + d);
+                q[n][s] = __builtin_bit_cast(bf16x8, signed_query(x, a.scale));
             }
         }
     }

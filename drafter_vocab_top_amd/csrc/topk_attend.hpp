@@ -324,6 +324,23 @@ __device__ __forceinline__ uint32_t only_finite(uint32_t x, uint32_t& odd) {
     return x & ~((b << 1) - (b >> 15));
 }
 
+// 0 times two bfloat16 values: 0, or NaN where one is not finite.
+__device__ __forceinline__ uint32_t times_zero(uint32_t x) {
+    const uint32_t b = ((x & 0x7F807F80u) + 0x00800080u) & 0x80008000u;  // (as above)
+    return ((b << 1) - (b >> 15)) & 0x7FFF7FFFu;
+}
+
+// Eight elements of a query as the products take them: such that the scores grow with the products, by a factor that
+// is positive.
+__device__ __forceinline__ u32x4 signed_query(u32x4 x, float scale) {
+    if (scale < 0.0f) x ^= 0x80008000u;
+    if (scale == 0.0f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = times_zero(x[i]);
+    }
+    return x;
+}
+
 // The weight of place `key` of 32 for this lane's query.
 __device__ __forceinline__ float weight_of(const bf16x8& weights, uint32_t key, uint32_t r) {
     const u32x4 y = __builtin_bit_cast(u32x4, weights);

@@ -269,9 +269,8 @@ __global__ __launch_bounds__(64 * (kGroups < 4 ? 4 : kGroups), DP < 256 ? 2 : 1)
                 for (int s = 0; s < I::kKeySteps; ++s) {
                     const int32_t d = s * 32 + (int32_t)g * 8;
                     u32x4 x = u32x4{0u, 0u, 0u, 0u};
-                    if ((kWhole || d < c.dim) && a.scale != 0.0f) x = *reinterpret_cast<const u32x4*>(from + d);
-                    if (a.scale < 0.0f) x ^= 0x80008000u;  // so that scores grow with the products
-                    q[n][s] = __builtin_bit_cast(bf16x8, x);
+                    if (kWhole || d < c.dim) x = *reinterpret_cast<const u32x4*>(from + d);
+                    q[n][s] = __builtin_bit_cast(bf16x8, signed_query(x, a.scale));
                 }
             }
         }

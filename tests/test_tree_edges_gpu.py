@@ -270,3 +270,31 @@ def test_attend_windows_and_masks(gpu, group):
             for out, seen in ((chain, (column <= j) & near), (whole, (column <= j) & (near | (column >= 0)))):
                 want, bound = dense(torch, q[own].double().view(n, H, group, dim), lane_k, lane_v, seen, dim**-0.5)
                 check(torch, out[own], want, bound, f"lane {l}, window {window}")
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("dim", [64, 112, 128, 208])
+@pytest.mark.parametrize("rows", ROWS)
+def test_attend_a_scale_of_zero(gpu, rows, dim, fp8):
+    """All places weigh alike, but for queries that are not finite: 0 times them is NaN."""
+    torch, T = gpu
+    g = torch.Generator(device="cuda").manual_seed(2)
+    L, bs, group, H = 2, 16, 4, 2
+    n = rows // group
+    lens = torch.tensor([70, 0], device="cuda")
+    width = (70 + n) // bs + 1
+    (k, ks, kd), (v, vs, vd) = (stored(torch, (L * width, bs, H, dim), fp8, g) for _ in range(2))
+    cache = T.KeyCache(k, v, *([ks, vs] if fp8 else []))
+    table = torch.full((L, 2_000_000 // bs), -1, dtype=torch.int32, device="cuda")  # (the room decides the items' sizes)
+    table[:, :width] = torch.randperm(L * width, generator=g, device="cuda").view(L, width)
+    q = torch.randn(L * n, H * group, dim, generator=g, device="cuda").to(torch.bfloat16)
+    for x in (math.nan, math.inf, -math.inf):
+        q[int(torch.randint(0, L * n, (), generator=g, device="cuda")), int(torch.randint(0, H * group, (), generator=g, device="cuda")), dim // 3] = x
+    for scale in (0.0, -0.0):
+        out = cache.attend(q, lens.int(), table, scale=scale)
+        for l in range(L):
+            own, p = slice(l * n, (l + 1) * n), torch.arange(int(lens[l]) + n, device="cuda")
+            lane_k, lane_v = (x.reshape(-1, H, dim)[table[l, p // bs].long() * bs + p % bs] for x in (kd, vd))
+            seen = p[None] - lens[l] <= torch.arange(n, device="cuda")[:, None]
+            want, bound = dense(torch, q[own].double().view(n, H, group, dim), lane_k, lane_v, seen, scale)
+            check(torch, out[own], want, bound, f"lane {l}, scale {scale}")
