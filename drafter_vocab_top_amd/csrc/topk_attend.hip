@@ -227,9 +227,10 @@ struct Item {
                 const int32_t d = operand_element(s, lane);
                 u32x4 x = u32x4{0u, 0u, 0u, 0u};
                 if (kWhole || d < args.cache.c.dim) x = *reinterpret_cast<const u32x4*>(from + d);
-                q[n][s] = __builtin_bit_cast(bf16x8, signed_query(x, a.scale));
+                q[n][s] = __builtin_bit_cast(bf16x8, x);
             }
         }
+        sign_queries(q, a.scale);
     }
 };
 

@@ -330,15 +330,20 @@ __device__ __forceinline__ uint32_t times_zero(uint32_t x) {
     return ((b << 1) - (b >> 15)) & 0x7FFF7FFFu;
 }
 
-// Eight elements of a query as the products take them: such that the scores grow with the products, by a factor that
-// is positive.
-__device__ __forceinline__ u32x4 signed_query(u32x4 x, float scale) {
-    if (scale < 0.0f) x ^= 0x80008000u;
-    if (scale == 0.0f) {
+// Queries as the products take them: such that the scores grow with the products, by a factor that is positive.  (One
+// branch, which positive scales skip: a choice for each element made one lane's columns over 2,048 places 2 % slower.)
+template <int kQueries, int kKeySteps>
+__device__ __forceinline__ void sign_queries(bf16x8 (&q)[kQueries][kKeySteps], float scale) {
+    if (scale > 0.0f) return;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = times_zero(x[i]);
-    }
-    return x;
+    for (int n = 0; n < kQueries; ++n)
+#pragma unroll
+        for (int s = 0; s < kKeySteps; ++s) {
+            u32x4 x = __builtin_bit_cast(u32x4, q[n][s]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = scale < 0.0f ? x[i] ^ 0x80008000u : times_zero(x[i]);
+            q[n][s] = __builtin_bit_cast(bf16x8, x);
+        }
 }
 
 // The weight of place `key` of 32 for this lane's query.

@@ -270,9 +270,10 @@ __global__ __launch_bounds__(64 * (kGroups < 4 ? 4 : kGroups), DP < 256 ? 2 : 1)
                     const int32_t d = s * 32 + (int32_t)g * 8;
                     u32x4 x = u32x4{0u, 0u, 0u, 0u};
                     if (kWhole || d < c.dim) x = *reinterpret_cast<const u32x4*>(from + d);
-                    q[n][s] = __builtin_bit_cast(bf16x8, signed_query(x, a.scale));
+                    q[n][s] = __builtin_bit_cast(bf16x8, x);
                 }
             }
+            sign_queries(q, a.scale);
         }
         if (a.window) {  // all rows of the item see the places from here up to the lane's columns
             if (threadIdx.x % 64u == 0u) lds_see[wave] = all_see;
