@@ -719,6 +719,8 @@ class KeyCache:
             raise ValueError("scales must be uint8 tensors of the keys' shape without dim")
         shape = tuple(keys.shape) if keys.dim() == 5 else (1, *keys.shape)
         self.layers, self.blocks, self.block_size, self.heads, self.dim = shape
+        if max(shape[2:]) > 2**31 - 1:  # (their fields are 32-bit numbers)
+            raise ValueError("block_size, heads and dim must be at most 2^31 - 1")
 
         def strides(a, b, what):
             # (a dimension of one entry has no stride)

@@ -298,3 +298,15 @@ def test_attend_a_scale_of_zero(gpu, rows, dim, fp8):
             seen = p[None] - lens[l] <= torch.arange(n, device="cuda")[:, None]
             want, bound = dense(torch, q[own].double().view(n, H, group, dim), lane_k, lane_v, seen, scale)
             check(torch, out[own], want, bound, f"lane {l}, scale {scale}")
+
+
+def test_caches_of_sizes_past_32_bits_are_refused(gpu):
+    """Sizes whose fields are 32-bit numbers are not cut to them."""
+    torch, T = gpu
+    row = torch.zeros(1, 1, 1, 1, 16, dtype=torch.bfloat16, device="cuda")
+    for dim in (2, 3):
+        shape = [1, 1, 1, 1, 16]
+        shape[dim] = 2**32 + 16
+        with pytest.raises(ValueError):
+            T.KeyCache(row.expand(shape), row.expand(shape))
+    T.KeyCache(row.expand(1, 1, 16, 16, 16), row.expand(1, 1, 16, 16, 16))
