@@ -29,7 +29,7 @@
 // and output in the workspace, and a second kernel joins them.
 //
 // Memory bounds it: 2 lanes of 6 columns over 98,304 bfloat16 places of 8 key
-// heads of 128 are 806 MB in 156 us, 5.2 TB/s where a large copy makes 5.4 (146
+// heads of 128 are 806 MB in 152 us, 5.3 TB/s where a large copy makes 5.4 (140
 // us of it in this kernel, 10 in the join).  An e4m3 cache, whose rows are 128
 // bytes, is read at 4.1 TB/s (64 lanes of 6 columns over 6,144 places: 826 MB in
 // 200 us; the same with every block in cache 111 us); twice as many places in

@@ -255,9 +255,12 @@ __device__ __forceinline__ uint32_t max_of_16(uint32_t x) {
 
 // Scores of 16 kQueries queries against 32 kTiles places become weights: lane 16 g + r has query r of each 16 and
 // places 4 g + i and 16 + 4 g + i of each 32.  m, sum and o (16 x 16 tiles, a query in each column) are the running
-// maximum, sum and output.  The sum is a product with ones: it is of the weights as they are rounded for the products
-// with values.  `seen`: with `masked`, the places that each query sees.  (m, sum and o may be of more queries: the first
-// ones are these.)
+// maximum, sum and output, all in binary32.  The weights are rounded to bfloat16, which the products with values take:
+// each is off by at most 2^-8 of itself, whatever its size (binary16 would be nearer, but neither it nor its products
+// reach as far as bfloat16 values do; two bfloat16 halves would be half as many products again).  The sum is a product
+// with ones, of the weights as they are rounded, so that a common part of their errors cancels.  Over 131,072 places
+// outputs are off by 0.0023 of their size on the whole, of which 0.0017 are their own rounding.  `seen`: with `masked`,
+// the places that each query sees.  (m, sum and o may be of more queries: the first ones are these.)
 template <int kTiles, int kQueries, int kOut, int kAll>
 __device__ __forceinline__ void weigh(f32x4 (&s)[kTiles][kQueries][2], bool masked, const uint32_t (&seen)[kTiles][kQueries], float factor,
                                       uint32_t g, float (&m)[kAll], f32x4 (&sum)[kAll], f32x4 (&o)[kAll][kOut],

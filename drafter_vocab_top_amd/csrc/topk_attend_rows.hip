@@ -14,9 +14,14 @@
 // 32 rows in items of 256 take 267 us (442 with all products made), 16 lanes of
 // 64 rows, bfloat16, 106 (137), full items of 128 rows 2 % longer.
 //
-// 64 lanes of 48 rows over 6,144 e4m3 places of 8 key heads of 128: 826 MB in 210
-// us, 3.9 TB/s (a large copy makes 5.4).  16 lanes of 192 rows, bfloat16: 418 MB
-// and 78 GFLOP in 144 us.  Neither memory nor the matrix cores (20 and 32 % of
+// Without a mask all places up to the lane's last column are passed for each of
+// its items, those behind an item's own columns among them: 8 prompts of 2,048
+// columns with 32 query heads take 880 us, 0.62 PFLOP/s of the products made and
+// half of that of the products needed.
+//
+// 64 lanes of 48 rows over 6,144 e4m3 places of 8 key heads of 128: 826 MB in 208
+// us, 4.0 TB/s (a large copy makes 5.4).  16 lanes of 192 rows, bfloat16: 418 MB
+// and 78 GFLOP in 139 us.  Neither memory nor the matrix cores (20 and 32 % of
 // the time) bound it: a wave's products, weights and staging follow one another,
 // and two waves on a SIMD overlap them in part.  Priorities for one of the two,
 // and scores of the next places made among the weights of these (which takes
