@@ -27,8 +27,9 @@ def worth(torch, bits, scales):
 def dense(torch, q, k, v, see, scale):
     """The columns q (n, heads, group, dim) of one lane over its places k, v (places, heads, dim), all float64; see
     (n, places).  Returns out and, for each element, what roundings move it by at most: a weight is rounded to bfloat16
-    (half a step, 2^-8), its score is a binary32 sum of dim products, scaled, less a maximum; then exponentials, the
-    sums over places in binary32, and the result's own rounding."""
+    (half a step, 2^-8), its score is a binary32 sum of dim products, scaled, less a maximum; then exponentials.  Weights
+    w (1 + r) with |r| <= rel move sum w v / sum w by at most (sum w rel |v| + |out| sum w rel) / sum w, but for products
+    of these.  Then the sums over places in binary32, and the result's own rounding."""
     n, heads, group, dim = q.shape
     eps = 2.0**-8
     s = scale * torch.matmul(q.permute(1, 0, 2, 3).reshape(heads, n * group, dim), k.permute(1, 2, 0)).view(heads, n, group, -1)
@@ -44,7 +45,7 @@ def dense(torch, q, k, v, see, scale):
     out = torch.matmul(w, values) / total
     rel = eps + (dim + 8) * 2.0**-24 * (spread + s.abs()) + 2.0**-22 * top.abs() + 2.0**-20
     rel = torch.where(s == -math.inf, eps, rel)
-    moved = torch.matmul(w * rel, values.abs()) / total + out.abs() * ((w * (rel - eps)).sum(-1, keepdim=True) / total)
+    moved = (torch.matmul(w * rel, values.abs()) + out.abs() * (w * rel).sum(-1, keepdim=True)) / total * (1 + 2.0**-6)
     sums = (see.sum(-1)[None, :, None, None] + 16) * 2.0**-23 * torch.matmul(w, values.abs()) / total
     bound = moved + sums + (out.abs() + moved + sums) * eps
     none = total == 0
