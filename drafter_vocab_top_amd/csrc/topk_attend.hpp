@@ -80,14 +80,16 @@ __device__ __forceinline__ uint64_t bcast(uint64_t x, uint32_t lane) {
 }
 
 // The steps of all lanes (the sum), or with `find` the lane that step `at` of
-// them belongs to; `before` gets the steps of the lanes before it.  All of a
-// wave's threads take part, 64 lanes at a time.
+// them belongs to; `before` gets the steps of the lanes before it.  It is looked
+// for from `lane` on, `before` being the steps of those before that one: a
+// workgroup's steps only grow, so it passes each lane once.  All of a wave's
+// threads take part, 64 lanes at a time.
 template <uint32_t kStep>
 __device__ __forceinline__ uint64_t all_steps(const AttendArgs& args, const Shape& sh, bool find, uint64_t at, uint64_t& before,
                                               uint32_t& lane, LaneWork& work) {
     const uint32_t lanes = (uint32_t)args.a.lanes, id = threadIdx.x & 63u;
-    uint64_t sum = 0;
-    for (uint32_t l0 = 0; l0 < lanes; l0 += 64u) {
+    uint64_t sum = find ? before : 0;
+    for (uint32_t l0 = find ? lane : 0; l0 < lanes; l0 += 64u) {
         const uint32_t l = min_u32(l0 + id, lanes - 1u);
         const int32_t* s = args.cols.at(l);
         const int32_t b = s[0], e = s[args.cols.start ? 1 : 0], len = args.a.lens[l];
@@ -160,7 +162,7 @@ struct Steps {
         if (!kept) total = all_steps<kStep>(args, sh, false, 0, before, lane, own);
     }
 
-    // The lane that step `at` belongs to, and the steps of those before it.
+    // The lane that step `at` belongs to, and the steps of those before it (at first those of a lane that is not behind it).
     __device__ __forceinline__ void find(const AttendArgs& args, const Shape& sh, uint64_t at, uint64_t& before, uint32_t& lane, LaneWork& w) const {
         if (!kept) {
             all_steps<kStep>(args, sh, true, at, before, lane, w);

@@ -311,3 +311,51 @@ def test_caches_of_sizes_past_32_bits_are_refused(gpu):
         with pytest.raises(ValueError):
             T.KeyCache(row.expand(shape), row.expand(shape))
     T.KeyCache(row.expand(1, 1, 16, 16, 16), row.expand(1, 1, 16, 16, 16))
+
+
+def test_rounds_of_very_many_lanes(gpu):
+    """More lanes than a grid is high, of two columns each: masks, attention, verification, moves."""
+    torch, T = gpu
+    g = torch.Generator(device="cuda").manual_seed(1)
+    L, n, bs, dim = 70000, 2, 4, 64
+    cs = torch.cumsum(torch.randint(0, n + 1, (L,), generator=g, device="cuda"), 0)  # some lanes have none
+    cs = torch.cat([torch.zeros(1, dtype=torch.long, device="cuda"), cs]).int()
+    (k, _, kd), (v, _, vd) = (stored(torch, (2 * L, bs, 1, dim), False, g) for _ in range(2))
+    cache = T.KeyCache(k, v)
+    table = torch.randperm(2 * L, generator=g, device="cuda").int().view(L, 2)
+    lens = torch.randint(0, 7, (L,), generator=g, device="cuda").int()
+    C = int(cs[-1])
+    lane = torch.repeat_interleave(torch.arange(L, device="cuda"), cs.diff().long())
+    j = torch.arange(C, device="cuda") - cs[lane].long()
+    mask, positions = T.tree((j - 1).int(), lens, cs, words=1)
+    assert torch.equal(mask[:, 0], torch.where(j == 0, 1, 3).int()) and torch.equal(positions, lens[lane] + j.int())
+    q = torch.randn(C, 2, dim, generator=g, device="cuda").to(torch.bfloat16)
+    out = cache.attend(q, lens, table, cs, mask=mask, positions=positions)
+    p = torch.arange(2 * bs, device="cuda")
+    at = table[:, p // bs].long() * bs + p % bs
+    lane_k, lane_v = (x.view(-1, dim)[at][lane] for x in (kd, vd))  # (C, places, dim)
+    seen = p[None] <= (lens[lane] + j)[:, None]
+    for part in range(0, C, 20000):
+        own = slice(part, min(part + 20000, C))
+        s = torch.matmul(q[own].double(), lane_k[own].transpose(1, 2)) * dim**-0.5
+        w = torch.softmax(torch.where(seen[own][:, None], s, -math.inf), -1)
+        want, size = torch.matmul(w, lane_v[own]), torch.matmul(w, lane_v[own].abs())
+        # weights are rounded to bfloat16 in the sum over values and in their own, the result once more, 2^-8 each; scores
+        # (64 products in binary32, 72 roundings of at most 16 in all magnitudes) and the products of errors are below 2^-13
+        assert ((out[own].double() - want).abs() <= (size + 2 * want.abs()) * (2.0**-8 + 2.0**-13)).all()
+    columns = torch.full((L, 2), -1, dtype=torch.int32, device="cuda")
+    columns[:, 0] = torch.randint(0, 2, (L,), generator=g, device="cuda").int()
+    flat = k.view(-1, dim).clone()
+    l = (columns[:, 0] == 1).nonzero()[:, 0]
+    to, of = (at[l, (lens[l] + i).long()] for i in (0, 1))  # the place behind the lane's tokens gets the next one's row
+    flat[to] = flat[of]
+    cache.move(lens, table, columns)
+    assert torch.equal(k.view(-1, dim), flat)
+    values = torch.sort(torch.randn(C, 4, generator=g, device="cuda"), descending=True)[0]
+    ids = torch.arange(4, device="cuda").int().expand(C, 4).contiguous()
+    tokens = torch.randint(0, 4, (C,), generator=g, device="cuda").int()
+    _, _, count = T.verify_tree(values, ids, cs, tokens, (j - 1).int(), torch.rand(C, 2, generator=g, device="cuda"),
+                                temperature=0.0, max_tokens=2)
+    accepted = torch.zeros(L, dtype=torch.int32, device="cuda")
+    accepted[lane[(j == 1) & (tokens == 0)]] = 1  # greedy: token 0 is every list's first
+    assert torch.equal(count, accepted + (cs.diff() > 0).int())
